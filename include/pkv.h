@@ -332,6 +332,163 @@ int pkv_paged_prefill(const pkv_kvcache *c, int32_t layer_id, const void *q, voi
                       float sm_scale, const pkv_workspace *ws, void *stream);
 
 /*
+ * Tables of a step, built on the GPU ("KVCache System": the page table, the
+ * slot maps and the prefix sums that the host otherwise computes from the
+ * requests' lengths).  Entry b < c->batch has context length n =
+ * c->seq_lens[b] INCLUDING its q = q_lens[b] new tokens (q_lens NULL: one new
+ * token for each entry with n > 0), which stand at positions [n - q, n) of
+ * request row r = c->req_pool_indices[b].  With ps = page_size:
+ *   - its pages ceil((n-q)/ps) .. ceil(n/ps)-1 are new: the entries take
+ *     them in entry order from free_pages[*free_start ..], lowest page of the
+ *     entry first, and they are written to req_to_page[r];
+ *   - *free_end = *free_start + the pages taken.  The two are different words
+ *     (a step that is replayed from a CUDA graph swaps or copies them);
+ *   - kv_indptr[b+1] and qo_indptr[b+1] (each may be NULL) are the prefix sums
+ *     of n and q, [0] = 0;
+ *   - new token i, in entry order (the order of qo_indptr), gets positions[i]
+ *     (may be NULL), out_cache_loc[i] = page * ps + position % ps with the
+ *     page of req_to_page, and, where req_to_token is given,
+ *     req_to_token[r, position] = the same slot.
+ * All arrays are int32 device arrays.  out_cache_loc and positions hold
+ * max_new entries; what lies behind the last new token is left as it was, and
+ * so are table columns of positions that are not new.  The pages of earlier
+ * positions (a partly filled last page, a cached prefix) are read from
+ * req_to_page.  One kernel; nothing is allocated.
+ * Reads c->batch, c->req_pool_indices, c->seq_lens, c->num_reqs,
+ * c->max_ctx_len (with req_to_token) and c->size (a multiple of page_size).
+ * Request rows of entries with new tokens must be distinct within a call
+ * (else the tables of a row that stands twice are unspecified).
+ * Device-data errors: a request row outside [0, num_reqs), n outside
+ * [0, max_pages * ps] (or beyond max_ctx_len with req_to_token), q outside
+ * [0, n] (such an entry counts as n = q = 0); more new tokens than max_new
+ * (those beyond are dropped); a prefix sum beyond 2^31 - 1; a page outside
+ * [0, size / ps) in req_to_page or free_pages, or a free list that runs out
+ * (the tokens concerned get slot -1, and new pages of theirs -1, which the
+ * write refuses in turn); *free_start outside [0, n_free].
+ */
+typedef struct pkv_tables {
+    const int32_t *q_lens;       /* [batch], or NULL */
+    int32_t *req_to_page;        /* [num_reqs, max_pages], in and out */
+    int32_t max_pages;
+    int32_t page_size;
+    const int32_t *free_pages;   /* [n_free] */
+    const int32_t *free_start;   /* [1] */
+    int32_t *free_end;           /* [1] */
+    int32_t n_free;
+    int32_t max_new;
+    int32_t *kv_indptr;          /* [batch + 1], or NULL */
+    int32_t *qo_indptr;          /* [batch + 1], or NULL */
+    int32_t *positions;          /* [max_new], or NULL */
+    int32_t *out_cache_loc;      /* [max_new] */
+    int32_t *req_to_token;       /* [num_reqs, max_ctx_len], or NULL */
+} pkv_tables;
+
+int pkv_build_tables(const pkv_kvcache *c, const pkv_tables *t, void *stream);
+
+/*
+ * Sparse decode: attention over the pages that a cheap score selects for each
+ * query.  The cache is a pool of pages of page_size consecutive slots behind a
+ * page table (as for pkv_paged_decode_pages; c->req_to_token and
+ * c->max_ctx_len are not read), and beside the pool stands, for each page and
+ * kv head, the channelwise minimum and maximum of the keys written to it:
+ *   page_bounds  [n_layers, size / page_size, n_kv_heads, 2, head_dim] of
+ *                c->dtype, minimum at [.., 0, :], maximum at [.., 1, :];
+ *   req_to_page  int32 [num_reqs, max_pages];
+ *   top_k        pages selected per (entry, kv head) at most; n_first and
+ *                n_last of them are the context's first and last pages
+ *                (n_first + n_last <= top_k).
+ * An entry of c->req_pool_indices / c->seq_lens is one query.  The queries of
+ * a prompt, or of a speculative draft, are entries that name the same request
+ * row with growing seq_lens.
+ */
+typedef struct pkv_pages {
+    void *page_bounds;
+    const int32_t *req_to_page;
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t top_k;
+    int32_t n_first;
+    int32_t n_last;
+} pkv_pages;
+
+/*
+ * Bring page_bounds of layer `layer_id` up to date with the n_new keys that
+ * were written to the slots c->out_cache_loc[0 .. n_new) of c->k_buffer (by
+ * pkv_kv_write, pkv_rope_kv_write or pkv_decode_step on the same stream).
+ * A key at the first slot of a page starts the page's bounds anew; other keys
+ * widen the bounds that the page has.  The new tokens of a page stand next to
+ * each other in out_cache_loc in ascending slot order, as pkv_build_tables
+ * and the prefill's order give them (else that page's bounds are
+ * unspecified).  Exact; a NaN key makes its channel's bounds NaN.  Requires
+ * 16-byte aligned page_bounds and head rows of a multiple of 16 bytes.  Slots
+ * outside [0, size) are device-data errors and are passed over.  n_new = 0 is a
+ * no-op.  Does not read req_to_page.
+ */
+int pkv_page_bounds(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, int32_t n_new,
+                    void *stream);
+
+/*
+ * Select pages.  For entry b with N = ceil(c->seq_lens[b] / page_size) pages,
+ * kv head g and page p:
+ *   score = max over the G query heads h of the group of
+ *           sum_c max(q[b,h,c] * minimum[c], q[b,h,c] * maximum[c]),
+ * the largest product that the query can have with any key inside the page's
+ * bounds.  With N <= top_k every page is selected; otherwise the first n_first
+ * and the last n_last pages, and of the rest the top_k - n_first - n_last of
+ * largest score.  The order is that of the scores in 64 bits: scores are
+ * computed in 32 bits with a bound on their error, and those that the bound
+ * leaves undecided are computed again in 64.  Equal scores go to the lowest
+ * page, NaN ranks above every number.
+ *   sel         int32 [batch, n_kv_heads, top_k]: logical pages, ascending,
+ *               then -1;
+ *   sel_counts  int32 [batch, n_kv_heads]: min(N, top_k).
+ * A context whose length is 0 gets the count 0.  q: [batch, n_heads,
+ * head_dim] of c->dtype.  Scores go to the workspace: ws->bytes must be
+ * pkv_select_workspace_bytes(...) at least (ws may be NULL while c->max_len
+ * needs no more than top_k pages).  A context has 2^30 pages at most.
+ * Supported: f32 and bf16, head_dim 64 or
+ * 128, G in {1, 2, 4, 8}.  A request row outside [0, num_reqs) (count 0), a
+ * length outside [0, c->max_len] (clamped) and a page outside [0, size /
+ * page_size) (page 0 in its place) are device-data errors.
+ */
+int pkv_select_pages(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const void *q,
+                     int32_t n_heads, int32_t *sel, int32_t *sel_counts, const pkv_workspace *ws,
+                     void *stream);
+
+/* Workspace bytes that pkv_select_pages needs (0 if any argument is < 1). */
+size_t pkv_select_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max_len,
+                                  int32_t page_size);
+
+/*
+ * Paged decode attention over selected pages: pkv_paged_decode_pages with the
+ * sum of entry b, kv head g running over the positions j < c->seq_lens[b] that
+ * lie in the logical pages sel[b, g, 0 .. sel_counts[b, g]) only.  sel:
+ * int32 [batch, n_kv_heads, pg->top_k] (any order; a page that is listed twice
+ * counts twice), sel_counts: int32 [batch, n_kv_heads].  No selected position
+ * gives o = 0.  Reads neither page_bounds nor n_first / n_last and needs no
+ * workspace: the CTAs that share an entry's kv head form a thread-block
+ * cluster and join their partials in shared memory.  Accumulation in fp32, one
+ * rounding to the output dtype.  Supported: f32 and bf16, head_dim 64 or 128,
+ * G in {1, 2, 4, 8}.  Device-data errors as for pkv_select_pages, and a count
+ * outside [0, top_k] (clamped) or a listed page outside the context (skipped).
+ */
+int pkv_paged_decode_selected(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg,
+                              const int32_t *sel, const int32_t *sel_counts, const void *q, void *o,
+                              int32_t n_heads, float sm_scale, void *stream);
+
+/*
+ * One sparse decode step of a layer: pkv_kv_write of k_new / v_new (n_new rows
+ * at c->out_cache_loc, n_new may be 0), pkv_page_bounds, pkv_select_pages and
+ * pkv_paged_decode_selected, made back to back on `stream` with the later
+ * launches overlapping the earlier ones.  Arguments, results and errors are
+ * those of the four calls; all are validated before any is enqueued.
+ */
+int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg,
+                           const void *k_new, const void *v_new, int32_t n_new, const void *q,
+                           void *o, int32_t n_heads, float sm_scale, int32_t *sel,
+                           int32_t *sel_counts, const pkv_workspace *ws, void *stream);
+
+/*
  * Paged decode for callers that cannot allocate device memory: code running
  * while another component holds a stream capture open in global mode (where
  * cudaMalloc is not allowed), plugins inside engines whose allocator owns all
@@ -371,7 +528,8 @@ int pkv_paged_decode_noalloc(const pkv_kvcache *c, int32_t layer_id, const void 
  *                  slots) differ from the first entry's (head_dim 128) or
  *                  from its group's first entry's (head_dim 64);
  *   -200000 - c    shared-prefix CTA c was handed more positions than it
- *                  stages (not expected: the host sizes the grid for it).
+ *                  stages (not expected: the host sizes the grid for it);
+ *   -300000 - b    the free list of pkv_build_tables ran out at entry b.
  * An offending value can itself be negative (a negative slot, say).
  */
 int pkv_last_device_error(void *stream, int64_t *detail);

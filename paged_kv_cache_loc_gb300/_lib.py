@@ -57,6 +57,39 @@ class PkvWorkspace(ctypes.Structure):
     ]
 
 
+class PkvTables(ctypes.Structure):
+    """struct pkv_tables."""
+    _fields_ = [
+        ("q_lens", _vp),
+        ("req_to_page", _vp),
+        ("max_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("free_pages", _vp),
+        ("free_start", _vp),
+        ("free_end", _vp),
+        ("n_free", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("kv_indptr", _vp),
+        ("qo_indptr", _vp),
+        ("positions", _vp),
+        ("out_cache_loc", _vp),
+        ("req_to_token", _vp),
+    ]
+
+
+class PkvPages(ctypes.Structure):
+    """struct pkv_pages."""
+    _fields_ = [
+        ("page_bounds", _vp),
+        ("req_to_page", _vp),
+        ("max_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("n_first", ctypes.c_int32),
+        ("n_last", ctypes.c_int32),
+    ]
+
+
 # name -> (restype, argtypes); every symbol declared in include/pkv.h
 SIGNATURES = {
     "pkv_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 4),
@@ -91,6 +124,20 @@ SIGNATURES = {
                                          ctypes.POINTER(PkvWorkspace), _vp]),
     "pkv_paged_decode_noalloc": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.c_int32, _vp,
                                                 _vp, ctypes.c_int32, ctypes.c_float, _vp]),
+    "pkv_build_tables": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.POINTER(PkvTables), _vp]),
+    "pkv_page_bounds": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.c_int32,
+                                       ctypes.POINTER(PkvPages), ctypes.c_int32, _vp]),
+    "pkv_select_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 4),
+    "pkv_select_pages": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.c_int32,
+                                        ctypes.POINTER(PkvPages), _vp, ctypes.c_int32, _vp, _vp,
+                                        ctypes.POINTER(PkvWorkspace), _vp]),
+    "pkv_paged_decode_selected": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.c_int32,
+                                                 ctypes.POINTER(PkvPages), _vp, _vp, _vp, _vp,
+                                                 ctypes.c_int32, ctypes.c_float, _vp]),
+    "pkv_sparse_decode_step": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.c_int32,
+                                              ctypes.POINTER(PkvPages), _vp, _vp, ctypes.c_int32,
+                                              _vp, _vp, ctypes.c_int32, ctypes.c_float, _vp, _vp,
+                                              ctypes.POINTER(PkvWorkspace), _vp]),
     "pkv_last_device_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_int64)]),
     # include/pkv_pool.h (host page allocator)
     "pkv_pool_create": (_vp, [ctypes.c_int32, ctypes.c_int32]),

@@ -612,6 +612,299 @@ int pkv_paged_prefill(const pkv_kvcache *c, int32_t layer_id, const void *q, voi
                                           static_cast<cudaStream_t>(stream)));
 }
 
+int pkv_build_tables(const pkv_kvcache *c, const pkv_tables *t, void *stream) {
+    if (!c || !t) return PKV_ERR_ARG;
+    if (c->batch < 0 || c->batch > 65535 || t->max_new < 0 || t->n_free < 0) return PKV_ERR_ARG;
+    if (c->num_reqs <= 0 || t->max_pages <= 0 || t->page_size <= 0) return PKV_ERR_ARG;
+    if (c->size <= 0 || c->size > INT32_MAX || c->size % t->page_size) return PKV_ERR_ARG;
+    if (static_cast<int64_t>(t->max_pages) * t->page_size > INT32_MAX) return PKV_ERR_ARG;
+    if (t->req_to_token && c->max_ctx_len <= 0) return PKV_ERR_ARG;
+    if (!t->req_to_page || !t->free_start || !t->free_end || t->free_start == t->free_end) return PKV_ERR_ARG;
+    if (c->batch > 0 && (!c->req_pool_indices || !c->seq_lens)) return PKV_ERR_ARG;
+    if ((t->n_free > 0 && !t->free_pages) || (t->max_new > 0 && !t->out_cache_loc)) return PKV_ERR_ARG;
+    DeviceInfo di;
+    int rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({c->req_pool_indices, c->seq_lens, t->q_lens, t->req_to_page, t->free_pages, t->free_start,
+                        t->free_end, t->kv_indptr, t->qo_indptr, t->positions, t->out_cache_loc, t->req_to_token});
+    if (rc) return rc;
+    pkv::TablesParams p{};
+    p.req_pool_indices = c->req_pool_indices;
+    p.seq_lens = c->seq_lens;
+    p.q_lens = t->q_lens;
+    p.req_to_page = t->req_to_page;
+    p.free_pages = t->free_pages;
+    p.free_start = t->free_start;
+    p.free_end = t->free_end;
+    p.kv_indptr = t->kv_indptr;
+    p.qo_indptr = t->qo_indptr;
+    p.positions = t->positions;
+    p.out_cache_loc = t->out_cache_loc;
+    p.req_to_token = t->req_to_token;
+    p.n_pages = c->size / t->page_size;
+    p.batch = c->batch;
+    p.num_reqs = c->num_reqs;
+    p.max_ctx_len = c->max_ctx_len;
+    p.max_len = t->max_pages * t->page_size;
+    if (t->req_to_token && c->max_ctx_len < p.max_len) p.max_len = c->max_ctx_len;
+    p.max_pages = t->max_pages;
+    p.page_size = t->page_size;
+    p.n_free = t->n_free;
+    p.max_new = t->max_new;
+    // every CTA sums all lengths, so a CTA gets 1024 tokens at least and the
+    // grid two CTAs per SM at most
+    const int64_t most = 2LL * (di.sms > 0 ? di.sms : 1);
+    int64_t chunk = (t->max_new + most - 1) / most;
+    p.chunk = static_cast<int32_t>(chunk < 1024 ? 1024 : chunk);
+    p.err = di.err;
+    return map_launch(pkv::launch_build_tables(p, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Checks of the pool and page-table sizes that the sparse entry points share.
+int check_pages(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg) {
+    int rc = check_pool(c, layer_id);
+    if (rc) return rc;
+    if (!pg || pg->page_size <= 0 || c->size % pg->page_size) return PKV_ERR_ARG;
+    return PKV_OK;
+}
+
+// Those of an entry point that attends or selects.
+int check_sparse(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const void *q, int32_t n_heads,
+                 const int32_t *sel, const int32_t *sel_counts, bool selects) {
+    int rc = check_pages(c, layer_id, pg);
+    if (rc) return rc;
+    if (!pg->req_to_page || pg->max_pages <= 0 || c->num_reqs <= 0) return PKV_ERR_ARG;
+    if (c->batch < 0 || c->batch > 65535 || c->max_len < 0) return PKV_ERR_ARG;
+    if (c->max_len > static_cast<int64_t>(pg->max_pages) * pg->page_size) return PKV_ERR_ARG;
+    if (n_heads <= 0 || n_heads % c->n_kv_heads || c->n_kv_heads > 65535) return PKV_ERR_ARG;
+    if (pg->top_k <= 0 || static_cast<int64_t>(pg->top_k) * pg->page_size > 1 << 30) return PKV_ERR_ARG;
+    if (selects && (pg->n_first < 0 || pg->n_last < 0 || static_cast<int64_t>(pg->n_first) + pg->n_last > pg->top_k))
+        return PKV_ERR_ARG;
+    if (c->batch > 0 && (!c->req_pool_indices || !c->seq_lens || !q || !aligned16(q) || !sel || !sel_counts))
+        return PKV_ERR_ARG;
+    if (!pkv::sparse_supported(c->dtype, c->head_dim, n_heads / c->n_kv_heads)) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+int bounds_prepare(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, int32_t n_new, const DeviceInfo &di,
+                   const void *keys, pkv::BoundsParams *out) {
+    pkv::BoundsParams &p = *out;
+    p = pkv::BoundsParams{};
+    const int elem = elem_bytes(c->dtype);
+    p.keys = keys;
+    p.k_buffer = c->k_buffer;
+    p.page_bounds = pg->page_bounds;
+    p.out_cache_loc = c->out_cache_loc;
+    p.size = c->size;
+    p.layer_row0 = static_cast<int64_t>(layer_id) * c->size;
+    p.layer_page0 = static_cast<int64_t>(layer_id) * (c->size / pg->page_size);
+    p.n_new = n_new;
+    p.page_size = pg->page_size;
+    p.row_chunks = c->n_kv_heads * c->head_dim * elem / 16;
+    p.head_chunks = c->head_dim * elem / 16;
+    p.dtype = c->dtype;
+    // about eight CTAs per SM; one token per CTA while the batch is small
+    const int64_t blocks = 8LL * (di.sms > 0 ? di.sms : 1);
+    const int64_t per = (n_new + blocks - 1) / blocks;
+    p.block_tokens = static_cast<int32_t>(per < 1 ? 1 : per > 64 ? 64 : per);
+    p.err = di.err;
+    return PKV_OK;
+}
+
+int check_bounds(const pkv_kvcache *c, const pkv_pages *pg, int32_t n_new) {
+    if (n_new < 0) return PKV_ERR_ARG;
+    if ((c->head_dim * elem_bytes(c->dtype)) % 16) return PKV_ERR_ARG;
+    if (n_new > 0 && (!c->out_cache_loc || !pg->page_bounds || !aligned16(pg->page_bounds))) return PKV_ERR_ARG;
+    if (static_cast<int64_t>(c->n_kv_heads) * c->head_dim * elem_bytes(c->dtype) / 16 > 65535 * 128) return PKV_ERR_ARG;
+    return PKV_OK;
+}
+
+// Pages of the longest context, and the scores' place in the workspace.
+int64_t select_page_cap(int32_t max_len, int32_t page_size) {
+    const int64_t pages = (static_cast<int64_t>(max_len) + page_size - 1) / page_size;
+    return (pages + pkv::kScoreGroup - 1) / pkv::kScoreGroup * pkv::kScoreGroup;
+}
+
+int select_prepare(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const void *q, int32_t n_heads,
+                   int32_t *sel, int32_t *sel_counts, const pkv_workspace *ws, const DeviceInfo &di,
+                   pkv::SelectParams *out) {
+    pkv::SelectParams &p = *out;
+    p = pkv::SelectParams{};
+    p.q = q;
+    p.page_bounds = pg->page_bounds;
+    p.req_to_page = pg->req_to_page;
+    p.req_pool_indices = c->req_pool_indices;
+    p.seq_lens = c->seq_lens;
+    p.sel = sel;
+    p.sel_counts = sel_counts;
+    p.n_pages = c->size / pg->page_size;
+    p.layer_page0 = static_cast<int64_t>(layer_id) * p.n_pages;
+    p.max_pages = pg->max_pages;
+    p.page_size = pg->page_size;
+    p.n_kv_heads = c->n_kv_heads;
+    p.n_heads = n_heads;
+    p.num_reqs = c->num_reqs;
+    p.batch = c->batch;
+    p.max_len = c->max_len;
+    p.top_k = pg->top_k;
+    p.n_first = pg->n_first;
+    p.n_last = pg->n_last;
+    p.err = di.err;
+    const int64_t cap = select_page_cap(c->max_len, pg->page_size);
+    if (cap > 1 << 30) return PKV_ERR_ARG;
+    p.page_cap = static_cast<int32_t>(cap);
+    if ((static_cast<int64_t>(c->max_len) + pg->page_size - 1) / pg->page_size > pg->top_k) {
+        const int rc = ws_check(ws);
+        if (rc) return rc;
+        if (!pg->page_bounds || !aligned16(pg->page_bounds)) return PKV_ERR_ARG;
+        if (ws->bytes < pkv_select_workspace_bytes(c->batch, c->n_kv_heads, c->max_len, pg->page_size))
+            return PKV_ERR_WORKSPACE;
+        p.scores = static_cast<float *>(ws->base);
+        p.group_max = p.scores + static_cast<int64_t>(c->batch) * c->n_kv_heads * cap;
+    }
+    return PKV_OK;
+}
+
+int selected_prepare(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const int32_t *sel,
+                     const int32_t *sel_counts, const void *q, void *o, int32_t n_heads, float sm_scale,
+                     const DeviceInfo &di, pkv::SelectedParams *out) {
+    pkv::SelectedParams &p = *out;
+    p = pkv::SelectedParams{};
+    p.q = q;
+    p.o = o;
+    p.k_buffer = c->k_buffer;
+    p.v_buffer = c->v_buffer;
+    p.req_to_page = pg->req_to_page;
+    p.req_pool_indices = c->req_pool_indices;
+    p.seq_lens = c->seq_lens;
+    p.sel = sel;
+    p.sel_counts = sel_counts;
+    p.layer_row0 = static_cast<int64_t>(layer_id) * c->size;
+    p.n_pages = c->size / pg->page_size;
+    p.max_pages = pg->max_pages;
+    p.page_size = pg->page_size;
+    p.n_kv_heads = c->n_kv_heads;
+    p.n_heads = n_heads;
+    p.num_reqs = c->num_reqs;
+    p.batch = c->batch;
+    p.max_len = c->max_len;
+    p.top_k = pg->top_k;
+    p.splits = pkv::selected_splits(c->batch, c->n_kv_heads, pg->top_k, pg->page_size, c->max_len, di.sms);
+    p.scale_log2 = sm_scale * 1.4426950408889634f;
+    p.err = di.err;
+    return PKV_OK;
+}
+
+}  // namespace
+
+int pkv_page_bounds(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, int32_t n_new, void *stream) {
+    int rc = check_pages(c, layer_id, pg);
+    if (rc) return rc;
+    rc = check_bounds(c, pg, n_new);
+    if (rc) return rc;
+    if (n_new == 0) return PKV_OK;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({c->k_buffer, c->out_cache_loc, pg->page_bounds});
+    if (rc) return rc;
+    pkv::BoundsParams p;
+    bounds_prepare(c, layer_id, pg, n_new, di, nullptr, &p);
+    return map_launch(pkv::launch_page_bounds(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pkv_select_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max_len, int32_t page_size) {
+    if (batch < 1 || n_kv_heads < 1 || max_len < 1 || page_size < 1) return 0;
+    const size_t cap = static_cast<size_t>(select_page_cap(max_len, page_size));
+    return static_cast<size_t>(batch) * n_kv_heads * (cap + cap / pkv::kScoreGroup) * sizeof(float);
+}
+
+int pkv_select_pages(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const void *q, int32_t n_heads,
+                     int32_t *sel, int32_t *sel_counts, const pkv_workspace *ws, void *stream) {
+    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, true);
+    if (rc) return rc;
+    if (c->batch == 0) return PKV_OK;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({pg->page_bounds, pg->req_to_page, c->req_pool_indices, c->seq_lens, q, sel, sel_counts,
+                        ws ? ws->base : nullptr});
+    if (rc) return rc;
+    pkv::SelectParams p;
+    rc = select_prepare(c, layer_id, pg, q, n_heads, sel, sel_counts, ws, di, &p);
+    if (rc) return rc;
+    return map_launch(pkv::launch_select_pages(p, c->dtype, c->head_dim, n_heads / c->n_kv_heads,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+int pkv_paged_decode_selected(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const int32_t *sel,
+                              const int32_t *sel_counts, const void *q, void *o, int32_t n_heads, float sm_scale,
+                              void *stream) {
+    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, false);
+    if (rc) return rc;
+    if (!isfinite(sm_scale)) return PKV_ERR_ARG;
+    if (c->batch == 0) return PKV_OK;
+    if (!o || !aligned16(o) || q == o) return PKV_ERR_ARG;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({c->k_buffer, c->v_buffer, pg->req_to_page, c->req_pool_indices, c->seq_lens, q, o, sel,
+                        sel_counts});
+    if (rc) return rc;
+    pkv::SelectedParams p;
+    selected_prepare(c, layer_id, pg, sel, sel_counts, q, o, n_heads, sm_scale, di, &p);
+    return map_launch(pkv::launch_decode_selected(p, c->dtype, c->head_dim, n_heads / c->n_kv_heads,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const void *k_new,
+                           const void *v_new, int32_t n_new, const void *q, void *o, int32_t n_heads, float sm_scale,
+                           int32_t *sel, int32_t *sel_counts, const pkv_workspace *ws, void *stream) {
+    // everything is validated before anything is enqueued
+    pkv::KvWriteParams wp;
+    bool no_write = false;
+    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, true);
+    if (rc) return rc;
+    rc = check_bounds(c, pg, n_new);
+    if (rc) return rc;
+    rc = kv_write_prepare(c, layer_id, k_new, v_new, n_new, nullptr, 0, nullptr, false, &wp, &no_write);
+    if (rc) return rc;
+    if (!isfinite(sm_scale)) return PKV_ERR_ARG;
+    const bool no_decode = c->batch == 0;
+    if (!no_decode && (!o || !aligned16(o) || q == o)) return PKV_ERR_ARG;
+    if (no_write && no_decode) return PKV_OK;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({c->k_buffer, c->v_buffer, pg->page_bounds, pg->req_to_page, c->req_pool_indices, c->seq_lens,
+                        q, o, sel, sel_counts, ws ? ws->base : nullptr});
+    if (rc) return rc;
+    pkv::BoundsParams bp;
+    bounds_prepare(c, layer_id, pg, n_new, di, k_new, &bp);
+    pkv::SelectParams sp;
+    pkv::SelectedParams ap;
+    if (!no_decode) {
+        rc = select_prepare(c, layer_id, pg, q, n_heads, sel, sel_counts, ws, di, &sp);
+        if (rc) return rc;
+        selected_prepare(c, layer_id, pg, sel, sel_counts, q, o, n_heads, sm_scale, di, &ap);
+    }
+    const int group = n_heads / c->n_kv_heads;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!no_write) {
+        rc = map_launch(pkv::launch_kv_write(wp, s, true));
+        if (rc) return rc;
+        rc = map_launch(pkv::launch_page_bounds(bp, s));
+        if (rc) return rc;
+    }
+    if (no_decode) return PKV_OK;
+    rc = map_launch(pkv::launch_select_pages(sp, c->dtype, c->head_dim, group, s));
+    if (rc) return rc;
+    ap.pdl = 1;
+    return map_launch(pkv::launch_decode_selected(ap, c->dtype, c->head_dim, group, s));
+}
+
 int pkv_last_device_error(void *stream, int64_t *detail) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
     DeviceInfo di;

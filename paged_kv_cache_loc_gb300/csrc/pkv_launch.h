@@ -149,6 +149,108 @@ struct PrefillParams {
     int64_t unit0;
 };
 
+// Tables of a step (pkv_tables.cu).
+struct TablesParams {
+    const int32_t *req_pool_indices;   // [batch]
+    const int32_t *seq_lens;           // [batch]
+    const int32_t *q_lens;             // [batch] or null
+    int32_t *req_to_page;              // [num_reqs, max_pages]
+    const int32_t *free_pages;         // [n_free]
+    const int32_t *free_start;         // [1]
+    int32_t *free_end;                 // [1]
+    int32_t *kv_indptr;                // [batch + 1] or null
+    int32_t *qo_indptr;                // [batch + 1] or null
+    int32_t *positions;                // [max_new] or null
+    int32_t *out_cache_loc;            // [max_new]
+    int32_t *req_to_token;             // [num_reqs, max_ctx_len] or null
+    int64_t n_pages;
+    int32_t batch;
+    int32_t num_reqs;
+    int32_t max_ctx_len;
+    int32_t max_len;                   // positions that a row of the tables holds
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t n_free;
+    int32_t max_new;
+    int32_t chunk;                     // new tokens per CTA
+    DevErr *err;
+};
+
+// Key bounds of pages (pkv_select.cu).
+struct BoundsParams {
+    const void *keys;             // rows of the new keys in out_cache_loc order, or null: read from the pool
+    const void *k_buffer;         // pool base
+    void *page_bounds;            // [n_layers, n_pages, n_kv_heads, 2, head_dim]
+    const int32_t *out_cache_loc;
+    int64_t size;
+    int64_t layer_row0;           // layer_id * size
+    int64_t layer_page0;          // layer_id * n_pages
+    int32_t n_new;
+    int32_t page_size;
+    int32_t row_chunks;           // 16-byte chunks per key row
+    int32_t head_chunks;          // of them per kv head
+    int32_t dtype;
+    int32_t block_tokens;         // consecutive new tokens per CTA
+    DevErr *err;
+};
+
+// Selection of pages (pkv_select.cu).
+struct SelectParams {
+    const void *q;                // [batch, n_heads, head_dim]
+    const void *page_bounds;
+    const int32_t *req_to_page;
+    const int32_t *req_pool_indices;
+    const int32_t *seq_lens;
+    int32_t *sel;                 // [batch, n_kv_heads, top_k]
+    int32_t *sel_counts;          // [batch, n_kv_heads]
+    float *scores;                // [batch, n_kv_heads, page_cap]
+    float *group_max;             // [batch, n_kv_heads, page_cap / kScoreGroup]: largest |bound| of a group of pages
+    int64_t layer_page0;
+    int64_t n_pages;
+    int32_t page_cap;             // pages of the longest context, rounded up to kScoreGroup
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t n_heads;
+    int32_t num_reqs;
+    int32_t batch;
+    int32_t max_len;
+    int32_t top_k;
+    int32_t n_first;
+    int32_t n_last;
+    int32_t pdl;                  // launched as a programmatic dependent of what writes the bounds
+    DevErr *err;
+};
+
+// Attention over selected pages (pkv_selected.cu).
+struct SelectedParams {
+    const void *q;                // [batch, n_heads, head_dim]
+    void *o;
+    const void *k_buffer;
+    const void *v_buffer;
+    const int32_t *req_to_page;
+    const int32_t *req_pool_indices;
+    const int32_t *seq_lens;
+    const int32_t *sel;
+    const int32_t *sel_counts;
+    int64_t layer_row0;
+    int64_t n_pages;
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t n_heads;
+    int32_t num_reqs;
+    int32_t batch;
+    int32_t max_len;
+    int32_t top_k;
+    int32_t splits;               // CTAs (one cluster) per entry and kv head
+    int32_t pdl;                  // launched as a programmatic dependent of the selection
+    float scale_log2;
+    DevErr *err;
+};
+
+constexpr int kScoreGroup = 16;         // pages scored together
+
 constexpr int kDecodeMaxChunk = 2048;   // slot indices staged per split (or per piece)
 constexpr int kDecodeMaxSplits = 1024;  // merge kernel limit
 constexpr int kPlanMaxBatch = 256;      // prefill entries ordered by the plan kernel (one CTA)
@@ -158,6 +260,16 @@ constexpr int kPlanMaxBatch = 256;      // prefill entries ordered by the plan k
 // step: the write of pkv_decode_step (see pkv_kv_write.cu)
 cudaError_t launch_kv_write(const KvWriteParams &p, cudaStream_t s, bool step = false);
 cudaError_t launch_rope_kv_write(const KvWriteParams &p, cudaStream_t s);
+cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t s);
+cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t s);
+// Whether the selection and the attention over it have a kernel for this shape.
+bool sparse_supported(int dtype, int head_dim, int group);
+cudaError_t launch_select_pages(const SelectParams &p, int dtype, int head_dim, int group,
+                                cudaStream_t s);
+// CTAs per (entry, kv head) of the attention over selected pages.
+int selected_splits(int64_t batch, int n_kv_heads, int64_t top_k, int64_t page_size, int64_t max_len, int sms);
+cudaError_t launch_decode_selected(const SelectedParams &p, int dtype, int head_dim, int group,
+                                   cudaStream_t s);
 cudaError_t launch_decode(const DecodeParams &p, int dtype, int head_dim, int group,
                           cudaStream_t s);
 bool decode_supported(int dtype, int head_dim, int group);

@@ -1,0 +1,594 @@
+// pkv_select.cu -- which pages a sparse decode attends to: the pages' key
+// bounds (pkv_page_bounds) and the selection by them (pkv_select_pages).
+//
+// Bounds: per page, kv head and channel the minimum and maximum of the keys
+// written.  The score of a page for a query q is the largest product that q
+// can have with any key inside the bounds,
+//   sum_c max(q_c lo_c, q_c hi_c) = q- . lo + q+ . hi   (q- <= 0 <= q+, q = q- + q+),
+// maximised over the G query heads of the group.
+//
+// The selection must not depend on how a sum was rounded, so it is decided in
+// two steps.  The score pass computes 32-bit scores s with |s - s*| <= e,
+// where s* is the exact score and, for the n = 2 D (or D) terms of a sum,
+//   e = kScoreEps * max_h sum_c |q[h, c]| * max |bound|  >=  n 2^-23 sum |terms|,
+// kScoreEps = 2^-14 covering n = 256 terms with every partial sum truncated
+// to 24 bits (2^-15) twice over.  With T the 32-bit score of rank
+// k, a page with s > T + 2e is in and one with s < T - 2e is out whatever the
+// rounding was; the few in between are scored again in 64 bits and ranked by
+// (score, page).
+#include "pkv_common.cuh"
+#include "pkv_launch.h"
+
+namespace pkv {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// Key bounds
+// ---------------------------------------------------------------------------
+
+// Minimum / maximum that keep a NaN.
+__device__ __forceinline__ uint32_t min_word(uint32_t a, uint32_t b, __nv_bfloat16) {
+    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b, __nv_bfloat16) {
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min_word(uint32_t a, uint32_t b, float) {
+    return __float_as_uint(min_nan(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b, float) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+}
+template <typename T>
+__device__ __forceinline__ void widen_bounds(uint4 &lo, uint4 &hi, const uint4 &l, const uint4 &h) {
+    lo = make_uint4(min_word(lo.x, l.x, T{}), min_word(lo.y, l.y, T{}), min_word(lo.z, l.z, T{}), min_word(lo.w, l.w, T{}));
+    hi = make_uint4(max_word(hi.x, h.x, T{}), max_word(hi.y, h.y, T{}), max_word(hi.z, h.z, T{}), max_word(hi.w, h.w, T{}));
+}
+
+constexpr int kBoundsThreads = 128;
+constexpr int kRowsAhead = 8;
+
+// A run is a maximal sequence of new tokens in consecutive slots of one page
+// (slots outside the pool, which are errors, are passed over).  A CTA takes the
+// runs that start among its block_tokens tokens (and follows a run beyond
+// them); thread c reduces 16-byte chunk c of the run's rows.  The bytes of the
+// new keys are read once, kRowsAhead rows in flight per thread.
+template <typename T>
+__global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const BoundsParams p) {
+    const int chunk = blockIdx.y * kBoundsThreads + threadIdx.x;
+    const int i_end = min(p.n_new, (static_cast<int>(blockIdx.x) + 1) * p.block_tokens);
+    const auto valid = [&](int slot) { return static_cast<unsigned>(slot) < static_cast<unsigned long long>(p.size); };
+    for (int i = blockIdx.x * p.block_tokens; i < i_end;) {
+        int loc = __ldg(p.out_cache_loc + i);
+        if (!valid(loc)) {
+            if (chunk == 0) record_error(p.err, loc);
+            ++i;
+            continue;
+        }
+        const int page = loc / p.page_size;
+        int off = loc - page * p.page_size;
+        bool begins = off == 0;
+        if (!begins) {
+            int j = i - 1;
+            while (j >= 0 && !valid(__ldg(p.out_cache_loc + j))) --j;
+            begins = j < 0 || __ldg(p.out_cache_loc + j) != loc - 1;
+        }
+        uint4 *dst = static_cast<uint4 *>(p.page_bounds) + (p.layer_page0 + page) * p.row_chunks * 2 +
+                     (chunk / p.head_chunks) * p.head_chunks * 2 + chunk % p.head_chunks;
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        bool have = false;                   // lo / hi hold something
+        const bool mine = begins && chunk < p.row_chunks;
+        if (mine && off != 0) {
+            lo = dst[0];
+            hi = dst[p.head_chunks];
+            have = true;
+        }
+        for (;;) {
+            // tokens i .. i + n - 1 are in consecutive slots of the page
+            const int most = min(p.n_new - i, p.page_size - off);
+            int n = 1;
+            for (;;) {
+                const int at = n + static_cast<int>(threadIdx.x & 31);
+                const bool next = at < most && __ldg(p.out_cache_loc + i + at) == loc + at;
+                const unsigned breaks = __ballot_sync(0xffffffffu, !next);
+                n += breaks ? __ffs(breaks) - 1 : 32;
+                if (breaks) break;
+            }
+            if (mine) {
+                const uint4 *row = (p.keys ? static_cast<const uint4 *>(p.keys) + static_cast<int64_t>(i) * p.row_chunks
+                                           : static_cast<const uint4 *>(p.k_buffer) + (p.layer_row0 + loc) * p.row_chunks) + chunk;
+                if (!have) lo = hi = row[0];
+                have = true;
+                for (int k = 0; k < n; k += kRowsAhead) {
+                    uint4 x[kRowsAhead];
+#pragma unroll
+                    for (int u = 0; u < kRowsAhead; ++u) x[u] = row[static_cast<int64_t>(min(k + u, n - 1)) * p.row_chunks];
+#pragma unroll
+                    for (int u = 0; u < kRowsAhead; ++u) widen_bounds<T>(lo, hi, x[u], x[u]);
+                }
+            }
+            i += n;
+            off += n;
+            loc += n;
+            if (!begins || off == p.page_size) break;
+            int j = i;
+            while (j < p.n_new && !valid(__ldg(p.out_cache_loc + j))) ++j;
+            if (j == i || j >= p.n_new || __ldg(p.out_cache_loc + j) != loc) break;
+            if (chunk == 0)
+                for (int x = i; x < j; ++x) record_error(p.err, __ldg(p.out_cache_loc + x));
+            i = j;
+        }
+        if (mine) {
+            dst[0] = lo;
+            dst[p.head_chunks] = hi;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Scores
+// ---------------------------------------------------------------------------
+
+constexpr float kScoreEps = 6.103515625e-5f;   // 2^-14
+constexpr float kScoreTiny = 1e-35f;           // 256 products lost below the smallest normal number, doubled
+
+// 4-byte words of a bounds or q row, widened.
+__device__ __forceinline__ void widen16(const uint4 &w, float (&x)[8], bf16) {
+    x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y); x[3] = bf16hi(w.y);
+    x[4] = bf16lo(w.z); x[5] = bf16hi(w.z); x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ void widen16(const uint4 &w, float (&x)[4], float) {
+    x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+}
+
+// Number of pages of entry b (0 with a request row out of range); the row.
+__device__ __forceinline__ int entry_pages(const SelectParams &p, int b, int *row, bool report) {
+    const int r = __ldg(p.req_pool_indices + b);
+    int n = __ldg(p.seq_lens + b);
+    if (static_cast<unsigned>(r) >= static_cast<unsigned>(p.num_reqs)) {
+        if (report) record_error(p.err, r);
+        *row = 0;
+        return 0;
+    }
+    *row = r;
+    if (n < 0 || n > p.max_len) {
+        if (report) record_error(p.err, n);
+        n = n < 0 ? 0 : p.max_len;
+    }
+    return n / p.page_size + (n % p.page_size != 0);
+}
+
+__device__ __forceinline__ long long page_at(const SelectParams &p, int row, int i) {
+    const int pg = __ldg(p.req_to_page + static_cast<int64_t>(row) * p.max_pages + i);
+    if (static_cast<unsigned>(pg) < static_cast<unsigned long long>(p.n_pages)) return pg;
+    record_error(p.err, pg);
+    return 0;
+}
+
+constexpr int kScoreWarps = 4;
+
+// CUDA-core scores: a warp takes kScoreGroup pages, eight lanes to a page,
+// each lane the 16-byte chunks c = lane % 8, c + 8, ... of the page's rows.
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kScoreWarps * 32) score_pages_kernel(const SelectParams p) {
+    constexpr int kElems = 16 / Elem<T>::bytes;
+    constexpr int kChunks = D / kElems;              // 16-byte chunks per row
+    __shared__ float q[G][D];
+    griddep_launch();
+    const int g = blockIdx.y, b = blockIdx.z;
+    int row;
+    const int n = entry_pages(p, b, &row, false);
+    for (int i = threadIdx.x; i < G * D; i += kScoreWarps * 32)
+        q[i / D][i % D] = Elem<T>::to_f(static_cast<const T *>(p.q)[(static_cast<int64_t>(b) * p.n_heads + g * G) * D + i]);
+    __syncthreads();
+    if (p.pdl) griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7;
+    const int group = blockIdx.x * kScoreWarps + warp;
+    if (n <= p.top_k || group * kScoreGroup >= n) return;
+    float biggest = 0.f;
+    const int64_t unit = static_cast<int64_t>(b) * p.n_kv_heads + g;
+#pragma unroll 1
+    for (int i = 0; i < kScoreGroup; i += 4) {
+        const int pg = group * kScoreGroup + i + (lane >> 3);
+        const int pc = min(pg, n - 1);
+        const uint4 *lo = static_cast<const uint4 *>(p.page_bounds) +
+                          ((p.layer_page0 + page_at(p, row, pc)) * p.n_kv_heads + g) * 2 * kChunks;
+        float s[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) s[h] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; c += 8) {
+            float l[kElems], u[kElems];
+            widen16(__ldg(lo + c + sub), l, T{});
+            widen16(__ldg(lo + kChunks + c + sub), u, T{});
+#pragma unroll
+            for (int x = 0; x < kElems; ++x) {
+                biggest = max_nan(biggest, max_nan(fabsf(l[x]), fabsf(u[x])));
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    const float qv = q[h][(c + sub) * kElems + x];
+                    s[h] = fmaf(qv, qv >= 0.f ? u[x] : l[x], s[h]);
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+#pragma unroll
+            for (int off = 4; off >= 1; off >>= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], off);
+        float best = s[0];
+#pragma unroll
+        for (int h = 1; h < G; ++h) best = max_nan(best, s[h]);
+        if (sub == 0 && pg < n) p.scores[unit * p.page_cap + pg] = best;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) biggest = max_nan(biggest, __shfl_xor_sync(0xffffffffu, biggest, off));
+    if (lane == 0) p.group_max[unit * (p.page_cap / kScoreGroup) + group] = biggest;
+}
+
+// ---------------------------------------------------------------------------
+// Selection
+// ---------------------------------------------------------------------------
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kUndecided = 512;          // scored in 64 bits from a list; more: by radix passes
+
+// Order-preserving integer keys; NaN above every number, -0 = +0.
+__device__ __forceinline__ uint32_t key32(float s) {
+    if (s != s) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(s + 0.f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unkey32(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ unsigned long long key64(double s) {
+    if (s != s) return ~0ull;
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(s + 0.0));
+    return u >> 63 ? ~u : u | (1ull << 63);
+}
+
+struct SelShared {
+    int warp_sum[kSelWarps];
+    float red[kSelWarps];
+    uint32_t lo[kSelWarps], hi[kSelWarps];
+    int hist[kBins];
+    int bin, above, count, total;
+};
+
+// Inclusive block scan of one int per thread (kSelThreads threads).
+__device__ __forceinline__ int block_scan(SelShared &sh, int v, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp_sum[warp] = v;
+    __syncthreads();
+    int t = 0;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+        if (w < warp) v += sh.warp_sum[w];
+        t += sh.warp_sum[w];
+    }
+    *total = t;
+    return v;
+}
+
+// The bin (from the top) that holds rank `rank` (1-based) of the histogram:
+// sh.bin, and sh.above = the count in higher bins.
+__device__ __forceinline__ void find_bin(SelShared &sh, int bins, int rank) {
+    const int per = (bins + kSelThreads - 1) / kSelThreads;
+    const int top = bins - 1 - static_cast<int>(threadIdx.x) * per;   // this thread: top, top - 1, ...
+    int own = 0, total;
+    for (int k = 0; k < per; ++k)
+        if (top - k >= 0) own += sh.hist[top - k];
+    const int inc = block_scan(sh, own, &total);
+    int before = inc - own;
+    if (before < rank && rank <= inc) {
+        for (int k = 0; k < per; ++k) {
+            const int c = sh.hist[top - k];
+            if (before + c >= rank) {
+                sh.bin = top - k;
+                sh.above = before;
+                break;
+            }
+            before += c;
+        }
+    }
+    __syncthreads();
+}
+
+// The 64-bit score of a page, by a warp: lane partial sums in a fixed order,
+// so equal bounds give equal scores.
+template <typename T, int D, int G>
+__device__ __forceinline__ unsigned long long exact_key(const SelectParams &p, const float (*q)[D], int row, int g, int pg) {
+    const int lane = threadIdx.x & 31;
+    const T *lo = static_cast<const T *>(p.page_bounds) +
+                  ((p.layer_page0 + page_at(p, row, pg)) * p.n_kv_heads + g) * 2 * D;
+    double s[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) s[h] = 0.0;
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+        const float l = Elem<T>::to_f(lo[c + lane]), u = Elem<T>::to_f(lo[D + c + lane]);
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float qv = q[h][c + lane];
+            s[h] = fma(static_cast<double>(qv), static_cast<double>(qv >= 0.f ? u : l), s[h]);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < G; ++h)
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], off);
+    unsigned long long best = key64(s[0]);
+#pragma unroll
+    for (int h = 1; h < G; ++h) best = max(best, key64(s[h]));
+    return best;
+}
+
+// One CTA per (kv head, entry).
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectParams p) {
+    __shared__ SelShared sh;
+    __shared__ float q[G][D];
+    __shared__ int und_page[kUndecided];
+    __shared__ unsigned long long und_key[kUndecided];
+    griddep_launch();
+    const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t unit = static_cast<int64_t>(b) * p.n_kv_heads + g;
+    int row;
+    const int n = entry_pages(p, b, &row, g == 0 && tid == 0);
+    int32_t *sel = p.sel + unit * p.top_k;
+    const int count = min(n, p.top_k);
+    if (tid == 0) p.sel_counts[unit] = count;
+    if (n <= p.top_k) {
+        for (int i = tid; i < p.top_k; i += kSelThreads) sel[i] = i < n ? i : -1;
+        griddep_wait();
+        return;
+    }
+    const int c0 = p.n_first, m = n - p.n_first - p.n_last;       // candidates c0 .. c0 + m - 1
+    const int keep = p.top_k - p.n_first - p.n_last;              // of them
+    for (int i = tid; i < p.n_first; i += kSelThreads) sel[i] = i;
+    for (int i = tid; i < p.n_last; i += kSelThreads) sel[p.top_k - p.n_last + i] = n - p.n_last + i;
+    for (int i = tid; i < G * D; i += kSelThreads)
+        q[i / D][i % D] = Elem<T>::to_f(static_cast<const T *>(p.q)[(static_cast<int64_t>(b) * p.n_heads + g * G) * D + i]);
+    griddep_wait();                                               // the scores
+    if (keep == 0) return;
+    float *score = p.scores + unit * p.page_cap + c0;
+    const float *gmax = p.group_max + unit * (p.page_cap / kScoreGroup);
+    __syncthreads();
+
+    // range of the keys, the error bound, and whether every score is finite
+    uint32_t klo = 0xffffffffu, khi = 0;
+    for (int i = tid; i < m; i += kSelThreads) {
+        const uint32_t k = key32(score[i]);
+        klo = min(klo, k);
+        khi = max(khi, k);
+    }
+    float big = 0.f;
+    for (int i = tid; i < (n + kScoreGroup - 1) / kScoreGroup; i += kSelThreads) big = max_nan(big, gmax[i]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        klo = min(klo, __shfl_xor_sync(0xffffffffu, klo, off));
+        khi = max(khi, __shfl_xor_sync(0xffffffffu, khi, off));
+        big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, off));
+    }
+    if (lane == 0) {
+        sh.lo[warp] = klo;
+        sh.hi[warp] = khi;
+        sh.red[warp] = big;
+    }
+    __syncthreads();
+    float norm = 0.f;                                             // max_h sum_c |q|, every warp by itself
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) s += fabsf(q[h][c + lane]);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        norm = max_nan(norm, s);
+    }
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+        klo = min(klo, sh.lo[w]);
+        khi = max(khi, sh.hi[w]);
+        big = max_nan(big, sh.red[w]);
+    }
+    const float slack = 2.f * kScoreEps * norm * big + kScoreTiny;   // 2e
+    const bool finite = klo > key32(-INFINITY) && khi < key32(INFINITY) && slack < INFINITY;
+
+    // the 32-bit threshold's bin [fl, fh], narrowed until few pages are undecided
+    float fl = -INFINITY, fh = INFINITY;
+    int decided = 0, undecided = m;
+    if (finite) {
+        uint32_t lo = klo, hi = khi;
+        int rank = keep;
+        for (;;) {
+            const int shift = max(0, 32 - __clz(hi - lo) - 11);
+            const int bins = static_cast<int>((hi - lo) >> shift) + 1;
+            for (int i = tid; i < bins; i += kSelThreads) sh.hist[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < m; i += kSelThreads) {
+                const uint32_t k = key32(score[i]);
+                if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
+            }
+            __syncthreads();
+            find_bin(sh, bins, rank);
+            rank -= sh.above;
+            lo += static_cast<uint32_t>(sh.bin) << shift;
+            hi = min(hi, lo + ((1u << shift) - 1u));
+            fl = unkey32(lo) - slack;
+            fh = unkey32(hi) + slack;
+            int in = 0, mid = 0;
+            for (int i = tid; i < m; i += kSelThreads) {
+                const float s = score[i];
+                in += s > fh;
+                mid += s >= fl && s <= fh;
+            }
+            int t;
+            block_scan(sh, in, &t);
+            decided = t;
+            block_scan(sh, mid, &t);
+            undecided = t;
+            __syncthreads();
+            if (undecided <= kUndecided || shift == 0) break;
+        }
+    }
+    const int need = keep - decided;                              // of the undecided
+    if (need < undecided) {
+        if (undecided <= kUndecided) {
+            // 64-bit scores from a list, ranked by (score, page)
+            if (tid == 0) sh.count = 0;
+            __syncthreads();
+            for (int i = tid; i < m; i += kSelThreads) {
+                const float s = score[i];
+                if (!finite || (s >= fl && s <= fh)) und_page[atomicAdd(&sh.count, 1)] = i;
+            }
+            __syncthreads();
+            for (int k = warp; k < undecided; k += kSelWarps) {
+                const unsigned long long x = exact_key<T, D, G>(p, q, row, g, c0 + und_page[k]);
+                if (lane == 0) und_key[k] = x;
+            }
+            __syncthreads();
+            for (int k = tid; k < undecided; k += kSelThreads) {
+                const unsigned long long x = und_key[k];
+                const int pg = und_page[k];
+                int rank = 0;
+                for (int j = 0; j < undecided; ++j) rank += und_key[j] > x || (und_key[j] == x && und_page[j] < pg);
+                score[pg] = rank < need ? INFINITY : -INFINITY;
+            }
+        } else {
+            // Many pages within rounding of the threshold (pages that are
+            // alike, or scores that are not finite): radix selection on the
+            // 64-bit keys, computed again in each of its eight passes.
+            unsigned long long prefix = 0;
+            int rank = need;
+            for (int byte = 7; byte >= 0; --byte) {
+                for (int i = tid; i < 256; i += kSelThreads) sh.hist[i] = 0;
+                __syncthreads();
+                for (int i = warp; i < m; i += kSelWarps) {
+                    const float s = score[i];
+                    if (finite && !(s >= fl && s <= fh)) continue;
+                    const unsigned long long x = exact_key<T, D, G>(p, q, row, g, c0 + i);
+                    if (lane == 0 && (byte == 7 || (x >> (8 * byte + 8)) == (prefix >> (8 * byte + 8))))
+                        atomicAdd(&sh.hist[(x >> (8 * byte)) & 255], 1);
+                }
+                __syncthreads();
+                find_bin(sh, 256, rank);
+                rank -= sh.above;
+                prefix |= static_cast<unsigned long long>(sh.bin) << (8 * byte);
+                __syncthreads();
+            }
+            // keys above the prefix are in, and the first `rank` that equal it
+            int equal = 0;
+            for (int i0 = 0; i0 < m; i0 += kSelWarps) {
+                const int i = i0 + warp;
+                const float s = i < m ? score[i] : 0.f;
+                const bool mine = i < m && (!finite || (s >= fl && s <= fh));
+                const unsigned long long x = mine ? exact_key<T, D, G>(p, q, row, g, c0 + i) : 0;
+                int t;
+                const int at = equal + block_scan(sh, mine && x == prefix && lane == 0, &t);
+                if (mine && lane == 0) score[i] = x > prefix || (x == prefix && at <= rank) ? INFINITY : -INFINITY;
+                equal += t;
+            }
+            __syncthreads();
+        }
+        if (!finite) fh = 3e38f;                                  // every score is now +-inf
+        __syncthreads();
+    }
+    // in ascending order: pages above the bin, and of the bin those marked +inf
+    // (all of it where its pages are all needed)
+    const float least = need < undecided ? fh : fl;
+    const bool whole = !(need < undecided);
+    const int per = (m + kSelThreads - 1) / kSelThreads;
+    const int i0 = min(m, tid * per), i1 = min(m, i0 + per);
+    int mine = 0, t;
+    for (int i = i0; i < i1; ++i) mine += whole ? score[i] >= least : score[i] > least;
+    int at = p.n_first + block_scan(sh, mine, &t) - mine;
+    for (int i = i0; i < i1; ++i)
+        if (whole ? score[i] >= least : score[i] > least) sel[at++] = c0 + i;
+}
+
+template <typename T, int D, int G>
+cudaError_t launch_select(const SelectParams &p, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const bool scored = p.scores != nullptr;
+    if (scored) {
+        const int groups = p.page_cap / kScoreGroup;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((groups + kScoreWarps - 1) / kScoreWarps, p.n_kv_heads, p.batch);
+        cfg.blockDim = dim3(kScoreWarps * 32);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = p.pdl ? 1 : 0;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, score_pages_kernel<T, D, G>, p);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_kv_heads, p.batch);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = scored || p.pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, select_pages_kernel<T, D, G>, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_select_g(const SelectParams &p, int group, cudaStream_t s) {
+    switch (group) {
+        case 1: return launch_select<T, D, 1>(p, s);
+        case 2: return launch_select<T, D, 2>(p, s);
+        case 4: return launch_select<T, D, 4>(p, s);
+        case 8: return launch_select<T, D, 8>(p, s);
+        default: return cudaErrorNotSupported;
+    }
+}
+
+}  // namespace
+
+bool sparse_supported(int dtype, int head_dim, int group) {
+    return (dtype == PKV_F32 || dtype == PKV_BF16) && (head_dim == 64 || head_dim == 128) &&
+           (group == 1 || group == 2 || group == 4 || group == 8);
+}
+
+cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t s) {
+    if (p.n_new == 0) return cudaSuccess;
+    const dim3 grid((p.n_new + p.block_tokens - 1) / p.block_tokens, (p.row_chunks + kBoundsThreads - 1) / kBoundsThreads);
+    if (p.dtype == PKV_BF16) page_bounds_kernel<bf16><<<grid, kBoundsThreads, 0, s>>>(p);
+    else page_bounds_kernel<float><<<grid, kBoundsThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_select_pages(const SelectParams &p, int dtype, int head_dim, int group, cudaStream_t s) {
+    if (!sparse_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
+    if (dtype == PKV_BF16)
+        return head_dim == 128 ? launch_select_g<bf16, 128>(p, group, s) : launch_select_g<bf16, 64>(p, group, s);
+    return head_dim == 128 ? launch_select_g<float, 128>(p, group, s) : launch_select_g<float, 64>(p, group, s);
+}
+
+}  // namespace pkv

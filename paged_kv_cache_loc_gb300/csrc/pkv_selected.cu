@@ -1,0 +1,346 @@
+// pkv_selected.cu -- decode attention over selected pages
+// (pkv_paged_decode_selected): for each entry and kv head the pages of a list,
+// read through the page table.
+//
+// Work split: one thread-block cluster per (entry, kv head).  Its CTAs share
+// the list's positions in blocks of kBlk, each warp takes blocks of its CTA's
+// run with an online softmax of its own (base 2), the warps' partials meet in
+// shared memory and the CTAs' partials in distributed shared memory, so there
+// is one launch and no workspace.  A list is bounded by top_k pages, and the
+// host picks the cluster size so that all SMs have work.
+#include <atomic>
+
+#include "pkv_common.cuh"
+#include "pkv_launch.h"
+
+namespace pkv {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kBlk = 16;              // positions per block
+constexpr int kStagePages = 512;      // list entries resolved to slots at a time
+constexpr int kMaxSplits = 8;         // CTAs per cluster (the portable limit)
+
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;\n" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(x) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ float weight(float m, float top) { return m == -INFINITY ? 0.f : fast_exp2(m - top); }
+
+// One listed page: its first slot and its first position (-1: not to be read).
+struct Run {
+    int slot, pos;
+};
+
+// Partial softmax states of a CTA's kParts parts of kHeads heads.
+template <int kParts, int kHeads, int D>
+struct Partials {
+    float m[kParts][kHeads];
+    float l[kParts][kHeads];
+    float o[kParts][kHeads][D];
+};
+
+// Joins the parts of every CTA of the cluster and writes o.  Part 0 becomes
+// the CTA's own partial; CTA r of the cluster then sums its share of the
+// outputs over all CTAs.
+template <typename T, int kParts, int kHeads, int D, int kThreads>
+__device__ __forceinline__ void join(Partials<kParts, kHeads, D> &sh, T *out, int rank, int splits) {
+    const int tid = threadIdx.x;
+    constexpr int kOut = kHeads * D;
+    float acc[(kOut + kThreads - 1) / kThreads];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < (kOut + kThreads - 1) / kThreads; ++i) {
+        const int e = tid + i * kThreads, h = e / D, c = e % D;
+        acc[i] = 0.f;
+        if (e < kOut) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kParts; ++w) top = fmaxf(top, sh.m[w][h]);
+#pragma unroll
+            for (int w = 0; w < kParts; ++w) {
+                if (sh.m[w][h] != -INFINITY) acc[i] = fmaf(weight(sh.m[w][h], top), sh.o[w][h][c], acc[i]);
+            }
+        }
+    }
+    float top = -INFINITY, sum = 0.f;
+    if (tid < kHeads) {
+#pragma unroll
+        for (int w = 0; w < kParts; ++w) top = fmaxf(top, sh.m[w][tid]);
+#pragma unroll
+        for (int w = 0; w < kParts; ++w) sum += sh.l[w][tid] * weight(sh.m[w][tid], top);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < (kOut + kThreads - 1) / kThreads; ++i) {
+        const int e = tid + i * kThreads;
+        if (e < kOut) sh.o[0][e / D][e % D] = acc[i];
+    }
+    if (tid < kHeads) {
+        sh.m[0][tid] = top;
+        sh.l[0][tid] = sum;
+    }
+    if (splits > 1) cluster_sync();
+    else __syncthreads();
+    const int e1 = kOut * (rank + 1) / splits;
+    for (int e = kOut * rank / splits + tid; e < e1; e += kThreads) {
+        const int h = e / D, c = e % D;
+        float all = -INFINITY, l = 0.f, x = 0.f;
+        for (int r = 0; r < splits; ++r) all = fmaxf(all, ld_cluster(cluster_addr(&sh.m[0][h], r)));
+        for (int r = 0; r < splits; ++r) {
+            const float mr = ld_cluster(cluster_addr(&sh.m[0][h], r));
+            if (mr != -INFINITY) {
+                const float f = weight(mr, all);
+                l = fmaf(f, ld_cluster(cluster_addr(&sh.l[0][h], r)), l);
+                x = fmaf(f, ld_cluster(cluster_addr(&sh.o[0][h][c], r)), x);
+            }
+        }
+        out[e] = Elem<T>::from_f(l == 0.f ? 0.f : x / l);
+    }
+    if (splits > 1) cluster_sync();      // no CTA leaves while its memory is read
+}
+
+// What a CTA attends to: blocks [t0, t1) of the list's flattened positions.
+struct Share {
+    int row, len, n_pages, t0, t1;
+};
+
+__device__ __forceinline__ Share cta_share(const SelectedParams &p, int g, int b, int rank, bool report) {
+    Share s;
+    s.row = __ldg(p.req_pool_indices + b);
+    s.len = __ldg(p.seq_lens + b);
+    int count = __ldg(p.sel_counts + static_cast<int64_t>(b) * p.n_kv_heads + g);
+    if (static_cast<unsigned>(s.row) >= static_cast<unsigned>(p.num_reqs)) {
+        if (report) record_error(p.err, s.row);
+        s.row = s.len = count = 0;
+    }
+    if (s.len < 0 || s.len > p.max_len) {
+        if (report) record_error(p.err, s.len);
+        s.len = s.len < 0 ? 0 : p.max_len;
+    }
+    if (count < 0 || count > p.top_k) {
+        if (report) record_error(p.err, count);
+        count = count < 0 ? 0 : p.top_k;
+    }
+    s.n_pages = s.len / p.page_size + (s.len % p.page_size != 0);
+    // top_k * page_size fits 31 bits (checked on the host)
+    const int total = count * p.page_size;
+    const int blocks = total / kBlk + (total % kBlk != 0);
+    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * rank / p.splits);
+    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / p.splits);
+    s.t0 = b0 * kBlk;
+    s.t1 = min(total, b1 * kBlk);
+    return s;
+}
+
+// Resolves list entries [i0, i1) to slots.
+template <int kThreads>
+__device__ __forceinline__ void stage_runs(const SelectedParams &p, const Share &s, const int32_t *sel, int i0, int i1, Run *runs) {
+    for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += kThreads) {
+        const int page = __ldg(sel + i);
+        Run r{0, -1};
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(s.n_pages)) {
+            record_error(p.err, page);
+        } else {
+            int phys = __ldg(p.req_to_page + static_cast<int64_t>(s.row) * p.max_pages + page);
+            if (static_cast<unsigned>(phys) >= static_cast<unsigned long long>(p.n_pages)) {
+                record_error(p.err, phys);
+                phys = 0;
+            }
+            r.slot = phys * p.page_size;
+            r.pos = page * p.page_size;
+        }
+        runs[i - i0] = r;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// CUDA cores: eight lanes to a position, kHeads query heads of the kv head
+// ---------------------------------------------------------------------------
+
+constexpr int kSimtWarps = 4;
+constexpr int kSimtThreads = kSimtWarps * 32;
+
+template <typename T, int D, int kHeads>
+__global__ void __launch_bounds__(kSimtThreads) selected_simt_kernel(const SelectedParams p) {
+    constexpr int kElems = 16 / Elem<T>::bytes;
+    constexpr int kChunks = D / kElems;
+    constexpr int kOwn = kChunks / 8;                // 16-byte chunks of a row per lane
+    __shared__ Partials<kSimtWarps, kHeads, D> sh;
+    __shared__ float q[kHeads][D];
+    __shared__ Run runs[kStagePages];
+    griddep_launch();
+    const int group = p.n_heads / p.n_kv_heads;
+    const int rank = blockIdx.x, h0 = blockIdx.y * kHeads, g = h0 / group, b = blockIdx.z;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & 7;
+    const int64_t out0 = (static_cast<int64_t>(b) * p.n_heads + h0) * D;
+    for (int i = tid; i < kHeads * D; i += kSimtThreads)
+        q[i / D][i % D] = Elem<T>::to_f(static_cast<const T *>(p.q)[out0 + i]) * p.scale_log2;
+    if (p.pdl) griddep_wait();
+    const Share s = cta_share(p, g, b, rank, rank == 0 && h0 % group == 0 && tid == 0);
+    const int32_t *sel = p.sel + (static_cast<int64_t>(b) * p.n_kv_heads + g) * p.top_k;
+
+    float m[kHeads], l[kHeads], o[kHeads][kOwn * kElems];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kOwn * kElems; ++c) o[h][c] = 0.f;
+    }
+    const int i_end = s.t1 > s.t0 ? (s.t1 - 1) / p.page_size + 1 : 0;
+    for (int i0 = s.t0 / p.page_size; i0 < i_end; i0 += kStagePages) {
+        const int i1 = min(i_end, i0 + kStagePages);
+        __syncthreads();
+        stage_runs<kSimtThreads>(p, s, sel, i0, i1, runs);
+        __syncthreads();
+        const int from = max(s.t0, i0 * p.page_size);
+        const int to = static_cast<int>(min(static_cast<int64_t>(s.t1), static_cast<int64_t>(i1) * p.page_size));
+        for (int t = from + warp * 4; t < to; t += kSimtWarps * 4) {     // warp-uniform
+            const int tt = min(t + (lane >> 3), to - 1);
+            const int i = tt / p.page_size, off = tt - i * p.page_size;
+            const Run r = runs[i - i0];
+            const bool seen = t + (lane >> 3) < to && r.pos >= 0 &&
+                              static_cast<unsigned>(r.pos) + off < static_cast<unsigned>(s.len);
+            const int64_t at = ((p.layer_row0 + r.slot + (seen ? off : 0)) * p.n_kv_heads + g) * kChunks + sub;
+            const uint4 *kr = static_cast<const uint4 *>(p.k_buffer) + at;
+            const uint4 *vr = static_cast<const uint4 *>(p.v_buffer) + at;
+            float w[kHeads];
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) w[h] = 0.f;
+            if (seen) {
+#pragma unroll
+                for (int c = 0; c < kOwn; ++c) {
+                    float x[kElems];
+                    load_widen<T, kElems>(reinterpret_cast<const T *>(kr + c * 8), x);
+#pragma unroll
+                    for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+                        for (int e = 0; e < kElems; ++e) w[h] = fmaf(q[h][(c * 8 + sub) * kElems + e], x[e], w[h]);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+#pragma unroll
+                for (int x = 4; x >= 1; x >>= 1) w[h] += __shfl_xor_sync(0xffffffffu, w[h], x);
+                if (!seen) w[h] = -INFINITY;
+            }
+            if (seen) {
+                float x[kOwn * kElems];
+#pragma unroll
+                for (int c = 0; c < kOwn; ++c) {
+                    float y[kElems];
+                    load_widen<T, kElems>(reinterpret_cast<const T *>(vr + c * 8), y);
+#pragma unroll
+                    for (int e = 0; e < kElems; ++e) x[c * kElems + e] = y[e];
+                }
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    const float top = fmaxf(m[h], w[h]);
+                    const float f = weight(m[h], top), pr = weight(w[h], top);
+                    m[h] = top;
+                    l[h] = fmaf(l[h], f, pr);
+#pragma unroll
+                    for (int c = 0; c < kOwn * kElems; ++c) o[h][c] = fmaf(o[h][c], f, pr * x[c]);
+                }
+            }
+        }
+    }
+    // the four positions of a warp, then the warps
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+        float top = m[h];
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float f = weight(m[h], top);
+        float sum = l[h] * f;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (lane == 0) {
+            sh.m[warp][h] = top;
+            sh.l[warp][h] = sum;
+        }
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c)
+#pragma unroll
+            for (int e = 0; e < kElems; ++e) {
+                float x = o[h][c * kElems + e] * f;
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                if (lane < 8) sh.o[warp][h][(c * 8 + sub) * kElems + e] = x;
+            }
+    }
+    join<T, kSimtWarps, kHeads, D, kSimtThreads>(sh, static_cast<T *>(p.o) + out0, rank, p.splits);
+}
+
+template <typename K>
+cudaError_t launch_cluster(K kernel, dim3 grid, int threads, const SelectedParams &p, cudaStream_t s) {
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (p.splits > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(p.splits);
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (p.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T, int D, int kHeads>
+cudaError_t run_simt(const SelectedParams &p, cudaStream_t s) {
+    return launch_cluster(selected_simt_kernel<T, D, kHeads>, dim3(p.splits, p.n_heads / kHeads, p.batch), kSimtThreads, p, s);
+}
+
+template <typename T, int D>
+cudaError_t run_simt_g(const SelectedParams &p, int group, cudaStream_t s) {
+    switch (group) {
+        case 1: return run_simt<T, D, 1>(p, s);
+        case 2: return run_simt<T, D, 2>(p, s);
+        default: return run_simt<T, D, 4>(p, s);     // eight heads: two CTAs of four
+    }
+}
+
+}  // namespace
+
+// Enough CTAs for two per SM, while a CTA keeps two blocks per warp.
+int selected_splits(int64_t batch, int n_kv_heads, int64_t top_k, int64_t page_size, int64_t max_len, int sms) {
+    const int64_t units = batch * n_kv_heads;
+    const int64_t pages = (max_len + page_size - 1) / page_size;
+    const int64_t blocks = (top_k < pages ? top_k : pages) * page_size / kBlk + 1;
+    int splits = 1;
+    while (splits < kMaxSplits && units * splits < 2LL * sms && blocks >= 4LL * splits * 2) splits *= 2;
+    return splits;
+}
+
+cudaError_t launch_decode_selected(const SelectedParams &p, int dtype, int head_dim, int group, cudaStream_t s) {
+    if (!sparse_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
+    if (p.splits < 1 || p.splits > kMaxSplits) return cudaErrorInvalidValue;
+    if (dtype == PKV_BF16) return head_dim == 128 ? run_simt_g<bf16, 128>(p, group, s) : run_simt_g<bf16, 64>(p, group, s);
+    return head_dim == 128 ? run_simt_g<float, 128>(p, group, s) : run_simt_g<float, 64>(p, group, s);
+}
+
+}  // namespace pkv
