@@ -242,6 +242,94 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_pages_kernel(const Sel
     if (lane == 0) p.group_max[unit * (p.page_cap / kScoreGroup) + group] = biggest;
 }
 
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Tensor-core scores (bf16): the score is a product, [hi, lo] of 16 pages times
+// [q+, q-] of the group's heads, so a warp takes kScoreGroup = 16 pages as the
+// rows and the heads as the 8 columns of m16n8k16.  A dot product may take its
+// terms in any order, so lane (r, t) = (lane / 4, lane % 4) supplies the
+// 16-byte chunks t, t + 4, ... of rows r and r + 8 (and of head r) straight
+// from memory: four lanes read 64 contiguous bytes, nothing is staged, and a
+// warp has all of its 8 KB (D = 128) in flight at once.
+template <int D, int G>
+__global__ void __launch_bounds__(kScoreWarps * 32) score_pages_mma_kernel(const SelectParams p) {
+    constexpr int kChunks = D / 8, kOwn = kChunks / 4;
+    griddep_launch();
+    const int g = blockIdx.y, b = blockIdx.z;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
+    const int group = blockIdx.x * kScoreWarps + warp;
+    int row;
+    const int n = entry_pages(p, b, &row, false);
+    if (n <= p.top_k || group * kScoreGroup >= n) {
+        if (p.pdl) griddep_wait();
+        return;
+    }
+    uint4 q[kOwn];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+        q[j] = r < G ? __ldg(static_cast<const uint4 *>(p.q) + (static_cast<int64_t>(b) * p.n_heads + g * G + r) * kChunks + t + 4 * j)
+                     : make_uint4(0, 0, 0, 0);
+    int page = static_cast<int>(page_at(p, row, min(group * kScoreGroup + (lane & 15), n - 1)));
+    if (p.pdl) griddep_wait();
+    const uint4 *base = static_cast<const uint4 *>(p.page_bounds) + t;
+    const uint4 *r0 = base + ((p.layer_page0 + __shfl_sync(0xffffffffu, page, r)) * p.n_kv_heads + g) * 2 * kChunks;
+    const uint4 *r1 = base + ((p.layer_page0 + __shfl_sync(0xffffffffu, page, r + 8)) * p.n_kv_heads + g) * 2 * kChunks;
+    uint4 l0[kOwn], l1[kOwn], h0[kOwn], h1[kOwn];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        l0[j] = __ldg(r0 + 4 * j);
+        l1[j] = __ldg(r1 + 4 * j);
+        h0[j] = __ldg(r0 + kChunks + 4 * j);
+        h1[j] = __ldg(r1 + kChunks + 4 * j);
+    }
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+    uint4 most = h0[0], least = l0[0];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const uint4 qn = make_uint4(min_word(q[j].x, 0, bf16{}), min_word(q[j].y, 0, bf16{}), min_word(q[j].z, 0, bf16{}), min_word(q[j].w, 0, bf16{}));
+        const uint4 qp = make_uint4(max_word(q[j].x, 0, bf16{}), max_word(q[j].y, 0, bf16{}), max_word(q[j].z, 0, bf16{}), max_word(q[j].w, 0, bf16{}));
+        mma16816(x, l0[j].x, l1[j].x, l0[j].y, l1[j].y, qn.x, qn.y);
+        mma16816(y, h0[j].x, h1[j].x, h0[j].y, h1[j].y, qp.x, qp.y);
+        mma16816(x, l0[j].z, l1[j].z, l0[j].w, l1[j].w, qn.z, qn.w);
+        mma16816(y, h0[j].z, h1[j].z, h0[j].w, h1[j].w, qp.z, qp.w);
+        widen_bounds<bf16>(least, most, l0[j], h0[j]);
+        widen_bounds<bf16>(least, most, l1[j], h1[j]);
+    }
+    // rows r and r + 8, heads 2t and 2t + 1
+    float s0 = -INFINITY, s1 = -INFINITY;
+    if (2 * t < G) {
+        s0 = x[0] + y[0];
+        s1 = x[2] + y[2];
+    }
+    if (2 * t + 1 < G) {
+        s0 = max_nan(s0, x[1] + y[1]);
+        s1 = max_nan(s1, x[3] + y[3]);
+    }
+    const uint32_t hi = max_word(max_word(most.x, most.y, bf16{}), max_word(most.z, most.w, bf16{}), bf16{});
+    const uint32_t lo = min_word(min_word(least.x, least.y, bf16{}), min_word(least.z, least.w, bf16{}), bf16{});
+    float biggest = max_nan(max_nan(bf16lo(hi), bf16hi(hi)), -min_nan(bf16lo(lo), bf16hi(lo)));
+#pragma unroll
+    for (int off = 1; off <= 2; off <<= 1) {
+        s0 = max_nan(s0, __shfl_xor_sync(0xffffffffu, s0, off));
+        s1 = max_nan(s1, __shfl_xor_sync(0xffffffffu, s1, off));
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) biggest = max_nan(biggest, __shfl_xor_sync(0xffffffffu, biggest, off));
+    const int64_t unit = static_cast<int64_t>(b) * p.n_kv_heads + g;
+    float *out = p.scores + unit * p.page_cap + group * kScoreGroup;      // page_cap is whole groups
+    if (t == 0) {
+        out[r] = s0;
+        out[r + 8] = s1;
+    }
+    if (lane == 0) p.group_max[unit * (p.page_cap / kScoreGroup) + group] = biggest;
+}
+
 // ---------------------------------------------------------------------------
 // Selection
 // ---------------------------------------------------------------------------
@@ -546,7 +634,9 @@ cudaError_t launch_select(const SelectParams &p, cudaStream_t s) {
         cfg.stream = s;
         cfg.attrs = attr;
         cfg.numAttrs = p.pdl ? 1 : 0;
-        cudaError_t e = cudaLaunchKernelEx(&cfg, score_pages_kernel<T, D, G>, p);
+        cudaError_t e;
+        if constexpr (Elem<T>::bytes == 2) e = cudaLaunchKernelEx(&cfg, score_pages_mma_kernel<D, G>, p);
+        else e = cudaLaunchKernelEx(&cfg, score_pages_kernel<T, D, G>, p);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

@@ -49,7 +49,7 @@ template <int kParts, int kHeads, int D>
 struct Partials {
     float m[kParts][kHeads];
     float l[kParts][kHeads];
-    float o[kParts][kHeads][D];
+    alignas(16) float o[kParts][kHeads][D];
 };
 
 // Joins the parts of every CTA of the cluster and writes o.  Part 0 becomes
@@ -285,6 +285,164 @@ __global__ void __launch_bounds__(kSimtThreads) selected_simt_kernel(const Selec
     join<T, kSimtWarps, kHeads, D, kSimtThreads>(sh, static_cast<T *>(p.o) + out0, rank, p.splits);
 }
 
+// ---------------------------------------------------------------------------
+// Tensor cores (bf16)
+// ---------------------------------------------------------------------------
+
+constexpr int kMmaWarps = 8;
+constexpr int kMmaThreads = kMmaWarps * 32;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// A warp takes a block of 16 positions at a time, with lane (r, t) = (lane / 4,
+// lane % 4).  Both products read their operands from memory straight into
+// fragments, so nothing is staged and there is no barrier in the loop:
+//   S[8 heads x 16]   = Q K^T: a dot product may take its terms in any order,
+//     so lane (r, t) loads the 16-byte chunks t, t + 4, ... of the K rows r and
+//     r + 8 (and of head r's q) and feeds them as the columns 2t, 2t + 1, 2t +
+//     8, 2t + 9 of successive k steps;
+//   O^T[D x 8 heads] += V^T P^T: P of positions 2t, 2t + 1, 2t + 8, 2t + 9 and
+//     head r is where S left it, and lane (r, t) loads the chunks r and r + 8
+//     of those four V rows; a byte permutation pairs two rows' channels, and
+//     output row r of step i stands for channel 8 r + 2 i, row r + 8 for the
+//     next one.
+// P goes in as two bf16 parts (hi + lo, 16 bits together): one part alone would
+// add an error of the size of the output's own rounding.
+template <int D, int G>
+__global__ void __launch_bounds__(kMmaThreads, 2) selected_mma_kernel(const SelectedParams p) {
+    constexpr int kChunks = D / 8, kOwn = kChunks / 4, kHalves = D / 64;
+    __shared__ Partials<kMmaWarps, G, D> sh;
+    __shared__ Run runs[kStagePages];
+    griddep_launch();
+    const int rank = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
+    const int64_t out0 = (static_cast<int64_t>(b) * p.n_heads + g * G) * D;
+    uint4 q[kOwn];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+        q[j] = r < G ? __ldg(static_cast<const uint4 *>(p.q) + out0 / 8 + r * kChunks + t + 4 * j) : make_uint4(0, 0, 0, 0);
+    if (p.pdl) griddep_wait();
+    const Share s = cta_share(p, g, b, rank, rank == 0 && threadIdx.x == 0);
+    const int32_t *sel = p.sel + (static_cast<int64_t>(b) * p.n_kv_heads + g) * p.top_k;
+
+    float m = -INFINITY, l = 0.f;            // head r; l over this lane's positions
+    float o[kHalves * 4][4];                 // channels 64 * (i / 4) + 8 r + 2 (i % 4) (+ 1), heads 2t, 2t + 1
+#pragma unroll
+    for (int i = 0; i < kHalves * 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+    const int i_end = s.t1 > s.t0 ? (s.t1 - 1) / p.page_size + 1 : 0;
+    for (int i0 = s.t0 / p.page_size; i0 < i_end; i0 += kStagePages) {
+        const int i1 = min(i_end, i0 + kStagePages);
+        __syncthreads();
+        stage_runs<kMmaThreads>(p, s, sel, i0, i1, runs);
+        __syncthreads();
+        const int from = max(s.t0, i0 * p.page_size);
+        const int to = static_cast<int>(min(static_cast<int64_t>(s.t1), static_cast<int64_t>(i1) * p.page_size));
+        for (int at = from + warp * kBlk; at < to; at += kMmaWarps * kBlk) {
+            int slot = -1;                   // of position lane % 16 of the block
+            if (at + (lane & 15) < to) {
+                const int x = at + (lane & 15), i = x / p.page_size, off = x - i * p.page_size;
+                const Run run = runs[i - i0];
+                if (run.pos >= 0 && static_cast<unsigned>(run.pos) + off < static_cast<unsigned>(s.len)) slot = run.slot + off;
+            }
+            const int ks[2] = {__shfl_sync(0xffffffffu, slot, r), __shfl_sync(0xffffffffu, slot, r + 8)};
+            uint4 k[2][kOwn], v[4][kHalves];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 *row = static_cast<const uint4 *>(p.k_buffer) + ((p.layer_row0 + ks[i]) * p.n_kv_heads + g) * kChunks + t;
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j) k[i][j] = ks[i] >= 0 ? __ldg(row + 4 * j) : make_uint4(0, 0, 0, 0);
+            }
+            bool seen[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int vs = __shfl_sync(0xffffffffu, slot, 2 * t + (i & 1) + 8 * (i >> 1));
+                seen[i] = vs >= 0;
+                const uint4 *row = static_cast<const uint4 *>(p.v_buffer) + ((p.layer_row0 + vs) * p.n_kv_heads + g) * kChunks + r;
+#pragma unroll
+                for (int j = 0; j < kHalves; ++j) v[i][j] = vs >= 0 ? __ldg(row + 8 * j) : make_uint4(0, 0, 0, 0);
+            }
+            float w[2][4] = {};
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mma16816(w[i], q[j].x, 0, q[j].y, 0, k[i][j].x, k[i][j].y);
+                    mma16816(w[i], q[j].z, 0, q[j].w, 0, k[i][j].z, k[i][j].w);
+                }
+            // head r, positions 2t, 2t + 1, 2t + 8, 2t + 9
+            float pr[4];
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pr[i] = seen[i] ? w[i >> 1][i & 1] * p.scale_log2 : -INFINITY;
+                top = fmaxf(top, pr[i]);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (__any_sync(0xffffffffu, top != m)) {
+                const float f = weight(m, top);
+                m = top;
+                l *= f;
+                const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+                for (int i = 0; i < kHalves * 4; ++i) {
+                    o[i][0] *= f0;
+                    o[i][1] *= f1;
+                    o[i][2] *= f0;
+                    o[i][3] *= f1;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pr[i] = weight(pr[i], m);
+                l += pr[i];
+            }
+            const uint32_t hi0 = pack_bf16(pr[0], pr[1]), hi1 = pack_bf16(pr[2], pr[3]);
+            const uint32_t lo0 = pack_bf16(pr[0] - bf16lo(hi0), pr[1] - bf16hi(hi0));
+            const uint32_t lo1 = pack_bf16(pr[2] - bf16lo(hi1), pr[3] - bf16hi(hi1));
+#pragma unroll
+            for (int j = 0; j < kHalves; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a0 = __byte_perm(word(v[0][j], i), word(v[1][j], i), 0x5410);
+                    const uint32_t a1 = __byte_perm(word(v[0][j], i), word(v[1][j], i), 0x7632);
+                    const uint32_t a2 = __byte_perm(word(v[2][j], i), word(v[3][j], i), 0x5410);
+                    const uint32_t a3 = __byte_perm(word(v[2][j], i), word(v[3][j], i), 0x7632);
+                    mma16816(o[j * 4 + i], a0, a1, a2, a3, hi0, hi1);
+                    mma16816(o[j * 4 + i], a0, a1, a2, a3, lo0, lo1);
+                }
+        }
+    }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (t == 0 && r < G) {
+        sh.m[warp][r] = m;
+        sh.l[warp][r] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < kHalves * 4; ++i) {
+        const int c = 64 * (i / 4) + 8 * r + 2 * (i % 4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (2 * t + e < G) *reinterpret_cast<float2 *>(&sh.o[warp][2 * t + e][c]) = make_float2(o[i][e], o[i][2 + e]);
+    }
+    join<bf16, kMmaWarps, G, D, kMmaThreads>(sh, static_cast<bf16 *>(p.o) + out0, rank, p.splits);
+}
+
 template <typename K>
 cudaError_t launch_cluster(K kernel, dim3 grid, int threads, const SelectedParams &p, cudaStream_t s) {
     cudaLaunchAttribute attr[2];
@@ -310,6 +468,21 @@ cudaError_t launch_cluster(K kernel, dim3 grid, int threads, const SelectedParam
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <int D, int G>
+cudaError_t run_mma(const SelectedParams &p, cudaStream_t s) {
+    return launch_cluster(selected_mma_kernel<D, G>, dim3(p.splits, p.n_kv_heads, p.batch), kMmaThreads, p, s);
+}
+
+template <int D>
+cudaError_t run_mma_g(const SelectedParams &p, int group, cudaStream_t s) {
+    switch (group) {
+        case 1: return run_mma<D, 1>(p, s);
+        case 2: return run_mma<D, 2>(p, s);
+        case 4: return run_mma<D, 4>(p, s);
+        default: return run_mma<D, 8>(p, s);
+    }
+}
+
 template <typename T, int D, int kHeads>
 cudaError_t run_simt(const SelectedParams &p, cudaStream_t s) {
     return launch_cluster(selected_simt_kernel<T, D, kHeads>, dim3(p.splits, p.n_heads / kHeads, p.batch), kSimtThreads, p, s);
@@ -332,14 +505,14 @@ int selected_splits(int64_t batch, int n_kv_heads, int64_t top_k, int64_t page_s
     const int64_t pages = (max_len + page_size - 1) / page_size;
     const int64_t blocks = (top_k < pages ? top_k : pages) * page_size / kBlk + 1;
     int splits = 1;
-    while (splits < kMaxSplits && units * splits < 2LL * sms && blocks >= 4LL * splits * 2) splits *= 2;
+    while (splits < kMaxSplits && units * splits < 2LL * sms && blocks >= static_cast<int64_t>(kMmaWarps) * splits * 2) splits *= 2;
     return splits;
 }
 
 cudaError_t launch_decode_selected(const SelectedParams &p, int dtype, int head_dim, int group, cudaStream_t s) {
     if (!sparse_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
     if (p.splits < 1 || p.splits > kMaxSplits) return cudaErrorInvalidValue;
-    if (dtype == PKV_BF16) return head_dim == 128 ? run_simt_g<bf16, 128>(p, group, s) : run_simt_g<bf16, 64>(p, group, s);
+    if (dtype == PKV_BF16) return head_dim == 128 ? run_mma_g<128>(p, group, s) : run_mma_g<64>(p, group, s);
     return head_dim == 128 ? run_simt_g<float, 128>(p, group, s) : run_simt_g<float, 64>(p, group, s);
 }
 
