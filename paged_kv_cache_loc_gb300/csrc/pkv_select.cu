@@ -334,8 +334,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_pages_mma_kernel(const
 // Selection
 // ---------------------------------------------------------------------------
 
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelOwn = 8;               // pages per thread whose scores stay in registers
 constexpr int kBins = 2048;
 constexpr int kUndecided = 512;          // scored in 64 bits from a list; more: by radix passes
 
@@ -354,16 +355,21 @@ __device__ __forceinline__ unsigned long long key64(double s) {
     return u >> 63 ? ~u : u | (1ull << 63);
 }
 
+template <int D, int G>
 struct SelShared {
+    float q[G][D];
+    int hist[kBins];
     int warp_sum[kSelWarps];
     float red[kSelWarps];
     uint32_t lo[kSelWarps], hi[kSelWarps];
-    int hist[kBins];
-    int bin, above, count, total;
+    int bin, above;
+    int und_page[kUndecided];
+    long long und_key[kUndecided];
+    uint32_t und_in[kUndecided / 32];
 };
 
-// Inclusive block scan of one int per thread (kSelThreads threads).
-__device__ __forceinline__ int block_scan(SelShared &sh, int v, int *total) {
+// Inclusive scan over the warps of a per-thread int.
+__device__ __forceinline__ int block_scan(int *warp_sum, int v, int *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -371,203 +377,230 @@ __device__ __forceinline__ int block_scan(SelShared &sh, int v, int *total) {
         if (lane >= off) v += y;
     }
     __syncthreads();
-    if (lane == 31) sh.warp_sum[warp] = v;
+    if (lane == 31) warp_sum[warp] = v;
     __syncthreads();
-    int t = 0;
+    int w = lane < kSelWarps ? warp_sum[lane] : 0;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-        if (w < warp) v += sh.warp_sum[w];
-        t += sh.warp_sum[w];
+    for (int off = 1; off < kSelWarps; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, off);
+        if (lane >= off) w += y;
     }
-    *total = t;
-    return v;
+    *total = __shfl_sync(0xffffffffu, w, kSelWarps - 1);
+    const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    return warp > 0 ? v + before : v;
 }
 
-// The bin (from the top) that holds rank `rank` (1-based) of the histogram:
-// sh.bin, and sh.above = the count in higher bins.
-__device__ __forceinline__ void find_bin(SelShared &sh, int bins, int rank) {
-    const int per = (bins + kSelThreads - 1) / kSelThreads;
-    const int top = bins - 1 - static_cast<int>(threadIdx.x) * per;   // this thread: top, top - 1, ...
-    int own = 0, total;
-    for (int k = 0; k < per; ++k)
-        if (top - k >= 0) own += sh.hist[top - k];
-    const int inc = block_scan(sh, own, &total);
+// The bin (from the top) that holds rank `rank` (1-based) of the histogram of
+// kBins bins: sh.bin, and sh.above = the count in higher bins.
+template <int D, int G>
+__device__ __forceinline__ void find_bin(SelShared<D, G> &sh, int rank) {
+    constexpr int kPer = kBins / kSelThreads;
+    const int top = kBins - 1 - static_cast<int>(threadIdx.x) * kPer;   // this thread: top, top - 1, ...
+    int c[kPer], own = 0, total;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) own += c[k] = sh.hist[top - k];
+    const int inc = block_scan(sh.warp_sum, own, &total);
     int before = inc - own;
     if (before < rank && rank <= inc) {
-        for (int k = 0; k < per; ++k) {
-            const int c = sh.hist[top - k];
-            if (before + c >= rank) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            if (before < rank && rank <= before + c[k]) {
                 sh.bin = top - k;
                 sh.above = before;
-                break;
             }
-            before += c;
+            before += c[k];
         }
     }
     __syncthreads();
 }
 
-// The 64-bit score of a page, by a warp: lane partial sums in a fixed order,
-// so equal bounds give equal scores.
-template <typename T, int D, int G>
-__device__ __forceinline__ unsigned long long exact_key(const SelectParams &p, const float (*q)[D], int row, int g, int pg) {
+// The 64-bit key of a page's score for query head h, by a warp: lane partial
+// sums in a fixed order, so equal bounds give equal keys.
+template <typename T, int D>
+__device__ __forceinline__ unsigned long long exact_head_key(const SelectParams &p, const float *q, int64_t bounds_row) {
     const int lane = threadIdx.x & 31;
-    const T *lo = static_cast<const T *>(p.page_bounds) +
-                  ((p.layer_page0 + page_at(p, row, pg)) * p.n_kv_heads + g) * 2 * D;
-    double s[G];
+    const T *lo = static_cast<const T *>(p.page_bounds) + bounds_row * 2 * D;
+    float l[D / 32], u[D / 32];
 #pragma unroll
-    for (int h = 0; h < G; ++h) s[h] = 0.0;
+    for (int c = 0; c < D / 32; ++c) {
+        l[c] = Elem<T>::to_f(lo[c * 32 + lane]);
+        u[c] = Elem<T>::to_f(lo[D + c * 32 + lane]);
+    }
+    double s = 0.0;
 #pragma unroll
-    for (int c = 0; c < D; c += 32) {
-        const float l = Elem<T>::to_f(lo[c + lane]), u = Elem<T>::to_f(lo[D + c + lane]);
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const float qv = q[h][c + lane];
-            s[h] = fma(static_cast<double>(qv), static_cast<double>(qv >= 0.f ? u : l), s[h]);
-        }
+    for (int c = 0; c < D / 32; ++c) {
+        const float qv = q[c * 32 + lane];
+        s = fma(static_cast<double>(qv), static_cast<double>(qv >= 0.f ? u[c] : l[c]), s);
     }
 #pragma unroll
-    for (int h = 0; h < G; ++h)
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], off);
-    unsigned long long best = key64(s[0]);
-#pragma unroll
-    for (int h = 1; h < G; ++h) best = max(best, key64(s[h]));
+    for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return key64(s);
+}
+
+template <typename T, int D, int G>
+__device__ __forceinline__ unsigned long long exact_key(const SelectParams &p, const SelShared<D, G> &sh, int row, int g, int pg) {
+    const int64_t at = (p.layer_page0 + page_at(p, row, pg)) * p.n_kv_heads + g;
+    unsigned long long best = 0;
+#pragma unroll 1
+    for (int h = 0; h < G; ++h) best = max(best, exact_head_key<T, D>(p, sh.q[h], at));
     return best;
 }
 
-// One CTA per (kv head, entry).
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectParams p) {
-    __shared__ SelShared sh;
-    __shared__ float q[G][D];
-    __shared__ int und_page[kUndecided];
-    __shared__ unsigned long long und_key[kUndecided];
-    griddep_launch();
-    const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t unit = static_cast<int64_t>(b) * p.n_kv_heads + g;
-    int row;
-    const int n = entry_pages(p, b, &row, g == 0 && tid == 0);
-    int32_t *sel = p.sel + unit * p.top_k;
-    const int count = min(n, p.top_k);
-    if (tid == 0) p.sel_counts[unit] = count;
-    if (n <= p.top_k) {
-        for (int i = tid; i < p.top_k; i += kSelThreads) sel[i] = i < n ? i : -1;
-        griddep_wait();
-        return;
-    }
-    const int c0 = p.n_first, m = n - p.n_first - p.n_last;       // candidates c0 .. c0 + m - 1
-    const int keep = p.top_k - p.n_first - p.n_last;              // of them
-    for (int i = tid; i < p.n_first; i += kSelThreads) sel[i] = i;
-    for (int i = tid; i < p.n_last; i += kSelThreads) sel[p.top_k - p.n_last + i] = n - p.n_last + i;
-    for (int i = tid; i < G * D; i += kSelThreads)
-        q[i / D][i % D] = Elem<T>::to_f(static_cast<const T *>(p.q)[(static_cast<int64_t>(b) * p.n_heads + g * G) * D + i]);
-    griddep_wait();                                               // the scores
-    if (keep == 0) return;
-    float *score = p.scores + unit * p.page_cap + c0;
-    const float *gmax = p.group_max + unit * (p.page_cap / kScoreGroup);
-    __syncthreads();
-
-    // range of the keys, the error bound, and whether every score is finite
-    uint32_t klo = 0xffffffffu, khi = 0;
-    for (int i = tid; i < m; i += kSelThreads) {
-        const uint32_t k = key32(score[i]);
-        klo = min(klo, k);
-        khi = max(khi, k);
-    }
-    float big = 0.f;
-    for (int i = tid; i < (n + kScoreGroup - 1) / kScoreGroup; i += kSelThreads) big = max_nan(big, gmax[i]);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        klo = min(klo, __shfl_xor_sync(0xffffffffu, klo, off));
-        khi = max(khi, __shfl_xor_sync(0xffffffffu, khi, off));
-        big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, off));
-    }
-    if (lane == 0) {
-        sh.lo[warp] = klo;
-        sh.hi[warp] = khi;
-        sh.red[warp] = big;
-    }
-    __syncthreads();
-    float norm = 0.f;                                             // max_h sum_c |q|, every warp by itself
+// Largest sum_c |q[h, c]| over the heads, every warp by itself.
+template <int D, int G>
+__device__ __forceinline__ float query_norm(const SelShared<D, G> &sh) {
+    const int lane = threadIdx.x & 31;
+    float norm = 0.f;
 #pragma unroll
     for (int h = 0; h < G; ++h) {
         float s = 0.f;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) s += fabsf(q[h][c + lane]);
+        for (int c = 0; c < D; c += 32) s += fabsf(sh.q[h][c + lane]);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         norm = max_nan(norm, s);
     }
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-        klo = min(klo, sh.lo[w]);
-        khi = max(khi, sh.hi[w]);
-        big = max_nan(big, sh.red[w]);
-    }
-    const float slack = 2.f * kScoreEps * norm * big + kScoreTiny;   // 2e
-    const bool finite = klo > key32(-INFINITY) && khi < key32(INFINITY) && slack < INFINITY;
+    return norm;
+}
 
-    // the 32-bit threshold's bin [fl, fh], narrowed until few pages are undecided
-    float fl = -INFINITY, fh = INFINITY;
-    int decided = 0, undecided = m;
-    if (finite) {
-        uint32_t lo = klo, hi = khi;
-        int rank = keep;
-        for (;;) {
-            const int shift = max(0, 32 - __clz(hi - lo) - 11);
-            const int bins = static_cast<int>((hi - lo) >> shift) + 1;
-            for (int i = tid; i < bins; i += kSelThreads) sh.hist[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < m; i += kSelThreads) {
-                const uint32_t k = key32(score[i]);
-                if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
-            }
-            __syncthreads();
-            find_bin(sh, bins, rank);
-            rank -= sh.above;
-            lo += static_cast<uint32_t>(sh.bin) << shift;
-            hi = min(hi, lo + ((1u << shift) - 1u));
-            fl = unkey32(lo) - slack;
-            fh = unkey32(hi) + slack;
-            int in = 0, mid = 0;
-            for (int i = tid; i < m; i += kSelThreads) {
-                const float s = score[i];
-                in += s > fh;
-                mid += s >= fl && s <= fh;
-            }
-            int t;
-            block_scan(sh, in, &t);
-            decided = t;
-            block_scan(sh, mid, &t);
-            undecided = t;
-            __syncthreads();
-            if (undecided <= kUndecided || shift == 0) break;
-        }
+// Scores in 64-bit fixed point.  With |score| <= norm * big < 2^e, a term
+// counts in units of 2^(e - 61): a bf16 product is exact in fp32, an fp32 one
+// is taken as its rounding and the remainder, and integer sums do not round,
+// so the order of the terms does not matter.  Each term is off by half a unit
+// at most, 2^-62 of the bound, where a sum in fp64 rounds to 2^-53 of the
+// partial sums; fp64 arithmetic itself is too slow on this chip (17 us of a
+// selection went there).  For scale exponents inside fp32's range; the general
+// path takes fp64 otherwise.
+__device__ __forceinline__ bool fixed_point_scale(float norm, float big, float *scale) {
+    int a = 0, b = 0;
+    frexpf(norm, &a);
+    frexpf(big, &b);
+    const int e = a + b + 1;                 // one more: norm is a rounded sum
+    *scale = ldexpf(1.f, 61 - (e < -40 ? -40 : e > 120 ? 120 : e));
+    return e >= -40 && e <= 120;
+}
+
+// A page's fixed-point score for the heads h < G, the largest, by a warp.
+template <typename T, int D, int G>
+__device__ __forceinline__ long long fixed_score(const SelectParams &p, const SelShared<D, G> &sh, int64_t bounds_row, float scale) {
+    const int lane = threadIdx.x & 31;
+    const T *lo = static_cast<const T *>(p.page_bounds) + bounds_row * 2 * D;
+    float l[D / 32], u[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        l[c] = Elem<T>::to_f(lo[c * 32 + lane]);
+        u[c] = Elem<T>::to_f(lo[D + c * 32 + lane]);
     }
-    const int need = keep - decided;                              // of the undecided
+    long long best = 0;
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+        long long s = 0;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const float qv = sh.q[h][c * 32 + lane], x = qv >= 0.f ? u[c] : l[c];
+            const float prod = qv * x;
+            s += __float2ll_rn(prod * scale);
+            if constexpr (Elem<T>::bytes == 4) s += __float2ll_rn(fmaf(qv, x, -prod) * scale);
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        best = h == 0 ? s : max(best, s);
+    }
+    return best;
+}
+
+// Ranks the `n` <= kUndecided pages of sh.und_page by their fixed-point scores
+// and sets the bits of sh.und_in for the first `need` of them.
+template <typename T, int D, int G>
+__device__ __forceinline__ void rank_undecided(const SelectParams &p, SelShared<D, G> &sh, int row, int g, int n, int need, float scale) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int k = warp; k < n; k += kSelWarps) {
+        const int64_t at = (p.layer_page0 + page_at(p, row, sh.und_page[k])) * p.n_kv_heads + g;
+        const long long key = fixed_score<T, D, G>(p, sh, at, scale);
+        if (lane == 0) sh.und_key[k] = key;
+    }
+    __syncthreads();
+    static_assert(kUndecided <= kSelThreads, "one undecided page per thread");
+    bool in = false;
+    if (tid < n) {
+        const long long key = sh.und_key[tid];
+        const int pg = sh.und_page[tid];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += sh.und_key[j] > key || (sh.und_key[j] == key && sh.und_page[j] < pg);
+        in = rank < need;
+    }
+    const unsigned bits = __ballot_sync(0xffffffffu, in);
+    if (lane == 0 && warp < kUndecided / 32) sh.und_in[warp] = bits;
+    __syncthreads();
+}
+
+// The threshold's bin [*fl, *fh] (the error bound included) of the 32-bit
+// scores, narrowed until at most kUndecided pages lie in it or a bin is one
+// key.  sh.hist is zero on entry.  each(f) calls f(key, score) for this
+// thread's candidates.
+// Returns the counts (above, inside) of all candidates; *before are those of
+// the threads before this one.
+template <int D, int G, typename Each>
+__device__ __forceinline__ int2 find_threshold(SelShared<D, G> &sh, uint32_t lo, uint32_t hi, int rank, float slack, Each each,
+                                               float *fl, float *fh, int2 *before) {
+    const int tid = threadIdx.x;
+    for (;;) {
+        const int shift = max(0, 32 - __clz(hi - lo) - 11);
+        each([&](uint32_t k, float) {
+            if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
+        });
+        __syncthreads();
+        find_bin(sh, rank);
+        rank -= sh.above;
+        lo += static_cast<uint32_t>(sh.bin) << shift;
+        hi = min(hi, lo + ((1u << shift) - 1u));
+        const float a = unkey32(lo) - slack, z = unkey32(hi) + slack;
+        int in = 0, mid = 0, t_in, t_mid;
+        each([&](uint32_t, float s) {
+            in += s > z;
+            mid += s >= a && s <= z;
+        });
+        before->x = block_scan(sh.warp_sum, in, &t_in) - in;
+        before->y = block_scan(sh.warp_sum, mid, &t_mid) - mid;
+        *fl = a;
+        *fh = z;
+        if (t_mid <= kUndecided || shift == 0) return make_int2(t_in, t_mid);
+        for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+        __syncthreads();
+    }
+}
+
+// The general path: scores stay in memory and are read in every pass; decided
+// pages are marked there by +-inf.  For contexts of more pages than the
+// registers hold, and where more than kUndecided pages are undecided.
+template <typename T, int D, int G>
+__device__ __noinline__ void select_general(const SelectParams &p, SelShared<D, G> &sh, int row, int g, int n, float *score, int32_t *sel,
+                                            uint32_t klo, uint32_t khi, float slack, bool finite, float scale) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c0 = p.n_first, m = n - p.n_first - p.n_last, keep = p.top_k - p.n_first - p.n_last;
+    score += c0;
+    float fl = -INFINITY, fh = INFINITY;
+    int2 count = make_int2(0, m), before;
+    const auto each = [&](auto f) {
+        for (int i = tid; i < m; i += kSelThreads) {
+            const float s = score[i];
+            f(key32(s), s);
+        }
+    };
+    if (finite) count = find_threshold(sh, klo, khi, keep, slack, each, &fl, &fh, &before);
+    const int need = keep - count.x, undecided = count.y;
     if (need < undecided) {
-        if (undecided <= kUndecided) {
-            // 64-bit scores from a list, ranked by (score, page)
-            if (tid == 0) sh.count = 0;
+        if (finite && undecided <= kUndecided) {
+            if (tid == 0) sh.bin = 0;
             __syncthreads();
             for (int i = tid; i < m; i += kSelThreads) {
                 const float s = score[i];
-                if (!finite || (s >= fl && s <= fh)) und_page[atomicAdd(&sh.count, 1)] = i;
+                if (s >= fl && s <= fh) sh.und_page[atomicAdd(&sh.bin, 1)] = c0 + i;
             }
             __syncthreads();
-            for (int k = warp; k < undecided; k += kSelWarps) {
-                const unsigned long long x = exact_key<T, D, G>(p, q, row, g, c0 + und_page[k]);
-                if (lane == 0) und_key[k] = x;
-            }
-            __syncthreads();
-            for (int k = tid; k < undecided; k += kSelThreads) {
-                const unsigned long long x = und_key[k];
-                const int pg = und_page[k];
-                int rank = 0;
-                for (int j = 0; j < undecided; ++j) rank += und_key[j] > x || (und_key[j] == x && und_page[j] < pg);
-                score[pg] = rank < need ? INFINITY : -INFINITY;
-            }
+            rank_undecided<T, D, G>(p, sh, row, g, undecided, need, scale);
+            for (int k = tid; k < undecided; k += kSelThreads)
+                score[sh.und_page[k] - c0] = sh.und_in[k / 32] >> (k % 32) & 1 ? INFINITY : -INFINITY;
         } else {
             // Many pages within rounding of the threshold (pages that are
             // alike, or scores that are not finite): radix selection on the
@@ -575,17 +608,17 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectP
             unsigned long long prefix = 0;
             int rank = need;
             for (int byte = 7; byte >= 0; --byte) {
-                for (int i = tid; i < 256; i += kSelThreads) sh.hist[i] = 0;
+                for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
                 __syncthreads();
                 for (int i = warp; i < m; i += kSelWarps) {
                     const float s = score[i];
                     if (finite && !(s >= fl && s <= fh)) continue;
-                    const unsigned long long x = exact_key<T, D, G>(p, q, row, g, c0 + i);
+                    const unsigned long long x = exact_key<T, D, G>(p, sh, row, g, c0 + i);
                     if (lane == 0 && (byte == 7 || (x >> (8 * byte + 8)) == (prefix >> (8 * byte + 8))))
                         atomicAdd(&sh.hist[(x >> (8 * byte)) & 255], 1);
                 }
                 __syncthreads();
-                find_bin(sh, 256, rank);
+                find_bin(sh, rank);
                 rank -= sh.above;
                 prefix |= static_cast<unsigned long long>(sh.bin) << (8 * byte);
                 __syncthreads();
@@ -596,28 +629,157 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectP
                 const int i = i0 + warp;
                 const float s = i < m ? score[i] : 0.f;
                 const bool mine = i < m && (!finite || (s >= fl && s <= fh));
-                const unsigned long long x = mine ? exact_key<T, D, G>(p, q, row, g, c0 + i) : 0;
+                const unsigned long long x = mine ? exact_key<T, D, G>(p, sh, row, g, c0 + i) : 0;
                 int t;
-                const int at = equal + block_scan(sh, mine && x == prefix && lane == 0, &t);
+                const int at = equal + block_scan(sh.warp_sum, mine && x == prefix && lane == 0, &t);
                 if (mine && lane == 0) score[i] = x > prefix || (x == prefix && at <= rank) ? INFINITY : -INFINITY;
                 equal += t;
             }
-            __syncthreads();
         }
-        if (!finite) fh = 3e38f;                                  // every score is now +-inf
         __syncthreads();
+        if (!finite) fh = 3e38f;                                  // every score is now +-inf
     }
     // in ascending order: pages above the bin, and of the bin those marked +inf
     // (all of it where its pages are all needed)
-    const float least = need < undecided ? fh : fl;
     const bool whole = !(need < undecided);
     const int per = (m + kSelThreads - 1) / kSelThreads;
     const int i0 = min(m, tid * per), i1 = min(m, i0 + per);
     int mine = 0, t;
-    for (int i = i0; i < i1; ++i) mine += whole ? score[i] >= least : score[i] > least;
-    int at = p.n_first + block_scan(sh, mine, &t) - mine;
+    for (int i = i0; i < i1; ++i) mine += whole ? score[i] >= fl : score[i] > fh;
+    int at = p.n_first + block_scan(sh.warp_sum, mine, &t) - mine;
     for (int i = i0; i < i1; ++i)
-        if (whole ? score[i] >= least : score[i] > least) sel[at++] = c0 + i;
+        if (whole ? score[i] >= fl : score[i] > fh) sel[at++] = c0 + i;
+}
+
+// One CTA per (kv head, entry).  Up to kSelThreads * kSelOwn pages, thread i
+// keeps the scores of pages kSelOwn * i ... in registers: they are read once,
+// and every later pass (range, histogram, counts, output) is on registers with
+// one block-wide scan.  What bounds it is the chain of these passes (latency);
+// the bytes are few.
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectParams p) {
+    __shared__ SelShared<D, G> sh;
+    griddep_launch();
+    const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t unit = static_cast<int64_t>(b) * p.n_kv_heads + g;
+    for (int i = tid; i < G * D; i += kSelThreads)
+        sh.q[i / D][i % D] = Elem<T>::to_f(static_cast<const T *>(p.q)[(static_cast<int64_t>(b) * p.n_heads + g * G) * D + i]);
+    for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+    int row;
+    const int n = entry_pages(p, b, &row, g == 0 && tid == 0);
+    int32_t *sel = p.sel + unit * p.top_k;
+    if (tid == 0) p.sel_counts[unit] = min(n, p.top_k);
+    if (n <= p.top_k) {
+        for (int i = tid; i < p.top_k; i += kSelThreads) sel[i] = i < n ? i : -1;
+        griddep_wait();
+        return;
+    }
+    const int keep = p.top_k - p.n_first - p.n_last, c1 = n - p.n_last;   // candidates: pages n_first .. c1 - 1
+    for (int i = tid; i < p.n_first; i += kSelThreads) sel[i] = i;
+    for (int i = tid; i < p.n_last; i += kSelThreads) sel[p.top_k - p.n_last + i] = c1 + i;
+    __syncthreads();
+    const float norm = query_norm(sh);
+    griddep_wait();                                               // the scores
+    if (keep == 0) return;
+    float *score = p.scores + unit * p.page_cap;
+    const float *gmax = p.group_max + unit * (p.page_cap / kScoreGroup);
+    const bool fits = n <= kSelThreads * kSelOwn;
+
+    float s[kSelOwn];
+    uint32_t klo = 0xffffffffu, khi = 0;
+    float big = 0.f;
+    for (int i = tid; i < (n + kScoreGroup - 1) / kScoreGroup; i += kSelThreads) big = max_nan(big, gmax[i]);
+    const int mine = tid * kSelOwn;                               // this thread's first page
+    if (fits) {
+        if (mine < n) {                                           // page_cap is a multiple of kScoreGroup
+#pragma unroll
+            for (int i = 0; i < kSelOwn; i += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(score + mine + i);
+                s[i] = x.x;
+                s[i + 1] = x.y;
+                s[i + 2] = x.z;
+                s[i + 3] = x.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kSelOwn; ++i) {
+            if (mine + i >= p.n_first && mine + i < c1) {
+                klo = min(klo, key32(s[i]));
+                khi = max(khi, key32(s[i]));
+            }
+        }
+    } else {
+        for (int i = p.n_first + tid; i < c1; i += kSelThreads) {
+            const uint32_t k = key32(score[i]);
+            klo = min(klo, k);
+            khi = max(khi, k);
+        }
+    }
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, off));
+    if (lane == 0) {
+        sh.lo[warp] = klo;
+        sh.hi[warp] = khi;
+        sh.red[warp] = big;
+    }
+    __syncthreads();
+    klo = __reduce_min_sync(0xffffffffu, sh.lo[lane % kSelWarps]);
+    khi = __reduce_max_sync(0xffffffffu, sh.hi[lane % kSelWarps]);
+    big = sh.red[lane % kSelWarps];
+#pragma unroll
+    for (int off = kSelWarps / 2; off >= 1; off >>= 1) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, off));
+    const float slack = 2.f * kScoreEps * norm * big + kScoreTiny;   // 2e
+    float scale = 0.f;
+    const bool finite = klo > key32(-INFINITY) && khi < key32(INFINITY) && slack < INFINITY && fixed_point_scale(norm, big, &scale);
+    if (!fits || !finite) {
+        select_general<T, D, G>(p, sh, row, g, n, score, sel, klo, khi, slack, finite, scale);
+        return;
+    }
+
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < kSelOwn; ++i)
+            if (mine + i >= p.n_first && mine + i < c1) f(key32(s[i]), s[i]);
+    };
+    float fl, fh;
+    int2 before;
+    const int2 count = find_threshold(sh, klo, khi, keep, slack, each, &fl, &fh, &before);
+    const int need = keep - count.x;
+    const bool whole = need >= count.y;                           // the bin's pages are all needed
+    if (!whole) {
+        if (count.y > kUndecided) {
+            for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+            __syncthreads();
+            select_general<T, D, G>(p, sh, row, g, n, score, sel, klo, khi, slack, finite, scale);
+            return;
+        }
+        int k = before.y;
+#pragma unroll
+        for (int i = 0; i < kSelOwn; ++i)
+            if (mine + i >= p.n_first && mine + i < c1 && s[i] >= fl && s[i] <= fh) sh.und_page[k++] = mine + i;
+        __syncthreads();
+        rank_undecided<T, D, G>(p, sh, row, g, count.y, need, scale);
+    }
+    // in ascending order; the list of undecided pages is ascending too
+    int at = p.n_first + before.x, k = before.y;
+    if (whole) {
+        at += before.y;
+    } else {
+        for (int w = 0; w < k / 32; ++w) at += __popc(sh.und_in[w]);
+        at += k % 32 ? __popc(sh.und_in[k / 32] & ((1u << (k % 32)) - 1u)) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kSelOwn; ++i) {
+        if (mine + i < p.n_first || mine + i >= c1) continue;
+        bool in = s[i] > fh;
+        if (s[i] >= fl && s[i] <= fh) {
+            in = whole || (sh.und_in[k / 32] >> (k % 32) & 1);
+            ++k;
+        }
+        if (in) sel[at++] = mine + i;
+    }
 }
 
 template <typename T, int D, int G>

@@ -97,16 +97,23 @@ __device__ __forceinline__ void join(Partials<kParts, kHeads, D> &sh, T *out, in
     const int e1 = kOut * (rank + 1) / splits;
     for (int e = kOut * rank / splits + tid; e < e1; e += kThreads) {
         const int h = e / D, c = e % D;
-        float all = -INFINITY, l = 0.f, x = 0.f;
-        for (int r = 0; r < splits; ++r) all = fmaxf(all, ld_cluster(cluster_addr(&sh.m[0][h], r)));
-        for (int r = 0; r < splits; ++r) {
-            const float mr = ld_cluster(cluster_addr(&sh.m[0][h], r));
-            if (mr != -INFINITY) {
-                const float f = weight(mr, all);
-                l = fmaf(f, ld_cluster(cluster_addr(&sh.l[0][h], r)), l);
-                x = fmaf(f, ld_cluster(cluster_addr(&sh.o[0][h][c], r)), x);
-            }
+        float mr[kMaxSplits], lr[kMaxSplits], xr[kMaxSplits], all = -INFINITY, l = 0.f, x = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r) {           // all in flight together
+            const bool there = r < splits;
+            mr[r] = there ? ld_cluster(cluster_addr(&sh.m[0][h], r)) : -INFINITY;
+            lr[r] = there ? ld_cluster(cluster_addr(&sh.l[0][h], r)) : 0.f;
+            xr[r] = there ? ld_cluster(cluster_addr(&sh.o[0][h][c], r)) : 0.f;
         }
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r) all = fmaxf(all, mr[r]);
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+            if (mr[r] != -INFINITY) {
+                const float f = weight(mr[r], all);
+                l = fmaf(f, lr[r], l);
+                x = fmaf(f, xr[r], x);
+            }
         out[e] = Elem<T>::from_f(l == 0.f ? 0.f : x / l);
     }
     if (splits > 1) cluster_sync();      // no CTA leaves while its memory is read
@@ -145,11 +152,25 @@ __device__ __forceinline__ Share cta_share(const SelectedParams &p, int g, int b
     return s;
 }
 
+// The list entry that this thread resolves first if the list is full: it is
+// loaded beside the count and not after it.
+struct Guess {
+    int first, page;
+};
+__device__ __forceinline__ Guess guess_entry(const SelectedParams &p, const int32_t *sel, int rank) {
+    const int blocks = (p.top_k * p.page_size + kBlk - 1) / kBlk;
+    Guess x;
+    x.first = static_cast<int>(static_cast<int64_t>(blocks) * rank / p.splits) * kBlk / p.page_size;
+    const int i = x.first + static_cast<int>(threadIdx.x);
+    x.page = i < p.top_k ? __ldg(sel + i) : 0;
+    return x;
+}
+
 // Resolves list entries [i0, i1) to slots.
 template <int kThreads>
-__device__ __forceinline__ void stage_runs(const SelectedParams &p, const Share &s, const int32_t *sel, int i0, int i1, Run *runs) {
+__device__ __forceinline__ void stage_runs(const SelectedParams &p, const Share &s, const int32_t *sel, const Guess &guess, int i0, int i1, Run *runs) {
     for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += kThreads) {
-        const int page = __ldg(sel + i);
+        const int page = i == guess.first + static_cast<int>(threadIdx.x) ? guess.page : __ldg(sel + i);
         Run r{0, -1};
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(s.n_pages)) {
             record_error(p.err, page);
@@ -189,8 +210,9 @@ __global__ void __launch_bounds__(kSimtThreads) selected_simt_kernel(const Selec
     for (int i = tid; i < kHeads * D; i += kSimtThreads)
         q[i / D][i % D] = Elem<T>::to_f(static_cast<const T *>(p.q)[out0 + i]) * p.scale_log2;
     if (p.pdl) griddep_wait();
-    const Share s = cta_share(p, g, b, rank, rank == 0 && h0 % group == 0 && tid == 0);
     const int32_t *sel = p.sel + (static_cast<int64_t>(b) * p.n_kv_heads + g) * p.top_k;
+    const Guess guess = guess_entry(p, sel, rank);
+    const Share s = cta_share(p, g, b, rank, rank == 0 && h0 % group == 0 && tid == 0);
 
     float m[kHeads], l[kHeads], o[kHeads][kOwn * kElems];
 #pragma unroll
@@ -204,7 +226,7 @@ __global__ void __launch_bounds__(kSimtThreads) selected_simt_kernel(const Selec
     for (int i0 = s.t0 / p.page_size; i0 < i_end; i0 += kStagePages) {
         const int i1 = min(i_end, i0 + kStagePages);
         __syncthreads();
-        stage_runs<kSimtThreads>(p, s, sel, i0, i1, runs);
+        stage_runs<kSimtThreads>(p, s, sel, guess, i0, i1, runs);
         __syncthreads();
         const int from = max(s.t0, i0 * p.page_size);
         const int to = static_cast<int>(min(static_cast<int64_t>(s.t1), static_cast<int64_t>(i1) * p.page_size));
@@ -289,7 +311,7 @@ __global__ void __launch_bounds__(kSimtThreads) selected_simt_kernel(const Selec
 // Tensor cores (bf16)
 // ---------------------------------------------------------------------------
 
-constexpr int kMmaWarps = 8;
+constexpr int kMmaWarps = 4;
 constexpr int kMmaThreads = kMmaWarps * 32;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -305,25 +327,54 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// A warp takes a block of 16 positions at a time, with lane (r, t) = (lane / 4,
-// lane % 4).  Both products read their operands from memory straight into
-// fragments, so nothing is staged and there is no barrier in the loop:
+// The slot of position lane % 16 of the block at `at`, -1 where there is none.
+__device__ __forceinline__ int slot_at(int at, int to, int i0, const Run *runs, const SelectedParams &p, int len) {
+    const int x = at + static_cast<int>(threadIdx.x & 15);
+    if (x >= to) return -1;
+    const int i = x / p.page_size, off = x - i * p.page_size;
+    const Run run = runs[i - i0];
+    return run.pos >= 0 && static_cast<unsigned>(run.pos) + off < static_cast<unsigned>(len) ? run.slot + off : -1;
+}
+
+// Shared memory of a CTA: each warp's ring of kRing half blocks (16 rows of K or
+// of V), whose space the partials take over in the end, and the staged runs.
+template <int D, int G>
+struct MmaShared {
+    static constexpr int kRing = 3;
+    static constexpr int kRows = kBlk * D;                        // elements of a half block
+    union {
+        bf16 ring[kMmaWarps][kRing][kRows];
+        Partials<kMmaWarps, G, D> parts;
+    };
+    Run runs[kStagePages];
+};
+
+// Where chunk c of a half block's row stands: the four lanes of a row (K) and
+// the eight lanes of four rows and two chunks (V) that read together hit
+// different banks.
+__device__ __forceinline__ int swizzle(int row, int c) { return c ^ ((row & 1) << 2) ^ (row & 6); }
+
+// A warp takes a block of 16 positions at a time.  K and V rows come by cp.async
+// into the warp's own ring, two half blocks ahead of the one in use, so there is
+// no barrier in the loop, and 16 warps keep 128 KB in flight per SM.  With lane
+// (r, t) = (lane / 4, lane % 4):
 //   S[8 heads x 16]   = Q K^T: a dot product may take its terms in any order,
-//     so lane (r, t) loads the 16-byte chunks t, t + 4, ... of the K rows r and
+//     so lane (r, t) takes the 16-byte chunks t, t + 4, ... of the K rows r and
 //     r + 8 (and of head r's q) and feeds them as the columns 2t, 2t + 1, 2t +
 //     8, 2t + 9 of successive k steps;
 //   O^T[D x 8 heads] += V^T P^T: P of positions 2t, 2t + 1, 2t + 8, 2t + 9 and
-//     head r is where S left it, and lane (r, t) loads the chunks r and r + 8
+//     head r is where S left it, and lane (r, t) takes the chunks r and r + 8
 //     of those four V rows; a byte permutation pairs two rows' channels, and
 //     output row r of step i stands for channel 8 r + 2 i, row r + 8 for the
 //     next one.
 // P goes in as two bf16 parts (hi + lo, 16 bits together): one part alone would
 // add an error of the size of the output's own rounding.
 template <int D, int G>
-__global__ void __launch_bounds__(kMmaThreads, 2) selected_mma_kernel(const SelectedParams p) {
-    constexpr int kChunks = D / 8, kOwn = kChunks / 4, kHalves = D / 64;
-    __shared__ Partials<kMmaWarps, G, D> sh;
-    __shared__ Run runs[kStagePages];
+__global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const SelectedParams p) {
+    using Sh = MmaShared<D, G>;
+    constexpr int kChunks = D / 8, kOwn = kChunks / 4, kHalves = D / 64, kRing = Sh::kRing;
+    extern __shared__ __align__(128) unsigned char smem[];
+    Sh &sh = *reinterpret_cast<Sh *>(smem);
     griddep_launch();
     const int rank = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
@@ -333,8 +384,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2) selected_mma_kernel(const Sele
     for (int j = 0; j < kOwn; ++j)
         q[j] = r < G ? __ldg(static_cast<const uint4 *>(p.q) + out0 / 8 + r * kChunks + t + 4 * j) : make_uint4(0, 0, 0, 0);
     if (p.pdl) griddep_wait();
-    const Share s = cta_share(p, g, b, rank, rank == 0 && threadIdx.x == 0);
     const int32_t *sel = p.sel + (static_cast<int64_t>(b) * p.n_kv_heads + g) * p.top_k;
+    const Guess guess = guess_entry(p, sel, rank);
+    const Share s = cta_share(p, g, b, rank, rank == 0 && threadIdx.x == 0);
 
     float m = -INFINITY, l = 0.f;            // head r; l over this lane's positions
     float o[kHalves * 4][4];                 // channels 64 * (i / 4) + 8 r + 2 (i % 4) (+ 1), heads 2t, 2t + 1
@@ -343,52 +395,62 @@ __global__ void __launch_bounds__(kMmaThreads, 2) selected_mma_kernel(const Sele
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
+    // a half block to ring place `to`: kRowLanes lanes to a row; an unseen position is filled with zeros
+    constexpr int kRowLanes = kChunks, kRowsPer = 32 / kRowLanes;
+    const auto fetch = [&](const void *pool, int slot, int to) {
+        bf16 *dst = sh.ring[warp][to];
+        const int c = lane % kRowLanes;
+#pragma unroll
+        for (int i = 0; i < kBlk / kRowsPer; ++i) {
+            const int row = i * kRowsPer + lane / kRowLanes;
+            const int from = __shfl_sync(0xffffffffu, slot, row);
+            const uint4 *src = static_cast<const uint4 *>(pool) +
+                               ((p.layer_row0 + (from >= 0 ? from : 0)) * p.n_kv_heads + g) * kChunks + c;
+            cp_async16(dst + row * D + swizzle(row, c) * 8, src, from >= 0 ? 16 : 0);
+        }
+        cp_async_commit();
+    };
+    const auto chunk = [&](int at, int row, int c) {
+        return *reinterpret_cast<const uint4 *>(&sh.ring[warp][at][row * D + swizzle(row, c) * 8]);
+    };
+
     const int i_end = s.t1 > s.t0 ? (s.t1 - 1) / p.page_size + 1 : 0;
     for (int i0 = s.t0 / p.page_size; i0 < i_end; i0 += kStagePages) {
         const int i1 = min(i_end, i0 + kStagePages);
         __syncthreads();
-        stage_runs<kMmaThreads>(p, s, sel, i0, i1, runs);
+        stage_runs<kMmaThreads>(p, s, sel, guess, i0, i1, sh.runs);
         __syncthreads();
         const int from = max(s.t0, i0 * p.page_size);
         const int to = static_cast<int>(min(static_cast<int64_t>(s.t1), static_cast<int64_t>(i1) * p.page_size));
-        for (int at = from + warp * kBlk; at < to; at += kMmaWarps * kBlk) {
-            int slot = -1;                   // of position lane % 16 of the block
-            if (at + (lane & 15) < to) {
-                const int x = at + (lane & 15), i = x / p.page_size, off = x - i * p.page_size;
-                const Run run = runs[i - i0];
-                if (run.pos >= 0 && static_cast<unsigned>(run.pos) + off < static_cast<unsigned>(s.len)) slot = run.slot + off;
-            }
-            const int ks[2] = {__shfl_sync(0xffffffffu, slot, r), __shfl_sync(0xffffffffu, slot, r + 8)};
-            uint4 k[2][kOwn], v[4][kHalves];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 *row = static_cast<const uint4 *>(p.k_buffer) + ((p.layer_row0 + ks[i]) * p.n_kv_heads + g) * kChunks + t;
-#pragma unroll
-                for (int j = 0; j < kOwn; ++j) k[i][j] = ks[i] >= 0 ? __ldg(row + 4 * j) : make_uint4(0, 0, 0, 0);
-            }
-            bool seen[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int vs = __shfl_sync(0xffffffffu, slot, 2 * t + (i & 1) + 8 * (i >> 1));
-                seen[i] = vs >= 0;
-                const uint4 *row = static_cast<const uint4 *>(p.v_buffer) + ((p.layer_row0 + vs) * p.n_kv_heads + g) * kChunks + r;
-#pragma unroll
-                for (int j = 0; j < kHalves; ++j) v[i][j] = vs >= 0 ? __ldg(row + 8 * j) : make_uint4(0, 0, 0, 0);
-            }
+        int at = from + warp * kBlk, x = 0;                       // x: ring place of the half block in use
+        if (at >= to) continue;
+        int slot = slot_at(at, to, i0, sh.runs, p, s.len);
+        fetch(p.k_buffer, slot, 0);
+        fetch(p.v_buffer, slot, 1);
+        const auto after = [&](int place, int by) { return place + by < kRing ? place + by : place + by - kRing; };
+        while (at < to) {
+            const int next = at + kMmaWarps * kBlk;
+            const int next_slot = slot_at(next, to, i0, sh.runs, p, s.len);
+            if (next < to) fetch(p.k_buffer, next_slot, after(x, 2));
+            else cp_async_commit();
+            cp_async_wait<2>();
+            __syncwarp();
             float w[2][4] = {};
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    mma16816(w[i], q[j].x, 0, q[j].y, 0, k[i][j].x, k[i][j].y);
-                    mma16816(w[i], q[j].z, 0, q[j].w, 0, k[i][j].z, k[i][j].w);
+                    const uint4 k = chunk(x, r + 8 * i, t + 4 * j);
+                    mma16816(w[i], q[j].x, 0, q[j].y, 0, k.x, k.y);
+                    mma16816(w[i], q[j].z, 0, q[j].w, 0, k.z, k.w);
                 }
             // head r, positions 2t, 2t + 1, 2t + 8, 2t + 9
             float pr[4];
             float top = m;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                pr[i] = seen[i] ? w[i >> 1][i & 1] * p.scale_log2 : -INFINITY;
+                const bool seen = __shfl_sync(0xffffffffu, slot, 2 * t + (i & 1) + 8 * (i >> 1)) >= 0;
+                pr[i] = seen ? w[i >> 1][i & 1] * p.scale_log2 : -INFINITY;
                 top = fmaxf(top, pr[i]);
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -414,37 +476,53 @@ __global__ void __launch_bounds__(kMmaThreads, 2) selected_mma_kernel(const Sele
             const uint32_t hi0 = pack_bf16(pr[0], pr[1]), hi1 = pack_bf16(pr[2], pr[3]);
             const uint32_t lo0 = pack_bf16(pr[0] - bf16lo(hi0), pr[1] - bf16hi(hi0));
             const uint32_t lo1 = pack_bf16(pr[2] - bf16lo(hi1), pr[3] - bf16hi(hi1));
+            __syncwarp();                                         // every lane has read the K rows
+            if (next < to) fetch(p.v_buffer, next_slot, x);
+            else cp_async_commit();
+            x = after(x, 1);
+            cp_async_wait<2>();
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < kHalves; ++j)
+            for (int j = 0; j < kHalves; ++j) {
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = chunk(x, 2 * t + (i & 1) + 8 * (i >> 1), r + 8 * j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t a0 = __byte_perm(word(v[0][j], i), word(v[1][j], i), 0x5410);
-                    const uint32_t a1 = __byte_perm(word(v[0][j], i), word(v[1][j], i), 0x7632);
-                    const uint32_t a2 = __byte_perm(word(v[2][j], i), word(v[3][j], i), 0x5410);
-                    const uint32_t a3 = __byte_perm(word(v[2][j], i), word(v[3][j], i), 0x7632);
+                    const uint32_t a0 = __byte_perm(word(v[0], i), word(v[1], i), 0x5410);
+                    const uint32_t a1 = __byte_perm(word(v[0], i), word(v[1], i), 0x7632);
+                    const uint32_t a2 = __byte_perm(word(v[2], i), word(v[3], i), 0x5410);
+                    const uint32_t a3 = __byte_perm(word(v[2], i), word(v[3], i), 0x7632);
                     mma16816(o[j * 4 + i], a0, a1, a2, a3, hi0, hi1);
                     mma16816(o[j * 4 + i], a0, a1, a2, a3, lo0, lo1);
                 }
+            }
+            __syncwarp();                                         // every lane has read the V rows
+            x = after(x, 1);
+            at = next;
+            slot = next_slot;
         }
     }
+    cp_async_wait<0>();
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    __syncthreads();                                              // the rings become the partials
     if (t == 0 && r < G) {
-        sh.m[warp][r] = m;
-        sh.l[warp][r] = l;
+        sh.parts.m[warp][r] = m;
+        sh.parts.l[warp][r] = l;
     }
 #pragma unroll
     for (int i = 0; i < kHalves * 4; ++i) {
         const int c = 64 * (i / 4) + 8 * r + 2 * (i % 4);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            if (2 * t + e < G) *reinterpret_cast<float2 *>(&sh.o[warp][2 * t + e][c]) = make_float2(o[i][e], o[i][2 + e]);
+            if (2 * t + e < G) *reinterpret_cast<float2 *>(&sh.parts.o[warp][2 * t + e][c]) = make_float2(o[i][e], o[i][2 + e]);
     }
-    join<bf16, kMmaWarps, G, D, kMmaThreads>(sh, static_cast<bf16 *>(p.o) + out0, rank, p.splits);
+    join<bf16, kMmaWarps, G, D, kMmaThreads>(sh.parts, static_cast<bf16 *>(p.o) + out0, rank, p.splits);
 }
 
 template <typename K>
-cudaError_t launch_cluster(K kernel, dim3 grid, int threads, const SelectedParams &p, cudaStream_t s) {
+cudaError_t launch_cluster(K kernel, dim3 grid, int threads, size_t smem, const SelectedParams &p, cudaStream_t s) {
     cudaLaunchAttribute attr[2];
     int n = 0;
     if (p.splits > 1) {
@@ -462,6 +540,7 @@ cudaError_t launch_cluster(K kernel, dim3 grid, int threads, const SelectedParam
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = n;
@@ -470,7 +549,18 @@ cudaError_t launch_cluster(K kernel, dim3 grid, int threads, const SelectedParam
 
 template <int D, int G>
 cudaError_t run_mma(const SelectedParams &p, cudaStream_t s) {
-    return launch_cluster(selected_mma_kernel<D, G>, dim3(p.splits, p.n_kv_heads, p.batch), kMmaThreads, p, s);
+    constexpr size_t smem = sizeof(MmaShared<D, G>);
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_done.load() & bit)) {
+        e = cudaFuncSetAttribute(selected_mma_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        attr_done.fetch_or(bit);
+    }
+    return launch_cluster(selected_mma_kernel<D, G>, dim3(p.splits, p.n_kv_heads, p.batch), kMmaThreads, smem, p, s);
 }
 
 template <int D>
@@ -485,7 +575,7 @@ cudaError_t run_mma_g(const SelectedParams &p, int group, cudaStream_t s) {
 
 template <typename T, int D, int kHeads>
 cudaError_t run_simt(const SelectedParams &p, cudaStream_t s) {
-    return launch_cluster(selected_simt_kernel<T, D, kHeads>, dim3(p.splits, p.n_heads / kHeads, p.batch), kSimtThreads, p, s);
+    return launch_cluster(selected_simt_kernel<T, D, kHeads>, dim3(p.splits, p.n_heads / kHeads, p.batch), kSimtThreads, 0, p, s);
 }
 
 template <typename T, int D>
@@ -499,14 +589,16 @@ cudaError_t run_simt_g(const SelectedParams &p, int group, cudaStream_t s) {
 
 }  // namespace
 
-// Enough CTAs for two per SM, while a CTA keeps two blocks per warp.
+// As many CTAs as are resident at once (four of four warps per SM), while each
+// warp keeps a block.
 int selected_splits(int64_t batch, int n_kv_heads, int64_t top_k, int64_t page_size, int64_t max_len, int sms) {
     const int64_t units = batch * n_kv_heads;
     const int64_t pages = (max_len + page_size - 1) / page_size;
-    const int64_t blocks = (top_k < pages ? top_k : pages) * page_size / kBlk + 1;
-    int splits = 1;
-    while (splits < kMaxSplits && units * splits < 2LL * sms && blocks >= static_cast<int64_t>(kMmaWarps) * splits * 2) splits *= 2;
-    return splits;
+    const int64_t blocks = ((top_k < pages ? top_k : pages) * page_size + kBlk - 1) / kBlk;
+    int64_t splits = 4LL * sms / units;
+    if (splits > blocks / kMmaWarps) splits = blocks / kMmaWarps;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    return splits < 1 ? 1 : static_cast<int>(splits);
 }
 
 cudaError_t launch_decode_selected(const SelectedParams &p, int dtype, int head_dim, int group, cudaStream_t s) {
