@@ -895,10 +895,12 @@ int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pag
     if (!no_write) {
         rc = map_launch(pkv::launch_kv_write(wp, s, true));
         if (rc) return rc;
+        bp.pdl = 1;
         rc = map_launch(pkv::launch_page_bounds(bp, s));
         if (rc) return rc;
     }
     if (no_decode) return PKV_OK;
+    sp.pdl = !no_write;
     rc = map_launch(pkv::launch_select_pages(sp, c->dtype, c->head_dim, group, s));
     if (rc) return rc;
     ap.pdl = 1;

@@ -191,6 +191,7 @@ struct BoundsParams {
     int32_t head_chunks;          // of them per kv head
     int32_t dtype;
     int32_t block_tokens;         // consecutive new tokens per CTA
+    int32_t pdl;                  // launched as a programmatic dependent of the write of `keys`
     DevErr *err;
 };
 

@@ -72,6 +72,7 @@ constexpr int kRowsAhead = 8;
 // new keys are read once, kRowsAhead rows in flight per thread.
 template <typename T>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const BoundsParams p) {
+    griddep_launch();
     const int chunk = blockIdx.y * kBoundsThreads + threadIdx.x;
     const int i_end = min(p.n_new, (static_cast<int>(blockIdx.x) + 1) * p.block_tokens);
     const auto valid = [&](int slot) { return static_cast<unsigned>(slot) < static_cast<unsigned long long>(p.size); };
@@ -140,6 +141,9 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
             dst[p.head_chunks] = hi;
         }
     }
+    // after the cache write, which it does not need itself: what waits for the
+    // bounds has waited for the write too
+    if (p.pdl) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -831,9 +835,16 @@ bool sparse_supported(int dtype, int head_dim, int group) {
 cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t s) {
     if (p.n_new == 0) return cudaSuccess;
     const dim3 grid((p.n_new + p.block_tokens - 1) / p.block_tokens, (p.row_chunks + kBoundsThreads - 1) / kBoundsThreads);
-    if (p.dtype == PKV_BF16) page_bounds_kernel<bf16><<<grid, kBoundsThreads, 0, s>>>(p);
-    else page_bounds_kernel<float><<<grid, kBoundsThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kBoundsThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.pdl ? 1 : 0;
+    return p.dtype == PKV_BF16 ? cudaLaunchKernelEx(&cfg, page_bounds_kernel<bf16>, p) : cudaLaunchKernelEx(&cfg, page_bounds_kernel<float>, p);
 }
 
 cudaError_t launch_select_pages(const SelectParams &p, int dtype, int head_dim, int group, cudaStream_t s) {

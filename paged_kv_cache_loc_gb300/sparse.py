@@ -25,15 +25,9 @@ from .ops import KVCache, Workspace, _DTYPES, _need
 def _ptr(t: torch.Tensor, name: str, dtype, index: int) -> int:
     """The address of a contiguous tensor of `dtype` on CUDA device `index`,
     or in pinned host memory (as in ops._need)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        return _need(t, name, dtype)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    return _need(t, name, dtype, torch.device("cuda", index))
 
 
 def _i32(t: Optional[torch.Tensor], name: str, index: int, n: int) -> Optional[int]:
@@ -75,6 +69,8 @@ class SparsePages:
         index = kb.get_device()
         if t.dim() != 2:
             raise ValueError("req_to_page must be [num_reqs, max_pages]")
+        if self.page_size < 1:
+            raise ValueError("page_size must be positive")
         bounds = self.page_bounds
         if bounds is not None:
             n_layers, size, n_kv_heads, head_dim = kb.shape
@@ -105,8 +101,17 @@ def _cache(cache: KVCache, table: torch.Tensor, table_name: str, max_ctx_len: in
         _ptr(kb, "k_buffer", kb.dtype, index), _ptr(vb, "v_buffer", kb.dtype, index), dtype, n_layers,
         n_kv_heads, head_dim, size, _ptr(table, table_name, torch.int32, index), table.shape[0], max_ctx_len,
         _ptr(rows, "req_pool_indices", torch.int32, index), _i32(lens, "seq_lens", index, batch), None, None,
-        _i32(cache.out_cache_loc, "out_cache_loc", index, n_new) if n_new else None, batch,
-        int(cache.max_len)), index
+        _slots(cache.out_cache_loc, index, n_new), batch, int(cache.max_len)), index
+
+
+def _slots(loc: Optional[torch.Tensor], index: int, n_new: int) -> Optional[int]:
+    """The address of out_cache_loc, which may be longer than what is written."""
+    if not n_new:
+        return None
+    p = _ptr(loc, "out_cache_loc", torch.int32, index)
+    if loc.numel() < n_new:
+        raise ValueError(f"out_cache_loc must have {n_new} elements at least, got {loc.numel()}")
+    return p
 
 
 def _rows(t: torch.Tensor, name: str, c: PkvKVCache, dtype, index: int, n: int, heads: int) -> int:
@@ -114,6 +119,12 @@ def _rows(t: torch.Tensor, name: str, c: PkvKVCache, dtype, index: int, n: int, 
     if t.dim() != 3 or t.shape[0] != n or t.shape[1] != heads or t.shape[2] != c.head_dim:
         raise ValueError(f"{name} must be [{n}, {heads}, {c.head_dim}], got {list(t.shape)}")
     return _ptr(t, name, dtype, index)
+
+
+def _heads(q: torch.Tensor) -> int:
+    if q.dim() != 3:
+        raise ValueError(f"q must be [batch, n_heads, head_dim], got {list(q.shape)}")
+    return q.shape[1]
 
 
 def _lists(sel: torch.Tensor, counts: torch.Tensor, c: PkvKVCache, top_k: int, index: int) -> Tuple[int, int]:
@@ -129,30 +140,26 @@ def _workspace(ws: Optional[Workspace], index: int):
     return ctypes.byref(ws.desc)
 
 
-class _On:
-    """The device of the cache and the stream of a call; `stream` None is the
+def _call(fn, index: int, stream, *args) -> None:
+    """Calls fn on the cache's device with the stream's handle; None is the
     device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream.cuda_stream)
+    if status:
+        check(status, fn.__name__)
 
-    def __init__(self, index: int, stream):
-        self.index = index
-        self.other = torch.cuda.current_device() != index
-        self.given = stream
-        self.handle = (stream if stream is not None else torch.cuda.current_stream(index)).cuda_stream
 
-    def call(self, fn, *args) -> None:
-        if self.other:
-            with torch.cuda.device(self.index):
-                status = fn(*args, self.handle)
-        else:
-            status = fn(*args, self.handle)
-        if status:
-            check(status, fn.__name__)
-
-    def empty(self, *shape, dtype) -> torch.Tensor:
-        if self.given is not None:      # the allocator ties memory to the stream that is current
-            with torch.cuda.stream(self.given):
-                return torch.empty(shape, dtype=dtype, device=f"cuda:{self.index}")
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{self.index}")
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output, allocated for the stream that the kernels run on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def build_tables(cache: KVCache, req_to_page: torch.Tensor, page_size: int, free_pages: torch.Tensor,
@@ -182,18 +189,20 @@ def build_tables(cache: KVCache, req_to_page: torch.Tensor, page_size: int, free
         _i32(cache.qo_indptr, "qo_indptr", index, c.batch + 1),
         _i32(positions, "positions", index, n_new), c.out_cache_loc,
         _ptr(cache.req_to_token, "req_to_token", torch.int32, index) if token_table else None)
-    _On(index, stream).call(_lib.load().pkv_build_tables, ctypes.byref(c), ctypes.byref(t))
+    _call(_lib.load().pkv_build_tables, index, stream, ctypes.byref(c), ctypes.byref(t))
 
 
-def page_bounds(cache: KVCache, layer_id: int, pages: SparsePages, stream=None) -> None:
+def page_bounds(cache: KVCache, layer_id: int, pages: SparsePages, n_new: Optional[int] = None,
+                stream=None) -> None:
     """Bring pages.page_bounds up to date with the keys written to the slots
-    cache.out_cache_loc of the layer."""
+    cache.out_cache_loc[:n_new] (None: all of them) of the layer."""
     if cache.out_cache_loc is None or pages.page_bounds is None:
         raise ValueError("out_cache_loc and page_bounds are needed")
-    n_new = cache.out_cache_loc.numel()
+    if n_new is None:
+        n_new = cache.out_cache_loc.numel()
     pg = pages.c_struct(cache)
     c, index = _cache(cache, pages.req_to_page, "req_to_page", 0, n_new, False)
-    _On(index, stream).call(_lib.load().pkv_page_bounds, ctypes.byref(c), layer_id, ctypes.byref(pg), n_new)
+    _call(_lib.load().pkv_page_bounds, index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg), n_new)
 
 
 def select_workspace_bytes(batch: int, n_kv_heads: int, max_len: int, page_size: int) -> int:
@@ -209,13 +218,12 @@ def select_pages(cache: KVCache, layer_id: int, pages: SparsePages, q: torch.Ten
     and sel_counts int32 [batch, n_kv_heads]."""
     pg = pages.c_struct(cache)
     c, index = _cache(cache, pages.req_to_page, "req_to_page", 0, 0, True)
-    on = _On(index, stream)
     if sel is None:
-        sel = on.empty(c.batch, c.n_kv_heads, pages.top_k, dtype=torch.int32)
+        sel = _empty((c.batch, c.n_kv_heads, pages.top_k), torch.int32, cache.k_buffer.device, stream)
     if sel_counts is None:
-        sel_counts = on.empty(c.batch, c.n_kv_heads, dtype=torch.int32)
-    on.call(_lib.load().pkv_select_pages, ctypes.byref(c), layer_id, ctypes.byref(pg),
-            _rows(q, "q", c, cache.k_buffer.dtype, index, c.batch, q.shape[1]), q.shape[1],
+        sel_counts = _empty((c.batch, c.n_kv_heads), torch.int32, cache.k_buffer.device, stream)
+    _call(_lib.load().pkv_select_pages, index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
+            _rows(q, "q", c, cache.k_buffer.dtype, index, c.batch, _heads(q)), q.shape[1],
             *_lists(sel, sel_counts, c, pages.top_k, index), _workspace(workspace, index))
     return sel, sel_counts
 
@@ -228,12 +236,11 @@ def paged_decode_selected(cache: KVCache, layer_id: int, pages: SparsePages, q: 
     [batch, n_heads, head_dim], sel and sel_counts as select_pages gives them."""
     pg = pages.c_struct(cache)
     c, index = _cache(cache, pages.req_to_page, "req_to_page", 0, 0, True)
-    on = _On(index, stream)
-    dtype, heads = cache.k_buffer.dtype, q.shape[1]
+    dtype, heads = cache.k_buffer.dtype, _heads(q)
     if o is None:
-        o = on.empty(*q.shape, dtype=q.dtype)
+        o = _empty(q.shape, q.dtype, cache.k_buffer.device, stream)
     scale = 1.0 / math.sqrt(c.head_dim) if sm_scale is None else float(sm_scale)
-    on.call(_lib.load().pkv_paged_decode_selected, ctypes.byref(c), layer_id, ctypes.byref(pg),
+    _call(_lib.load().pkv_paged_decode_selected, index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
             *_lists(sel, sel_counts, c, pages.top_k, index),
             _rows(q, "q", c, dtype, index, c.batch, heads), _rows(o, "o", c, dtype, index, c.batch, heads),
             heads, scale)
@@ -247,18 +254,17 @@ def sparse_decode_step(cache: KVCache, layer_id: int, pages: SparsePages, k_new:
                        stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """kv_write of k_new / v_new at cache.out_cache_loc, page_bounds,
     select_pages and paged_decode_selected as one call: (o, sel, sel_counts)."""
-    n_new, heads, dtype = k_new.shape[0], q.shape[1], cache.k_buffer.dtype
+    n_new, heads, dtype = k_new.shape[0], _heads(q), cache.k_buffer.dtype
     pg = pages.c_struct(cache)
     c, index = _cache(cache, pages.req_to_page, "req_to_page", 0, n_new, True)
-    on = _On(index, stream)
     if o is None:
-        o = on.empty(*q.shape, dtype=q.dtype)
+        o = _empty(q.shape, q.dtype, cache.k_buffer.device, stream)
     if sel is None:
-        sel = on.empty(c.batch, c.n_kv_heads, pages.top_k, dtype=torch.int32)
+        sel = _empty((c.batch, c.n_kv_heads, pages.top_k), torch.int32, cache.k_buffer.device, stream)
     if sel_counts is None:
-        sel_counts = on.empty(c.batch, c.n_kv_heads, dtype=torch.int32)
+        sel_counts = _empty((c.batch, c.n_kv_heads), torch.int32, cache.k_buffer.device, stream)
     scale = 1.0 / math.sqrt(c.head_dim) if sm_scale is None else float(sm_scale)
-    on.call(_lib.load().pkv_sparse_decode_step, ctypes.byref(c), layer_id, ctypes.byref(pg),
+    _call(_lib.load().pkv_sparse_decode_step, index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
             _rows(k_new, "k_new", c, dtype, index, n_new, c.n_kv_heads),
             _rows(v_new, "v_new", c, dtype, index, n_new, c.n_kv_heads), n_new,
             _rows(q, "q", c, dtype, index, c.batch, heads), _rows(o, "o", c, dtype, index, c.batch, heads),

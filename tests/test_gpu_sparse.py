@@ -719,6 +719,21 @@ def test_step_of_a_prompt_chunk():
     check_step(case, lens, "bf16", lambda: pkv.sparse_decode_step(cache, 1, pg, kn, vn, q, workspace=ws_for(n, 2, cache.max_len, ps)))
 
 
+def test_step_writes_the_rows_that_it_gets_of_a_longer_slot_list():
+    """out_cache_loc may be a buffer of a fixed capacity: what stands behind
+    the new rows is not read."""
+    rng = np.random.default_rng(47)
+    lens = np.array([90, 200])
+    case = step_case(rng, "bf16", 8, 2, 64, 8, lens, 6)
+    cache, pg, q, kn, vn, table, rows, loc = case
+    cache.out_cache_loc = dev(np.r_[loc, 10 ** 6, -5])
+    pg2 = dataclasses.replace(pg, page_bounds=pg.page_bounds.clone())
+    check_step(case, lens, "bf16", lambda: pkv.sparse_decode_step(cache, 1, pg, kn, vn, q, workspace=ws_for(2, 2, 200, 8)))
+    pkv.page_bounds(cache, 1, pg2, n_new=2)
+    clean()
+    assert torch.equal(pg.page_bounds, pg2.page_bounds)
+
+
 def test_step_with_nothing_to_write_and_without_entries():
     rng = np.random.default_rng(42)
     lens = np.array([90, 200])
@@ -801,7 +816,10 @@ def test_binding_refuses_shapes_types_and_devices():
            lambda: pkv.select_pages(cache, 1, r(pg, page_bounds=pg.page_bounds.float()), q),
            lambda: pkv.select_pages(r(cache, seq_lens=cache.seq_lens[:1]), 1, pg, q),
            lambda: pkv.select_pages(r(cache, seq_lens=None), 1, pg, q),
-           lambda: pkv.sparse_decode_step(cache, 1, pg, kn[:1].contiguous(), vn[:1].contiguous(), q),
+           lambda: pkv.sparse_decode_step(r(cache, out_cache_loc=dev(loc[:1])), 1, pg, kn, vn, q),
+           lambda: pkv.page_bounds(cache, 1, pg, n_new=3),
+           lambda: pkv.select_pages(cache, 1, r(pg, page_size=0), q),
+           lambda: pkv.select_pages(cache, 1, pg, q[0]),
            lambda: pkv.sparse_decode_step(cache, 1, pg, kn, vn[:1].contiguous(), q),
            lambda: pkv.page_bounds(r(cache, out_cache_loc=None), 1, pg),
            lambda: pkv.page_bounds(cache, 1, r(pg, page_bounds=None))]
