@@ -689,12 +689,14 @@ int check_sparse(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, co
 }
 
 int bounds_prepare(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, int32_t n_new, const DeviceInfo &di,
-                   const void *keys, pkv::BoundsParams *out) {
+                   const void *keys, const void *values, pkv::BoundsParams *out) {
     pkv::BoundsParams &p = *out;
     p = pkv::BoundsParams{};
     const int elem = elem_bytes(c->dtype);
     p.keys = keys;
+    p.values = values;
     p.k_buffer = c->k_buffer;
+    p.v_buffer = c->v_buffer;
     p.page_bounds = pg->page_bounds;
     p.out_cache_loc = c->out_cache_loc;
     p.size = c->size;
@@ -811,7 +813,7 @@ int pkv_page_bounds(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg,
     rc = check_visible({c->k_buffer, c->out_cache_loc, pg->page_bounds});
     if (rc) return rc;
     pkv::BoundsParams p;
-    bounds_prepare(c, layer_id, pg, n_new, di, nullptr, &p);
+    bounds_prepare(c, layer_id, pg, n_new, di, nullptr, nullptr, &p);
     return map_launch(pkv::launch_page_bounds(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -882,7 +884,7 @@ int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pag
                         q, o, sel, sel_counts, ws ? ws->base : nullptr});
     if (rc) return rc;
     pkv::BoundsParams bp;
-    bounds_prepare(c, layer_id, pg, n_new, di, k_new, &bp);
+    bounds_prepare(c, layer_id, pg, n_new, di, k_new, v_new, &bp);
     pkv::SelectParams sp;
     pkv::SelectedParams ap;
     if (!no_decode) {
@@ -893,10 +895,7 @@ int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pag
     const int group = n_heads / c->n_kv_heads;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!no_write) {
-        rc = map_launch(pkv::launch_kv_write(wp, s, true));
-        if (rc) return rc;
-        bp.pdl = 1;
-        rc = map_launch(pkv::launch_page_bounds(bp, s));
+        rc = map_launch(pkv::launch_page_bounds(bp, s));   // the write too
         if (rc) return rc;
     }
     if (no_decode) return PKV_OK;

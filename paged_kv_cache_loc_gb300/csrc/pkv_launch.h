@@ -178,8 +178,10 @@ struct TablesParams {
 
 // Key bounds of pages (pkv_select.cu).
 struct BoundsParams {
-    const void *keys;             // rows of the new keys in out_cache_loc order, or null: read from the pool
-    const void *k_buffer;         // pool base
+    const void *keys;             // with the cache write: the new rows in out_cache_loc order (else null: the
+    const void *values;           // new keys are read from the pool)
+    void *k_buffer;               // pool base
+    void *v_buffer;
     void *page_bounds;            // [n_layers, n_pages, n_kv_heads, 2, head_dim]
     const int32_t *out_cache_loc;
     int64_t size;
@@ -191,7 +193,6 @@ struct BoundsParams {
     int32_t head_chunks;          // of them per kv head
     int32_t dtype;
     int32_t block_tokens;         // consecutive new tokens per CTA
-    int32_t pdl;                  // launched as a programmatic dependent of the write of `keys`
     DevErr *err;
 };
 

@@ -70,12 +70,40 @@ constexpr int kRowsAhead = 8;
 // runs that start among its block_tokens tokens (and follows a run beyond
 // them); thread c reduces 16-byte chunk c of the run's rows.  The bytes of the
 // new keys are read once, kRowsAhead rows in flight per thread.
-template <typename T>
+//
+// kWrite: the cache write too (a sparse decode step).  A CTA then first copies
+// its own tokens' K and V rows to the pool; the bounds come from the new rows,
+// not from the pool, so nothing waits for another CTA's copy, and a step has
+// one launch less (2.6 + 3.3 us of kernels apart for one token).
+template <typename T, bool kWrite>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const BoundsParams p) {
     griddep_launch();
     const int chunk = blockIdx.y * kBoundsThreads + threadIdx.x;
     const int i_end = min(p.n_new, (static_cast<int>(blockIdx.x) + 1) * p.block_tokens);
     const auto valid = [&](int slot) { return static_cast<unsigned>(slot) < static_cast<unsigned long long>(p.size); };
+    if constexpr (kWrite) {
+        constexpr int kAhead = 4;
+        if (chunk < p.row_chunks) {
+            for (int i = blockIdx.x * p.block_tokens; i < i_end; i += kAhead) {
+                int slot[kAhead];
+                uint4 k[kAhead], v[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int64_t at = static_cast<int64_t>(min(i + u, i_end - 1)) * p.row_chunks + chunk;
+                    slot[u] = __ldg(p.out_cache_loc + min(i + u, i_end - 1));
+                    k[u] = __ldg(static_cast<const uint4 *>(p.keys) + at);
+                    v[u] = __ldg(static_cast<const uint4 *>(p.values) + at);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (i + u >= i_end || !valid(slot[u])) continue;   // the loop below reports a bad slot
+                    const int64_t to = (p.layer_row0 + slot[u]) * p.row_chunks + chunk;
+                    static_cast<uint4 *>(p.k_buffer)[to] = k[u];
+                    static_cast<uint4 *>(p.v_buffer)[to] = v[u];
+                }
+            }
+        }
+    }
     for (int i = blockIdx.x * p.block_tokens; i < i_end;) {
         int loc = __ldg(p.out_cache_loc + i);
         if (!valid(loc)) {
@@ -113,7 +141,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
                 if (breaks) break;
             }
             if (mine) {
-                const uint4 *row = (p.keys ? static_cast<const uint4 *>(p.keys) + static_cast<int64_t>(i) * p.row_chunks
+                const uint4 *row = (kWrite ? static_cast<const uint4 *>(p.keys) + static_cast<int64_t>(i) * p.row_chunks
                                            : static_cast<const uint4 *>(p.k_buffer) + (p.layer_row0 + loc) * p.row_chunks) + chunk;
                 if (!have) lo = hi = row[0];
                 have = true;
@@ -141,9 +169,6 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
             dst[p.head_chunks] = hi;
         }
     }
-    // after the cache write, which it does not need itself: what waits for the
-    // bounds has waited for the write too
-    if (p.pdl) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -340,7 +365,6 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_pages_mma_kernel(const
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelOwn = 8;               // pages per thread whose scores stay in registers
 constexpr int kBins = 2048;
 constexpr int kUndecided = 512;          // scored in 64 bits from a list; more: by radix passes
 
@@ -363,34 +387,34 @@ template <int D, int G>
 struct SelShared {
     float q[G][D];
     int hist[kBins];
-    int warp_sum[kSelWarps];
-    float red[kSelWarps];
-    uint32_t lo[kSelWarps], hi[kSelWarps];
+    unsigned long long warp_sum[kSelWarps];
+    uint32_t lo[kSelWarps], hi[kSelWarps], big[kSelWarps];
     int bin, above;
-    int und_page[kUndecided];
+    int und_page[kUndecided], und_phys[kUndecided];
     long long und_key[kUndecided];
     uint32_t und_in[kUndecided / 32];
 };
 
-// Inclusive scan over the warps of a per-thread int.
-__device__ __forceinline__ int block_scan(int *warp_sum, int v, int *total) {
+// Inclusive scan over the block of a whole number per thread.
+template <typename N>
+__device__ __forceinline__ N block_scan(unsigned long long *warp_sum, N v, N *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, off);
+        const N y = __shfl_up_sync(0xffffffffu, v, off);
         if (lane >= off) v += y;
     }
     __syncthreads();
     if (lane == 31) warp_sum[warp] = v;
     __syncthreads();
-    int w = lane < kSelWarps ? warp_sum[lane] : 0;
+    N w = lane < kSelWarps ? static_cast<N>(warp_sum[lane]) : N(0);
 #pragma unroll
     for (int off = 1; off < kSelWarps; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, off);
+        const N y = __shfl_up_sync(0xffffffffu, w, off);
         if (lane >= off) w += y;
     }
     *total = __shfl_sync(0xffffffffu, w, kSelWarps - 1);
-    const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    const N before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
     return warp > 0 ? v + before : v;
 }
 
@@ -484,44 +508,49 @@ __device__ __forceinline__ bool fixed_point_scale(float norm, float big, float *
     return e >= -40 && e <= 120;
 }
 
-// A page's fixed-point score for the heads h < G, the largest, by a warp.
-template <typename T, int D, int G>
-__device__ __forceinline__ long long fixed_score(const SelectParams &p, const SelShared<D, G> &sh, int64_t bounds_row, float scale) {
-    const int lane = threadIdx.x & 31;
-    const T *lo = static_cast<const T *>(p.page_bounds) + bounds_row * 2 * D;
-    float l[D / 32], u[D / 32];
+// A page's fixed-point score for one query head, by eight lanes of a warp (sub =
+// lane % 8), each the 16-byte chunks sub, sub + 8, ...
+template <typename T, int D>
+__device__ __forceinline__ long long fixed_score(const SelectParams &p, const float *q, int64_t bounds_row, float scale, int sub) {
+    constexpr int kElems = 16 / Elem<T>::bytes, kChunks = D / kElems;
+    const uint4 *lo = static_cast<const uint4 *>(p.page_bounds) + bounds_row * 2 * kChunks + sub;
+    uint4 l[kChunks / 8], u[kChunks / 8];
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-        l[c] = Elem<T>::to_f(lo[c * 32 + lane]);
-        u[c] = Elem<T>::to_f(lo[D + c * 32 + lane]);
+    for (int c = 0; c < kChunks / 8; ++c) {
+        l[c] = __ldg(lo + 8 * c);
+        u[c] = __ldg(lo + kChunks + 8 * c);
     }
-    long long best = 0;
+    long long s = 0;
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-        long long s = 0;
+    for (int c = 0; c < kChunks / 8; ++c) {
+        float a[kElems], b[kElems];
+        widen16(l[c], a, T{});
+        widen16(u[c], b, T{});
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            const float qv = sh.q[h][c * 32 + lane], x = qv >= 0.f ? u[c] : l[c];
-            const float prod = qv * x;
+        for (int e = 0; e < kElems; ++e) {
+            const float qv = q[(8 * c + sub) * kElems + e], x = qv >= 0.f ? b[e] : a[e], prod = qv * x;
             s += __float2ll_rn(prod * scale);
             if constexpr (Elem<T>::bytes == 4) s += __float2ll_rn(fmaf(qv, x, -prod) * scale);
         }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        best = h == 0 ? s : max(best, s);
     }
-    return best;
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return s;
 }
 
+constexpr long long kLeastKey = -0x7fffffffffffffffLL - 1;
+
 // Ranks the `n` <= kUndecided pages of sh.und_page by their fixed-point scores
-// and sets the bits of sh.und_in for the first `need` of them.
+// and sets the bits of sh.und_in for the first `need` of them.  On entry
+// sh.und_phys holds their physical pages and sh.und_key is kLeastKey.
 template <typename T, int D, int G>
-__device__ __forceinline__ void rank_undecided(const SelectParams &p, SelShared<D, G> &sh, int row, int g, int n, int need, float scale) {
+__device__ __forceinline__ void rank_undecided(const SelectParams &p, SelShared<D, G> &sh, int g, int n, int need, float scale) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int k = warp; k < n; k += kSelWarps) {
-        const int64_t at = (p.layer_page0 + page_at(p, row, sh.und_page[k])) * p.n_kv_heads + g;
-        const long long key = fixed_score<T, D, G>(p, sh, at, scale);
-        if (lane == 0) sh.und_key[k] = key;
+    for (int x0 = warp * 4; x0 < n * G; x0 += kSelWarps * 4) {    // eight lanes per (page, head)
+        const int x = min(x0 + lane / 8, n * G - 1), k = x / G, h = x % G;
+        const int64_t at = (p.layer_page0 + sh.und_phys[k]) * p.n_kv_heads + g;
+        const long long key = fixed_score<T, D>(p, sh.q[h], at, scale, lane % 8);
+        if (lane % 8 == 0) atomicMax(&sh.und_key[k], key);
     }
     __syncthreads();
     static_assert(kUndecided <= kSelThreads, "one undecided page per thread");
@@ -538,19 +567,21 @@ __device__ __forceinline__ void rank_undecided(const SelectParams &p, SelShared<
     __syncthreads();
 }
 
-// The threshold's bin [*fl, *fh] (the error bound included) of the 32-bit
-// scores, narrowed until at most kUndecided pages lie in it or a bin is one
-// key.  sh.hist is zero on entry.  each(f) calls f(key, score) for this
+// The threshold's bin, the error bound on both sides included, as keys [lo, hi]
+// of the 32-bit scores, narrowed until at most kUndecided pages lie in it or a
+// bin is one key.  sh.hist is zero on entry.  each(f) calls f(key) for this
 // thread's candidates.
-// Returns the counts (above, inside) of all candidates; *before are those of
-// the threads before this one.
+struct Threshold {
+    uint32_t lo, hi;
+    int in, mid;                             // candidates above it and inside
+    int in_before, mid_before;               // of the threads before this one
+};
 template <int D, int G, typename Each>
-__device__ __forceinline__ int2 find_threshold(SelShared<D, G> &sh, uint32_t lo, uint32_t hi, int rank, float slack, Each each,
-                                               float *fl, float *fh, int2 *before) {
+__device__ __forceinline__ Threshold find_threshold(SelShared<D, G> &sh, uint32_t lo, uint32_t hi, int rank, float slack, Each each) {
     const int tid = threadIdx.x;
     for (;;) {
         const int shift = max(0, 32 - __clz(hi - lo) - 11);
-        each([&](uint32_t k, float) {
+        each([&](uint32_t k) {
             if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
         });
         __syncthreads();
@@ -558,53 +589,55 @@ __device__ __forceinline__ int2 find_threshold(SelShared<D, G> &sh, uint32_t lo,
         rank -= sh.above;
         lo += static_cast<uint32_t>(sh.bin) << shift;
         hi = min(hi, lo + ((1u << shift) - 1u));
-        const float a = unkey32(lo) - slack, z = unkey32(hi) + slack;
-        int in = 0, mid = 0, t_in, t_mid;
-        each([&](uint32_t, float s) {
-            in += s > z;
-            mid += s >= a && s <= z;
-        });
-        before->x = block_scan(sh.warp_sum, in, &t_in) - in;
-        before->y = block_scan(sh.warp_sum, mid, &t_mid) - mid;
-        *fl = a;
-        *fh = z;
-        if (t_mid <= kUndecided || shift == 0) return make_int2(t_in, t_mid);
+        Threshold x;
+        x.lo = key32(unkey32(lo) - slack);
+        x.hi = key32(unkey32(hi) + slack);
+        unsigned long long both = 0;
+        each([&](uint32_t k) { both += k > x.hi ? 1ull << 32 : k >= x.lo ? 1ull : 0ull; });
+        unsigned long long total;
+        const unsigned long long before = block_scan(sh.warp_sum, both, &total) - both;
+        x.in = static_cast<int>(total >> 32);
+        x.mid = static_cast<int>(total);
+        x.in_before = static_cast<int>(before >> 32);
+        x.mid_before = static_cast<int>(before);
+        if (x.mid <= kUndecided || shift == 0) return x;
         for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
         __syncthreads();
     }
 }
 
 // The general path: scores stay in memory and are read in every pass; decided
-// pages are marked there by +-inf.  For contexts of more pages than the
+// pages are marked there by NaN (in: its key is above all) and -inf.  For contexts of more pages than the
 // registers hold, and where more than kUndecided pages are undecided.
 template <typename T, int D, int G>
 __device__ __noinline__ void select_general(const SelectParams &p, SelShared<D, G> &sh, int row, int g, int n, float *score, int32_t *sel,
                                             uint32_t klo, uint32_t khi, float slack, bool finite, float scale) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float kIn = __uint_as_float(0x7fffffffu);
     const int c0 = p.n_first, m = n - p.n_first - p.n_last, keep = p.top_k - p.n_first - p.n_last;
     score += c0;
-    float fl = -INFINITY, fh = INFINITY;
-    int2 count = make_int2(0, m), before;
+    Threshold th{0u, 0xffffffffu, 0, m, 0, 0};
     const auto each = [&](auto f) {
-        for (int i = tid; i < m; i += kSelThreads) {
-            const float s = score[i];
-            f(key32(s), s);
-        }
+        for (int i = tid; i < m; i += kSelThreads) f(key32(score[i]));
     };
-    if (finite) count = find_threshold(sh, klo, khi, keep, slack, each, &fl, &fh, &before);
-    const int need = keep - count.x, undecided = count.y;
+    if (finite) th = find_threshold(sh, klo, khi, keep, slack, each);
+    const auto inside = [&](float s) { return key32(s) >= th.lo && key32(s) <= th.hi; };
+    const int need = keep - th.in, undecided = th.mid;
     if (need < undecided) {
         if (finite && undecided <= kUndecided) {
             if (tid == 0) sh.bin = 0;
             __syncthreads();
-            for (int i = tid; i < m; i += kSelThreads) {
-                const float s = score[i];
-                if (s >= fl && s <= fh) sh.und_page[atomicAdd(&sh.bin, 1)] = c0 + i;
-            }
+            for (int i = tid; i < m; i += kSelThreads)
+                if (inside(score[i])) {
+                    const int k = atomicAdd(&sh.bin, 1);
+                    sh.und_page[k] = c0 + i;
+                    sh.und_phys[k] = static_cast<int>(page_at(p, row, c0 + i));
+                    sh.und_key[k] = kLeastKey;
+                }
             __syncthreads();
-            rank_undecided<T, D, G>(p, sh, row, g, undecided, need, scale);
+            rank_undecided<T, D, G>(p, sh, g, undecided, need, scale);
             for (int k = tid; k < undecided; k += kSelThreads)
-                score[sh.und_page[k] - c0] = sh.und_in[k / 32] >> (k % 32) & 1 ? INFINITY : -INFINITY;
+                score[sh.und_page[k] - c0] = sh.und_in[k / 32] >> (k % 32) & 1 ? kIn : -INFINITY;
         } else {
             // Many pages within rounding of the threshold (pages that are
             // alike, or scores that are not finite): radix selection on the
@@ -615,8 +648,7 @@ __device__ __noinline__ void select_general(const SelectParams &p, SelShared<D, 
                 for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
                 __syncthreads();
                 for (int i = warp; i < m; i += kSelWarps) {
-                    const float s = score[i];
-                    if (finite && !(s >= fl && s <= fh)) continue;
+                    if (!inside(score[i])) continue;
                     const unsigned long long x = exact_key<T, D, G>(p, sh, row, g, c0 + i);
                     if (lane == 0 && (byte == 7 || (x >> (8 * byte + 8)) == (prefix >> (8 * byte + 8))))
                         atomicAdd(&sh.hist[(x >> (8 * byte)) & 255], 1);
@@ -631,36 +663,35 @@ __device__ __noinline__ void select_general(const SelectParams &p, SelShared<D, 
             int equal = 0;
             for (int i0 = 0; i0 < m; i0 += kSelWarps) {
                 const int i = i0 + warp;
-                const float s = i < m ? score[i] : 0.f;
-                const bool mine = i < m && (!finite || (s >= fl && s <= fh));
+                const bool mine = i < m && inside(score[i]);
                 const unsigned long long x = mine ? exact_key<T, D, G>(p, sh, row, g, c0 + i) : 0;
                 int t;
-                const int at = equal + block_scan(sh.warp_sum, mine && x == prefix && lane == 0, &t);
-                if (mine && lane == 0) score[i] = x > prefix || (x == prefix && at <= rank) ? INFINITY : -INFINITY;
+                const int at = equal + block_scan(sh.warp_sum, static_cast<int>(mine && x == prefix && lane == 0), &t);
+                if (mine && lane == 0) score[i] = x > prefix || (x == prefix && at <= rank) ? kIn : -INFINITY;
                 equal += t;
             }
         }
         __syncthreads();
-        if (!finite) fh = 3e38f;                                  // every score is now +-inf
     }
-    // in ascending order: pages above the bin, and of the bin those marked +inf
-    // (all of it where its pages are all needed)
-    const bool whole = !(need < undecided);
+    // in ascending order: pages above the bin, and of the bin those marked in
+    // (all of it where its pages are all needed; with scores that are not
+    // finite every page is marked)
+    const uint32_t least = need >= undecided ? th.lo : finite ? th.hi + 1 : key32(kIn);
     const int per = (m + kSelThreads - 1) / kSelThreads;
     const int i0 = min(m, tid * per), i1 = min(m, i0 + per);
     int mine = 0, t;
-    for (int i = i0; i < i1; ++i) mine += whole ? score[i] >= fl : score[i] > fh;
+    for (int i = i0; i < i1; ++i) mine += key32(score[i]) >= least;
     int at = p.n_first + block_scan(sh.warp_sum, mine, &t) - mine;
     for (int i = i0; i < i1; ++i)
-        if (whole ? score[i] >= fl : score[i] > fh) sel[at++] = c0 + i;
+        if (key32(score[i]) >= least) sel[at++] = c0 + i;
 }
 
-// One CTA per (kv head, entry).  Up to kSelThreads * kSelOwn pages, thread i
-// keeps the scores of pages kSelOwn * i ... in registers: they are read once,
-// and every later pass (range, histogram, counts, output) is on registers with
-// one block-wide scan.  What bounds it is the chain of these passes (latency);
-// the bytes are few.
-template <typename T, int D, int G>
+// One CTA per (kv head, entry).  Up to kSelThreads * kOwn pages, thread i keeps
+// the keys of pages kOwn * i ... in registers: the scores are read once, and
+// every later pass (range, histogram, counts, output) is on registers with one
+// block-wide scan.  What bounds it is the chain of these passes (latency); the
+// bytes are few.
+template <typename T, int D, int G, int kOwn>
 __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectParams p) {
     __shared__ SelShared<D, G> sh;
     griddep_launch();
@@ -681,37 +712,43 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectP
     const int keep = p.top_k - p.n_first - p.n_last, c1 = n - p.n_last;   // candidates: pages n_first .. c1 - 1
     for (int i = tid; i < p.n_first; i += kSelThreads) sel[i] = i;
     for (int i = tid; i < p.n_last; i += kSelThreads) sel[p.top_k - p.n_last + i] = c1 + i;
+    // the physical pages of this thread's pages, in case they are undecided
+    const int mine = tid * kOwn;                                  // this thread's first page
+    int phys[kOwn > 0 ? kOwn : 1];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        phys[i] = mine + i < n ? __ldg(p.req_to_page + static_cast<int64_t>(row) * p.max_pages + mine + i) : 0;
+        if (static_cast<unsigned>(phys[i]) >= static_cast<unsigned long long>(p.n_pages)) phys[i] = 0;   // the score pass reported it
+    }
     __syncthreads();
     const float norm = query_norm(sh);
     griddep_wait();                                               // the scores
     if (keep == 0) return;
     float *score = p.scores + unit * p.page_cap;
     const float *gmax = p.group_max + unit * (p.page_cap / kScoreGroup);
-    const bool fits = n <= kSelThreads * kSelOwn;
 
-    float s[kSelOwn];
-    uint32_t klo = 0xffffffffu, khi = 0;
     float big = 0.f;
     for (int i = tid; i < (n + kScoreGroup - 1) / kScoreGroup; i += kSelThreads) big = max_nan(big, gmax[i]);
-    const int mine = tid * kSelOwn;                               // this thread's first page
-    if (fits) {
+    uint32_t klo = 0xffffffffu, khi = 0;
+    uint32_t key[kOwn > 0 ? kOwn : 1];
+    const auto owned = [&](int i) { return mine + i >= p.n_first && mine + i < c1; };
+    if constexpr (kOwn > 0) {
         if (mine < n) {                                           // page_cap is a multiple of kScoreGroup
 #pragma unroll
-            for (int i = 0; i < kSelOwn; i += 4) {
+            for (int i = 0; i < kOwn; i += 4) {
                 const float4 x = *reinterpret_cast<const float4 *>(score + mine + i);
-                s[i] = x.x;
-                s[i + 1] = x.y;
-                s[i + 2] = x.z;
-                s[i + 3] = x.w;
+                key[i] = key32(x.x);
+                key[i + 1] = key32(x.y);
+                key[i + 2] = key32(x.z);
+                key[i + 3] = key32(x.w);
             }
         }
 #pragma unroll
-        for (int i = 0; i < kSelOwn; ++i) {
-            if (mine + i >= p.n_first && mine + i < c1) {
-                klo = min(klo, key32(s[i]));
-                khi = max(khi, key32(s[i]));
+        for (int i = 0; i < kOwn; ++i)
+            if (owned(i)) {
+                klo = min(klo, key[i]);
+                khi = max(khi, key[i]);
             }
-        }
     } else {
         for (int i = p.n_first + tid; i < c1; i += kSelThreads) {
             const uint32_t k = key32(score[i]);
@@ -721,68 +758,69 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectP
     }
     klo = __reduce_min_sync(0xffffffffu, klo);
     khi = __reduce_max_sync(0xffffffffu, khi);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, off));
+    // |bounds| and NaN order like their bits
+    const uint32_t big_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(big) & 0x7fffffffu);
     if (lane == 0) {
         sh.lo[warp] = klo;
         sh.hi[warp] = khi;
-        sh.red[warp] = big;
+        sh.big[warp] = big_bits;
     }
     __syncthreads();
     klo = __reduce_min_sync(0xffffffffu, sh.lo[lane % kSelWarps]);
     khi = __reduce_max_sync(0xffffffffu, sh.hi[lane % kSelWarps]);
-    big = sh.red[lane % kSelWarps];
-#pragma unroll
-    for (int off = kSelWarps / 2; off >= 1; off >>= 1) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, off));
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, sh.big[lane % kSelWarps]));
     const float slack = 2.f * kScoreEps * norm * big + kScoreTiny;   // 2e
     float scale = 0.f;
     const bool finite = klo > key32(-INFINITY) && khi < key32(INFINITY) && slack < INFINITY && fixed_point_scale(norm, big, &scale);
-    if (!fits || !finite) {
+    if (kOwn == 0 || !finite) {
         select_general<T, D, G>(p, sh, row, g, n, score, sel, klo, khi, slack, finite, scale);
         return;
     }
-
-    const auto each = [&](auto f) {
+    if constexpr (kOwn > 0) {
+        const auto each = [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < kSelOwn; ++i)
-            if (mine + i >= p.n_first && mine + i < c1) f(key32(s[i]), s[i]);
-    };
-    float fl, fh;
-    int2 before;
-    const int2 count = find_threshold(sh, klo, khi, keep, slack, each, &fl, &fh, &before);
-    const int need = keep - count.x;
-    const bool whole = need >= count.y;                           // the bin's pages are all needed
-    if (!whole) {
-        if (count.y > kUndecided) {
-            for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+            for (int i = 0; i < kOwn; ++i)
+                if (owned(i)) f(key[i]);
+        };
+        const Threshold th = find_threshold(sh, klo, khi, keep, slack, each);
+        const int need = keep - th.in;
+        const bool whole = need >= th.mid;                        // the bin's pages are all needed
+        if (!whole) {
+            if (th.mid > kUndecided) {
+                for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+                __syncthreads();
+                select_general<T, D, G>(p, sh, row, g, n, score, sel, klo, khi, slack, finite, scale);
+                return;
+            }
+            int k = th.mid_before;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i)
+                if (owned(i) && key[i] >= th.lo && key[i] <= th.hi) {
+                    sh.und_page[k] = mine + i;
+                    sh.und_phys[k] = phys[i];
+                    sh.und_key[k++] = kLeastKey;
+                }
             __syncthreads();
-            select_general<T, D, G>(p, sh, row, g, n, score, sel, klo, khi, slack, finite, scale);
-            return;
+            rank_undecided<T, D, G>(p, sh, g, th.mid, need, scale);
         }
-        int k = before.y;
-#pragma unroll
-        for (int i = 0; i < kSelOwn; ++i)
-            if (mine + i >= p.n_first && mine + i < c1 && s[i] >= fl && s[i] <= fh) sh.und_page[k++] = mine + i;
-        __syncthreads();
-        rank_undecided<T, D, G>(p, sh, row, g, count.y, need, scale);
-    }
-    // in ascending order; the list of undecided pages is ascending too
-    int at = p.n_first + before.x, k = before.y;
-    if (whole) {
-        at += before.y;
-    } else {
-        for (int w = 0; w < k / 32; ++w) at += __popc(sh.und_in[w]);
-        at += k % 32 ? __popc(sh.und_in[k / 32] & ((1u << (k % 32)) - 1u)) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kSelOwn; ++i) {
-        if (mine + i < p.n_first || mine + i >= c1) continue;
-        bool in = s[i] > fh;
-        if (s[i] >= fl && s[i] <= fh) {
-            in = whole || (sh.und_in[k / 32] >> (k % 32) & 1);
-            ++k;
+        // in ascending order; the list of undecided pages is ascending too
+        int at = p.n_first + th.in_before, k = th.mid_before;
+        if (whole) {
+            at += k;
+        } else {
+            for (int w = 0; w < k / 32; ++w) at += __popc(sh.und_in[w]);
+            at += k % 32 ? __popc(sh.und_in[k / 32] & ((1u << (k % 32)) - 1u)) : 0;
         }
-        if (in) sel[at++] = mine + i;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            if (!owned(i) || key[i] < th.lo) continue;
+            bool in = true;
+            if (key[i] <= th.hi) {
+                in = whole || (sh.und_in[k / 32] >> (k % 32) & 1);
+                ++k;
+            }
+            if (in) sel[at++] = mine + i;
+        }
     }
 }
 
@@ -811,7 +849,11 @@ cudaError_t launch_select(const SelectParams &p, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = scored || p.pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, select_pages_kernel<T, D, G>, p);
+    // pages per thread that the longest context needs; beyond eight the scores
+    // stay in memory
+    if (p.page_cap <= 4 * kSelThreads) return cudaLaunchKernelEx(&cfg, select_pages_kernel<T, D, G, 4>, p);
+    if (p.page_cap <= 8 * kSelThreads) return cudaLaunchKernelEx(&cfg, select_pages_kernel<T, D, G, 8>, p);
+    return cudaLaunchKernelEx(&cfg, select_pages_kernel<T, D, G, 0>, p);
 }
 
 template <typename T, int D>
@@ -835,16 +877,14 @@ bool sparse_supported(int dtype, int head_dim, int group) {
 cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t s) {
     if (p.n_new == 0) return cudaSuccess;
     const dim3 grid((p.n_new + p.block_tokens - 1) / p.block_tokens, (p.row_chunks + kBoundsThreads - 1) / kBoundsThreads);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kBoundsThreads);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.pdl ? 1 : 0;
-    return p.dtype == PKV_BF16 ? cudaLaunchKernelEx(&cfg, page_bounds_kernel<bf16>, p) : cudaLaunchKernelEx(&cfg, page_bounds_kernel<float>, p);
+    if (p.values) {
+        if (p.dtype == PKV_BF16) page_bounds_kernel<bf16, true><<<grid, kBoundsThreads, 0, s>>>(p);
+        else page_bounds_kernel<float, true><<<grid, kBoundsThreads, 0, s>>>(p);
+    } else {
+        if (p.dtype == PKV_BF16) page_bounds_kernel<bf16, false><<<grid, kBoundsThreads, 0, s>>>(p);
+        else page_bounds_kernel<float, false><<<grid, kBoundsThreads, 0, s>>>(p);
+    }
+    return cudaGetLastError();
 }
 
 cudaError_t launch_select_pages(const SelectParams &p, int dtype, int head_dim, int group, cudaStream_t s) {
