@@ -763,8 +763,11 @@ int select_prepare(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, 
         if (!pg->page_bounds || !aligned16(pg->page_bounds)) return PKV_ERR_ARG;
         if (ws->bytes < pkv_select_workspace_bytes(c->batch, c->n_kv_heads, c->max_len, pg->page_size))
             return PKV_ERR_WORKSPACE;
-        p.scores = static_cast<float *>(ws->base);
-        p.group_max = p.scores + static_cast<int64_t>(c->batch) * c->n_kv_heads * cap;
+        p.keys = static_cast<uint32_t *>(ws->base);
+        p.group_max = reinterpret_cast<float *>(p.keys + static_cast<int64_t>(c->batch) * c->n_kv_heads * cap);
+        pkv::select_plan(&p, di.sms);
+    } else {
+        p.splits = 1;             // every page is selected: nothing to score
     }
     return PKV_OK;
 }

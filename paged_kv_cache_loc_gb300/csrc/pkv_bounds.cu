@@ -1,0 +1,137 @@
+// pkv_bounds.cu -- the pages' key bounds of the sparse decode (pkv_page_bounds):
+// per page, kv head and channel the minimum and maximum of the keys written,
+// brought up to date with a batch of new keys, and the same together with the
+// cache write (a sparse decode step).  Bound by the bytes of the new rows.
+#include "pkv_launch.h"
+#include "pkv_sparse.cuh"
+
+namespace pkv {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kBoundsThreads = 128;
+constexpr int kRowsAhead = 8;
+
+// A run is a maximal sequence of new tokens in consecutive slots of one page
+// (slots outside the pool, which are errors, are passed over).  A CTA takes the
+// runs that start among its block_tokens tokens (and follows a run beyond
+// them); thread c reduces 16-byte chunk c of the run's rows.  The bytes of the
+// new keys are read once, kRowsAhead rows in flight per thread.
+//
+// kWrite: the cache write too (a sparse decode step).  A CTA then first copies
+// its own tokens' K and V rows to the pool; the bounds come from the new rows,
+// not from the pool, so nothing waits for another CTA's copy, and a step has
+// one launch less (2.6 + 3.3 us of kernels apart for one token).
+template <typename T, bool kWrite>
+__global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const BoundsParams p) {
+    griddep_launch();
+    const int chunk = blockIdx.y * kBoundsThreads + threadIdx.x;
+    const int i_end = min(p.n_new, (static_cast<int>(blockIdx.x) + 1) * p.block_tokens);
+    const auto valid = [&](int slot) { return static_cast<unsigned>(slot) < static_cast<unsigned long long>(p.size); };
+    if constexpr (kWrite) {
+        constexpr int kAhead = 4;
+        if (chunk < p.row_chunks) {
+            for (int i = blockIdx.x * p.block_tokens; i < i_end; i += kAhead) {
+                int slot[kAhead];
+                uint4 k[kAhead], v[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int64_t at = static_cast<int64_t>(min(i + u, i_end - 1)) * p.row_chunks + chunk;
+                    slot[u] = __ldg(p.out_cache_loc + min(i + u, i_end - 1));
+                    k[u] = __ldg(static_cast<const uint4 *>(p.keys) + at);
+                    v[u] = __ldg(static_cast<const uint4 *>(p.values) + at);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (i + u >= i_end || !valid(slot[u])) continue;   // the loop below reports a bad slot
+                    const int64_t to = (p.layer_row0 + slot[u]) * p.row_chunks + chunk;
+                    static_cast<uint4 *>(p.k_buffer)[to] = k[u];
+                    static_cast<uint4 *>(p.v_buffer)[to] = v[u];
+                }
+            }
+        }
+    }
+    for (int i = blockIdx.x * p.block_tokens; i < i_end;) {
+        int loc = __ldg(p.out_cache_loc + i);
+        if (!valid(loc)) {
+            if (chunk == 0) record_error(p.err, loc);
+            ++i;
+            continue;
+        }
+        const int page = loc / p.page_size;
+        int off = loc - page * p.page_size;
+        bool begins = off == 0;
+        if (!begins) {
+            int j = i - 1;
+            while (j >= 0 && !valid(__ldg(p.out_cache_loc + j))) --j;
+            begins = j < 0 || __ldg(p.out_cache_loc + j) != loc - 1;
+        }
+        uint4 *dst = static_cast<uint4 *>(p.page_bounds) + (p.layer_page0 + page) * p.row_chunks * 2 +
+                     (chunk / p.head_chunks) * p.head_chunks * 2 + chunk % p.head_chunks;
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        bool have = false;                   // lo / hi hold something
+        const bool mine = begins && chunk < p.row_chunks;
+        if (mine && off != 0) {
+            lo = dst[0];
+            hi = dst[p.head_chunks];
+            have = true;
+        }
+        for (;;) {
+            // tokens i .. i + n - 1 are in consecutive slots of the page
+            const int most = min(p.n_new - i, p.page_size - off);
+            int n = 1;
+            for (;;) {
+                const int at = n + static_cast<int>(threadIdx.x & 31);
+                const bool next = at < most && __ldg(p.out_cache_loc + i + at) == loc + at;
+                const unsigned breaks = __ballot_sync(0xffffffffu, !next);
+                n += breaks ? __ffs(breaks) - 1 : 32;
+                if (breaks) break;
+            }
+            if (mine) {
+                const uint4 *row = (kWrite ? static_cast<const uint4 *>(p.keys) + static_cast<int64_t>(i) * p.row_chunks
+                                           : static_cast<const uint4 *>(p.k_buffer) + (p.layer_row0 + loc) * p.row_chunks) + chunk;
+                if (!have) lo = hi = row[0];
+                have = true;
+                for (int k = 0; k < n; k += kRowsAhead) {
+                    uint4 x[kRowsAhead];
+#pragma unroll
+                    for (int u = 0; u < kRowsAhead; ++u) x[u] = row[static_cast<int64_t>(min(k + u, n - 1)) * p.row_chunks];
+#pragma unroll
+                    for (int u = 0; u < kRowsAhead; ++u) widen_bounds<T>(lo, hi, x[u], x[u]);
+                }
+            }
+            i += n;
+            off += n;
+            loc += n;
+            if (!begins || off == p.page_size) break;
+            int j = i;
+            while (j < p.n_new && !valid(__ldg(p.out_cache_loc + j))) ++j;
+            if (j == i || j >= p.n_new || __ldg(p.out_cache_loc + j) != loc) break;
+            if (chunk == 0)
+                for (int x = i; x < j; ++x) record_error(p.err, __ldg(p.out_cache_loc + x));
+            i = j;
+        }
+        if (mine) {
+            dst[0] = lo;
+            dst[p.head_chunks] = hi;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t s) {
+    if (p.n_new == 0) return cudaSuccess;
+    const dim3 grid((p.n_new + p.block_tokens - 1) / p.block_tokens, (p.row_chunks + kBoundsThreads - 1) / kBoundsThreads);
+    if (p.values) {
+        if (p.dtype == PKV_BF16) page_bounds_kernel<bf16, true><<<grid, kBoundsThreads, 0, s>>>(p);
+        else page_bounds_kernel<float, true><<<grid, kBoundsThreads, 0, s>>>(p);
+    } else {
+        if (p.dtype == PKV_BF16) page_bounds_kernel<bf16, false><<<grid, kBoundsThreads, 0, s>>>(p);
+        else page_bounds_kernel<float, false><<<grid, kBoundsThreads, 0, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace pkv

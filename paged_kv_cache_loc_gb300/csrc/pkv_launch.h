@@ -176,7 +176,7 @@ struct TablesParams {
     DevErr *err;
 };
 
-// Key bounds of pages (pkv_select.cu).
+// Key bounds of pages (pkv_bounds.cu).
 struct BoundsParams {
     const void *keys;             // with the cache write: the new rows in out_cache_loc order (else null: the
     const void *values;           // new keys are read from the pool)
@@ -205,7 +205,7 @@ struct SelectParams {
     const int32_t *seq_lens;
     int32_t *sel;                 // [batch, n_kv_heads, top_k]
     int32_t *sel_counts;          // [batch, n_kv_heads]
-    float *scores;                // [batch, n_kv_heads, page_cap]
+    uint32_t *keys;               // [batch, n_kv_heads, page_cap]: order-preserving keys of the 32-bit scores
     float *group_max;             // [batch, n_kv_heads, page_cap / kScoreGroup]: largest |bound| of a group of pages
     int64_t layer_page0;
     int64_t n_pages;
@@ -220,6 +220,8 @@ struct SelectParams {
     int32_t top_k;
     int32_t n_first;
     int32_t n_last;
+    int32_t splits;               // CTAs (one cluster) per entry and kv head; 0: scores by a kernel of their own
+    int32_t entries;              // consecutive entries per warp of that kernel
     int32_t pdl;                  // launched as a programmatic dependent of what writes the bounds
     DevErr *err;
 };
@@ -266,6 +268,8 @@ cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t s);
 cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t s);
 // Whether the selection and the attention over it have a kernel for this shape.
 bool sparse_supported(int dtype, int head_dim, int group);
+// Sets p->splits and p->entries.
+void select_plan(SelectParams *p, int sms);
 cudaError_t launch_select_pages(const SelectParams &p, int dtype, int head_dim, int group,
                                 cudaStream_t s);
 // CTAs per (entry, kv head) of the attention over selected pages.

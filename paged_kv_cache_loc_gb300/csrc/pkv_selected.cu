@@ -10,8 +10,8 @@
 // host picks the cluster size so that all SMs have work.
 #include <atomic>
 
-#include "pkv_common.cuh"
 #include "pkv_launch.h"
+#include "pkv_sparse.cuh"
 
 namespace pkv {
 namespace {
@@ -22,21 +22,6 @@ constexpr int kBlk = 16;              // positions per block
 constexpr int kStagePages = 512;      // list entries resolved to slots at a time
 constexpr int kMaxSplits = 8;         // CTAs per cluster (the portable limit)
 
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;\n" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ float ld_cluster(uint32_t a) {
-    float x;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(x) : "r"(a) : "memory");
-    return x;
-}
 __device__ __forceinline__ float weight(float m, float top) { return m == -INFINITY ? 0.f : fast_exp2(m - top); }
 
 // One listed page: its first slot and its first position (-1: not to be read).
@@ -314,13 +299,6 @@ __global__ void __launch_bounds__(kSimtThreads) selected_simt_kernel(const Selec
 constexpr int kMmaWarps = 4;
 constexpr int kMmaThreads = kMmaWarps * 32;
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -441,8 +419,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint4 k = chunk(x, r + 8 * i, t + 4 * j);
-                    mma16816(w[i], q[j].x, 0, q[j].y, 0, k.x, k.y);
-                    mma16816(w[i], q[j].z, 0, q[j].w, 0, k.z, k.w);
+                    mma_bf16(w[i], q[j].x, 0, q[j].y, 0, k.x, k.y);
+                    mma_bf16(w[i], q[j].z, 0, q[j].w, 0, k.z, k.w);
                 }
             // head r, positions 2t, 2t + 1, 2t + 8, 2t + 9
             float pr[4];
@@ -493,8 +471,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
                     const uint32_t a1 = __byte_perm(word(v[0], i), word(v[1], i), 0x7632);
                     const uint32_t a2 = __byte_perm(word(v[2], i), word(v[3], i), 0x5410);
                     const uint32_t a3 = __byte_perm(word(v[2], i), word(v[3], i), 0x7632);
-                    mma16816(o[j * 4 + i], a0, a1, a2, a3, hi0, hi1);
-                    mma16816(o[j * 4 + i], a0, a1, a2, a3, lo0, lo1);
+                    mma_bf16(o[j * 4 + i], a0, a1, a2, a3, hi0, hi1);
+                    mma_bf16(o[j * 4 + i], a0, a1, a2, a3, lo0, lo1);
                 }
             }
             __syncwarp();                                         // every lane has read the V rows
