@@ -65,49 +65,51 @@ class SparsePages:
         return cls(bounds, req_to_page, page_size, top_k, n_first, n_last)
 
     def c_struct(self, cache: KVCache) -> PkvPages:
-        kb, t = cache.k_buffer, self.req_to_page
+        kb, t, bounds, ps = cache.k_buffer, self.req_to_page, self.page_bounds, self.page_size
         index = kb.get_device()
         if t.dim() != 2:
             raise ValueError("req_to_page must be [num_reqs, max_pages]")
-        if self.page_size < 1:
+        if ps < 1:
             raise ValueError("page_size must be positive")
-        bounds = self.page_bounds
         if bounds is not None:
             n_layers, size, n_kv_heads, head_dim = kb.shape
-            if tuple(bounds.shape) != (n_layers, size // self.page_size, n_kv_heads, 2, head_dim):
+            if bounds.shape != (n_layers, size // ps, n_kv_heads, 2, head_dim):
                 raise ValueError("page_bounds must be [n_layers, size // page_size, n_kv_heads, 2, head_dim]")
             bounds = _ptr(bounds, "page_bounds", kb.dtype, index)
-        return PkvPages(bounds, _ptr(t, "req_to_page", torch.int32, index), t.shape[1], self.page_size,
-                        self.top_k, self.n_first, self.n_last)
+        return PkvPages(bounds, _ptr(t, "req_to_page", torch.int32, index), t.shape[1], ps, self.top_k, self.n_first,
+                        self.n_last)
 
 
-def _cache(cache: KVCache, table: torch.Tensor, table_name: str, max_ctx_len: int, n_new: int,
+def _cache(cache: KVCache, table: torch.Tensor, table_ptr: int, max_ctx_len: int, n_new: int,
            decode: bool) -> Tuple[PkvKVCache, int]:
-    """The descriptor of a cache whose request rows are those of `table`."""
+    """The descriptor of a cache whose request rows are those of `table`
+    (already checked, at table_ptr)."""
     kb, vb, rows, lens = cache.k_buffer, cache.v_buffer, cache.req_pool_indices, cache.seq_lens
-    if kb.dim() != 4 or vb.shape != kb.shape:
+    dtype = kb.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported storage dtype {dtype}")
+    shape = kb.shape
+    if len(shape) != 4 or vb.shape != shape:
         raise ValueError("k_buffer/v_buffer must both be [n_layers, size, n_kv_heads, head_dim]")
-    dtype = _DTYPES.get(kb.dtype)
-    if dtype is None:
-        raise TypeError(f"unsupported storage dtype {kb.dtype}")
-    if not kb.is_cuda:
-        raise ValueError("k_buffer must be a CUDA tensor (there is no CPU path)")
     index = kb.get_device()
-    n_layers, size, n_kv_heads, head_dim = kb.shape
+    if index < 0:
+        raise ValueError("k_buffer must be a CUDA tensor (there is no CPU path)")
     batch = rows.numel()
-    if decode and lens is None:
+    if lens is not None:
+        lens = _i32(lens, "seq_lens", index, batch)
+    elif decode:
         raise ValueError("seq_lens is needed")
+    n_layers, size, n_kv_heads, head_dim = shape
     return PkvKVCache(
-        _ptr(kb, "k_buffer", kb.dtype, index), _ptr(vb, "v_buffer", kb.dtype, index), dtype, n_layers,
-        n_kv_heads, head_dim, size, _ptr(table, table_name, torch.int32, index), table.shape[0], max_ctx_len,
-        _ptr(rows, "req_pool_indices", torch.int32, index), _i32(lens, "seq_lens", index, batch), None, None,
-        _slots(cache.out_cache_loc, index, n_new), batch, int(cache.max_len)), index
+        _ptr(kb, "k_buffer", dtype, index), _ptr(vb, "v_buffer", dtype, index), code, n_layers, n_kv_heads,
+        head_dim, size, table_ptr, table.shape[0], max_ctx_len,
+        _ptr(rows, "req_pool_indices", torch.int32, index), lens, None, None,
+        _slots(cache.out_cache_loc, index, n_new) if n_new else None, batch, int(cache.max_len)), index
 
 
-def _slots(loc: Optional[torch.Tensor], index: int, n_new: int) -> Optional[int]:
+def _slots(loc: Optional[torch.Tensor], index: int, n_new: int) -> int:
     """The address of out_cache_loc, which may be longer than what is written."""
-    if not n_new:
-        return None
     p = _ptr(loc, "out_cache_loc", torch.int32, index)
     if loc.numel() < n_new:
         raise ValueError(f"out_cache_loc must have {n_new} elements at least, got {loc.numel()}")
@@ -116,7 +118,7 @@ def _slots(loc: Optional[torch.Tensor], index: int, n_new: int) -> Optional[int]
 
 def _rows(t: torch.Tensor, name: str, c: PkvKVCache, dtype, index: int, n: int, heads: int) -> int:
     """The address of [n, heads, head_dim] rows of the cache's dtype."""
-    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != heads or t.shape[2] != c.head_dim:
+    if t.shape != (n, heads, c.head_dim):
         raise ValueError(f"{name} must be [{n}, {heads}, {c.head_dim}], got {list(t.shape)}")
     return _ptr(t, name, dtype, index)
 
@@ -140,18 +142,23 @@ def _workspace(ws: Optional[Workspace], index: int):
     return ctypes.byref(ws.desc)
 
 
-def _call(fn, index: int, stream, *args) -> None:
-    """Calls fn on the cache's device with the stream's handle; None is the
-    device's current stream."""
-    if stream is None:
-        stream = torch.cuda.current_stream(index)
+# the handle of a device's current stream, without the object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(name: str, index: int, stream, *args) -> None:
+    """Calls the library's `name` on the cache's device with the stream's
+    handle; None is the device's current stream."""
+    fn = getattr(_lib._lib or _lib.load(), name)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == index:
-        status = fn(*args, stream.cuda_stream)
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, handle)
     if status:
-        check(status, fn.__name__)
+        check(status, name)
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -180,7 +187,7 @@ def build_tables(cache: KVCache, req_to_page: torch.Tensor, page_size: int, free
         raise ValueError("req_to_page and req_to_token must have the same rows")
     loc = cache.out_cache_loc
     n_new = 0 if loc is None else loc.numel()
-    c, index = _cache(cache, req_to_page, "req_to_page", cache.req_to_token.shape[1], n_new, True)
+    c, index = _cache(cache, req_to_page, _ptr(req_to_page, "req_to_page", torch.int32, cache.k_buffer.get_device()), cache.req_to_token.shape[1], n_new, True)
     t = PkvTables(
         _i32(q_lens, "q_lens", index, c.batch), c.req_to_token, req_to_page.shape[1], int(page_size),
         _ptr(free_pages, "free_pages", torch.int32, index), _i32(free_start, "free_start", index, 1),
@@ -189,7 +196,7 @@ def build_tables(cache: KVCache, req_to_page: torch.Tensor, page_size: int, free
         _i32(cache.qo_indptr, "qo_indptr", index, c.batch + 1),
         _i32(positions, "positions", index, n_new), c.out_cache_loc,
         _ptr(cache.req_to_token, "req_to_token", torch.int32, index) if token_table else None)
-    _call(_lib.load().pkv_build_tables, index, stream, ctypes.byref(c), ctypes.byref(t))
+    _call("pkv_build_tables", index, stream, ctypes.byref(c), ctypes.byref(t))
 
 
 def page_bounds(cache: KVCache, layer_id: int, pages: SparsePages, n_new: Optional[int] = None,
@@ -201,8 +208,8 @@ def page_bounds(cache: KVCache, layer_id: int, pages: SparsePages, n_new: Option
     if n_new is None:
         n_new = cache.out_cache_loc.numel()
     pg = pages.c_struct(cache)
-    c, index = _cache(cache, pages.req_to_page, "req_to_page", 0, n_new, False)
-    _call(_lib.load().pkv_page_bounds, index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg), n_new)
+    c, index = _cache(cache, pages.req_to_page, pg.req_to_page, 0, n_new, False)
+    _call("pkv_page_bounds", index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg), n_new)
 
 
 def select_workspace_bytes(batch: int, n_kv_heads: int, max_len: int, page_size: int) -> int:
@@ -217,12 +224,12 @@ def select_pages(cache: KVCache, layer_id: int, pages: SparsePages, q: torch.Ten
     sel int32 [batch, n_kv_heads, top_k] (logical pages, ascending, then -1)
     and sel_counts int32 [batch, n_kv_heads]."""
     pg = pages.c_struct(cache)
-    c, index = _cache(cache, pages.req_to_page, "req_to_page", 0, 0, True)
+    c, index = _cache(cache, pages.req_to_page, pg.req_to_page, 0, 0, True)
     if sel is None:
         sel = _empty((c.batch, c.n_kv_heads, pages.top_k), torch.int32, cache.k_buffer.device, stream)
     if sel_counts is None:
         sel_counts = _empty((c.batch, c.n_kv_heads), torch.int32, cache.k_buffer.device, stream)
-    _call(_lib.load().pkv_select_pages, index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
+    _call("pkv_select_pages", index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
             _rows(q, "q", c, cache.k_buffer.dtype, index, c.batch, _heads(q)), q.shape[1],
             *_lists(sel, sel_counts, c, pages.top_k, index), _workspace(workspace, index))
     return sel, sel_counts
@@ -235,12 +242,12 @@ def paged_decode_selected(cache: KVCache, layer_id: int, pages: SparsePages, q: 
     """paged_decode over the positions of the selected pages only; q, o:
     [batch, n_heads, head_dim], sel and sel_counts as select_pages gives them."""
     pg = pages.c_struct(cache)
-    c, index = _cache(cache, pages.req_to_page, "req_to_page", 0, 0, True)
+    c, index = _cache(cache, pages.req_to_page, pg.req_to_page, 0, 0, True)
     dtype, heads = cache.k_buffer.dtype, _heads(q)
     if o is None:
         o = _empty(q.shape, q.dtype, cache.k_buffer.device, stream)
     scale = 1.0 / math.sqrt(c.head_dim) if sm_scale is None else float(sm_scale)
-    _call(_lib.load().pkv_paged_decode_selected, index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
+    _call("pkv_paged_decode_selected", index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
             *_lists(sel, sel_counts, c, pages.top_k, index),
             _rows(q, "q", c, dtype, index, c.batch, heads), _rows(o, "o", c, dtype, index, c.batch, heads),
             heads, scale)
@@ -256,7 +263,7 @@ def sparse_decode_step(cache: KVCache, layer_id: int, pages: SparsePages, k_new:
     select_pages and paged_decode_selected as one call: (o, sel, sel_counts)."""
     n_new, heads, dtype = k_new.shape[0], _heads(q), cache.k_buffer.dtype
     pg = pages.c_struct(cache)
-    c, index = _cache(cache, pages.req_to_page, "req_to_page", 0, n_new, True)
+    c, index = _cache(cache, pages.req_to_page, pg.req_to_page, 0, n_new, True)
     if o is None:
         o = _empty(q.shape, q.dtype, cache.k_buffer.device, stream)
     if sel is None:
@@ -264,7 +271,7 @@ def sparse_decode_step(cache: KVCache, layer_id: int, pages: SparsePages, k_new:
     if sel_counts is None:
         sel_counts = _empty((c.batch, c.n_kv_heads), torch.int32, cache.k_buffer.device, stream)
     scale = 1.0 / math.sqrt(c.head_dim) if sm_scale is None else float(sm_scale)
-    _call(_lib.load().pkv_sparse_decode_step, index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
+    _call("pkv_sparse_decode_step", index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
             _rows(k_new, "k_new", c, dtype, index, n_new, c.n_kv_heads),
             _rows(v_new, "v_new", c, dtype, index, n_new, c.n_kv_heads), n_new,
             _rows(q, "q", c, dtype, index, c.batch, heads), _rows(o, "o", c, dtype, index, c.batch, heads),
