@@ -796,6 +796,9 @@ int selected_prepare(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg
     p.batch = c->batch;
     p.max_len = c->max_len;
     p.top_k = pg->top_k;
+    p.page_shift = -1;
+    for (int k = 0; k < 31; ++k)
+        if (1 << k == pg->page_size) p.page_shift = k;
     p.splits = pkv::selected_splits(c->batch, c->n_kv_heads, pg->top_k, pg->page_size, c->max_len, di.sms);
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.err = di.err;

@@ -247,6 +247,7 @@ struct SelectedParams {
     int32_t batch;
     int32_t max_len;
     int32_t top_k;
+    int32_t page_shift;           // log2 of page_size where it is a power of two, else -1
     int32_t splits;               // CTAs (one cluster) per entry and kv head
     int32_t pdl;                  // launched as a programmatic dependent of the selection
     float scale_log2;

@@ -309,9 +309,24 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 
 __device__ __forceinline__ int slot_at(int at, int to, int i0, const Run *runs, const SelectedParams &p, int len) {
     const int x = at + static_cast<int>(threadIdx.x & 15);
     if (x >= to) return -1;
-    const int i = x / p.page_size, off = x - i * p.page_size;
+    const int i = p.page_shift >= 0 ? x >> p.page_shift : x / p.page_size, off = x - i * p.page_size;
     const Run run = runs[i - i0];
     return run.pos >= 0 && static_cast<unsigned>(run.pos) + off < static_cast<unsigned>(len) ? run.slot + off : -1;
+}
+
+// 2^x to 2^-22 of the value, 0 for -inf.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ void cp_async16_at(uint32_t to, const void *from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
 // Shared memory of a CTA: each warp's ring of kRing half blocks (16 rows of K or
@@ -373,24 +388,44 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-    // a half block to ring place `to`: kRowLanes lanes to a row; an unseen position is filled with zeros
-    constexpr int kRowLanes = kChunks, kRowsPer = 32 / kRowLanes;
-    const auto fetch = [&](const void *pool, int slot, int to) {
-        bf16 *dst = sh.ring[warp][to];
-        const int c = lane % kRowLanes;
+    // A half block to ring place `to`: kRowLanes lanes to a row.  An unseen
+    // position's K is slot 0's (its score is masked), its V zeros.
+    constexpr int kRowLanes = kChunks, kRowsPer = 32 / kRowLanes, kRowBytes = D * 2, kPlaceBytes = Sh::kRows * 2;
+    const uint32_t ring = smem_u32(sh.ring[warp][0]);
+    const int64_t lane0 = (p.layer_row0 * p.n_kv_heads + g) * kRowBytes + lane % kRowLanes * 16;
+    const char *kp = static_cast<const char *>(p.k_buffer) + lane0, *vp = static_cast<const char *>(p.v_buffer) + lane0;
+    const uint32_t slot_bytes = static_cast<uint32_t>(p.n_kv_heads) * kRowBytes;
+    uint32_t put[kRowsPer == 2 ? 4 : 2];     // this lane's places in a half block: rows i * kRowsPer + lane / kRowLanes
+#pragma unroll
+    for (int i = 0; i < 8 / kRowsPer; ++i) {
+        const int row = i * kRowsPer + lane / kRowLanes;          // rows 8 and more: the same, 8 rows on
+        put[i] = row * kRowBytes + swizzle(row, lane % kRowLanes) * 16;
+    }
+    const auto fetch_k = [&](int slot, int to) {
+        const int safe = max(slot, 0);
 #pragma unroll
         for (int i = 0; i < kBlk / kRowsPer; ++i) {
-            const int row = i * kRowsPer + lane / kRowLanes;
-            const int from = __shfl_sync(0xffffffffu, slot, row);
-            const uint4 *src = static_cast<const uint4 *>(pool) +
-                               ((p.layer_row0 + (from >= 0 ? from : 0)) * p.n_kv_heads + g) * kChunks + c;
-            cp_async16(dst + row * D + swizzle(row, c) * 8, src, from >= 0 ? 16 : 0);
+            const uint32_t from = __shfl_sync(0xffffffffu, safe, i * kRowsPer + lane / kRowLanes);
+            cp_async16_at(ring + to * kPlaceBytes + put[i % (8 / kRowsPer)] + i / (8 / kRowsPer) * 8 * kRowBytes,
+                          kp + static_cast<uint64_t>(from) * slot_bytes, 16);
         }
         cp_async_commit();
     };
-    const auto chunk = [&](int at, int row, int c) {
-        return *reinterpret_cast<const uint4 *>(&sh.ring[warp][at][row * D + swizzle(row, c) * 8]);
+    const auto fetch_v = [&](int slot, int to) {
+#pragma unroll
+        for (int i = 0; i < kBlk / kRowsPer; ++i) {
+            const int from = __shfl_sync(0xffffffffu, slot, i * kRowsPer + lane / kRowLanes);
+            cp_async16_at(ring + to * kPlaceBytes + put[i % (8 / kRowsPer)] + i / (8 / kRowsPer) * 8 * kRowBytes,
+                          vp + static_cast<uint64_t>(static_cast<uint32_t>(max(from, 0))) * slot_bytes, from >= 0 ? 16 : 0);
+        }
+        cp_async_commit();
     };
+    // Places of this lane's chunks: K row r, chunks t + 4 j for j even and odd
+    // (128 bytes on for each j / 2, eight rows on for row r + 8); V rows 2t and
+    // 2t + 1, chunk r (the same steps).
+    const uint32_t k_even = ring + r * kRowBytes + swizzle(r, t) * 16, k_odd = ring + r * kRowBytes + swizzle(r, t + 4) * 16;
+    const uint32_t v_even = ring + 2 * t * kRowBytes + swizzle(2 * t, r) * 16;
+    const uint32_t v_odd = ring + (2 * t + 1) * kRowBytes + swizzle(2 * t + 1, r) * 16;
 
     const int i_end = s.t1 > s.t0 ? (s.t1 - 1) / p.page_size + 1 : 0;
     for (int i0 = s.t0 / p.page_size; i0 < i_end; i0 += kStagePages) {
@@ -403,14 +438,15 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
         int at = from + warp * kBlk, x = 0;                       // x: ring place of the half block in use
         if (at >= to) continue;
         int slot = slot_at(at, to, i0, sh.runs, p, s.len);
-        fetch(p.k_buffer, slot, 0);
-        fetch(p.v_buffer, slot, 1);
+        fetch_k(slot, 0);
+        fetch_v(slot, 1);
         const auto after = [&](int place, int by) { return place + by < kRing ? place + by : place + by - kRing; };
         while (at < to) {
             const int next = at + kMmaWarps * kBlk;
             const int next_slot = slot_at(next, to, i0, sh.runs, p, s.len);
-            if (next < to) fetch(p.k_buffer, next_slot, after(x, 2));
+            if (next < to) fetch_k(next_slot, after(x, 2));
             else cp_async_commit();
+            const unsigned unseen = ~__ballot_sync(0xffffffffu, slot >= 0);
             cp_async_wait<2>();
             __syncwarp();
             float w[2][4] = {};
@@ -418,19 +454,18 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
             for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint4 k = chunk(x, r + 8 * i, t + 4 * j);
+                    const uint4 k = lds16((j & 1 ? k_odd : k_even) + x * kPlaceBytes + (j / 2) * 128 + i * 8 * kRowBytes);
                     mma_bf16(w[i], q[j].x, 0, q[j].y, 0, k.x, k.y);
                     mma_bf16(w[i], q[j].z, 0, q[j].w, 0, k.z, k.w);
                 }
             // head r, positions 2t, 2t + 1, 2t + 8, 2t + 9
-            float pr[4];
-            float top = m;
+            float pr[4] = {w[0][0] * p.scale_log2, w[0][1] * p.scale_log2, w[1][0] * p.scale_log2, w[1][1] * p.scale_log2};
+            if (unseen) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool seen = __shfl_sync(0xffffffffu, slot, 2 * t + (i & 1) + 8 * (i >> 1)) >= 0;
-                pr[i] = seen ? w[i >> 1][i & 1] * p.scale_log2 : -INFINITY;
-                top = fmaxf(top, pr[i]);
+                for (int i = 0; i < 4; ++i)
+                    if (unseen >> (2 * t + (i & 1) + 8 * (i >> 1)) & 1) pr[i] = -INFINITY;
             }
+            float top = fmaxf(fmaxf(fmaxf(pr[0], pr[1]), fmaxf(pr[2], pr[3])), m);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             if (__any_sync(0xffffffffu, top != m)) {
@@ -446,16 +481,17 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
                     o[i][3] *= f1;
                 }
             }
+            const float zero = m == -INFINITY ? 0.f : m;          // nothing seen yet: weights exp2(-inf) = 0
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                pr[i] = weight(pr[i], m);
+                pr[i] = exp2_approx(pr[i] - zero);
                 l += pr[i];
             }
             const uint32_t hi0 = pack_bf16(pr[0], pr[1]), hi1 = pack_bf16(pr[2], pr[3]);
             const uint32_t lo0 = pack_bf16(pr[0] - bf16lo(hi0), pr[1] - bf16hi(hi0));
             const uint32_t lo1 = pack_bf16(pr[2] - bf16lo(hi1), pr[3] - bf16hi(hi1));
             __syncwarp();                                         // every lane has read the K rows
-            if (next < to) fetch(p.v_buffer, next_slot, x);
+            if (next < to) fetch_v(next_slot, x);
             else cp_async_commit();
             x = after(x, 1);
             cp_async_wait<2>();
@@ -464,7 +500,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
             for (int j = 0; j < kHalves; ++j) {
                 uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = chunk(x, 2 * t + (i & 1) + 8 * (i >> 1), r + 8 * j);
+                for (int i = 0; i < 4; ++i) v[i] = lds16((i & 1 ? v_odd : v_even) + x * kPlaceBytes + (i >> 1) * 8 * kRowBytes + j * 128);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t a0 = __byte_perm(word(v[0], i), word(v[1], i), 0x5410);
