@@ -76,12 +76,12 @@ struct Scorer {
     static constexpr int kChunks = D / 8, kOwn = kChunks / 4;
     uint4 l0[kOwn], l1[kOwn], h0[kOwn], h1[kOwn], q[kOwn];
 
-    // rows: the group's G rows of q.
-    __device__ __forceinline__ void load_q(const T *rows) {
+    // rows: n <= 8 rows of q, one for each column.
+    __device__ __forceinline__ void load_q(const T *rows, int n) {
         const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
-            q[j] = r < G ? reinterpret_cast<const uint4 *>(rows)[r * kChunks + t + 4 * j] : make_uint4(0, 0, 0, 0);
+            q[j] = r < n ? reinterpret_cast<const uint4 *>(rows)[r * kChunks + t + 4 * j] : make_uint4(0, 0, 0, 0);
     }
     // Starts the loads of a group; phys: the physical page of its page lane % 16.
     __device__ __forceinline__ void load(const SelectParams &p, int g, int phys) {
@@ -111,10 +111,10 @@ struct Scorer {
         // non-negative numbers and NaN order like their bits
         return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big) & 0x7fffffffu));
     }
-    // The score of page lane % 16 of the group.
-    __device__ __forceinline__ float score() const {
-        const int lane = threadIdx.x & 31, t = lane & 3;
-        float x[4] = {}, y[4] = {}, z[4] = {}, w[4] = {};         // four chains
+    // x: pages r (x[0], x[1]) and r + 8 of the group by columns 2t and 2t + 1.
+    __device__ __forceinline__ void products(float (&x)[4]) const {
+        x[0] = x[1] = x[2] = x[3] = 0.f;
+        float y[4] = {}, z[4] = {}, w[4] = {};                    // four chains
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
             const uint4 qn = make_uint4(min_word(q[j].x, 0, T{}), min_word(q[j].y, 0, T{}), min_word(q[j].z, 0, T{}), min_word(q[j].w, 0, T{}));
@@ -126,7 +126,12 @@ struct Scorer {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = (x[i] + z[i]) + (y[i] + w[i]);
-        // rows r and r + 8, heads 2t and 2t + 1
+    }
+    // The score of page lane % 16 of the group for the first G columns.
+    __device__ __forceinline__ float score() const {
+        const int lane = threadIdx.x & 31, t = lane & 3;
+        float x[4];
+        products(x);
         float s0 = -INFINITY, s1 = -INFINITY;
         if (2 * t < G) {
             s0 = x[0];
@@ -145,6 +150,32 @@ struct Scorer {
         s1 = __shfl_sync(0xffffffffu, s1, 4 * (lane & 7));
         return lane & 8 ? s1 : s0;
     }
+    // The columns hold the G heads of each of kSets entries: put(entry, page of
+    // the group, score), each from one lane.
+    static constexpr int kSets = 8 / G;
+    template <typename Put>
+    __device__ __forceinline__ void score_sets(Put put) const {
+        const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+        float x[4];
+        products(x);
+        if constexpr (G == 1) {
+            put(2 * t, r, x[0]);
+            put(2 * t, r + 8, x[2]);
+            put(2 * t + 1, r, x[1]);
+            put(2 * t + 1, r + 8, x[3]);
+        } else {
+            float s0 = max_nan(x[0], x[1]), s1 = max_nan(x[2], x[3]);
+#pragma unroll
+            for (int off = 1; off < G / 2; off <<= 1) {
+                s0 = max_nan(s0, __shfl_xor_sync(0xffffffffu, s0, off));
+                s1 = max_nan(s1, __shfl_xor_sync(0xffffffffu, s1, off));
+            }
+            if (t % (G / 2) == 0) {
+                put(2 * t / G, r, s0);
+                put(2 * t / G, r + 8, s1);
+            }
+        }
+    }
 };
 
 // CUDA cores (fp32): eight lanes to a page, four pages at a time, each lane
@@ -155,7 +186,7 @@ struct Scorer<float, D, G> {
     const float *q;
     float s, big;
 
-    __device__ __forceinline__ void load_q(const float *rows) { q = rows; }
+    __device__ __forceinline__ void load_q(const float *rows, int) { q = rows; }
     __device__ __forceinline__ void load(const SelectParams &p, int g, int phys) {
         const int lane = threadIdx.x & 31, sub = lane & 7;
         s = big = 0.f;
@@ -196,6 +227,12 @@ struct Scorer<float, D, G> {
         return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big) & 0x7fffffffu));
     }
     __device__ __forceinline__ float score() const { return s; }
+    static constexpr int kSets = 1;
+    template <typename Put>
+    __device__ __forceinline__ void score_sets(Put put) const {
+        const int lane = threadIdx.x & 31;
+        if (lane < 16) put(0, lane, s);
+    }
 };
 
 // ---------------------------------------------------------------------------
@@ -617,8 +654,8 @@ __global__ void __launch_bounds__(kClusterThreads, 2) select_cluster_kernel(cons
     Scorer<T, D, G> sc;
     int at = lookup(group);
     __syncthreads();
-    if constexpr (Elem<T>::bytes == 4) sc.load_q(&sh.q[0][0]);
-    else sc.load_q(static_cast<const T *>(p.q) + (static_cast<int64_t>(b) * p.n_heads + g * G) * D);
+    if constexpr (Elem<T>::bytes == 4) sc.load_q(&sh.q[0][0], G);
+    else sc.load_q(static_cast<const T *>(p.q) + (static_cast<int64_t>(b) * p.n_heads + g * G) * D, G);
     if (p.pdl) griddep_wait();                                    // the bounds
     if (p.splits > 1) cluster_wait();
     float big = 0.f;
@@ -650,15 +687,22 @@ __global__ void __launch_bounds__(kClusterThreads, 2) select_cluster_kernel(cons
 //
 // A warp scores one group of pages for p.entries consecutive entries, and reads
 // the bounds again only where the request row changes: the queries of a prompt
-// or a draft share them (256 queries over 1024 pages: 64 us with eight entries
-// per warp, 110 us with one).  Their q rows wait in shared memory.
+// or a draft share them, and 8 / G of them share a product's columns.  Their q
+// rows wait in shared memory.  256 queries of one prompt over 1024 pages: 110 us
+// entry by entry, 52 with the bounds shared, 38 with the columns shared.
 constexpr int kScoreWarps = 4;
-constexpr int kMaxEntries = 8;
+constexpr int kMaxEntries = 16;
+// Entries whose q rows take 32 KB at most.
+template <typename T, int D, int G>
+constexpr int max_entries() {
+    return 32768 / (G * D * Elem<T>::bytes) < kMaxEntries ? 32768 / (G * D * Elem<T>::bytes) : kMaxEntries;
+}
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kScoreWarps * 32) score_pages_kernel(const SelectParams p) {
-    __shared__ __align__(16) T q[kMaxEntries][G * D];
-    __shared__ int rows[kMaxEntries], pages[kMaxEntries];
+    constexpr int kEntries = max_entries<T, D, G>();              // p.entries at most
+    __shared__ __align__(16) T q[kEntries][G * D];
+    __shared__ int rows[kEntries], pages[kEntries];
     griddep_launch();
     const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b0 = static_cast<int>(blockIdx.z) * p.entries, entries = min(p.entries, p.batch - b0);
@@ -673,25 +717,31 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_pages_kernel(const Sel
     Scorer<T, D, G> sc;
     int held_row = -1, held_pages = 0;       // what sc holds the bounds of
     float big = 0.f;
-    for (int e = 0; e < entries; ++e) {
-        const int row = rows[e], n = pages[e];
+    for (int e = 0, count; e < entries; e += count) {
+        // entries e .. e + count - 1 are of one request
+        const int row = rows[e];
+        int n = pages[e];
+        for (count = 1; count < Scorer<T, D, G>::kSets && e + count < entries && rows[e + count] == row; ++count) n = max(n, pages[e + count]);
         if (n <= p.top_k || first >= n) continue;
-        sc.load_q(q[e]);
+        sc.load_q(q[e], count * G);
         if (Elem<T>::bytes == 4 || row != held_row || (n > held_pages && first + kScoreGroup > held_pages)) {
             sc.load(p, g, static_cast<int>(page_at(p, row, min(first + (lane & 15), n - 1))));
             big = sc.largest();
             held_row = row;
             held_pages = n;
         }
-        const float s = sc.score();
         const int64_t unit = static_cast<int64_t>(b0 + e) * p.n_kv_heads + g;
-        if (lane < 16) p.keys[unit * p.page_cap + first + lane] = key32(s);
-        if (lane == 0) p.group_max[unit * (p.page_cap / kScoreGroup) + group] = big;
+        uint32_t *keys = p.keys + unit * p.page_cap + first;      // page_cap is whole groups
+        const int64_t stride = static_cast<int64_t>(p.n_kv_heads) * p.page_cap;
+        sc.score_sets([&](int set, int page, float s) {
+            if (set < count) keys[set * stride + page] = key32(s);
+        });
+        if (lane < count) p.group_max[(unit + static_cast<int64_t>(lane) * p.n_kv_heads) * (p.page_cap / kScoreGroup) + group] = big;
     }
 }
 
 template <typename T, int D, int G, int NT>
-__global__ void __launch_bounds__(NT) select_pages_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 6 : 2) select_pages_kernel(const SelectParams p) {
     __shared__ SelShared<D, G, NT> sh;
     extern __shared__ __align__(16) unsigned char staged[];
     griddep_launch();
@@ -734,7 +784,8 @@ cudaError_t allow_smem(K kernel, std::atomic<uint64_t> &done, size_t bytes) {
 }
 
 template <typename T, int D, int G>
-cudaError_t launch_select(const SelectParams &p, cudaStream_t s) {
+cudaError_t launch_select(SelectParams p, cudaStream_t s) {
+    if (p.entries > max_entries<T, D, G>()) p.entries = max_entries<T, D, G>();
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -465,6 +465,40 @@ def test_select_pages_queries_of_one_request():
     check_select(*select_case(rng, "bf16", 8, 2, 128, 4, 500 + np.arange(37), 12, 1, 1, shared_row=True))
 
 
+@pytest.mark.parametrize("dtype,group,kv,d", [("bf16", 1, 8, 64), ("bf16", 2, 8, 128), ("bf16", 4, 8, 128), ("bf16", 8, 8, 128), ("f32", 8, 8, 128), ("f32", 1, 8, 64)])
+def test_select_pages_of_many_entries(dtype, group, kv, d):
+    """Large batches, whose scores have a launch of their own: runs of entries
+    of one request of any length (queries of prompts whose last pages differ),
+    short and empty contexts among them."""
+    rng = np.random.default_rng(group * d)
+    batch, ps = 700, 4
+    cache, pg, q, (table, rows, lens) = select_case(rng, dtype, group * kv, kv, d, ps, rng.integers(0, 60 * ps, batch), 7, 1, 1)
+    at = 0
+    while at < batch:
+        n = int(rng.integers(1, 40))
+        row = int(rng.integers(0, batch))
+        rows[at:at + n] = row
+        lens[at:at + n] = np.minimum(60 * ps - 1, int(rng.integers(0, 50 * ps)) + np.arange(n))[:len(lens[at:at + n])]
+        at += n + int(rng.integers(0, 5))
+    perm = rng.permutation(pg.page_bounds.shape[1])[:table.shape[1]]
+    table[:, :] = perm[None]                             # every row holds pages: its own order of the same ones
+    for r in range(table.shape[0]):
+        table[r] = np.roll(perm, r)
+    cache.req_pool_indices, cache.seq_lens, cache.max_len = dev(rows), dev(lens), 60 * ps
+    pg = dataclasses.replace(pg, req_to_page=dev(table))
+    check_select(cache, pg, q, (table, rows, lens))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_select_pages_of_a_batch_of_long_contexts(dtype):
+    """Two launches with more pages than a small batch's, ties among them."""
+    rng = np.random.default_rng(29)
+    lens = np.array([5000, 4100, 10, 4999, 3000, 0, 4500, 2500])
+    kind = bounds_of(rng, 40, 8, 64, dtype)[0]
+    check_select(*select_case(rng, dtype, 16, 8, 64, 1, lens, 100, 1, 1))
+    check_select(*select_case(rng, dtype, 16, 8, 64, 1, lens, 100, 1, 1, bounds=lambda n: kind[torch.from_numpy(rng.integers(0, 40, n)).cuda()][None].contiguous()))
+
+
 def test_select_pages_reports_bad_device_data():
     rng = np.random.default_rng(28)
     cache, pg, q, (table, rows, lens) = select_case(rng, "bf16", 8, 2, 64, 4, np.array([200, 180, 90]), 6)
