@@ -3,16 +3,17 @@
 pkv_paged_decode_selected, pkv_sparse_decode_step).
 
 Argument marshalling only, like ops.py.  These calls run once per layer and
-step, so the shapes are checked with plain comparisons and the descriptors are
-filled in one constructor call.  They work on the device of the cache, whatever
-the current one is; outputs that are not given are allocated for the stream
-that the kernels run on.
+step, and their kernels take less time than a few dozen Python calls, so a
+tensor is checked by plain comparisons and a descriptor is packed in one call.
+They work on the device of the cache, whatever the current one is; outputs that
+are not given are allocated for the stream that the kernels run on.
 """
 from __future__ import annotations
 
 import ctypes
 import dataclasses
 import math
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -20,6 +21,34 @@ import torch
 from . import _lib
 from ._lib import PkvKVCache, PkvPages, PkvTables, check
 from .ops import KVCache, Workspace, _DTYPES, _need
+
+# The descriptors as bytes, field by field as in _lib (native sizes and alignment).
+_pack_cache = struct.Struct("PPiiiiqPiiPPPPPii")
+_pack_pages = struct.Struct("PPiiiii")
+_pack_tables = struct.Struct("PPiiPPPiiPPPPP")
+for _s, _c in ((_pack_cache, PkvKVCache), (_pack_pages, PkvPages), (_pack_tables, PkvTables)):
+    assert _s.size <= ctypes.sizeof(_c) < _s.size + 8       # but for padding at the end
+_i32, _f32 = ctypes.c_int32, ctypes.c_float
+_vp, _st = ctypes.c_void_p, ctypes.c_char_p                 # _st: a packed descriptor
+# name -> argtypes, with the descriptors as bytes
+_ARGS = {
+    "pkv_build_tables": [_st, _st, _vp],
+    "pkv_page_bounds": [_st, _i32, _st, _i32, _vp],
+    "pkv_select_pages": [_st, _i32, _st, _vp, _i32, _vp, _vp, _vp, _vp],
+    "pkv_paged_decode_selected": [_st, _i32, _st, _vp, _vp, _vp, _vp, _i32, _f32, _vp],
+    "pkv_sparse_decode_step": [_st, _i32, _st, _vp, _vp, _i32, _vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp],
+}
+_functions = {}
+
+
+def _function(name: str):
+    """The library's function, loaded at its first call."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _lib.load()[name]              # an object of its own beside the library's attribute
+        fn.restype, fn.argtypes = ctypes.c_int, _ARGS[name]
+        _functions[name] = fn
+    return fn
 
 
 def _ptr(t: torch.Tensor, name: str, dtype, index: int) -> int:
@@ -30,10 +59,10 @@ def _ptr(t: torch.Tensor, name: str, dtype, index: int) -> int:
     return _need(t, name, dtype, torch.device("cuda", index))
 
 
-def _i32(t: Optional[torch.Tensor], name: str, index: int, n: int) -> Optional[int]:
-    """The address of an int32 array of n elements; None stays None."""
+def _ints(t: Optional[torch.Tensor], name: str, index: int, n: int) -> int:
+    """The address of an int32 array of n elements; 0 for None."""
     if t is None:
-        return None
+        return 0
     p = _ptr(t, name, torch.int32, index)
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
@@ -64,62 +93,58 @@ class SparsePages:
                              dtype=cache.k_buffer.dtype, device=cache.device)
         return cls(bounds, req_to_page, page_size, top_k, n_first, n_last)
 
-    def c_struct(self, cache: KVCache) -> PkvPages:
-        kb, t, bounds, ps = cache.k_buffer, self.req_to_page, self.page_bounds, self.page_size
-        index = kb.get_device()
-        if t.dim() != 2:
-            raise ValueError("req_to_page must be [num_reqs, max_pages]")
-        if ps < 1:
-            raise ValueError("page_size must be positive")
-        if bounds is not None:
-            n_layers, size, n_kv_heads, head_dim = kb.shape
-            if bounds.shape != (n_layers, size // ps, n_kv_heads, 2, head_dim):
-                raise ValueError("page_bounds must be [n_layers, size // page_size, n_kv_heads, 2, head_dim]")
-            bounds = _ptr(bounds, "page_bounds", kb.dtype, index)
-        return PkvPages(bounds, _ptr(t, "req_to_page", torch.int32, index), t.shape[1], ps, self.top_k, self.n_first,
-                        self.n_last)
 
-
-def _cache(cache: KVCache, table: torch.Tensor, table_ptr: int, max_ctx_len: int, n_new: int,
-           decode: bool) -> Tuple[PkvKVCache, int]:
-    """The descriptor of a cache whose request rows are those of `table`
-    (already checked, at table_ptr)."""
+def _describe(cache: KVCache, table: torch.Tensor, max_ctx_len: int, n_new: int, decode: bool):
+    """The packed descriptor of a cache whose request rows are those of
+    `table`: (bytes, address of the table, device index, storage dtype, shape of
+    the pool, batch)."""
     kb, vb, rows, lens = cache.k_buffer, cache.v_buffer, cache.req_pool_indices, cache.seq_lens
-    dtype = kb.dtype
+    dtype, shape, index = kb.dtype, kb.shape, kb.get_device()
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"unsupported storage dtype {dtype}")
-    shape = kb.shape
     if len(shape) != 4 or vb.shape != shape:
         raise ValueError("k_buffer/v_buffer must both be [n_layers, size, n_kv_heads, head_dim]")
-    index = kb.get_device()
     if index < 0:
         raise ValueError("k_buffer must be a CUDA tensor (there is no CPU path)")
-    batch = rows.numel()
-    if lens is not None:
-        lens = _i32(lens, "seq_lens", index, batch)
-    elif decode:
+    if table.dim() != 2:
+        raise ValueError("req_to_page must be [num_reqs, max_pages]")
+    if lens is None and decode:
         raise ValueError("seq_lens is needed")
+    batch = rows.numel()
+    loc = 0
+    if n_new:
+        loc = _ptr(cache.out_cache_loc, "out_cache_loc", torch.int32, index)
+        if cache.out_cache_loc.numel() < n_new:     # it may be longer than what is written
+            raise ValueError(f"out_cache_loc must have {n_new} elements at least, got {cache.out_cache_loc.numel()}")
     n_layers, size, n_kv_heads, head_dim = shape
-    return PkvKVCache(
+    at = _ptr(table, "req_to_page", torch.int32, index)
+    c = _pack_cache.pack(
         _ptr(kb, "k_buffer", dtype, index), _ptr(vb, "v_buffer", dtype, index), code, n_layers, n_kv_heads,
-        head_dim, size, table_ptr, table.shape[0], max_ctx_len,
-        _ptr(rows, "req_pool_indices", torch.int32, index), lens, None, None,
-        _slots(cache.out_cache_loc, index, n_new) if n_new else None, batch, int(cache.max_len)), index
+        head_dim, size, at, table.shape[0], max_ctx_len, _ptr(rows, "req_pool_indices", torch.int32, index),
+        _ints(lens, "seq_lens", index, batch), 0, 0, loc, batch, cache.max_len)
+    return c, at, index, dtype, shape, batch
 
 
-def _slots(loc: Optional[torch.Tensor], index: int, n_new: int) -> int:
-    """The address of out_cache_loc, which may be longer than what is written."""
-    p = _ptr(loc, "out_cache_loc", torch.int32, index)
-    if loc.numel() < n_new:
-        raise ValueError(f"out_cache_loc must have {n_new} elements at least, got {loc.numel()}")
-    return p
+def _describe_pages(pages: SparsePages, at: int, index: int, dtype, shape) -> bytes:
+    """The packed descriptor of pages whose table is at `at`."""
+    bounds, ps = pages.page_bounds, pages.page_size
+    if ps < 1:
+        raise ValueError("page_size must be positive")
+    if bounds is None:
+        p = 0
+    else:
+        n_layers, size, n_kv_heads, head_dim = shape
+        if bounds.shape != (n_layers, size // ps, n_kv_heads, 2, head_dim):
+            raise ValueError("page_bounds must be [n_layers, size // page_size, n_kv_heads, 2, head_dim]")
+        p = _ptr(bounds, "page_bounds", dtype, index)
+    return _pack_pages.pack(p, at, pages.req_to_page.shape[1], ps, pages.top_k, pages.n_first, pages.n_last)
 
 
-def _rows(t: torch.Tensor, name: str, c: PkvKVCache, dtype, index: int, n: int, heads: int) -> int:
-    """The address of [n, heads, head_dim] rows of the cache's dtype."""
-    if t.shape != (n, heads, c.head_dim):
-        raise ValueError(f"{name} must be [{n}, {heads}, {c.head_dim}], got {list(t.shape)}")
+def _rows(t: torch.Tensor, name: str, dtype, index: int, n: int, heads: int, head_dim: int) -> int:
+    """The address of [n, heads, head_dim] rows."""
+    if t.shape != (n, heads, head_dim):
+        raise ValueError(f"{name} must be [{n}, {heads}, {head_dim}], got {list(t.shape)}")
     return _ptr(t, name, dtype, index)
 
 
@@ -127,11 +152,6 @@ def _heads(q: torch.Tensor) -> int:
     if q.dim() != 3:
         raise ValueError(f"q must be [batch, n_heads, head_dim], got {list(q.shape)}")
     return q.shape[1]
-
-
-def _lists(sel: torch.Tensor, counts: torch.Tensor, c: PkvKVCache, top_k: int, index: int) -> Tuple[int, int]:
-    n = c.batch * c.n_kv_heads
-    return _i32(sel, "sel", index, n * top_k), _i32(counts, "sel_counts", index, n)
 
 
 def _workspace(ws: Optional[Workspace], index: int):
@@ -150,7 +170,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 def _call(name: str, index: int, stream, *args) -> None:
     """Calls the library's `name` on the cache's device with the stream's
     handle; None is the device's current stream."""
-    fn = getattr(_lib._lib or _lib.load(), name)
+    fn = _functions.get(name) or _function(name)
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == index:
         status = fn(*args, handle)
@@ -181,22 +201,21 @@ def build_tables(cache: KVCache, req_to_page: torch.Tensor, page_size: int, free
     tokens' entries of cache.req_to_token unless token_table is False.  Tokens
     beyond out_cache_loc's length are an error on the device; entries of
     out_cache_loc behind the last new token stay as they are."""
-    if req_to_page.dim() != 2 or cache.req_to_token.dim() != 2:
-        raise ValueError("req_to_page must be [num_reqs, max_pages], req_to_token [num_reqs, max_ctx_len]")
-    if token_table and cache.req_to_token.shape[0] != req_to_page.shape[0]:
-        raise ValueError("req_to_page and req_to_token must have the same rows")
-    loc = cache.out_cache_loc
+    tokens, loc = cache.req_to_token, cache.out_cache_loc
+    if tokens.dim() != 2:
+        raise ValueError("req_to_token must be [num_reqs, max_ctx_len]")
     n_new = 0 if loc is None else loc.numel()
-    c, index = _cache(cache, req_to_page, _ptr(req_to_page, "req_to_page", torch.int32, cache.k_buffer.get_device()), cache.req_to_token.shape[1], n_new, True)
-    t = PkvTables(
-        _i32(q_lens, "q_lens", index, c.batch), c.req_to_token, req_to_page.shape[1], int(page_size),
-        _ptr(free_pages, "free_pages", torch.int32, index), _i32(free_start, "free_start", index, 1),
-        _i32(free_end, "free_end", index, 1), free_pages.numel(), n_new,
-        _i32(cache.kv_indptr, "kv_indptr", index, c.batch + 1),
-        _i32(cache.qo_indptr, "qo_indptr", index, c.batch + 1),
-        _i32(positions, "positions", index, n_new), c.out_cache_loc,
-        _ptr(cache.req_to_token, "req_to_token", torch.int32, index) if token_table else None)
-    _call("pkv_build_tables", index, stream, ctypes.byref(c), ctypes.byref(t))
+    c, at, index, _, _, batch = _describe(cache, req_to_page, tokens.shape[1], n_new, True)
+    if token_table and tokens.shape[0] != req_to_page.shape[0]:
+        raise ValueError("req_to_page and req_to_token must have the same rows")
+    t = _pack_tables.pack(
+        _ints(q_lens, "q_lens", index, batch), at, req_to_page.shape[1], page_size,
+        _ptr(free_pages, "free_pages", torch.int32, index), _ints(free_start, "free_start", index, 1),
+        _ints(free_end, "free_end", index, 1), free_pages.numel(), n_new,
+        _ints(cache.kv_indptr, "kv_indptr", index, batch + 1), _ints(cache.qo_indptr, "qo_indptr", index, batch + 1),
+        _ints(positions, "positions", index, n_new), loc.data_ptr() if n_new else 0,
+        _ptr(tokens, "req_to_token", torch.int32, index) if token_table else 0)
+    _call("pkv_build_tables", index, stream, c, t)
 
 
 def page_bounds(cache: KVCache, layer_id: int, pages: SparsePages, n_new: Optional[int] = None,
@@ -207,9 +226,8 @@ def page_bounds(cache: KVCache, layer_id: int, pages: SparsePages, n_new: Option
         raise ValueError("out_cache_loc and page_bounds are needed")
     if n_new is None:
         n_new = cache.out_cache_loc.numel()
-    pg = pages.c_struct(cache)
-    c, index = _cache(cache, pages.req_to_page, pg.req_to_page, 0, n_new, False)
-    _call("pkv_page_bounds", index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg), n_new)
+    c, at, index, dtype, shape, _ = _describe(cache, pages.req_to_page, 0, n_new, False)
+    _call("pkv_page_bounds", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape), n_new)
 
 
 def select_workspace_bytes(batch: int, n_kv_heads: int, max_len: int, page_size: int) -> int:
@@ -223,15 +241,15 @@ def select_pages(cache: KVCache, layer_id: int, pages: SparsePages, q: torch.Ten
     """The pages that each query of q [batch, n_heads, head_dim] attends to:
     sel int32 [batch, n_kv_heads, top_k] (logical pages, ascending, then -1)
     and sel_counts int32 [batch, n_kv_heads]."""
-    pg = pages.c_struct(cache)
-    c, index = _cache(cache, pages.req_to_page, pg.req_to_page, 0, 0, True)
+    c, at, index, dtype, shape, batch = _describe(cache, pages.req_to_page, 0, 0, True)
+    heads, kv, top_k = _heads(q), shape[2], pages.top_k
     if sel is None:
-        sel = _empty((c.batch, c.n_kv_heads, pages.top_k), torch.int32, cache.k_buffer.device, stream)
+        sel = _empty((batch, kv, top_k), torch.int32, cache.k_buffer.device, stream)
     if sel_counts is None:
-        sel_counts = _empty((c.batch, c.n_kv_heads), torch.int32, cache.k_buffer.device, stream)
-    _call("pkv_select_pages", index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
-            _rows(q, "q", c, cache.k_buffer.dtype, index, c.batch, _heads(q)), q.shape[1],
-            *_lists(sel, sel_counts, c, pages.top_k, index), _workspace(workspace, index))
+        sel_counts = _empty((batch, kv), torch.int32, cache.k_buffer.device, stream)
+    _call("pkv_select_pages", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape),
+          _rows(q, "q", dtype, index, batch, heads, shape[3]), heads, _ints(sel, "sel", index, batch * kv * top_k),
+          _ints(sel_counts, "sel_counts", index, batch * kv), _workspace(workspace, index))
     return sel, sel_counts
 
 
@@ -241,16 +259,14 @@ def paged_decode_selected(cache: KVCache, layer_id: int, pages: SparsePages, q: 
                           stream=None) -> torch.Tensor:
     """paged_decode over the positions of the selected pages only; q, o:
     [batch, n_heads, head_dim], sel and sel_counts as select_pages gives them."""
-    pg = pages.c_struct(cache)
-    c, index = _cache(cache, pages.req_to_page, pg.req_to_page, 0, 0, True)
-    dtype, heads = cache.k_buffer.dtype, _heads(q)
+    c, at, index, dtype, shape, batch = _describe(cache, pages.req_to_page, 0, 0, True)
+    heads, kv, head_dim = _heads(q), shape[2], shape[3]
     if o is None:
-        o = _empty(q.shape, q.dtype, cache.k_buffer.device, stream)
-    scale = 1.0 / math.sqrt(c.head_dim) if sm_scale is None else float(sm_scale)
-    _call("pkv_paged_decode_selected", index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
-            *_lists(sel, sel_counts, c, pages.top_k, index),
-            _rows(q, "q", c, dtype, index, c.batch, heads), _rows(o, "o", c, dtype, index, c.batch, heads),
-            heads, scale)
+        o = _empty(q.shape, dtype, cache.k_buffer.device, stream)
+    _call("pkv_paged_decode_selected", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape),
+          _ints(sel, "sel", index, batch * kv * pages.top_k), _ints(sel_counts, "sel_counts", index, batch * kv),
+          _rows(q, "q", dtype, index, batch, heads, head_dim), _rows(o, "o", dtype, index, batch, heads, head_dim),
+          heads, 1.0 / math.sqrt(head_dim) if sm_scale is None else sm_scale)
     return o
 
 
@@ -261,19 +277,20 @@ def sparse_decode_step(cache: KVCache, layer_id: int, pages: SparsePages, k_new:
                        stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """kv_write of k_new / v_new at cache.out_cache_loc, page_bounds,
     select_pages and paged_decode_selected as one call: (o, sel, sel_counts)."""
-    n_new, heads, dtype = k_new.shape[0], _heads(q), cache.k_buffer.dtype
-    pg = pages.c_struct(cache)
-    c, index = _cache(cache, pages.req_to_page, pg.req_to_page, 0, n_new, True)
+    n_new, heads = k_new.shape[0], _heads(q)
+    c, at, index, dtype, shape, batch = _describe(cache, pages.req_to_page, 0, n_new, True)
+    kv, head_dim, top_k = shape[2], shape[3], pages.top_k
     if o is None:
-        o = _empty(q.shape, q.dtype, cache.k_buffer.device, stream)
+        o = _empty(q.shape, dtype, cache.k_buffer.device, stream)
     if sel is None:
-        sel = _empty((c.batch, c.n_kv_heads, pages.top_k), torch.int32, cache.k_buffer.device, stream)
+        sel = _empty((batch, kv, top_k), torch.int32, cache.k_buffer.device, stream)
     if sel_counts is None:
-        sel_counts = _empty((c.batch, c.n_kv_heads), torch.int32, cache.k_buffer.device, stream)
-    scale = 1.0 / math.sqrt(c.head_dim) if sm_scale is None else float(sm_scale)
-    _call("pkv_sparse_decode_step", index, stream, ctypes.byref(c), layer_id, ctypes.byref(pg),
-            _rows(k_new, "k_new", c, dtype, index, n_new, c.n_kv_heads),
-            _rows(v_new, "v_new", c, dtype, index, n_new, c.n_kv_heads), n_new,
-            _rows(q, "q", c, dtype, index, c.batch, heads), _rows(o, "o", c, dtype, index, c.batch, heads),
-            heads, scale, *_lists(sel, sel_counts, c, pages.top_k, index), _workspace(workspace, index))
+        sel_counts = _empty((batch, kv), torch.int32, cache.k_buffer.device, stream)
+    _call("pkv_sparse_decode_step", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape),
+          _rows(k_new, "k_new", dtype, index, n_new, kv, head_dim),
+          _rows(v_new, "v_new", dtype, index, n_new, kv, head_dim), n_new,
+          _rows(q, "q", dtype, index, batch, heads, head_dim), _rows(o, "o", dtype, index, batch, heads, head_dim),
+          heads, 1.0 / math.sqrt(head_dim) if sm_scale is None else sm_scale,
+          _ints(sel, "sel", index, batch * kv * top_k), _ints(sel_counts, "sel_counts", index, batch * kv),
+          _workspace(workspace, index))
     return o, sel, sel_counts
