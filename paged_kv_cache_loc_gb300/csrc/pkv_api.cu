@@ -707,8 +707,8 @@ int bounds_prepare(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, 
     p.row_chunks = c->n_kv_heads * c->head_dim * elem / 16;
     p.head_chunks = c->head_dim * elem / 16;
     p.dtype = c->dtype;
-    // about eight CTAs per SM; one token per CTA while the batch is small
-    const int64_t blocks = 8LL * (di.sms > 0 ? di.sms : 1);
+    // about twelve CTAs per SM; one token per CTA while the batch is small
+    const int64_t blocks = 12LL * (di.sms > 0 ? di.sms : 1);
     const int64_t per = (n_new + blocks - 1) / blocks;
     p.block_tokens = static_cast<int32_t>(per < 1 ? 1 : per > 64 ? 64 : per);
     p.err = di.err;
@@ -886,8 +886,8 @@ int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pag
     DeviceInfo di;
     rc = device_info(&di);
     if (rc) return rc;
-    rc = check_visible({c->k_buffer, c->v_buffer, pg->page_bounds, pg->req_to_page, c->req_pool_indices, c->seq_lens,
-                        q, o, sel, sel_counts, ws ? ws->base : nullptr});
+    rc = check_visible({no_write ? c->k_buffer : nullptr, no_write ? c->v_buffer : nullptr, pg->page_bounds,   // else checked
+                        pg->req_to_page, c->req_pool_indices, c->seq_lens, q, o, sel, sel_counts, ws ? ws->base : nullptr});
     if (rc) return rc;
     pkv::BoundsParams bp;
     bounds_prepare(c, layer_id, pg, n_new, di, k_new, v_new, &bp);

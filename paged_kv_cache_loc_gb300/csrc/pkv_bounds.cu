@@ -24,7 +24,7 @@ constexpr int kRowsAhead = 8;
 // not from the pool, so nothing waits for another CTA's copy, and a step has
 // one launch less (2.6 + 3.3 us of kernels apart for one token).
 template <typename T, bool kWrite>
-__global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kBoundsThreads, 8) page_bounds_kernel(const BoundsParams p) {
     griddep_launch();
     const int chunk = blockIdx.y * kBoundsThreads + threadIdx.x;
     const int i_end = min(p.n_new, (static_cast<int>(blockIdx.x) + 1) * p.block_tokens);
@@ -52,8 +52,20 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
             }
         }
     }
+    // lane l of a warp holds the slot of token base + l: one load for a page or two
+    const int lane = threadIdx.x & 31;
+    int base = 0, window = 0;
+    const auto look = [&](int from) {
+        base = from;
+        window = __ldg(p.out_cache_loc + max(0, min(from + lane, p.n_new - 1)));
+    };
+    const auto slot_of = [&](int i) {
+        if (i < base || i >= base + 32) look(i);
+        return __shfl_sync(0xffffffffu, window, i - base);
+    };
+    look(blockIdx.x * p.block_tokens - 1);
     for (int i = blockIdx.x * p.block_tokens; i < i_end;) {
-        int loc = __ldg(p.out_cache_loc + i);
+        int loc = slot_of(i);
         if (!valid(loc)) {
             if (chunk == 0) record_error(p.err, loc);
             ++i;
@@ -63,9 +75,9 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
         int off = loc - page * p.page_size;
         bool begins = off == 0;
         if (!begins) {
-            int j = i - 1;
-            while (j >= 0 && !valid(__ldg(p.out_cache_loc + j))) --j;
-            begins = j < 0 || __ldg(p.out_cache_loc + j) != loc - 1;
+            int j = i - 1, before = 0;
+            while (j >= 0 && !valid(before = slot_of(j))) --j;
+            begins = j < 0 || before != loc - 1;
         }
         uint4 *dst = static_cast<uint4 *>(p.page_bounds) + (p.layer_page0 + page) * p.row_chunks * 2 +
                      (chunk / p.head_chunks) * p.head_chunks * 2 + chunk % p.head_chunks;
@@ -81,13 +93,17 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
             // tokens i .. i + n - 1 are in consecutive slots of the page
             const int most = min(p.n_new - i, p.page_size - off);
             int n = 1;
-            for (;;) {
-                const int at = n + static_cast<int>(threadIdx.x & 31);
-                const bool next = at < most && __ldg(p.out_cache_loc + i + at) == loc + at;
-                const unsigned breaks = __ballot_sync(0xffffffffu, !next);
-                n += breaks ? __ffs(breaks) - 1 : 32;
-                if (breaks) break;
+            while (n < most) {
+                if (i + n < base || i + n >= base + 32) look(i + n);
+                const int k = base + lane - i;                    // this lane's token, counted from i
+                const unsigned breaks = __ballot_sync(0xffffffffu, k >= n && (k >= most || window != loc + k));
+                if (breaks) {
+                    n = base + __ffs(breaks) - 1 - i;
+                    break;
+                }
+                n = base + 32 - i;
             }
+            n = min(n, most);
             if (mine) {
                 const uint4 *row = (kWrite ? static_cast<const uint4 *>(p.keys) + static_cast<int64_t>(i) * p.row_chunks
                                            : static_cast<const uint4 *>(p.k_buffer) + (p.layer_row0 + loc) * p.row_chunks) + chunk;
@@ -96,18 +112,20 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
                 for (int k = 0; k < n; k += kRowsAhead) {
                     uint4 x[kRowsAhead];
 #pragma unroll
-                    for (int u = 0; u < kRowsAhead; ++u) x[u] = row[static_cast<int64_t>(min(k + u, n - 1)) * p.row_chunks];
+                    for (int u = 0; u < kRowsAhead; ++u)
+                        if (k + u < n) x[u] = row[static_cast<int64_t>(k + u) * p.row_chunks];
 #pragma unroll
-                    for (int u = 0; u < kRowsAhead; ++u) widen_bounds<T>(lo, hi, x[u], x[u]);
+                    for (int u = 0; u < kRowsAhead; ++u)
+                        if (k + u < n) widen_bounds<T>(lo, hi, x[u], x[u]);
                 }
             }
             i += n;
             off += n;
             loc += n;
             if (!begins || off == p.page_size) break;
-            int j = i;
-            while (j < p.n_new && !valid(__ldg(p.out_cache_loc + j))) ++j;
-            if (j == i || j >= p.n_new || __ldg(p.out_cache_loc + j) != loc) break;
+            int j = i, after = 0;
+            while (j < p.n_new && !valid(after = slot_of(j))) ++j;
+            if (j == i || j >= p.n_new || after != loc) break;
             if (chunk == 0)
                 for (int x = i; x < j; ++x) record_error(p.err, __ldg(p.out_cache_loc + x));
             i = j;
