@@ -719,7 +719,8 @@ int check_bounds(const pkv_kvcache *c, const pkv_pages *pg, int32_t n_new) {
     if (n_new < 0) return PKV_ERR_ARG;
     if ((c->head_dim * elem_bytes(c->dtype)) % 16) return PKV_ERR_ARG;
     if (n_new > 0 && (!c->out_cache_loc || !pg->page_bounds || !aligned16(pg->page_bounds))) return PKV_ERR_ARG;
-    if (static_cast<int64_t>(c->n_kv_heads) * c->head_dim * elem_bytes(c->dtype) / 16 > 65535 * 128) return PKV_ERR_ARG;
+    const int64_t row_chunks = static_cast<int64_t>(c->n_kv_heads) * c->head_dim * elem_bytes(c->dtype) / 16;
+    if (row_chunks > 65535 * 128 || 2 * static_cast<int64_t>(n_new) * row_chunks >= INT32_MAX) return PKV_ERR_ARG;   // as the write
     return PKV_OK;
 }
 

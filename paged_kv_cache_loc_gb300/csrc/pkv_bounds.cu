@@ -29,6 +29,18 @@ __global__ void __launch_bounds__(kBoundsThreads, 8) page_bounds_kernel(const Bo
     const int chunk = blockIdx.y * kBoundsThreads + threadIdx.x;
     const int i_end = min(p.n_new, (static_cast<int>(blockIdx.x) + 1) * p.block_tokens);
     const auto valid = [&](int slot) { return static_cast<unsigned>(slot) < static_cast<unsigned long long>(p.size); };
+    // lane l of a warp holds the slot of token base + l: one load for a page or two
+    const int lane = threadIdx.x & 31;
+    int base = 0, window = 0;
+    const auto look = [&](int from) {
+        base = from;
+        window = __ldg(p.out_cache_loc + max(0, min(from + lane, p.n_new - 1)));
+    };
+    const auto slot_of = [&](int i) {
+        if (i < base || i >= base + 32) look(i);
+        return __shfl_sync(0xffffffffu, window, i - base);
+    };
+    look(blockIdx.x * p.block_tokens - 1);
     if constexpr (kWrite) {
         constexpr int kAhead = 4;
         if (chunk < p.row_chunks) {
@@ -52,18 +64,6 @@ __global__ void __launch_bounds__(kBoundsThreads, 8) page_bounds_kernel(const Bo
             }
         }
     }
-    // lane l of a warp holds the slot of token base + l: one load for a page or two
-    const int lane = threadIdx.x & 31;
-    int base = 0, window = 0;
-    const auto look = [&](int from) {
-        base = from;
-        window = __ldg(p.out_cache_loc + max(0, min(from + lane, p.n_new - 1)));
-    };
-    const auto slot_of = [&](int i) {
-        if (i < base || i >= base + 32) look(i);
-        return __shfl_sync(0xffffffffu, window, i - base);
-    };
-    look(blockIdx.x * p.block_tokens - 1);
     for (int i = blockIdx.x * p.block_tokens; i < i_end;) {
         int loc = slot_of(i);
         if (!valid(loc)) {

@@ -521,7 +521,7 @@ __device__ __forceinline__ void select_from_keys(const SelectParams &p, SelShare
     klo = __reduce_min_sync(0xffffffffu, sh.lo[lane % (NT / 32)]);
     khi = __reduce_max_sync(0xffffffffu, sh.hi[lane % (NT / 32)]);
     big = __uint_as_float(__reduce_max_sync(0xffffffffu, sh.big[lane % (NT / 32)]));
-    if (norm == 0.f || big == 0.f) {         // every score is 0: the lowest pages
+    if ((norm == 0.f || big == 0.f) && norm < INFINITY && big < INFINITY) {   // every score is 0: the lowest pages
         for (int i = tid; i < keep; i += NT) sel[c0 + i] = c0 + i;
         return;
     }
@@ -625,11 +625,8 @@ __device__ __forceinline__ int begin_entry(const SelectParams &p, SelShared<D, G
 }
 
 // Scores and selection in one launch: a cluster per (kv head, entry), whose
-// warps share the groups of pages and put the scores into the first CTA's
-// shared memory; that CTA selects.  For batches that do not fill the SMs many
-// times over: against scores through memory and a second launch, one request
-// of 32K positions (2048 pages) and 16 of 32K to 128K take less (see the
-// launch rule below).
+// warps share the groups of pages and put the scores' keys into the first CTA's
+// shared memory; that CTA selects.
 constexpr int kClusterThreads = 256;
 
 template <typename T, int D, int G>

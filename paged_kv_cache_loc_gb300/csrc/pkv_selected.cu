@@ -361,7 +361,8 @@ __device__ __forceinline__ int swizzle(int row, int c) { return c ^ ((row & 1) <
 //     output row r of step i stands for channel 8 r + 2 i, row r + 8 for the
 //     next one.
 // P goes in as two bf16 parts (hi + lo, 16 bits together): one part alone would
-// add an error of the size of the output's own rounding.
+// add an error of the size of the output's own rounding.  (A V that is infinite
+// then gives NaN, 0 times infinity, and not infinity.)
 template <int D, int G>
 __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const SelectedParams p) {
     using Sh = MmaShared<D, G>;

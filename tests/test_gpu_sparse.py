@@ -426,6 +426,50 @@ def test_select_pages_zero_queries_and_zero_bounds():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pages", [40, 900])
+def test_select_pages_zero_times_infinity_ranks_first(dtype, pages):
+    """Queries of zeros over bounds of which some are infinite: those scores
+    are NaN, the others zero."""
+    rng = np.random.default_rng(pages)
+    q = torch.zeros(2, 8, 64, dtype=DT[dtype], device="cuda")
+    q[1, 3, 5] = 1.0
+
+    def bounds(n):
+        b = bounds_of(rng, n, 2, 64, dtype)
+        b[0, torch.from_numpy(rng.permutation(n)[:5]).cuda(), 1, 1, 7] = math.inf
+        return b
+    check_select(*select_case(rng, dtype, 8, 2, 64, 1, np.array([pages, pages - 3]), 9, 0, 1, bounds=bounds, q=q))
+
+
+def test_page_bounds_of_rotated_keys():
+    """The bounds are those of what the cache holds: here after the fused
+    rotary write."""
+    rng = np.random.default_rng(48)
+    k, v = pool(rng, 1, 10, 8, 2, 64, "bf16")
+    loc = np.r_[16:24, 40:43, 9:11]
+    cache = pkv.KVCache(k_buffer=k, v_buffer=v, req_to_token=dev(np.zeros((1, 1))), req_pool_indices=dev([0]), out_cache_loc=dev(loc))
+    pg = pkv.SparsePages.for_cache(cache, dev(np.zeros((1, 1))), 8, 4)
+    angle = torch.arange(32, device="cuda")[None] * torch.arange(20, device="cuda")[:, None] * 0.01
+    pkv.rope_kv_write(cache, 0, torch.randn(13, 2, 64, device="cuda").bfloat16(), torch.randn(13, 2, 64, device="cuda").bfloat16(),
+                      torch.stack([angle.cos(), angle.sin()], -1).contiguous(), dev(np.arange(13)))
+    pkv.page_bounds(cache, 0, pg)
+    clean()
+    assert np.array_equal(host(pg.page_bounds)[0], S.page_bounds(np.zeros((10, 2, 2, 64)), host(k)[0][loc], loc, 8))
+
+
+def test_build_tables_of_an_empty_batch():
+    rng = np.random.default_rng(49)
+    t, _, _ = tables_case(rng, np.array([5]), np.array([5]), 4)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    t.cache.req_pool_indices = t.cache.seq_lens = t.q = none
+    t.cache.kv_indptr, t.cache.qo_indptr = (torch.full((1,), 7, dtype=torch.int32, device="cuda") for _ in range(2))
+    t.run()
+    clean()
+    assert int(t.end) == int(t.start) and int(t.cache.kv_indptr) == 0 and int(t.cache.qo_indptr) == 0
+    assert (host(t.cache.out_cache_loc) == -9).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_select_pages_scores_that_32_bits_do_not_tell_apart(dtype):
     """Large channels that cancel, and differences of one small channel far
     below the rounding of the sum: the order is the 64-bit one."""
