@@ -83,19 +83,24 @@ struct Scorer {
         for (int j = 0; j < kOwn; ++j)
             q[j] = r < n ? reinterpret_cast<const uint4 *>(rows)[r * kChunks + t + 4 * j] : make_uint4(0, 0, 0, 0);
     }
-    // Starts the loads of a group; phys: the physical page of its page lane % 16.
-    __device__ __forceinline__ void load(const SelectParams &p, int g, int phys) {
+    const uint4 *r0, *r1;                    // rows r and r + 8 of the group to load
+
+    // The group to load next; phys: the physical page of its page lane % 16.
+    __device__ __forceinline__ void aim(const SelectParams &p, int g, int phys) {
         const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
         const uint4 *base = static_cast<const uint4 *>(p.page_bounds) + t;
-        const uint4 *r0 = base + ((p.layer_page0 + __shfl_sync(0xffffffffu, phys, r)) * p.n_kv_heads + g) * 2 * kChunks;
-        const uint4 *r1 = base + ((p.layer_page0 + __shfl_sync(0xffffffffu, phys, r + 8)) * p.n_kv_heads + g) * 2 * kChunks;
+        r0 = base + ((p.layer_page0 + __shfl_sync(0xffffffffu, phys, r)) * p.n_kv_heads + g) * 2 * kChunks;
+        r1 = base + ((p.layer_page0 + __shfl_sync(0xffffffffu, phys, r + 8)) * p.n_kv_heads + g) * 2 * kChunks;
+    }
+    __device__ __forceinline__ void load_chunk(int j) {
+        l0[j] = __ldg(r0 + 4 * j);
+        l1[j] = __ldg(r1 + 4 * j);
+        h0[j] = __ldg(r0 + kChunks + 4 * j);
+        h1[j] = __ldg(r1 + kChunks + 4 * j);
+    }
+    __device__ __forceinline__ void load() {
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j) {
-            l0[j] = __ldg(r0 + 4 * j);
-            l1[j] = __ldg(r1 + 4 * j);
-            h0[j] = __ldg(r0 + kChunks + 4 * j);
-            h1[j] = __ldg(r1 + kChunks + 4 * j);
-        }
+        for (int j = 0; j < kOwn; ++j) load_chunk(j);
     }
     // The largest |bound| of the group that is loaded (NaN kept).
     __device__ __forceinline__ float largest() const {
@@ -112,7 +117,11 @@ struct Scorer {
         return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big) & 0x7fffffffu));
     }
     // x: pages r (x[0], x[1]) and r + 8 of the group by columns 2t and 2t + 1.
-    __device__ __forceinline__ void products(float (&x)[4]) const {
+    // kNext: each chunk is
+    // loaded again, from the group aimed at, as soon as it is used, so that a
+    // warp's loads never pause.
+    template <bool kNext>
+    __device__ __forceinline__ void products(float (&x)[4]) {
         x[0] = x[1] = x[2] = x[3] = 0.f;
         float y[4] = {}, z[4] = {}, w[4] = {};                    // four chains
 #pragma unroll
@@ -123,15 +132,17 @@ struct Scorer {
             mma_bf16(y, h0[j].x, h1[j].x, h0[j].y, h1[j].y, qp.x, qp.y);
             mma_bf16(z, l0[j].z, l1[j].z, l0[j].w, l1[j].w, qn.z, qn.w);
             mma_bf16(w, h0[j].z, h1[j].z, h0[j].w, h1[j].w, qp.z, qp.w);
+            if (kNext) load_chunk(j);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = (x[i] + z[i]) + (y[i] + w[i]);
     }
     // The score of page lane % 16 of the group for the first G columns.
-    __device__ __forceinline__ float score() const {
+    template <bool kNext>
+    __device__ __forceinline__ float score() {
         const int lane = threadIdx.x & 31, t = lane & 3;
         float x[4];
-        products(x);
+        products<kNext>(x);
         float s0 = -INFINITY, s1 = -INFINITY;
         if (2 * t < G) {
             s0 = x[0];
@@ -154,10 +165,10 @@ struct Scorer {
     // the group, score), each from one lane.
     static constexpr int kSets = 8 / G;
     template <typename Put>
-    __device__ __forceinline__ void score_sets(Put put) const {
+    __device__ __forceinline__ void score_sets(Put put) {
         const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
         float x[4];
-        products(x);
+        products<false>(x);
         if constexpr (G == 1) {
             put(2 * t, r, x[0]);
             put(2 * t, r + 8, x[2]);
@@ -184,16 +195,31 @@ template <int D, int G>
 struct Scorer<float, D, G> {
     static constexpr int kChunks = D / 4;
     const float *q;
-    float s, big;
+    int page;                                // the physical page of page lane % 16 of the group
 
     __device__ __forceinline__ void load_q(const float *rows, int) { q = rows; }
-    __device__ __forceinline__ void load(const SelectParams &p, int g, int phys) {
+    __device__ __forceinline__ void aim(const SelectParams &p, int g, int phys) {
+        page = phys;
+        base = static_cast<const uint4 *>(p.page_bounds) + (p.layer_page0 * p.n_kv_heads + g) * 2 * kChunks + (threadIdx.x & 7);
+        step = static_cast<int64_t>(p.n_kv_heads) * 2 * kChunks;
+    }
+    __device__ __forceinline__ void load() { held = page; }
+    const uint4 *base;
+    int64_t step;
+    int held;
+    float big;
+    // Of the group that was scored last.
+    __device__ __forceinline__ float largest() const {
+        return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big) & 0x7fffffffu));
+    }
+    template <bool kNext>
+    __device__ __forceinline__ float score() {
         const int lane = threadIdx.x & 31, sub = lane & 7;
-        s = big = 0.f;
+        float s = 0.f;
+        big = 0.f;
 #pragma unroll 1
         for (int i = 0; i < kScoreGroup; i += 4) {
-            const uint4 *lo = static_cast<const uint4 *>(p.page_bounds) +
-                              ((p.layer_page0 + __shfl_sync(0xffffffffu, phys, i + (lane >> 3))) * p.n_kv_heads + g) * 2 * kChunks + sub;
+            const uint4 *lo = base + __shfl_sync(0xffffffffu, held, i + (lane >> 3)) * step;
             float x[G];
 #pragma unroll
             for (int h = 0; h < G; ++h) x[h] = 0.f;
@@ -222,14 +248,13 @@ struct Scorer<float, D, G> {
             best = __shfl_sync(0xffffffffu, best, (lane & 3) * 8);
             if ((lane & 15) / 4 == i / 4) s = best;
         }
+        if (kNext) load();
+        return s;
     }
-    __device__ __forceinline__ float largest() const {
-        return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big) & 0x7fffffffu));
-    }
-    __device__ __forceinline__ float score() const { return s; }
     static constexpr int kSets = 1;
     template <typename Put>
-    __device__ __forceinline__ void score_sets(Put put) const {
+    __device__ __forceinline__ void score_sets(Put put) {
+        const float s = score<false>();
         const int lane = threadIdx.x & 31;
         if (lane < 16) put(0, lane, s);
     }
@@ -656,11 +681,22 @@ __global__ void __launch_bounds__(kClusterThreads, 2) select_cluster_kernel(cons
     if (p.pdl) griddep_wait();                                    // the bounds
     if (p.splits > 1) cluster_wait();
     float big = 0.f;
+    if (group < groups) {
+        sc.aim(p, g, at);
+        sc.load();
+    }
     while (group < groups) {
         const int next = lookup(group + step);
-        sc.load(p, g, at);
-        big = max_nan(big, sc.largest());
-        const float s = sc.score();
+        constexpr bool kAfter = Elem<T>::bytes == 4;              // fp32 knows its largest bound after the scores
+        if (!kAfter) big = max_nan(big, sc.largest());
+        float s;
+        if (group + step < groups) {
+            sc.aim(p, g, next);
+            s = sc.template score<true>();
+        } else {
+            s = sc.template score<false>();
+        }
+        if (kAfter) big = max_nan(big, sc.largest());
         if (lane < 16) {
             const int page = group * kScoreGroup + lane;
             st_cluster(cluster_addr(keys + page, 0), key32(s));
@@ -721,9 +757,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_pages_kernel(const Sel
         for (count = 1; count < Scorer<T, D, G>::kSets && e + count < entries && rows[e + count] == row; ++count) n = max(n, pages[e + count]);
         if (n <= p.top_k || first >= n) continue;
         sc.load_q(q[e], count * G);
-        if (Elem<T>::bytes == 4 || row != held_row || (n > held_pages && first + kScoreGroup > held_pages)) {
-            sc.load(p, g, static_cast<int>(page_at(p, row, min(first + (lane & 15), n - 1))));
-            big = sc.largest();
+        constexpr bool kAfter = Elem<T>::bytes == 4;              // fp32 knows its largest bound after the scores
+        if (row != held_row || (n > held_pages && first + kScoreGroup > held_pages)) {
+            sc.aim(p, g, static_cast<int>(page_at(p, row, min(first + (lane & 15), n - 1))));
+            sc.load();
+            if (!kAfter) big = sc.largest();
             held_row = row;
             held_pages = n;
         }
@@ -733,6 +771,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_pages_kernel(const Sel
         sc.score_sets([&](int set, int page, float s) {
             if (set < count) keys[set * stride + page] = key32(s);
         });
+        if (kAfter) big = sc.largest();
         if (lane < count) p.group_max[(unit + static_cast<int64_t>(lane) * p.n_kv_heads) * (p.page_cap / kScoreGroup) + group] = big;
     }
 }
