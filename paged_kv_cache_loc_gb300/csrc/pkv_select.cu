@@ -14,7 +14,8 @@
 // whose last two factors bound sum |terms|.  kScoreEps = 2^-16: a chain of four
 // 16-term tensor-core products adds 17 numbers at a time, each off by 2^-23 of
 // the largest at most when 24 bits are kept of what is aligned to it, 68 2^-23 <
-// 2^-16.9 in all (fp32 units: 16 products and 3 additions a lane, less).  With
+// 2^-16.9 in all (fp32 units: 16 products and 3 additions a lane, less); the
+// largest seen on this chip is 2^-20.6, on terms of very unlike sizes.  With
 // T the 32-bit score of rank
 // k, a page with s > T + 2e is in and one with s < T - 2e is out whatever the
 // rounding was; the few in between are scored again in 64 bits and ranked by

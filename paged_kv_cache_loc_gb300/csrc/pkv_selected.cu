@@ -173,14 +173,15 @@ __device__ __forceinline__ void stage_runs(const SelectedParams &p, const Share 
 }
 
 // ---------------------------------------------------------------------------
-// CUDA cores: eight lanes to a position, kHeads query heads of the kv head
+// CUDA cores (fp32): eight lanes to a position, kHeads query heads of the kv head
 // ---------------------------------------------------------------------------
 
 constexpr int kSimtWarps = 4;
 constexpr int kSimtThreads = kSimtWarps * 32;
 
-template <typename T, int D, int kHeads>
+template <int D, int kHeads>
 __global__ void __launch_bounds__(kSimtThreads) selected_simt_kernel(const SelectedParams p) {
+    using T = float;
     constexpr int kElems = 16 / Elem<T>::bytes;
     constexpr int kChunks = D / kElems;
     constexpr int kOwn = kChunks / 8;                // 16-byte chunks of a row per lane
@@ -594,17 +595,17 @@ cudaError_t run_mma_g(const SelectedParams &p, int group, cudaStream_t s) {
     }
 }
 
-template <typename T, int D, int kHeads>
+template <int D, int kHeads>
 cudaError_t run_simt(const SelectedParams &p, cudaStream_t s) {
-    return launch_cluster(selected_simt_kernel<T, D, kHeads>, dim3(p.splits, p.n_heads / kHeads, p.batch), kSimtThreads, 0, p, s);
+    return launch_cluster(selected_simt_kernel<D, kHeads>, dim3(p.splits, p.n_heads / kHeads, p.batch), kSimtThreads, 0, p, s);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run_simt_g(const SelectedParams &p, int group, cudaStream_t s) {
     switch (group) {
-        case 1: return run_simt<T, D, 1>(p, s);
-        case 2: return run_simt<T, D, 2>(p, s);
-        default: return run_simt<T, D, 4>(p, s);     // eight heads: two CTAs of four
+        case 1: return run_simt<D, 1>(p, s);
+        case 2: return run_simt<D, 2>(p, s);
+        default: return run_simt<D, 4>(p, s);        // eight heads: two CTAs of four
     }
 }
 
@@ -628,7 +629,7 @@ cudaError_t launch_decode_selected(const SelectedParams &p, int dtype, int head_
     if (!sparse_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
     if (p.splits < 1 || p.splits > kMaxSplits) return cudaErrorInvalidValue;
     if (dtype == PKV_BF16) return head_dim == 128 ? run_mma_g<128>(p, group, s) : run_mma_g<64>(p, group, s);
-    return head_dim == 128 ? run_simt_g<float, 128>(p, group, s) : run_simt_g<float, 64>(p, group, s);
+    return head_dim == 128 ? run_simt_g<128>(p, group, s) : run_simt_g<64>(p, group, s);
 }
 
 }  // namespace pkv

@@ -148,6 +148,30 @@ def _rows(t: torch.Tensor, name: str, dtype, index: int, n: int, heads: int, hea
     return _ptr(t, name, dtype, index)
 
 
+def _outputs(sel: Optional[torch.Tensor], counts: Optional[torch.Tensor], batch: int, kv: int, top_k: int, device,
+             index: int, stream):
+    """sel and sel_counts, allocated where they are not given, and their addresses."""
+    if sel is None:
+        sel = _empty((batch, kv, top_k), torch.int32, device, stream)
+        p = sel.data_ptr()
+    else:
+        p = _ints(sel, "sel", index, batch * kv * top_k)
+    if counts is None:
+        counts = _empty((batch, kv), torch.int32, device, stream)
+        return sel, counts, p, counts.data_ptr()
+    return sel, counts, p, _ints(counts, "sel_counts", index, batch * kv)
+
+
+def _output(o: Optional[torch.Tensor], q: torch.Tensor, dtype, index: int, stream):
+    """o, allocated like q where it is not given, and its address."""
+    if o is None:
+        o = _empty_like(q, stream) if q.is_cuda else _empty(q.shape, dtype, torch.device("cuda", index), stream)
+        return o, o.data_ptr()
+    if o.shape != q.shape:
+        raise ValueError(f"o must be {list(q.shape)}, got {list(o.shape)}")
+    return o, _ptr(o, "o", dtype, index)
+
+
 def _heads(q: torch.Tensor) -> int:
     if q.dim() != 3:
         raise ValueError(f"q must be [batch, n_heads, head_dim], got {list(q.shape)}")
@@ -187,6 +211,13 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(q: torch.Tensor, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty_like(q)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(q)
 
 
 def build_tables(cache: KVCache, req_to_page: torch.Tensor, page_size: int, free_pages: torch.Tensor,
@@ -242,14 +273,11 @@ def select_pages(cache: KVCache, layer_id: int, pages: SparsePages, q: torch.Ten
     sel int32 [batch, n_kv_heads, top_k] (logical pages, ascending, then -1)
     and sel_counts int32 [batch, n_kv_heads]."""
     c, at, index, dtype, shape, batch = _describe(cache, pages.req_to_page, 0, 0, True)
-    heads, kv, top_k = _heads(q), shape[2], pages.top_k
-    if sel is None:
-        sel = _empty((batch, kv, top_k), torch.int32, cache.k_buffer.device, stream)
-    if sel_counts is None:
-        sel_counts = _empty((batch, kv), torch.int32, cache.k_buffer.device, stream)
-    _call("pkv_select_pages", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape),
-          _rows(q, "q", dtype, index, batch, heads, shape[3]), heads, _ints(sel, "sel", index, batch * kv * top_k),
-          _ints(sel_counts, "sel_counts", index, batch * kv), _workspace(workspace, index))
+    heads, kv = _heads(q), shape[2]
+    qp = _rows(q, "q", dtype, index, batch, heads, shape[3])
+    sel, sel_counts, sp, cp = _outputs(sel, sel_counts, batch, kv, pages.top_k, cache.k_buffer.device, index, stream)
+    _call("pkv_select_pages", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape), qp, heads, sp, cp,
+          _workspace(workspace, index))
     return sel, sel_counts
 
 
@@ -261,11 +289,10 @@ def paged_decode_selected(cache: KVCache, layer_id: int, pages: SparsePages, q: 
     [batch, n_heads, head_dim], sel and sel_counts as select_pages gives them."""
     c, at, index, dtype, shape, batch = _describe(cache, pages.req_to_page, 0, 0, True)
     heads, kv, head_dim = _heads(q), shape[2], shape[3]
-    if o is None:
-        o = _empty(q.shape, dtype, cache.k_buffer.device, stream)
+    qp = _rows(q, "q", dtype, index, batch, heads, head_dim)
+    o, op = _output(o, q, dtype, index, stream)
     _call("pkv_paged_decode_selected", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape),
-          _ints(sel, "sel", index, batch * kv * pages.top_k), _ints(sel_counts, "sel_counts", index, batch * kv),
-          _rows(q, "q", dtype, index, batch, heads, head_dim), _rows(o, "o", dtype, index, batch, heads, head_dim),
+          _ints(sel, "sel", index, batch * kv * pages.top_k), _ints(sel_counts, "sel_counts", index, batch * kv), qp, op,
           heads, 1.0 / math.sqrt(head_dim) if sm_scale is None else sm_scale)
     return o
 
@@ -279,18 +306,12 @@ def sparse_decode_step(cache: KVCache, layer_id: int, pages: SparsePages, k_new:
     select_pages and paged_decode_selected as one call: (o, sel, sel_counts)."""
     n_new, heads = k_new.shape[0], _heads(q)
     c, at, index, dtype, shape, batch = _describe(cache, pages.req_to_page, 0, n_new, True)
-    kv, head_dim, top_k = shape[2], shape[3], pages.top_k
-    if o is None:
-        o = _empty(q.shape, dtype, cache.k_buffer.device, stream)
-    if sel is None:
-        sel = _empty((batch, kv, top_k), torch.int32, cache.k_buffer.device, stream)
-    if sel_counts is None:
-        sel_counts = _empty((batch, kv), torch.int32, cache.k_buffer.device, stream)
-    _call("pkv_sparse_decode_step", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape),
-          _rows(k_new, "k_new", dtype, index, n_new, kv, head_dim),
-          _rows(v_new, "v_new", dtype, index, n_new, kv, head_dim), n_new,
-          _rows(q, "q", dtype, index, batch, heads, head_dim), _rows(o, "o", dtype, index, batch, heads, head_dim),
-          heads, 1.0 / math.sqrt(head_dim) if sm_scale is None else sm_scale,
-          _ints(sel, "sel", index, batch * kv * top_k), _ints(sel_counts, "sel_counts", index, batch * kv),
-          _workspace(workspace, index))
+    kv, head_dim = shape[2], shape[3]
+    qp = _rows(q, "q", dtype, index, batch, heads, head_dim)
+    kp = _rows(k_new, "k_new", dtype, index, n_new, kv, head_dim)
+    vp = _rows(v_new, "v_new", dtype, index, n_new, kv, head_dim)
+    o, op = _output(o, q, dtype, index, stream)
+    sel, sel_counts, sp, cp = _outputs(sel, sel_counts, batch, kv, pages.top_k, cache.k_buffer.device, index, stream)
+    _call("pkv_sparse_decode_step", index, stream, c, layer_id, _describe_pages(pages, at, index, dtype, shape), kp, vp, n_new,
+          qp, op, heads, 1.0 / math.sqrt(head_dim) if sm_scale is None else sm_scale, sp, cp, _workspace(workspace, index))
     return o, sel, sel_counts

@@ -330,6 +330,38 @@ def test_page_bounds_and_selection_behind_4_gb():
     close(o, ref, reach, kk, 6, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_step_on_rows_behind_4_gb(dtype):
+    """The pool's rows, and with them every row that the step writes and reads,
+    lie past 2^32 bytes."""
+    rng = np.random.default_rng(50)
+    size = (1 << 21 if dtype == "bf16" else 1 << 20) + 2048
+    ps, kv, d, n = 16, 8, 128, 1000
+    k, v = (torch.zeros(1, size, kv, d, dtype=DT[dtype], device="cuda") for _ in range(2))
+    assert (size - 2048) * kv * d * k.element_size() >= 1 << 32
+    table = (size - 2048) // ps + rng.permutation(128)[None, :63]
+    p = np.arange(n)
+    slots = table[0, p // ps] * ps + p % ps
+    k[0, dev(slots).long()], v[0, dev(slots).long()] = (torch.randn(n, kv, d, device="cuda").to(DT[dtype]) for _ in range(2))
+    cache = pkv.KVCache(k_buffer=k, v_buffer=v, req_to_token=dev(np.zeros((1, 1))), req_pool_indices=dev([0]), seq_lens=dev([n]),
+                        out_cache_loc=dev(slots[:-1]), max_len=n)
+    pg = pkv.SparsePages.for_cache(cache, dev(table), ps, 12)
+    pkv.page_bounds(cache, 0, pg)
+    cache.out_cache_loc = dev(slots[-1:])
+    kn, vn, q = (torch.randn(1, h, d, device="cuda").to(DT[dtype]) for h in (kv, kv, 32))
+    o, sel, counts = pkv.sparse_decode_step(cache, 0, pg, kn, vn, q, workspace=ws_for(1, kv, n, ps))
+    clean()
+    lo = size - 2048
+    assert torch.equal(k[0, dev(slots[-1:]).long()], kn) and not k[0, :lo].any() and not v[0, :lo].any()
+    kk, vv = host(k[0, lo:]), host(v[0, lo:])
+    bounds = S.page_bounds(np.zeros((128, kv, 2, d)), kk[slots - lo], slots - lo, ps)
+    assert np.array_equal(host(pg.page_bounds[0, lo // ps:]), bounds) and not pg.page_bounds[0, :lo // ps].any()
+    want = S.select_pages(bounds, table - lo // ps, [0], [n], host(q), ps, 12, 1, 1)
+    assert np.array_equal(host(sel), want[0])
+    ref, reach = S.decode_selected(kk, vv, table - lo // ps, [0], [n], *want, host(q), ps, d ** -0.5)
+    close(o, ref, reach, vv, 12 * ps, dtype)
+
+
 # ---------------------------------------------------------------------------
 # select_pages
 # ---------------------------------------------------------------------------
