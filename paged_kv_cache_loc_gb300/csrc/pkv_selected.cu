@@ -298,14 +298,13 @@ __global__ void __launch_bounds__(kSimtThreads) selected_simt_kernel(const Selec
 // ---------------------------------------------------------------------------
 
 constexpr int kMmaWarps = 4;
+constexpr float kRaise = 8.f;
 constexpr int kMmaThreads = kMmaWarps * 32;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
 // The slot of position lane % 16 of the block at `at`, -1 where there is none.
 __device__ __forceinline__ int slot_at(int at, int to, int i0, const Run *runs, const SelectedParams &p, int len) {
     const int x = at + static_cast<int>(threadIdx.x & 15);
@@ -343,14 +342,23 @@ struct MmaShared {
     Run runs[kStagePages];
 };
 
-// Where chunk c of a half block's row stands: the four lanes of a row (K) and
-// the eight lanes of four rows and two chunks (V) that read together hit
-// different banks.
-__device__ __forceinline__ int swizzle(int row, int c) { return c ^ ((row & 1) << 2) ^ (row & 6); }
+// Where chunk c of a half block's row stands, so that lanes that read together
+// hit different banks: two rows by four chunks of K, eight rows by a chunk of V.
+__device__ __forceinline__ int swizzle_k(int row, int c) { return c ^ (row & 1) << 2; }
+__device__ __forceinline__ int swizzle_v(int row, int c) { return c ^ (row & 7); }
+
+// Four 8 x 8 blocks of 16-bit elements, transposed: lane l gives the address of
+// row l % 8 of block l / 8.
+__device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
 
 // Bound by the bytes of the selected rows: 64 requests x 2048 positions of 8 kv
-// heads (537 MB, gathered in runs of 256 bytes) take 95 us, 5.6 TB/s, 0.83 of the
-// copy rate; one request is bound by the chain list -> page table -> rows ->
+// heads (537 MB, gathered in runs of 256 bytes) take 94 us, 5.7 TB/s, 0.84 of the
+// copy rate; 256 queries of one prompt, whose 1.07 GB come from L2, take 95 us
+// and are bound by instruction issue (104 with V transposed by byte permutations
+// and a rescaling whenever the maximum moved); one request is bound by the chain list -> page table -> rows ->
 // join (8 us).
 //
 // A warp takes a block of 16 positions at a time.  K and V rows come by cp.async
@@ -363,17 +371,17 @@ __device__ __forceinline__ int swizzle(int row, int c) { return c ^ ((row & 1) <
 //     r + 8 (and of head r's q) and feeds them as the columns 2t, 2t + 1, 2t +
 //     8, 2t + 9 of successive k steps;
 //   O^T[D x 8 heads] += V^T P^T: P of positions 2t, 2t + 1, 2t + 8, 2t + 9 and
-//     head r is where S left it, and lane (r, t) takes the chunks r and r + 8
-//     of those four V rows; a byte permutation pairs two rows' channels, and
-//     output row r of step i stands for channel 8 r + 2 i, row r + 8 for the
-//     next one.
+//     head r is where S left it, and ldmatrix transposes V.
+// The weights are relative to a reference m that is raised only when a score
+// passes it by kRaise (2^8): sums and outputs keep their 24 bits, and most blocks
+// need neither the maximum across lanes nor a rescaling.
 // P goes in as two bf16 parts (hi + lo, 16 bits together): one part alone would
 // add an error of the size of the output's own rounding.  (A V that is infinite
 // then gives NaN, 0 times infinity, and not infinity.)
 template <int D, int G>
 __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const SelectedParams p) {
     using Sh = MmaShared<D, G>;
-    constexpr int kChunks = D / 8, kOwn = kChunks / 4, kHalves = D / 64, kRing = Sh::kRing;
+    constexpr int kChunks = D / 8, kOwn = kChunks / 4, kRing = Sh::kRing;
     extern __shared__ __align__(128) unsigned char smem[];
     Sh &sh = *reinterpret_cast<Sh *>(smem);
     griddep_launch();
@@ -390,9 +398,9 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
     const Share s = cta_share(p, g, b, rank, rank == 0 && threadIdx.x == 0);
 
     float m = -INFINITY, l = 0.f;            // head r; l over this lane's positions
-    float o[kHalves * 4][4];                 // channels 64 * (i / 4) + 8 r + 2 (i % 4) (+ 1), heads 2t, 2t + 1
+    float o[D / 16][4];                      // channels 16 i + r and 16 i + r + 8, heads 2t, 2t + 1 of each
 #pragma unroll
-    for (int i = 0; i < kHalves * 4; ++i)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
@@ -403,37 +411,49 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
     const int64_t lane0 = (p.layer_row0 * p.n_kv_heads + g) * kRowBytes + lane % kRowLanes * 16;
     const char *kp = static_cast<const char *>(p.k_buffer) + lane0, *vp = static_cast<const char *>(p.v_buffer) + lane0;
     const uint32_t slot_bytes = static_cast<uint32_t>(p.n_kv_heads) * kRowBytes;
-    uint32_t put[kRowsPer == 2 ? 4 : 2];     // this lane's places in a half block: rows i * kRowsPer + lane / kRowLanes
+    constexpr int kFills = 8 / kRowsPer;     // places of a lane among eight rows; eight rows on the same again
+    uint32_t put_k[kFills], put_v[kFills];
 #pragma unroll
-    for (int i = 0; i < 8 / kRowsPer; ++i) {
-        const int row = i * kRowsPer + lane / kRowLanes;          // rows 8 and more: the same, 8 rows on
-        put[i] = row * kRowBytes + swizzle(row, lane % kRowLanes) * 16;
+    for (int i = 0; i < kFills; ++i) {
+        const int row = i * kRowsPer + lane / kRowLanes;
+        put_k[i] = row * kRowBytes + swizzle_k(row, lane % kRowLanes) * 16;
+        put_v[i] = row * kRowBytes + swizzle_v(row, lane % kRowLanes) * 16;
     }
     const auto fetch_k = [&](int slot, int to) {
         const int safe = max(slot, 0);
+        const uint32_t place = ring + to * kPlaceBytes;
 #pragma unroll
         for (int i = 0; i < kBlk / kRowsPer; ++i) {
             const uint32_t from = __shfl_sync(0xffffffffu, safe, i * kRowsPer + lane / kRowLanes);
-            cp_async16_at(ring + to * kPlaceBytes + put[i % (8 / kRowsPer)] + i / (8 / kRowsPer) * 8 * kRowBytes,
-                          kp + static_cast<uint64_t>(from) * slot_bytes, 16);
+            cp_async16_at(place + put_k[i % kFills] + i / kFills * 8 * kRowBytes, kp + static_cast<uint64_t>(from) * slot_bytes, 16);
         }
         cp_async_commit();
     };
     const auto fetch_v = [&](int slot, int to) {
+        const uint32_t place = ring + to * kPlaceBytes;
+        if (__all_sync(0xffffffffu, slot >= 0)) {
 #pragma unroll
-        for (int i = 0; i < kBlk / kRowsPer; ++i) {
-            const int from = __shfl_sync(0xffffffffu, slot, i * kRowsPer + lane / kRowLanes);
-            cp_async16_at(ring + to * kPlaceBytes + put[i % (8 / kRowsPer)] + i / (8 / kRowsPer) * 8 * kRowBytes,
-                          vp + static_cast<uint64_t>(static_cast<uint32_t>(max(from, 0))) * slot_bytes, from >= 0 ? 16 : 0);
+            for (int i = 0; i < kBlk / kRowsPer; ++i) {
+                const uint32_t from = __shfl_sync(0xffffffffu, slot, i * kRowsPer + lane / kRowLanes);
+                cp_async16_at(place + put_v[i % kFills] + i / kFills * 8 * kRowBytes, vp + static_cast<uint64_t>(from) * slot_bytes, 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBlk / kRowsPer; ++i) {
+                const int from = __shfl_sync(0xffffffffu, slot, i * kRowsPer + lane / kRowLanes);
+                cp_async16_at(place + put_v[i % kFills] + i / kFills * 8 * kRowBytes,
+                              vp + static_cast<uint64_t>(static_cast<uint32_t>(max(from, 0))) * slot_bytes, from >= 0 ? 16 : 0);
+            }
         }
         cp_async_commit();
     };
     // Places of this lane's chunks: K row r, chunks t + 4 j for j even and odd
-    // (128 bytes on for each j / 2, eight rows on for row r + 8); V rows 2t and
-    // 2t + 1, chunk r (the same steps).
-    const uint32_t k_even = ring + r * kRowBytes + swizzle(r, t) * 16, k_odd = ring + r * kRowBytes + swizzle(r, t + 4) * 16;
-    const uint32_t v_even = ring + 2 * t * kRowBytes + swizzle(2 * t, r) * 16;
-    const uint32_t v_odd = ring + (2 * t + 1) * kRowBytes + swizzle(2 * t + 1, r) * 16;
+    // (128 bytes on for each j / 2, eight rows on for row r + 8); V row lane % 8
+    // (+ 8 for the upper half of the lanes), chunk lane / 8 % 2: 2 i + that chunk
+    // is 32 i bytes away by exclusive or.
+    const uint32_t k_even = ring + r * kRowBytes + swizzle_k(r, t) * 16, k_odd = ring + r * kRowBytes + swizzle_k(r, t + 4) * 16;
+    const int v_row = (lane & 7) + (lane >> 4) * 8;
+    const uint32_t v_at = ring + v_row * kRowBytes + swizzle_v(v_row, lane >> 3 & 1) * 16;
 
     const int i_end = s.t1 > s.t0 ? (s.t1 - 1) / p.page_size + 1 : 0;
     for (int i0 = s.t0 / p.page_size; i0 < i_end; i0 += kStagePages) {
@@ -473,16 +493,17 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
                 for (int i = 0; i < 4; ++i)
                     if (unseen >> (2 * t + (i & 1) + 8 * (i >> 1)) & 1) pr[i] = -INFINITY;
             }
-            float top = fmaxf(fmaxf(fmaxf(pr[0], pr[1]), fmaxf(pr[2], pr[3])), m);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (__any_sync(0xffffffffu, top != m)) {
+            float top = fmaxf(fmaxf(pr[0], pr[1]), fmaxf(pr[2], pr[3]));
+            if (__any_sync(0xffffffffu, top > m + kRaise)) {      // m = -inf: as soon as something is seen
+                top = fmaxf(top, m);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const float f = weight(m, top);
                 m = top;
                 l *= f;
                 const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
-                for (int i = 0; i < kHalves * 4; ++i) {
+                for (int i = 0; i < D / 16; ++i) {
                     o[i][0] *= f0;
                     o[i][1] *= f1;
                     o[i][2] *= f0;
@@ -504,20 +525,13 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
             x = after(x, 1);
             cp_async_wait<2>();
             __syncwarp();
+            const uint32_t v_place = v_at + x * kPlaceBytes;
 #pragma unroll
-            for (int j = 0; j < kHalves; ++j) {
-                uint4 v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = lds16((i & 1 ? v_odd : v_even) + x * kPlaceBytes + (i >> 1) * 8 * kRowBytes + j * 128);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a0 = __byte_perm(word(v[0], i), word(v[1], i), 0x5410);
-                    const uint32_t a1 = __byte_perm(word(v[0], i), word(v[1], i), 0x7632);
-                    const uint32_t a2 = __byte_perm(word(v[2], i), word(v[3], i), 0x5410);
-                    const uint32_t a3 = __byte_perm(word(v[2], i), word(v[3], i), 0x7632);
-                    mma_bf16(o[j * 4 + i], a0, a1, a2, a3, hi0, hi1);
-                    mma_bf16(o[j * 4 + i], a0, a1, a2, a3, lo0, lo1);
-                }
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t v[4];
+                ldmatrix_t(v, (v_place ^ (i % 4) * 32) + i / 4 * 128);
+                mma_bf16(o[i], v[0], v[1], v[2], v[3], hi0, hi1);
+                mma_bf16(o[i], v[0], v[1], v[2], v[3], lo0, lo1);
             }
             __syncwarp();                                         // every lane has read the V rows
             x = after(x, 1);
@@ -534,12 +548,10 @@ __global__ void __launch_bounds__(kMmaThreads, 4) selected_mma_kernel(const Sele
         sh.parts.l[warp][r] = l;
     }
 #pragma unroll
-    for (int i = 0; i < kHalves * 4; ++i) {
-        const int c = 64 * (i / 4) + 8 * r + 2 * (i % 4);
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (2 * t + e < G) *reinterpret_cast<float2 *>(&sh.parts.o[warp][2 * t + e][c]) = make_float2(o[i][e], o[i][2 + e]);
-    }
+        for (int e = 0; e < 4; ++e)
+            if (2 * t + (e & 1) < G) sh.parts.o[warp][2 * t + (e & 1)][16 * i + r + (e >> 1) * 8] = o[i][e];
     join<bf16, kMmaWarps, G, D, kMmaThreads>(sh.parts, static_cast<bf16 *>(p.o) + out0, rank, p.splits);
 }
 
