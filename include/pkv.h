@@ -433,7 +433,8 @@ int pkv_page_bounds(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg,
  *   score = max over the G query heads h of the group of
  *           sum_c max(q[b,h,c] * minimum[c], q[b,h,c] * maximum[c]),
  * the largest product that the query can have with any key inside the page's
- * bounds.  With N <= top_k every page is selected; otherwise the first n_first
+ * bounds (those of every key written to the page, also behind the query's own
+ * context).  With N <= top_k every page is selected; otherwise the first n_first
  * and the last n_last pages, and of the rest the top_k - n_first - n_last of
  * largest score.  The order is that of the scores in 64 bits: scores are
  * computed in 32 bits with a bound on their error, and those that the bound
