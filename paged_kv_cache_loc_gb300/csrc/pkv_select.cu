@@ -1,25 +1,22 @@
-// pkv_select.cu -- which pages a sparse decode attends to: the pages' key
-// bounds (pkv_page_bounds) and the selection by them (pkv_select_pages).
+// pkv_select.cu -- which pages a sparse decode attends to (pkv_select_pages).
 //
-// Bounds: per page, kv head and channel the minimum and maximum of the keys
-// written.  The score of a page for a query q is the largest product that q
-// can have with any key inside the bounds,
+// The score of a page for a query q is the largest product that q can have with
+// any key inside the page's bounds [lo, hi] (pkv_bounds.cu),
 //   sum_c max(q_c lo_c, q_c hi_c) = q- . lo + q+ . hi   (q- <= 0 <= q+, q = q- + q+),
 // maximised over the G query heads of the group.
 //
 // The selection must not depend on how a sum was rounded, so it is decided in
 // two steps.  The score pass computes 32-bit scores s with |s - s*| <= e,
-// where s* is the exact score and, for the n = 2 D (or D) terms of a sum,
+// where s* is the exact score and
 //   e = kScoreEps * max_h sum_c |q[h, c]| * max |bound|,
 // whose last two factors bound sum |terms|.  kScoreEps = 2^-16: a chain of four
 // 16-term tensor-core products adds 17 numbers at a time, each off by 2^-23 of
 // the largest at most when 24 bits are kept of what is aligned to it, 68 2^-23 <
 // 2^-16.9 in all (fp32 units: 16 products and 3 additions a lane, less); the
-// largest seen on this chip is 2^-20.6, on terms of very unlike sizes.  With
-// T the 32-bit score of rank
-// k, a page with s > T + 2e is in and one with s < T - 2e is out whatever the
-// rounding was; the few in between are scored again in 64 bits and ranked by
-// (score, page).
+// largest seen on this chip is 2^-20.6, on terms of very unlike sizes.  With T
+// the 32-bit score of rank k, a page with s > T + 2e is in and one with s < T - 2e
+// is out whatever the rounding was; the few in between are scored again in 64
+// bits and ranked by (score, page).
 #include <atomic>
 
 #include "pkv_launch.h"
@@ -84,7 +81,10 @@ struct Scorer {
         for (int j = 0; j < kOwn; ++j)
             q[j] = r < n ? reinterpret_cast<const uint4 *>(rows)[r * kChunks + t + 4 * j] : make_uint4(0, 0, 0, 0);
     }
-    const uint4 *r0, *r1;                    // rows r and r + 8 of the group to load
+    // Rows r and r + 8 of the group to load.  Bounds are read by plain loads: in a
+    // step the kernel before this one writes them while this one is already
+    // resident, and a load through the read-only path may be moved before the wait.
+    const uint4 *r0, *r1;
 
     // The group to load next; phys: the physical page of its page lane % 16.
     __device__ __forceinline__ void aim(const SelectParams &p, int g, int phys) {
@@ -94,10 +94,10 @@ struct Scorer {
         r1 = base + ((p.layer_page0 + __shfl_sync(0xffffffffu, phys, r + 8)) * p.n_kv_heads + g) * 2 * kChunks;
     }
     __device__ __forceinline__ void load_chunk(int j) {
-        l0[j] = __ldg(r0 + 4 * j);
-        l1[j] = __ldg(r1 + 4 * j);
-        h0[j] = __ldg(r0 + kChunks + 4 * j);
-        h1[j] = __ldg(r1 + kChunks + 4 * j);
+        l0[j] = r0[4 * j];
+        l1[j] = r1[4 * j];
+        h0[j] = r0[kChunks + 4 * j];
+        h1[j] = r1[kChunks + 4 * j];
     }
     __device__ __forceinline__ void load() {
 #pragma unroll
@@ -227,8 +227,8 @@ struct Scorer<float, D, G> {
 #pragma unroll
             for (int c = 0; c < kChunks; c += 8) {
                 float l[4], u[4];
-                widen16(__ldg(lo + c), l, float{});
-                widen16(__ldg(lo + kChunks + c), u, float{});
+                widen16(lo[c], l, float{});
+                widen16(lo[kChunks + c], u, float{});
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     big = max_nan(big, max_nan(fabsf(l[e]), fabsf(u[e])));

@@ -104,7 +104,9 @@ __device__ __forceinline__ void join(Partials<kParts, kHeads, D> &sh, T *out, in
     if (splits > 1) cluster_sync();      // no CTA leaves while its memory is read
 }
 
-// What a CTA attends to: blocks [t0, t1) of the list's flattened positions.
+// What a CTA attends to: blocks [t0, t1) of the list's flattened positions.  The
+// lists are read by plain loads: in a step the selection writes them while this
+// kernel is already resident.
 struct Share {
     int row, len, n_pages, t0, t1;
 };
@@ -113,7 +115,7 @@ __device__ __forceinline__ Share cta_share(const SelectedParams &p, int g, int b
     Share s;
     s.row = __ldg(p.req_pool_indices + b);
     s.len = __ldg(p.seq_lens + b);
-    int count = __ldg(p.sel_counts + static_cast<int64_t>(b) * p.n_kv_heads + g);
+    int count = p.sel_counts[static_cast<int64_t>(b) * p.n_kv_heads + g];
     if (static_cast<unsigned>(s.row) >= static_cast<unsigned>(p.num_reqs)) {
         if (report) record_error(p.err, s.row);
         s.row = s.len = count = 0;
@@ -147,7 +149,7 @@ __device__ __forceinline__ Guess guess_entry(const SelectedParams &p, const int3
     Guess x;
     x.first = static_cast<int>(static_cast<int64_t>(blocks) * rank / p.splits) * kBlk / p.page_size;
     const int i = x.first + static_cast<int>(threadIdx.x);
-    x.page = i < p.top_k ? __ldg(sel + i) : 0;
+    x.page = i < p.top_k ? sel[i] : 0;
     return x;
 }
 
@@ -155,7 +157,7 @@ __device__ __forceinline__ Guess guess_entry(const SelectedParams &p, const int3
 template <int kThreads>
 __device__ __forceinline__ void stage_runs(const SelectedParams &p, const Share &s, const int32_t *sel, const Guess &guess, int i0, int i1, Run *runs) {
     for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += kThreads) {
-        const int page = i == guess.first + static_cast<int>(threadIdx.x) ? guess.page : __ldg(sel + i);
+        const int page = i == guess.first + static_cast<int>(threadIdx.x) ? guess.page : sel[i];
         Run r{0, -1};
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(s.n_pages)) {
             record_error(p.err, page);
