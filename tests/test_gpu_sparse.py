@@ -896,6 +896,32 @@ def test_step_replayed_from_a_graph_and_on_other_streams():
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+@pytest.mark.parametrize("dtype,batch", [("bf16", 3), ("bf16", 90), ("f32", 5)])
+def test_steps_without_a_wait_between_them(dtype, batch):
+    """Each step's launches overlap the step before it: sixteen of them equal
+    the four calls made one by one, bit for bit."""
+    rng = np.random.default_rng(51)
+    lens = rng.integers(300, 1200, batch)
+    cache, pg, q, kn, vn, table, rows, loc = step_case(rng, dtype, 16, 4, 64, 4, lens, 14)
+    ws = ws_for(batch, 4, 1200, 4)
+    copy = dataclasses.replace(cache, k_buffer=cache.k_buffer.clone(), v_buffer=cache.v_buffer.clone())
+    pg2 = dataclasses.replace(pg, page_bounds=pg.page_bounds.clone())
+    steps = [tuple((torch.randn_like(x.float()) * (1 + i % 3)).to(DT[dtype]) for x in (kn, vn, q)) for i in range(16)]
+    torch.cuda.synchronize()
+    got = [pkv.sparse_decode_step(cache, 1, pg, *s, workspace=ws) for s in steps]
+    clean()
+    for (k, v, qq), (o, sel, counts) in zip(steps, got):
+        pkv.kv_write(copy, 1, k, v)
+        pkv.page_bounds(copy, 1, pg2)
+        torch.cuda.synchronize()
+        sel2, counts2 = pkv.select_pages(copy, 1, pg2, qq, workspace=ws)
+        torch.cuda.synchronize()
+        o2 = pkv.paged_decode_selected(copy, 1, pg2, qq, sel2, counts2)
+        clean()
+        assert torch.equal(sel, sel2) and torch.equal(counts, counts2) and torch.equal(o, o2)
+    assert torch.equal(pg.page_bounds, pg2.page_bounds) and torch.equal(cache.k_buffer, copy.k_buffer)
+
+
 def test_step_with_inputs_in_pinned_host_memory():
     rng = np.random.default_rng(44)
     lens = np.array([130, 400])
