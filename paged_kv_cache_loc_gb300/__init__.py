@@ -23,10 +23,10 @@ from .ops import (KVCache, Workspace, decode_plan, decode_step, kv_write,  # noq
                   last_device_error, paged_decode, paged_decode_noalloc, paged_decode_pages,
                   paged_decode_shared, paged_prefill, rope_kv_write)
 from .sparse import (SparsePages, build_tables, page_bounds, paged_decode_selected,  # noqa: F401
-                     select_pages, select_workspace_bytes, sparse_decode_step)
+                     select_pages, select_workspace, select_workspace_bytes, sparse_decode_step)
 from ._lib import PkvError, load  # noqa: F401
 
 __all__ = ["KVCache", "Workspace", "kv_write", "rope_kv_write", "paged_decode", "decode_step",
            "paged_decode_pages", "paged_decode_shared", "paged_prefill", "paged_decode_noalloc", "decode_plan",
-           "SparsePages", "build_tables", "page_bounds", "select_pages", "select_workspace_bytes",
+           "SparsePages", "build_tables", "page_bounds", "select_pages", "select_workspace", "select_workspace_bytes",
            "paged_decode_selected", "sparse_decode_step", "last_device_error", "PkvError", "load"]

@@ -679,6 +679,7 @@ __global__ void __launch_bounds__(kClusterThreads, 2) select_cluster_kernel(cons
     __syncthreads();
     if constexpr (Elem<T>::bytes == 4) sc.load_q(&sh.q[0][0], G);
     else sc.load_q(static_cast<const T *>(p.q) + (static_cast<int64_t>(b) * p.n_heads + g * G) * D, G);
+    const float norm = rank == 0 ? query_norm(sh) : 0.f;
     if (p.pdl) griddep_wait();                                    // the bounds
     if (p.splits > 1) cluster_wait();
     float big = 0.f;
@@ -710,7 +711,6 @@ __global__ void __launch_bounds__(kClusterThreads, 2) select_cluster_kernel(cons
     if (p.splits > 1) cluster_sync();
     else __syncthreads();
     if (rank != 0) return;                                        // nobody reads its memory
-    const float norm = query_norm(sh);
     big = static_cast<int>(threadIdx.x) < p.splits * kWarps ? __uint_as_float(sh.big[threadIdx.x]) : 0.f;
     __syncthreads();                                              // sh.big is reused
     select_from_keys<T, D, G, NT>(p, sh, g, n, keys, big, norm, p.sel + (static_cast<int64_t>(b) * p.n_kv_heads + g) * p.top_k,

@@ -29,6 +29,7 @@ _pack_tables = struct.Struct("PPiiPPPiiPPPPP")
 for _s, _c in ((_pack_cache, PkvKVCache), (_pack_pages, PkvPages), (_pack_tables, PkvTables)):
     assert _s.size <= ctypes.sizeof(_c) < _s.size + 8       # but for padding at the end
 _i32, _f32 = ctypes.c_int32, ctypes.c_float
+_Tensor, _int32, _byref, _device = torch.Tensor, torch.int32, ctypes.byref, torch.cuda.current_device
 _vp, _st = ctypes.c_void_p, ctypes.c_char_p                 # _st: a packed descriptor
 # name -> argtypes, with the descriptors as bytes
 _ARGS = {
@@ -54,7 +55,7 @@ def _function(name: str):
 def _ptr(t: torch.Tensor, name: str, dtype, index: int) -> int:
     """The address of a contiguous tensor of `dtype` on CUDA device `index`,
     or in pinned host memory (as in ops._need)."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+    if type(t) is _Tensor and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
     return _need(t, name, dtype, torch.device("cuda", index))
 
@@ -63,7 +64,7 @@ def _ints(t: Optional[torch.Tensor], name: str, index: int, n: int) -> int:
     """The address of an int32 array of n elements; 0 for None."""
     if t is None:
         return 0
-    p = _ptr(t, name, torch.int32, index)
+    p = _ptr(t, name, _int32, index)
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
     return p
@@ -114,14 +115,14 @@ def _describe(cache: KVCache, table: torch.Tensor, max_ctx_len: int, n_new: int,
     batch = rows.numel()
     loc = 0
     if n_new:
-        loc = _ptr(cache.out_cache_loc, "out_cache_loc", torch.int32, index)
+        loc = _ptr(cache.out_cache_loc, "out_cache_loc", _int32, index)
         if cache.out_cache_loc.numel() < n_new:     # it may be longer than what is written
             raise ValueError(f"out_cache_loc must have {n_new} elements at least, got {cache.out_cache_loc.numel()}")
     n_layers, size, n_kv_heads, head_dim = shape
-    at = _ptr(table, "req_to_page", torch.int32, index)
+    at = _ptr(table, "req_to_page", _int32, index)
     c = _pack_cache.pack(
         _ptr(kb, "k_buffer", dtype, index), _ptr(vb, "v_buffer", dtype, index), code, n_layers, n_kv_heads,
-        head_dim, size, at, table.shape[0], max_ctx_len, _ptr(rows, "req_pool_indices", torch.int32, index),
+        head_dim, size, at, table.shape[0], max_ctx_len, _ptr(rows, "req_pool_indices", _int32, index),
         _ints(lens, "seq_lens", index, batch), 0, 0, loc, batch, cache.max_len)
     return c, at, index, dtype, shape, batch
 
@@ -152,12 +153,12 @@ def _outputs(sel: Optional[torch.Tensor], counts: Optional[torch.Tensor], batch:
              index: int, stream):
     """sel and sel_counts, allocated where they are not given, and their addresses."""
     if sel is None:
-        sel = _empty((batch, kv, top_k), torch.int32, device, stream)
+        sel = _empty((batch, kv, top_k), _int32, device, stream)
         p = sel.data_ptr()
     else:
         p = _ints(sel, "sel", index, batch * kv * top_k)
     if counts is None:
-        counts = _empty((batch, kv), torch.int32, device, stream)
+        counts = _empty((batch, kv), _int32, device, stream)
         return sel, counts, p, counts.data_ptr()
     return sel, counts, p, _ints(counts, "sel_counts", index, batch * kv)
 
@@ -183,7 +184,7 @@ def _workspace(ws: Optional[Workspace], index: int):
         return None
     if ws.buffer.get_device() != index:
         raise ValueError(f"workspace is on {ws.buffer.device}, expected cuda:{index}")
-    return ctypes.byref(ws.desc)
+    return _byref(ws.desc)
 
 
 # the handle of a device's current stream, without the object around it
@@ -196,7 +197,7 @@ def _call(name: str, index: int, stream, *args) -> None:
     handle; None is the device's current stream."""
     fn = _functions.get(name) or _function(name)
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if _device() == index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -241,11 +242,11 @@ def build_tables(cache: KVCache, req_to_page: torch.Tensor, page_size: int, free
         raise ValueError("req_to_page and req_to_token must have the same rows")
     t = _pack_tables.pack(
         _ints(q_lens, "q_lens", index, batch), at, req_to_page.shape[1], page_size,
-        _ptr(free_pages, "free_pages", torch.int32, index), _ints(free_start, "free_start", index, 1),
+        _ptr(free_pages, "free_pages", _int32, index), _ints(free_start, "free_start", index, 1),
         _ints(free_end, "free_end", index, 1), free_pages.numel(), n_new,
         _ints(cache.kv_indptr, "kv_indptr", index, batch + 1), _ints(cache.qo_indptr, "qo_indptr", index, batch + 1),
         _ints(positions, "positions", index, n_new), loc.data_ptr() if n_new else 0,
-        _ptr(tokens, "req_to_token", torch.int32, index) if token_table else 0)
+        _ptr(tokens, "req_to_token", _int32, index) if token_table else 0)
     _call("pkv_build_tables", index, stream, c, t)
 
 
@@ -264,6 +265,14 @@ def page_bounds(cache: KVCache, layer_id: int, pages: SparsePages, n_new: Option
 def select_workspace_bytes(batch: int, n_kv_heads: int, max_len: int, page_size: int) -> int:
     """Workspace bytes that select_pages and sparse_decode_step need."""
     return _lib.load().pkv_select_workspace_bytes(batch, n_kv_heads, max_len, page_size)
+
+
+def select_workspace(max_batch: int, n_kv_heads: int, max_len: int, page_size: int, device="cuda") -> Workspace:
+    """A workspace for select_pages and sparse_decode_step of these sizes."""
+    need = select_workspace_bytes(max_batch, n_kv_heads, max_len, page_size)
+    if need == 0:
+        raise ValueError("workspace dimensions must be positive")
+    return Workspace(1, 1, 64, -(-need // 256), device=device)      # 256 bytes of partials per split
 
 
 def select_pages(cache: KVCache, layer_id: int, pages: SparsePages, q: torch.Tensor,

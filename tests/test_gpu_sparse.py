@@ -56,8 +56,7 @@ def error():
 
 
 def ws_for(batch, kv, max_len, ps, device="cuda"):
-    need = max(1, pkv.select_workspace_bytes(max(1, batch), kv, max(1, max_len), ps))
-    return pkv.Workspace(1, 1, 64, -(-need // 256), device=device)
+    return pkv.select_workspace(max(1, batch), kv, max(1, max_len), ps, device=device)
 
 
 # ---------------------------------------------------------------------------

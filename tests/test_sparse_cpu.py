@@ -201,6 +201,9 @@ def test_select_workspace_bytes(lib):
     assert f(3, 8, 256, 16) == 3 * 8 * (16 + 1) * 4              # 16 pages: one group
     assert f(3, 8, 257, 16) == 3 * 8 * (32 + 2) * 4
     assert f(65535, 8, 1 << 30, 1) == 65535 * 8 * ((1 << 30) + (1 << 26)) * 4
+    assert pkv.select_workspace(3, 8, 257, 16, device="cpu").desc.bytes >= f(3, 8, 257, 16)
+    with pytest.raises(ValueError):
+        pkv.select_workspace(0, 8, 257, 16, device="cpu")
 
 
 def test_binding_refuses_cpu_tensors():
