@@ -488,6 +488,37 @@ def test_page_bounds_of_rotated_keys():
     assert np.array_equal(host(pg.page_bounds)[0], S.page_bounds(np.zeros((10, 2, 2, 64)), host(k)[0][loc], loc, 8))
 
 
+def test_build_tables_a_row_named_twice_leaves_the_others_exact():
+    """What such a row's tables hold is unspecified; the pages taken, the sums,
+    the positions and the other rows are not."""
+    rng = np.random.default_rng(52)
+    q = np.array([9, 14, 9, 3])
+    t, want, n = tables_case(rng, q + np.array([0, 5, 0, 20]), q, 4)
+    rows = host(t.cache.req_pool_indices)
+    rows[2] = rows[0]
+    t.cache.req_pool_indices = dev(rows)
+    t.run()
+    clean()
+    assert np.array_equal(host(t.cache.kv_indptr), want["kv_indptr"]) and int(t.end) == want["free_end"]
+    assert np.array_equal(host(t.positions)[:n], want["positions"])
+    single = np.r_[9:23, 32:35]                          # the tokens of entries 1 and 3
+    assert np.array_equal(host(t.cache.out_cache_loc)[single], want["out_cache_loc"][single])
+    assert np.array_equal(host(t.table)[rows[[1, 3]]], want["req_to_page"][rows[[1, 3]]])
+
+
+def test_page_bounds_a_slot_given_twice_leaves_the_other_pages_exact():
+    rng = np.random.default_rng(53)
+    k, v = pool(rng, 1, 12, 4, 2, 64, "bf16")
+    loc = np.r_[8:12, 9, 20:24, 20:22, 40:43]
+    cache = pkv.KVCache(k_buffer=k, v_buffer=v, req_to_token=dev(np.zeros((1, 1))), req_pool_indices=dev([0]), out_cache_loc=dev(loc))
+    pg = pkv.SparsePages.for_cache(cache, dev(np.zeros((1, 1))), 4, 4)
+    pkv.page_bounds(cache, 0, pg)
+    clean()
+    want = S.page_bounds(np.zeros((12, 2, 2, 64)), host(k)[0][40:43], np.r_[40:43], 4)
+    others = [p for p in range(12) if p not in (2, 5)]
+    assert np.array_equal(host(pg.page_bounds)[0][others], want[others])
+
+
 def test_build_tables_of_an_empty_batch():
     rng = np.random.default_rng(49)
     t, _, _ = tables_case(rng, np.array([5]), np.array([5]), 4)
