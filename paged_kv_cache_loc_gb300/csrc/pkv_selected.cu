@@ -34,51 +34,66 @@ template <int kParts, int kHeads, int D>
 struct Partials {
     float m[kParts][kHeads];
     float l[kParts][kHeads];
+    float scale[kParts][kHeads];         // of the parts towards their common maximum
+    float top[kHeads], sum[kHeads];      // the CTA's maximum and denominator
     alignas(16) float o[kParts][kHeads][D];
 };
 
-// Joins the parts of every CTA of the cluster and writes o.  Part 0 becomes
-// the CTA's own partial; CTA r of the cluster then sums its share of the
-// outputs over all CTAs.
+template <typename T>
+__device__ __forceinline__ void store4(T *to, const float4 &x) {
+    if constexpr (Elem<T>::bytes == 4) {
+        *reinterpret_cast<float4 *>(to) = x;
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+        *reinterpret_cast<uint2 *>(to) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+}
+
+// Joins the parts of every CTA of the cluster and writes o.  A CTA alone writes
+// its sums; in a cluster part 0 becomes the CTA's own partial, and CTA r sums
+// its share of the outputs over all CTAs.
 template <typename T, int kParts, int kHeads, int D, int kThreads>
 __device__ __forceinline__ void join(Partials<kParts, kHeads, D> &sh, T *out, int rank, int splits) {
     const int tid = threadIdx.x;
     constexpr int kOut = kHeads * D;
-    float acc[(kOut + kThreads - 1) / kThreads];
+    __syncthreads();
+    if (tid < kHeads) {
+        float top = sh.m[0][tid], sum = 0.f;
+#pragma unroll
+        for (int w = 1; w < kParts; ++w) top = fmaxf(top, sh.m[w][tid]);
+#pragma unroll
+        for (int w = 0; w < kParts; ++w) {
+            const float f = weight(sh.m[w][tid], top);
+            sh.scale[w][tid] = f;
+            sum = fmaf(sh.l[w][tid], f, sum);
+        }
+        sh.top[tid] = top;
+        sh.sum[tid] = sum;
+    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < (kOut + kThreads - 1) / kThreads; ++i) {
-        const int e = tid + i * kThreads, h = e / D, c = e % D;
-        acc[i] = 0.f;
-        if (e < kOut) {
-            float top = -INFINITY;
+    for (int i = 0; i < (kOut + kThreads * 4 - 1) / (kThreads * 4); ++i) {
+        const int e = (tid + i * kThreads) * 4, h = e / D, c = e % D;
+        if (e >= kOut) break;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kParts; ++w) top = fmaxf(top, sh.m[w][h]);
-#pragma unroll
-            for (int w = 0; w < kParts; ++w) {
-                if (sh.m[w][h] != -INFINITY) acc[i] = fmaf(weight(sh.m[w][h], top), sh.o[w][h][c], acc[i]);
-            }
+        for (int w = 0; w < kParts; ++w) {
+            const float f = sh.scale[w][h];
+            const float4 x = *reinterpret_cast<const float4 *>(&sh.o[w][h][c]);
+            acc.x = fmaf(f, x.x, acc.x);
+            acc.y = fmaf(f, x.y, acc.y);
+            acc.z = fmaf(f, x.z, acc.z);
+            acc.w = fmaf(f, x.w, acc.w);
+        }
+        if (splits == 1) {
+            const float l = sh.sum[h], inv = l == 0.f ? 0.f : 1.f / l;
+            store4(out + e, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        } else {
+            *reinterpret_cast<float4 *>(&sh.o[0][h][c]) = acc;    // read by this thread alone so far
         }
     }
-    float top = -INFINITY, sum = 0.f;
-    if (tid < kHeads) {
-#pragma unroll
-        for (int w = 0; w < kParts; ++w) top = fmaxf(top, sh.m[w][tid]);
-#pragma unroll
-        for (int w = 0; w < kParts; ++w) sum += sh.l[w][tid] * weight(sh.m[w][tid], top);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < (kOut + kThreads - 1) / kThreads; ++i) {
-        const int e = tid + i * kThreads;
-        if (e < kOut) sh.o[0][e / D][e % D] = acc[i];
-    }
-    if (tid < kHeads) {
-        sh.m[0][tid] = top;
-        sh.l[0][tid] = sum;
-    }
-    if (splits > 1) cluster_sync();
-    else __syncthreads();
+    if (splits == 1) return;
+    cluster_sync();
     const int e1 = kOut * (rank + 1) / splits;
     for (int e = kOut * rank / splits + tid; e < e1; e += kThreads) {
         const int h = e / D, c = e % D;
@@ -86,22 +101,21 @@ __device__ __forceinline__ void join(Partials<kParts, kHeads, D> &sh, T *out, in
 #pragma unroll
         for (int r = 0; r < kMaxSplits; ++r) {           // all in flight together
             const bool there = r < splits;
-            mr[r] = there ? ld_cluster(cluster_addr(&sh.m[0][h], r)) : -INFINITY;
-            lr[r] = there ? ld_cluster(cluster_addr(&sh.l[0][h], r)) : 0.f;
+            mr[r] = there ? ld_cluster(cluster_addr(&sh.top[h], r)) : -INFINITY;
+            lr[r] = there ? ld_cluster(cluster_addr(&sh.sum[h], r)) : 0.f;
             xr[r] = there ? ld_cluster(cluster_addr(&sh.o[0][h][c], r)) : 0.f;
         }
 #pragma unroll
         for (int r = 0; r < kMaxSplits; ++r) all = fmaxf(all, mr[r]);
 #pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r)
-            if (mr[r] != -INFINITY) {
-                const float f = weight(mr[r], all);
-                l = fmaf(f, lr[r], l);
-                x = fmaf(f, xr[r], x);
-            }
+        for (int r = 0; r < kMaxSplits; ++r) {
+            const float f = weight(mr[r], all);
+            l = fmaf(f, lr[r], l);
+            x = fmaf(f, xr[r], x);
+        }
         out[e] = Elem<T>::from_f(l == 0.f ? 0.f : x / l);
     }
-    if (splits > 1) cluster_sync();      // no CTA leaves while its memory is read
+    cluster_sync();                      // no CTA leaves while its memory is read
 }
 
 // What a CTA attends to: blocks [t0, t1) of the list's flattened positions.  The
