@@ -371,11 +371,12 @@ __device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t a) {
 }
 
 // Bound by the bytes of the selected rows: 64 requests x 2048 positions of 8 kv
-// heads (537 MB, gathered in runs of 256 bytes) take 94 us, 5.7 TB/s, 0.84 of the
-// copy rate; 256 queries of one prompt, whose 1.07 GB come from L2, take 95 us
+// heads (537 MB, gathered in runs of 256 bytes) take 89 us, 6.0 TB/s, 0.89 of the
+// copy rate; 256 queries of one prompt, whose 1.07 GB come from L2, take 85 us
 // and are bound by instruction issue (104 with V transposed by byte permutations
-// and a rescaling whenever the maximum moved); one request is bound by the chain list -> page table -> rows ->
-// join (8 us).
+// and a rescaling whenever the maximum moved, 95 with the join's weights formed
+// for every output); one request is bound by the chain list -> page table ->
+// rows -> join (7 us).
 //
 // A warp takes a block of 16 positions at a time.  K and V rows come by cp.async
 // into the warp's own ring, two half blocks ahead of the one in use, so there is
@@ -640,9 +641,9 @@ cudaError_t run_simt_g(const SelectedParams &p, int group, cudaStream_t s) {
 }  // namespace
 
 // As many CTAs as are resident at once (four of four warps per SM), while each
-// warp keeps a block.  With half as many a step of 16 requests x 4K positions
-// takes 29.4 us, with twice as many 29.0, so 23.2; 64 requests have a CTA per
-// (entry, kv head) either way.
+// warp keeps a block.  A step of 16 requests x 4K positions takes 22.2 us so, 29
+// with half as many CTAs, 27.3 with twice as many; 64 requests x 2048 positions
+// (a CTA per entry and kv head) take 88.8 us so, 89 to 94 with two and four.
 int selected_splits(int64_t batch, int n_kv_heads, int64_t top_k, int64_t page_size, int64_t max_len, int sms) {
     const int64_t units = batch * n_kv_heads;
     const int64_t pages = (max_len + page_size - 1) / page_size;
