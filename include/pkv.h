@@ -350,7 +350,7 @@ int pkv_paged_prefill(const pkv_kvcache *c, int32_t layer_id, const void *q, voi
  *     page of req_to_page, and, where req_to_token is given,
  *     req_to_token[r, position] = the same slot.
  * All arrays are int32 device arrays.  out_cache_loc and positions hold
- * max_new entries; what lies behind the last new token is left as it was, and
+ * max_new entries (2^30 at most); what lies behind the last new token is left as it was, and
  * so are table columns of positions that are not new.  The pages of earlier
  * positions (a partly filled last page, a cached prefix) are read from
  * req_to_page.  One kernel; nothing is allocated.

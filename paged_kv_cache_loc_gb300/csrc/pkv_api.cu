@@ -614,7 +614,7 @@ int pkv_paged_prefill(const pkv_kvcache *c, int32_t layer_id, const void *q, voi
 
 int pkv_build_tables(const pkv_kvcache *c, const pkv_tables *t, void *stream) {
     if (!c || !t) return PKV_ERR_ARG;
-    if (c->batch < 0 || c->batch > 65535 || t->max_new < 0 || t->n_free < 0) return PKV_ERR_ARG;
+    if (c->batch < 0 || c->batch > 65535 || t->max_new < 0 || t->max_new > 1 << 30 || t->n_free < 0) return PKV_ERR_ARG;
     if (c->num_reqs <= 0 || t->max_pages <= 0 || t->page_size <= 0) return PKV_ERR_ARG;
     if (c->size <= 0 || c->size > INT32_MAX || c->size % t->page_size) return PKV_ERR_ARG;
     if (static_cast<int64_t>(t->max_pages) * t->page_size > INT32_MAX) return PKV_ERR_ARG;

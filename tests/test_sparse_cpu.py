@@ -112,7 +112,7 @@ def tables(**kw):
 
 @pytest.mark.parametrize("kw", [dict(req_to_page=0), dict(free_start=0), dict(free_end=0), dict(free_end=0x40000),
                                 dict(free_pages=0), dict(out_cache_loc=0), dict(max_pages=0), dict(page_size=0),
-                                dict(page_size=24), dict(n_free=-1), dict(max_new=-1), dict(max_pages=1 << 30)])
+                                dict(page_size=24), dict(n_free=-1), dict(max_new=-1), dict(max_new=(1 << 30) + 1), dict(max_pages=1 << 30)])
 def test_build_tables_refuses(lib, kw):
     assert lib.pkv_build_tables(ctypes.byref(fake_cache()), ctypes.byref(tables(**kw)), None) == _lib.PKV_ERR_ARG
 
