@@ -22,12 +22,12 @@ from . import _lib
 from ._lib import PkvKVCache, PkvPages, PkvTables, check
 from .ops import KVCache, Workspace, _DTYPES, _need
 
-# The descriptors as bytes, field by field as in _lib (native sizes and alignment).
+# The descriptors as bytes, field by field as in _lib (native sizes and alignment, padding at the end included).
 _pack_cache = struct.Struct("PPiiiiqPiiPPPPPii")
-_pack_pages = struct.Struct("PPiiiii")
+_pack_pages = struct.Struct("PPiiiii0P")
 _pack_tables = struct.Struct("PPiiPPPiiPPPPP")
 for _s, _c in ((_pack_cache, PkvKVCache), (_pack_pages, PkvPages), (_pack_tables, PkvTables)):
-    assert _s.size <= ctypes.sizeof(_c) < _s.size + 8       # but for padding at the end
+    assert _s.size == ctypes.sizeof(_c)
 _i32, _f32 = ctypes.c_int32, ctypes.c_float
 _Tensor, _int32, _byref, _device = torch.Tensor, torch.int32, ctypes.byref, torch.cuda.current_device
 _vp, _st = ctypes.c_void_p, ctypes.c_char_p                 # _st: a packed descriptor
