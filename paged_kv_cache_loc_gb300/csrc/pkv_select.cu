@@ -18,6 +18,7 @@
 // is out whatever the rounding was; the few in between are scored again in 64
 // bits and ranked by (score, page).
 #include <atomic>
+#include <type_traits>
 
 #include "pkv_launch.h"
 #include "pkv_sparse.cuh"
@@ -294,7 +295,7 @@ struct SelShared {
     uint32_t big[kMaxSplits * kWarps];    // the scoring warps' largest |bound|
     int bin, above;
     int und_page[kUndecided];
-    long long und_key[kUndecided];
+    unsigned long long und_key[kUndecided];
     uint32_t und_in[kUndecided / 32];
 };
 
@@ -362,71 +363,92 @@ __device__ __forceinline__ float query_norm(const SelShared<D, G, NT> &sh) {
     return norm;
 }
 
-// Scores in 64-bit fixed point.  With |score| <= norm * big < 2^e, a term
-// counts in units of 2^(e - 61): a bf16 product is exact in fp32, an fp32 one
-// is taken as its rounding and the remainder, and integer sums do not round,
-// so the order of the terms does not matter.  Each term is off by less than one
-// unit, 2^-61 of the bound, where a sum in fp64 rounds to 2^-53 of the partial
-// sums.  On integer units: fp64 arithmetic, and conversions to 64-bit integers
-// with it, are so slow on this chip that a dozen pages took 4 to 9 us.
-// For exponents within fp32's range; the radix path takes fp64 otherwise.
-__device__ __forceinline__ bool fixed_point_exponent(float norm, float big, int *e) {
-    // x < 2^(exponent bits - 126); one more: norm is a rounded sum
-    const int a = static_cast<int>(__float_as_uint(norm) >> 23) - 126, b = static_cast<int>(__float_as_uint(big) >> 23) - 126;
-    *e = a + b + 1;
-    return *e >= -40 && *e <= 120;
-}
-// x in units of 2^(e - 61), towards zero; |x| < 2^e.
-__device__ __forceinline__ long long to_fixed(float x, int e) {
-    const uint32_t u = __float_as_uint(x);
-    const int exponent = static_cast<int>(u >> 23 & 255);
-    const int shift = exponent - 89 - e;     // of the 24-bit significand: 37 at most
-    const unsigned long long m = exponent ? (u & 0x7fffffu) | 0x800000u : 0u;
-    const long long v = static_cast<long long>(shift >= 0 ? m << shift : shift > -24 ? m >> -shift : 0ull);
-    return u >> 31 ? -v : v;
+// Scores in 64-bit integers.  A product of two numbers of 24 bits is m 2^x with a
+// whole m < 2^48.  A page's score for one query head is summed in units of
+// 2^(X - 8), X the largest x of its own products: a term is below 2^56 units and
+// the sum of 128 below 2^63.  Terms whose last bits fall below the unit lose them,
+// less than 2^-54 of a product with X (a sum in fp64 is off by 2^-53 of each
+// partial sum), the others are exact, and integer sums do not round, so the order
+// of the terms does not matter.  The unit is the page's own: one taken from the
+// largest bound of the entry would lose the whole score of pages beside one with
+// an outlying channel.  The sum is then rounded to 53 bits, which makes it
+// comparable with those of other units.  On integer units: fp64 arithmetic, and
+// conversions to 64-bit integers with it, are so slow on this chip that a dozen
+// pages took 4 to 9 us.
+
+// key64 of v 2^x, rounded to 53 bits (ties to even); x within -1000 .. 900.
+__device__ __forceinline__ unsigned long long key_of_sum(long long v, int x) {
+    if (v == 0) return 1ull << 63;
+    const unsigned long long size = v < 0 ? 0ull - static_cast<unsigned long long>(v) : static_cast<unsigned long long>(v);
+    const int lz = __clzll(static_cast<long long>(size));
+    const unsigned long long m = size << lz;                      // its first bit counts 2^(x - lz + 63)
+    unsigned long long u = (static_cast<unsigned long long>(x - lz + 63 + 1023) << 52) + (m >> 11 & 0xfffffffffffffull);
+    const unsigned rest = static_cast<unsigned>(m) & 0x7ffu;
+    u += rest > 0x400u || (rest == 0x400u && (u & 1));
+    return v < 0 ? ~(u | 1ull << 63) : u | 1ull << 63;
 }
 
-// A page's fixed-point score for one query head, by a warp.
+// The key of a page's score for one query head, by a warp whose lanes hold the
+// page's bounds.  q and the bounds are finite; bf16 ones have 8 bits in place of
+// 24, and products of 32 bits.
 template <typename T, int D>
-__device__ __forceinline__ long long fixed_score(const SelectParams &p, const float *q, int64_t bounds_row, int exponent) {
+__device__ __forceinline__ unsigned long long integer_key(const float *q, const float (&l)[D / 32], const float (&u)[D / 32]) {
+    constexpr int kLow = Elem<T>::bytes == 2 ? 16 : 0;            // bits of a significand that are 0
+    using Product = typename std::conditional<kLow == 16, uint32_t, unsigned long long>::type;
     const int lane = threadIdx.x & 31;
-    const T *lo = static_cast<const T *>(p.page_bounds) + bounds_row * 2 * D;
-    float l[D / 32], u[D / 32];
+    Product m[D / 32];                       // the product is m 2^(x - 300 + 2 kLow)
+    int x[D / 32], most = 0;
+    uint32_t sign[D / 32];
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
-        l[c] = Elem<T>::to_f(lo[c * 32 + lane]);
-        u[c] = Elem<T>::to_f(lo[D + c * 32 + lane]);
+        const float qv = q[c * 32 + lane];
+        const uint32_t a = __float_as_uint(qv), b = __float_as_uint(qv >= 0.f ? u[c] : l[c]);
+        const uint32_t ea = a >> 23 & 255u, eb = b >> 23 & 255u;
+        const uint32_t ma = (a & 0x7fffffu) | (ea ? 0x800000u : 0u), mb = (b & 0x7fffffu) | (eb ? 0x800000u : 0u);
+        m[c] = static_cast<Product>(ma >> kLow) * (mb >> kLow);
+        x[c] = static_cast<int>(max(ea, 1u) + max(eb, 1u));
+        sign[c] = a ^ b;
+        if (m[c]) most = max(most, x[c]);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
     long long s = 0;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-        const float qv = q[c * 32 + lane], x = qv >= 0.f ? u[c] : l[c], prod = qv * x;
-        s += to_fixed(prod, exponent);
-        if constexpr (Elem<T>::bytes == 4) s += to_fixed(fmaf(qv, x, -prod), exponent);
+    for (int c = 0; c < D / 32; ++c) {       // a product of 0 may have any x
+        const long long units = static_cast<long long>((static_cast<unsigned long long>(m[c]) << (8 + 2 * kLow)) >> min(max(most - x[c], 0), 63));
+        s += sign[c] >> 31 ? -units : units;
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    return s;
+    return key_of_sum(s, most - 308);
 }
 
-constexpr long long kLeastKey = -0x7fffffffffffffffLL - 1;
-
-// Ranks the `n` <= kUndecided pages of sh.und_page by their fixed-point scores
-// and sets the bits of sh.und_in for the first `need` of them.  sh.und_key is
-// kLeastKey on entry.
+// Ranks the `n` <= kUndecided pages of sh.und_page by their integer scores and
+// sets the bits of sh.und_in for the first `need` of them.  sh.und_key is 0 on
+// entry, below every key.  A warp takes a page and as many of the heads, which
+// share the loaded bounds, as keep all warps in work.
 template <typename T, int D, int G, int NT, typename Phys>
-__device__ __forceinline__ void rank_undecided(const SelectParams &p, SelShared<D, G, NT> &sh, int g, int n, int need, int exponent, Phys phys) {
+__device__ __forceinline__ void rank_undecided(const SelectParams &p, SelShared<D, G, NT> &sh, int g, int n, int need, Phys phys) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int x = warp; x < n * G; x += NT / 32) {                 // a warp per (page, head)
-        const int k = x / G, h = x % G;
-        const int64_t at = (p.layer_page0 + phys(sh.und_page[k])) * p.n_kv_heads + g;
-        const long long key = fixed_score<T, D>(p, sh.q[h], at, exponent);
+    int heads = 1;
+    while (heads < G && n * (G / heads) > NT / 32) heads *= 2;
+    for (int x = warp; x < n * (G / heads); x += NT / 32) {
+        const int k = x / (G / heads), h0 = x % (G / heads) * heads;
+        const T *lo = static_cast<const T *>(p.page_bounds) + ((p.layer_page0 + phys(sh.und_page[k])) * p.n_kv_heads + g) * 2 * D;
+        float l[D / 32], u[D / 32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            l[c] = Elem<T>::to_f(lo[c * 32 + lane]);
+            u[c] = Elem<T>::to_f(lo[D + c * 32 + lane]);
+        }
+        unsigned long long key = 0;
+#pragma unroll 1
+        for (int h = h0; h < h0 + heads; ++h) key = max(key, integer_key<T, D>(sh.q[h], l, u));
         if (lane == 0) atomicMax(&sh.und_key[k], key);
     }
     __syncthreads();
     bool in = false;
     if (tid < n) {
-        const long long key = sh.und_key[tid];
+        const unsigned long long key = sh.und_key[tid];
         const int pg = sh.und_page[tid];
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += sh.und_key[j] > key || (sh.und_key[j] == key && sh.und_page[j] < pg);
@@ -552,8 +574,7 @@ __device__ __forceinline__ void select_from_keys(const SelectParams &p, SelShare
         return;
     }
     const float slack = 2.f * kScoreEps * norm * big + kScoreTiny;   // 2e
-    int exponent = 0;
-    const bool finite = klo > key32(-INFINITY) && khi < key32(INFINITY) && slack < INFINITY && fixed_point_exponent(norm, big, &exponent);
+    const bool finite = klo > key32(-INFINITY) && khi < key32(INFINITY) && slack < INFINITY;   // q, bounds and scores
 
     // the threshold's bin, the error bound on both sides included, as keys
     // [lo, hi], narrowed until few pages lie in it or a bin is one key
@@ -594,11 +615,11 @@ __device__ __forceinline__ void select_from_keys(const SelectParams &p, SelShare
         each([&](uint32_t key, int page) {
             if (key >= lo && key <= hi) {
                 sh.und_page[k] = page;
-                sh.und_key[k++] = kLeastKey;
+                sh.und_key[k++] = 0;
             }
         });
         __syncthreads();
-        rank_undecided<T, D, G, NT>(p, sh, g, inside, need, exponent, phys);
+        rank_undecided<T, D, G, NT>(p, sh, g, inside, need, phys);
     } else if (need < inside) {
         select_by_radix<T, D, G, NT>(p, sh, g, keys, c0, c1, lo, hi, need, phys);
         least = finite ? hi + 1 : kMarkIn;                        // those marked in

@@ -565,6 +565,25 @@ def test_select_pages_nan_infinite_and_huge_bounds(dtype):
             check_select(*select_case(rng, dtype, 4, 2, 64, 1, np.array([1500, 40]), 17, 1, 1, bounds=bounds))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pages", [40, 250, 900])
+@pytest.mark.parametrize("where", ["any", "first", "unasked"])
+def test_select_pages_beside_a_few_outlying_bounds(dtype, pages, where):
+    """A few pages with one finite channel of 1e10 to 1e30 (any pages, the page
+    that is always in, a channel where q is 0): the error bound leaves all the
+    others undecided, and their order is that of their own scores."""
+    rng = np.random.default_rng(54)
+    for size in (1e10, 1e17, 1e20, 1e30):
+        cache, pg, q, (table, rows, lens) = select_case(rng, dtype, 4, 2, 64, 1, np.array([pages, 30]), 17, 1, 1)
+        if where == "unasked":
+            q[:, :, 3] = 0
+        for i, page in enumerate([0] if where == "first" else [5, 17, 30]):
+            phys = int(table[rows[0], page])
+            pg.page_bounds[0, phys, :, 1, 3] = size * (i + 1)
+            pg.page_bounds[0, phys, :, 0, 4] = -size * (i + 2)
+        check_select(cache, pg, q, (table, rows, lens))
+
+
 def test_select_pages_queries_of_one_request():
     """The queries of a prompt: entries that name one row with growing lengths."""
     rng = np.random.default_rng(27)
