@@ -417,9 +417,9 @@ typedef struct pkv_pages {
  * pkv_kv_write, pkv_rope_kv_write or pkv_decode_step on the same stream).
  * A key at the first slot of a page starts the page's bounds anew; other keys
  * widen the bounds that the page has.  The new tokens of a page stand next to
- * each other in out_cache_loc in ascending slot order, as pkv_build_tables
- * and the prefill's order give them (else that page's bounds are
- * unspecified).  Exact; a NaN key makes its channel's bounds NaN.  Requires
+ * each other in out_cache_loc in ascending slot order, with or without gaps, as
+ * pkv_build_tables and the prefill's order give them (else that page's bounds
+ * are unspecified).  Exact; a NaN key makes its channel's bounds NaN.  Requires
  * 16-byte aligned page_bounds and head rows of a multiple of 16 bytes.  Slots
  * outside [0, size) are device-data errors and are passed over.  n_new = 0 is a
  * no-op.  Does not read req_to_page.

@@ -16,11 +16,12 @@ using bf16 = __nv_bfloat16;
 constexpr int kBoundsThreads = 128;
 constexpr int kRowsAhead = 8;
 
-// A run is a maximal sequence of new tokens in consecutive slots of one page
-// (slots outside the pool, which are errors, are passed over).  A CTA takes the
-// runs that start among its block_tokens tokens (and follows a run beyond
-// them); thread c reduces 16-byte chunk c of the run's rows.  The bytes of the
-// new keys are read once, kRowsAhead rows in flight per thread.
+// A run is a maximal sequence of new tokens in one page, with or without gaps
+// between their slots (slots outside the pool, which are errors, are passed
+// over).  A CTA takes the runs that start among its block_tokens tokens (and
+// follows a run beyond them), so no page is updated by two CTAs; thread c reduces
+// 16-byte chunk c of the run's rows.  The bytes of the new keys are read once,
+// kRowsAhead rows of consecutive slots in flight per thread.
 //
 // kWrite: the cache write too (a sparse decode step).  A CTA then first copies
 // its own tokens' K and V rows to the pool; the bounds come from the new rows,
@@ -67,6 +68,8 @@ __global__ void __launch_bounds__(kBoundsThreads, 8) page_bounds_kernel(const Bo
             }
         }
     }
+    constexpr int kNotLooked = -2;
+    int before = kNotLooked;                 // the slot of the last token before i that is in the pool, -1: none
     for (int i = blockIdx.x * p.block_tokens; i < i_end;) {
         int loc = slot_of(i);
         if (!valid(loc)) {
@@ -74,27 +77,29 @@ __global__ void __launch_bounds__(kBoundsThreads, 8) page_bounds_kernel(const Bo
             ++i;
             continue;
         }
-        const int page = loc / p.page_size;
-        int off = loc - page * p.page_size;
-        bool begins = off == 0;
-        if (!begins) {
-            int j = i - 1, before = 0;
-            while (j >= 0 && !valid(before = slot_of(j))) --j;
-            begins = j < 0 || before != loc - 1;
+        const int page = loc / p.page_size, page0 = page * p.page_size;
+        const auto in_page = [&](int slot) { return static_cast<unsigned>(slot - page0) < static_cast<unsigned>(p.page_size); };
+        if (before == kNotLooked) {
+            before = -1;
+            for (int j = i - 1; j >= 0 && before < 0; --j) {
+                const int slot = slot_of(j);
+                if (valid(slot)) before = slot;
+            }
         }
+        const bool begins = before < 0 || !in_page(before);
         uint4 *dst = static_cast<uint4 *>(p.page_bounds) + (p.layer_page0 + page) * p.row_chunks * 2 +
                      (chunk / p.head_chunks) * p.head_chunks * 2 + chunk % p.head_chunks;
         uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
         bool have = false;                   // lo / hi hold something
         const bool mine = begins && chunk < p.row_chunks;
-        if (mine && off != 0) {
+        if (mine && loc != page0) {
             lo = dst[0];
             hi = dst[p.head_chunks];
             have = true;
         }
         for (;;) {
             // tokens i .. i + n - 1 are in consecutive slots of the page
-            const int most = min(p.n_new - i, p.page_size - off);
+            const int most = min(p.n_new - i, p.page_size - (loc - page0));
             int n = 1;
             while (n < most) {
                 if (i + n < base || i + n >= base + 32) look(i + n);
@@ -123,15 +128,16 @@ __global__ void __launch_bounds__(kBoundsThreads, 8) page_bounds_kernel(const Bo
                 }
             }
             i += n;
-            off += n;
             loc += n;
-            if (!begins || off == p.page_size) break;
+            before = loc - 1;
+            if (!begins) break;              // the CTA before goes on with this page
             int j = i, after = 0;
             while (j < p.n_new && !valid(after = slot_of(j))) ++j;
-            if (j == i || j >= p.n_new || after != loc) break;
+            if (j >= p.n_new || !in_page(after)) break;
             if (chunk == 0)
                 for (int x = i; x < j; ++x) record_error(p.err, __ldg(p.out_cache_loc + x));
             i = j;
+            loc = after;
         }
         if (mine) {
             dst[0] = lo;

@@ -304,6 +304,32 @@ def test_page_bounds_bad_slots_and_nan():
     assert np.array_equal(host(pg.page_bounds)[0], want, equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ps,n_pages,stay", [(4, 30, 0.6), (16, 80, 0.5), (16, 900, 0.8), (70, 60, 0.9)])
+def test_page_bounds_of_slots_with_gaps(dtype, ps, n_pages, stay):
+    """A page's new tokens in ascending slots that are not consecutive, a page
+    begun anew or not, spread over several CTAs, with the write and without; a
+    slot that stands twice in a row (not the page's first) counts as one page's."""
+    rng = np.random.default_rng(ps + n_pages)
+    k, v = pool(rng, 1, n_pages, ps, 2, 64, dtype)
+    loc = []
+    for page in rng.permutation(n_pages):
+        slots = page * ps + np.flatnonzero(rng.random(ps) < stay)
+        loc += list(slots) + [x for x in slots[-1:] if x % ps and rng.random() < 0.2]
+    cache = pkv.KVCache(k_buffer=k, v_buffer=v, req_to_token=dev(np.zeros((1, 1))), req_pool_indices=dev([]), seq_lens=dev([]), out_cache_loc=dev(loc))
+    pg = pkv.SparsePages.for_cache(cache, dev(np.zeros((1, 1))), ps, 4)
+    pg.page_bounds.copy_(torch.from_numpy(rng.standard_normal(pg.page_bounds.shape)))
+    before = pg.page_bounds.clone()
+    pkv.page_bounds(cache, 0, pg)
+    clean()
+    assert np.array_equal(host(pg.page_bounds)[0], S.page_bounds(host(before)[0], host(k)[0][loc], loc, ps))
+    pg.page_bounds.copy_(before)
+    kn, vn = (torch.randn(len(loc), 2, 64, device="cuda").to(DT[dtype]) for _ in range(2))
+    pkv.sparse_decode_step(cache, 0, pg, kn, vn, torch.zeros(0, 8, 64, dtype=DT[dtype], device="cuda"))
+    clean()
+    assert np.array_equal(host(pg.page_bounds)[0], S.page_bounds(host(before)[0], host(kn), loc, ps))
+
+
 def test_page_bounds_and_selection_behind_4_gb():
     """Bounds rows whose offset passes 2^32 bytes, in the second layer."""
     rng = np.random.default_rng(2)
