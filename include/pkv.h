@@ -361,7 +361,8 @@ int pkv_paged_prefill(const pkv_kvcache *c, int32_t layer_id, const void *q, voi
  * Device-data errors: a request row outside [0, num_reqs), n outside
  * [0, max_pages * ps] (or beyond max_ctx_len with req_to_token), q outside
  * [0, n] (such an entry counts as n = q = 0); more new tokens than max_new
- * (those beyond are dropped); a prefix sum beyond 2^31 - 1; a page outside
+ * (those beyond get no slot; the pages of all are taken and entered in
+ * req_to_page); a prefix sum beyond 2^31 - 1; a page outside
  * [0, size / ps) in req_to_page or free_pages, or a free list that runs out
  * (the tokens concerned get slot -1, and new pages of theirs -1, which the
  * write refuses in turn); *free_start outside [0, n_free].

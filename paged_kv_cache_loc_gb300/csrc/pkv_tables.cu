@@ -54,7 +54,29 @@ __device__ __forceinline__ Entry load_entry(const TablesParams &p, int b, bool r
 
 __device__ __forceinline__ int clamp31(long long x) { return static_cast<int>(x < 0x7fffffffLL ? x : 0x7fffffffLL); }
 
-__global__ void __launch_bounds__(kThreads) build_tables_kernel(const TablesParams p) {
+// The tokens beyond max_new get no slot, but their pages are taken: they go to
+// the table too, which otherwise would keep another request's pages.  Entries b0
+// .. b0 + n, by one CTA (out of line: an error's path, off the others' code).
+__device__ __noinline__ void enter_pages_without_slots(const TablesParams &p, const int *tok_off, const int *page_off, int b0, int n) {
+    const int lane = threadIdx.x & 31;
+    for (int a = threadIdx.x >> 5; a < n; a += kThreads / 32) {
+        const Entry x = load_entry(p, b0 + a, false);
+        const int old = x.len - x.q, fresh = ceil_div(old, p.page_size);
+        const long long kept = static_cast<long long>(p.max_new) - tok_off[a] + old;   // positions before it have slots
+        const long long from = kept > 0 ? max(static_cast<long long>(fresh), (kept + p.page_size - 1) / p.page_size) : fresh;
+        for (long long idx = from + lane; idx < fresh + x.need; idx += 32) {
+            const long long at = page_off[a] + (idx - fresh);
+            int page = at < p.n_free ? __ldg(p.free_pages + at) : -1;
+            if (static_cast<unsigned>(page) >= static_cast<unsigned long long>(p.n_pages)) {
+                record_error(p.err, at < p.n_free ? page : -300000LL - (b0 + a));
+                page = -1;
+            }
+            p.req_to_page[static_cast<int64_t>(x.row) * p.max_pages + idx] = page;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) build_tables_kernel(const __grid_constant__ TablesParams p) {
     __shared__ int tok_off[kTile];           // first new token of each entry of the tile
     __shared__ int page_off[kTile];          // its first place in the free list
     __shared__ long long warp_sum[kThreads / 32][3];
@@ -153,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TablesPara
             if (p.positions) p.positions[t] = pos;
             if (p.req_to_token) p.req_to_token[static_cast<int64_t>(x.row) * p.max_ctx_len + pos] = slot;
         }
+        if (first && total[0] > p.max_new) enter_pages_without_slots(p, tok_off, page_off, b0, n_tile);
         toks = total[0];
         pages = total[1];
         kvs = total[2];

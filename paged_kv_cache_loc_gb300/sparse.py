@@ -231,7 +231,8 @@ def build_tables(cache: KVCache, req_to_page: torch.Tensor, page_size: int, free
     becomes the next free place.  Writes cache.out_cache_loc, positions,
     cache.kv_indptr and cache.qo_indptr (each where it is given), and the new
     tokens' entries of cache.req_to_token unless token_table is False.  Tokens
-    beyond out_cache_loc's length are an error on the device; entries of
+    beyond out_cache_loc's length are an error on the device (they get no slot,
+    but their pages are taken and entered in req_to_page); entries of
     out_cache_loc behind the last new token stay as they are."""
     tokens, loc = cache.req_to_token, cache.out_cache_loc
     if tokens.dim() != 2:

@@ -250,6 +250,33 @@ def test_build_tables_too_many_tokens_and_bad_pages():
     assert error() == -2 and (host(t.cache.out_cache_loc)[:n] == -1).all()
 
 
+@pytest.mark.parametrize("batch,ps,room", [(2, 8, 12), (2, 8, 0), (7, 16, 1), (300, 4, 900), (5000, 2, 3000), (40, 1, 39)])
+def test_build_tables_pages_of_tokens_without_a_slot(batch, ps, room):
+    """With more tokens than out_cache_loc holds, the page table, the prefix sums
+    and the free list's place are those of all tokens: no page is lost, and no
+    column keeps a page of another request.  A list that runs out gives -1."""
+    rng = np.random.default_rng(batch + room)
+    q = rng.integers(0, 40, batch)
+    q[-1] = max(q[-1], room - int(q[:-1].sum()) + 1)
+    t, want, n = tables_case(rng, q + rng.integers(0, 30, batch), q, ps, spare=0, extra_free=0)
+    assert n > room
+    for cut in (0, 3):                                   # pages that the list lacks
+        free = t.free[:t.free.numel() - cut].contiguous()
+        table, loc, positions = t.table.clone(), t.cache.out_cache_loc[:room].clone(), t.positions[:room].clone()
+        cache = dataclasses.replace(t.cache, out_cache_loc=loc if room else None)
+        pkv.build_tables(cache, table, ps, free, t.start, t.end, positions if room else None, t.q)
+        detail = error()
+        assert detail == n or (cut and -300000 - batch < detail <= -300000)
+        gone = host(t.free)[free.numel():]
+        full = np.where(np.isin(want["req_to_page"], gone) & (host(t.table) != want["req_to_page"]), -1, want["req_to_page"])
+        assert np.array_equal(host(table), full)
+        assert int(t.end) == want["free_end"] - cut
+        assert np.array_equal(host(cache.kv_indptr), want["kv_indptr"]) and np.array_equal(host(cache.qo_indptr), want["qo_indptr"])
+        slots = want["out_cache_loc"][:room]
+        assert np.array_equal(host(loc), np.where(np.isin(slots // ps, gone), -1, slots))
+        assert np.array_equal(host(positions), want["positions"][:room])
+
+
 # ---------------------------------------------------------------------------
 # page_bounds
 # ---------------------------------------------------------------------------
