@@ -278,12 +278,6 @@ __device__ __forceinline__ uint32_t key32(float s) {
 __device__ __forceinline__ float unkey32(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
-__device__ __forceinline__ unsigned long long key64(double s) {
-    if (s != s) return ~0ull;
-    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(s + 0.0));
-    return u >> 63 ? ~u : u | (1ull << 63);
-}
-
 // NT: threads of the selecting CTA.
 template <int D, int G, int NT>
 struct SelShared {
@@ -376,7 +370,8 @@ __device__ __forceinline__ float query_norm(const SelShared<D, G, NT> &sh) {
 // conversions to 64-bit integers with it, are so slow on this chip that a dozen
 // pages took 4 to 9 us.
 
-// key64 of v 2^x, rounded to 53 bits (ties to even); x within -1000 .. 900.
+// An order-preserving key of v 2^x, rounded to the 53 bits of an fp64 number
+// (ties to even); x within -1000 .. 900.  ~0 stands for NaN.
 __device__ __forceinline__ unsigned long long key_of_sum(long long v, int x) {
     if (v == 0) return 1ull << 63;
     const unsigned long long size = v < 0 ? 0ull - static_cast<unsigned long long>(v) : static_cast<unsigned long long>(v);
@@ -459,10 +454,11 @@ __device__ __forceinline__ void rank_undecided(const SelectParams &p, SelShared<
     __syncthreads();
 }
 
-// The 64-bit key of a page's score for query head h, by a warp: lane partial
-// sums in a fixed order, so equal bounds give equal keys.
-template <typename T, int D>
-__device__ __forceinline__ unsigned long long exact_head_key(const SelectParams &p, const float *q, int64_t bounds_row) {
+// The key of a page's score over the group's heads, by a warp, for any q and
+// bounds: with numbers that are not finite among them the score is infinite or
+// NaN, as its products say.
+template <typename T, int D, int G>
+__device__ __forceinline__ unsigned long long any_key(const SelectParams &p, const float (&q)[G][D], int64_t bounds_row) {
     const int lane = threadIdx.x & 31;
     const T *lo = static_cast<const T *>(p.page_bounds) + bounds_row * 2 * D;
     float l[D / 32], u[D / 32];
@@ -471,60 +467,104 @@ __device__ __forceinline__ unsigned long long exact_head_key(const SelectParams 
         l[c] = Elem<T>::to_f(lo[c * 32 + lane]);
         u[c] = Elem<T>::to_f(lo[D + c * 32 + lane]);
     }
-    double s = 0.0;
+    unsigned long long key = 0;
+#pragma unroll 1
+    for (int h = 0; h < G; ++h) {
+        bool nan = false, up = false, down = false;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-        const float qv = q[c * 32 + lane];
-        s = fma(static_cast<double>(qv), static_cast<double>(qv >= 0.f ? u[c] : l[c]), s);
+        for (int c = 0; c < D / 32; ++c) {
+            const float qv = q[h][c * 32 + lane], x = qv >= 0.f ? u[c] : l[c], y = qv * x;
+            if (isfinite(qv) && isfinite(x)) continue;            // y may still overflow
+            nan |= y != y;
+            up |= y == INFINITY;
+            down |= y == -INFINITY;
+        }
+        nan = __any_sync(0xffffffffu, nan);
+        up = __any_sync(0xffffffffu, up);
+        down = __any_sync(0xffffffffu, down);
+        if (nan || (up && down)) return ~0ull;
+        key = max(key, up ? 0xfffull << 52 : down ? ~(0xfffull << 52) : integer_key<T, D>(q[h], l, u));
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    return key64(s);
+    return key;
 }
 
 // Many pages within rounding of the threshold (pages that are alike), or scores
-// that are not finite: radix selection on 64-bit keys, computed again in each
-// of its eight passes.  Sets the keys of the `need` best of the candidates with
-// keys in [lo, hi] to kMarkIn and those of the others to 0.
+// that are not finite: radix selection on 64-bit keys.  Each candidate's key is
+// formed once and its upper half takes the place of its 32-bit score; the lower
+// halves are formed again for those alone whose upper half is the threshold's,
+// where these are too many.  Sets the keys of the `keep` best candidates to
+// kMarkIn and those of the others to 0; candidates with scores above hi are in,
+// those below lo out.  One request at 32K positions, pages of 16 with a NaN among
+// them: 0.6 ms for the selection, all alike: 1.2 (13.4 with fp64 scores in each of
+// nine passes).  Out of line, so that its registers are not the others'; p by
+// reference wants a __grid_constant__ parameter, or every thread of the kernel
+// begins with a copy in local memory (selection of 32 x 4K: 11.9 us, not 10.4).
 template <typename T, int D, int G, int NT, typename Phys>
 __device__ __noinline__ void select_by_radix(const SelectParams &p, SelShared<D, G, NT> &sh, int g, uint32_t *keys, int c0, int c1, uint32_t lo,
-                                             uint32_t hi, int need, Phys phys) {
+                                             uint32_t hi, int keep, Phys phys) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const auto inside = [&](uint32_t k) { return k >= lo && k <= hi; };
-    const auto key_of = [&](int page) {
-        const int64_t at = (p.layer_page0 + phys(page)) * p.n_kv_heads + g;
-        unsigned long long best = 0;
-#pragma unroll 1
-        for (int h = 0; h < G; ++h) best = max(best, exact_head_key<T, D>(p, sh.q[h], at));
-        return best;
-    };
-    unsigned long long prefix = 0;
-    int rank = need;
-    for (int byte = 7; byte >= 0; --byte) {
+    const auto key_of = [&](int page) { return any_key<T, D, G>(p, sh.q, (p.layer_page0 + phys(page)) * p.n_kv_heads + g); };
+    for (int i = c0 + warp; i < c1; i += NT / 32) {
+        const uint32_t k = keys[i];
+        const uint32_t x = k > hi ? kMarkIn : k < lo ? 0u : static_cast<uint32_t>(key_of(i) >> 32);
+        __syncwarp();
+        if (lane == 0) keys[i] = x;
+    }
+    // the threshold, eight bits at a time; rank: how many of those equal to it are in
+    int rank = keep;
+    const auto narrow = [&](uint32_t &found, int shift, auto count) {
         for (int i = tid; i < kBins; i += NT) sh.hist[i] = 0;
         __syncthreads();
-        for (int i = c0 + warp; i < c1; i += (NT / 32)) {
-            if (!inside(keys[i])) continue;
-            const unsigned long long x = key_of(i);
-            if (lane == 0 && (byte == 7 || (x >> (8 * byte + 8)) == (prefix >> (8 * byte + 8))))
-                atomicAdd(&sh.hist[(x >> (8 * byte)) & 255], 1);
-        }
+        count([&](uint32_t x) {
+            if (shift == 24 || (x ^ found) >> (shift + 8) == 0) atomicAdd(&sh.hist[x >> shift & 255u], 1);
+        });
         __syncthreads();
         find_bin(sh, rank);
         rank -= sh.above;
-        prefix |= static_cast<unsigned long long>(sh.bin) << (8 * byte);
+        found |= static_cast<uint32_t>(sh.bin) << shift;
+    };
+    uint32_t top = 0;
+    for (int shift = 24; shift >= 0; shift -= 8)
+        narrow(top, shift, [&](auto add) {
+            for (int i = c0 + tid; i < c1; i += NT) add(keys[i]);
+        });
+    if (rank < sh.hist[sh.bin]) {            // the lower halves decide
+        const auto each_low = [&](auto f) {
+            for (int i = c0 + warp; i < c1; i += NT / 32)
+                if (keys[i] == top) {
+                    const uint32_t x = static_cast<uint32_t>(key_of(i));
+                    if (lane == 0) f(x, i);
+                }
+        };
         __syncthreads();
+        if (tid == 0) {
+            sh.lo[0] = 0xffffffffu;
+            sh.hi[0] = 0;
+        }
+        __syncthreads();
+        each_low([&](uint32_t x, int) {
+            atomicMin(&sh.lo[0], x);
+            atomicMax(&sh.hi[0], x);
+        });
+        __syncthreads();
+        if (sh.lo[0] != sh.hi[0]) {          // neither marked in nor out nor NaN: 0 < top < kMarkIn
+            uint32_t low = 0;
+            for (int shift = 24; shift >= 0; shift -= 8)
+                narrow(low, shift, [&](auto add) { each_low([&](uint32_t x, int) { add(x); }); });
+            each_low([&](uint32_t x, int i) {
+                if (x != low) keys[i] = x > low ? kMarkIn : 0u;
+            });
+        }
     }
-    // keys above the prefix are in, and the first `rank` that equal it
-    int equal = 0;
-    for (int i0 = c0; i0 < c1; i0 += (NT / 32)) {
-        const int i = i0 + warp;
-        const bool mine = i < c1 && inside(keys[i]);
-        const unsigned long long x = mine ? key_of(i) : 0;
-        int t;
-        const int at = equal + block_scan<NT / 32>(sh.warp_sum, static_cast<int>(mine && x == prefix && lane == 0), &t);
-        if (mine && lane == 0) keys[i] = x > prefix || (x == prefix && at <= rank) ? kMarkIn : 0u;
-        equal += t;
+    __syncthreads();
+    // those above the threshold are in, and the first `rank` that equal it
+    const int per = (c1 - c0 + NT - 1) / NT, i0 = min(c1, c0 + tid * per), i1 = min(c1, i0 + per);
+    int equal = 0, total;
+    for (int i = i0; i < i1; ++i) equal += keys[i] == top;
+    int before = block_scan<NT / 32>(sh.warp_sum, equal, &total) - equal;
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t k = keys[i];
+        keys[i] = k > top || (k == top && before++ < rank) ? kMarkIn : 0u;
     }
     __syncthreads();
 }
@@ -621,8 +661,8 @@ __device__ __forceinline__ void select_from_keys(const SelectParams &p, SelShare
         __syncthreads();
         rank_undecided<T, D, G, NT>(p, sh, g, inside, need, phys);
     } else if (need < inside) {
-        select_by_radix<T, D, G, NT>(p, sh, g, keys, c0, c1, lo, hi, need, phys);
-        least = finite ? hi + 1 : kMarkIn;                        // those marked in
+        select_by_radix<T, D, G, NT>(p, sh, g, keys, c0, c1, lo, hi, keep, phys);
+        least = kMarkIn;                     // those marked in
         int count = 0, total;
         each([&](uint32_t key, int) { count += key >= least; });
         mine_above = block_scan<NT / 32>(sh.warp_sum, count, &total) - count;
@@ -677,7 +717,7 @@ __device__ __forceinline__ int begin_entry(const SelectParams &p, SelShared<D, G
 constexpr int kClusterThreads = 256;
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kClusterThreads, 2) select_cluster_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kClusterThreads, 2) select_cluster_kernel(const __grid_constant__ SelectParams p) {
     constexpr int NT = kClusterThreads, kWarps = NT / 32;
     __shared__ SelShared<D, G, NT> sh;
     extern __shared__ __align__(16) unsigned char staged[];
@@ -799,7 +839,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_pages_kernel(const Sel
 }
 
 template <typename T, int D, int G, int NT>
-__global__ void __launch_bounds__(NT, NT == 256 ? 6 : 2) select_pages_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 6 : 2) select_pages_kernel(const __grid_constant__ SelectParams p) {
     __shared__ SelShared<D, G, NT> sh;
     extern __shared__ __align__(16) unsigned char staged[];
     griddep_launch();

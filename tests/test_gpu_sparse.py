@@ -637,6 +637,29 @@ def test_select_pages_beside_a_few_outlying_bounds(dtype, pages, where):
         check_select(cache, pg, q, (table, rows, lens))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pages", [700, 3000, 9000])
+@pytest.mark.parametrize("steps,other", [(1, None), (200, None), (200, math.nan), (200, -math.inf), (3, math.inf), (200, 1e30)])
+def test_select_pages_many_alike(dtype, pages, steps, other):
+    """More pages than a list holds whose scores are 2^20 and `steps` different
+    remainders of 2^-6 (the upper half of an fp64 score is the same), a few pages
+    with one other bound among them: the 64-bit order, ties to the lowest.  Small
+    contexts in one launch, long ones with their scores in the workspace."""
+    rng = np.random.default_rng(pages + steps)
+    q = torch.zeros(2, 4, 64, device="cuda")
+    q[:, :, 0] = 1.0
+    q[:, ::2, 1], q[:, 1::2, 1] = 1.0, -1.0
+
+    def bounds(n):
+        b = torch.zeros(1, n, 2, 2, 64, device="cuda")
+        b[..., 0] = 2.0 ** 20
+        b[..., 1] = dev(rng.integers(0, steps, (n, 2, 1)), torch.float32) * 2.0 ** -6
+        if other is not None:
+            b[0, dev(rng.permutation(n)[:7]).long(), :, 1, 1] = other
+        return b.to(DT[dtype])
+    check_select(*select_case(rng, dtype, 4, 2, 64, 1, np.array([pages, pages - 5]), 100, 1, 1, bounds=bounds, q=q.to(DT[dtype])))
+
+
 def test_select_pages_queries_of_one_request():
     """The queries of a prompt: entries that name one row with growing lengths."""
     rng = np.random.default_rng(27)
