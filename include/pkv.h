@@ -472,7 +472,8 @@ size_t pkv_select_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max
  * cluster and join their partials in shared memory.  Accumulation in fp32, one
  * rounding to the output dtype.  A selected value that is not finite makes its
  * channel of its group's outputs not finite.  Supported: f32 and bf16, head_dim
- * 64 or 128, G in {1, 2, 4, 8}.  Device-data errors as for pkv_select_pages, and a count
+ * 64 or 128, G in {1, 2, 4, 8}, 65535 kv heads at most (32767 for f32 with G =
+ * 8).  Device-data errors as for pkv_select_pages, and a count
  * outside [0, top_k] (clamped) or a listed page outside the context (skipped).
  */
 int pkv_paged_decode_selected(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg,

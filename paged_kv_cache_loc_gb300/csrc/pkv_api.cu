@@ -672,13 +672,15 @@ int check_pages(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg) {
 
 // Those of an entry point that attends or selects.
 int check_sparse(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const void *q, int32_t n_heads,
-                 const int32_t *sel, const int32_t *sel_counts, bool selects) {
+                 const int32_t *sel, const int32_t *sel_counts, bool selects, bool attends) {
     int rc = check_pages(c, layer_id, pg);
     if (rc) return rc;
     if (!pg->req_to_page || pg->max_pages <= 0 || c->num_reqs <= 0) return PKV_ERR_ARG;
     if (c->batch < 0 || c->batch > 65535 || c->max_len < 0) return PKV_ERR_ARG;
     if (c->max_len > static_cast<int64_t>(pg->max_pages) * pg->page_size) return PKV_ERR_ARG;
     if (n_heads <= 0 || n_heads % c->n_kv_heads || c->n_kv_heads > 65535) return PKV_ERR_ARG;
+    // grid y; fp32 attention takes a group of eight heads as two CTAs
+    if (attends && c->dtype == PKV_F32 && n_heads / c->n_kv_heads == 8 && c->n_kv_heads > 65535 / 2) return PKV_ERR_ARG;
     if (pg->top_k <= 0 || static_cast<int64_t>(pg->top_k) * pg->page_size > 1 << 30) return PKV_ERR_ARG;
     if (selects && (pg->n_first < 0 || pg->n_last < 0 || static_cast<int64_t>(pg->n_first) + pg->n_last > pg->top_k))
         return PKV_ERR_ARG;
@@ -832,7 +834,7 @@ size_t pkv_select_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t max
 
 int pkv_select_pages(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const void *q, int32_t n_heads,
                      int32_t *sel, int32_t *sel_counts, const pkv_workspace *ws, void *stream) {
-    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, true);
+    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, true, false);
     if (rc) return rc;
     if (c->batch == 0) return PKV_OK;
     DeviceInfo di;
@@ -851,7 +853,7 @@ int pkv_select_pages(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg
 int pkv_paged_decode_selected(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg, const int32_t *sel,
                               const int32_t *sel_counts, const void *q, void *o, int32_t n_heads, float sm_scale,
                               void *stream) {
-    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, false);
+    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, false, true);
     if (rc) return rc;
     if (!isfinite(sm_scale)) return PKV_ERR_ARG;
     if (c->batch == 0) return PKV_OK;
@@ -874,7 +876,7 @@ int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pag
     // everything is validated before anything is enqueued
     pkv::KvWriteParams wp;
     bool no_write = false;
-    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, true);
+    int rc = check_sparse(c, layer_id, pg, q, n_heads, sel, sel_counts, true, true);
     if (rc) return rc;
     rc = check_bounds(c, pg, n_new);
     if (rc) return rc;

@@ -185,6 +185,14 @@ def test_sparse_calls_refuse_arguments(lib):
     assert calls(lib, fake_cache(batch=0), p) == [_lib.PKV_OK] * 3       # nothing to do, no CUDA call
 
 
+def test_attention_refuses_more_kv_heads_than_a_grid_holds(lib):
+    """fp32 attention over a group of eight heads takes two CTAs per kv head."""
+    def f(n):
+        return calls(lib, fake_cache(dtype=_lib.PKV_F32, head_dim=64, n_kv_heads=n, batch=0), pages(), heads=8 * n)
+    assert f(32767) == [_lib.PKV_OK] * 3 and f(32768) == [_lib.PKV_OK, _lib.PKV_ERR_ARG, _lib.PKV_ERR_ARG]
+    assert calls(lib, fake_cache(n_kv_heads=65536), pages(), heads=65536) == BAD
+
+
 def test_page_bounds_refuses(lib):
     def f(c=fake_cache(), p=pages(), n=4, layer=2):
         return lib.pkv_page_bounds(ctypes.byref(c), layer, ctypes.byref(p), n, None)
