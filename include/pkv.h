@@ -445,7 +445,8 @@ int pkv_page_bounds(const pkv_kvcache *c, int32_t layer_id, const pkv_pages *pg,
  *               then -1;
  *   sel_counts  int32 [batch, n_kv_heads]: min(N, top_k).
  * A context whose length is 0 gets the count 0.  q: [batch, n_heads,
- * head_dim] of c->dtype.  Scores go to the workspace: ws->bytes must be
+ * head_dim] of c->dtype.  Scores go to the workspace, which serves one call at
+ * a time: ws->bytes must be
  * pkv_select_workspace_bytes(...) at least (ws may be NULL while c->max_len
  * needs no more than top_k pages).  A context has 2^30 pages at most.
  * Supported: f32 and bf16, head_dim 64 or

@@ -601,6 +601,47 @@ def test_select_pages_scores_that_32_bits_do_not_tell_apart(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_select_pages_scores_are_within_their_error_bound(dtype):
+    """What the order of the selection rests on: a 32-bit score is off from the
+    exact one by 2^-16 of max_h sum |q| times the largest |bound| at most (the
+    scores' order-preserving keys stand at the start of the workspace in the form
+    with two launches, which the size of the batch chooses)."""
+    batch, kv, group, d, n = 256, 8, 4, 128, 320
+    gen = torch.Generator("cuda").manual_seed(56)
+
+    def rnd(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+    ramp = 2.0 ** torch.linspace(-10, 10, d, device="cuda")
+    for kind in ("alike", "cancelling", "of all sizes", "two large", "ramps"):
+        q, b = rnd(batch, kv * group, d), rnd(n, kv, 2, d)
+        if kind == "cancelling":
+            q, b = q.sign() * (1 + 0.01 * q), b * 0.01 + 1000
+        elif kind == "of all sizes":
+            q, b = q * torch.exp(3 * rnd(batch, kv * group, d)), b * torch.exp(4 * rnd(n, kv, 1, d))
+        elif kind == "two large":
+            b[..., 7], b[..., 9] = 3e4, -3e4
+            q[..., 9] = q[..., 7]
+        elif kind == "ramps":
+            q, b = q.sign() * ramp.flip(0), b.sign() * ramp
+        q, b = q.to(DT[dtype]), b.to(DT[dtype])
+        b = torch.stack([b.amin(2), b.amax(2)], 2)[None].contiguous()
+        k = torch.zeros(1, n, kv, d, dtype=DT[dtype], device="cuda")
+        cache = pkv.KVCache(k_buffer=k, v_buffer=k, req_to_token=dev(np.zeros((1, 1))), req_pool_indices=dev(np.zeros(batch)),
+                            seq_lens=dev(np.full(batch, n)), max_len=n)
+        pg = pkv.SparsePages(b, dev(np.arange(n)[None]), 1, 8)
+        ws = ws_for(batch, kv, n, 1)
+        pkv.select_pages(cache, 0, pg, q, workspace=ws)
+        clean()
+        at = (ws.desc.base - ws.buffer.data_ptr())
+        keys = ws.buffer[at:at + batch * kv * n * 4].view(torch.int32).view(batch, kv, n)
+        score = torch.where(keys < 0, keys & 0x7fffffff, ~keys).view(torch.float32).double()
+        x, y = q.double().view(batch, kv, group * d).transpose(0, 1).reshape(kv, batch * group, d), b[0].double().permute(1, 2, 3, 0)
+        exact = (x.clamp(max=0) @ y[:, 0] + x.clamp(min=0) @ y[:, 1]).view(kv, batch, group, n).amax(2).transpose(0, 1)
+        bound = 2.0 ** -16 * q.double().abs().sum(-1).view(batch, kv, group).amax(2) * b.double().abs().max()
+        assert ((score - exact).abs() <= bound[:, :, None]).all(), kind
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_select_pages_nan_infinite_and_huge_bounds(dtype):
     rng = np.random.default_rng(26)
     for fill in (math.nan, math.inf, 3e38, -math.inf):
@@ -843,6 +884,25 @@ def test_attend_nan_and_infinite_values_reach_their_own_head_only():
     clean()
     assert torch.isnan(o[0, :4, 7]).all() and torch.isfinite(o[0, 4:]).all()
     assert torch.isfinite(o[0, :4, :7]).all() and torch.isfinite(o[0, :4, 8:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", [math.inf, -math.inf])
+def test_attend_an_infinite_value_makes_its_channel_not_finite(dtype, what):
+    """An infinite value in a selected position (bf16 weights go in as two parts,
+    so it may come out as NaN): not finite in its channel of its group's outputs,
+    every other output has the bits that it has without it."""
+    rng = np.random.default_rng(55)
+    lens = np.array([64, 300])
+    cache, pg, q, table, rows, sel, counts = attend_case(rng, dtype, 8, 2, 64, 8, lens, 8)
+    want = pkv.paged_decode_selected(cache, 1, pg, q, dev(sel), dev(counts)).clone()
+    for b, page in ((0, 3), (1, int(sel[1, 0, 4]))):
+        cache.v_buffer[1, int(table[rows[b], page]) * 8 + 2, 0, 7] = what
+    o = pkv.paged_decode_selected(cache, 1, pg, q, dev(sel), dev(counts))
+    clean()
+    assert not torch.isfinite(o[:, :4, 7]).any()
+    o[:, :4, 7] = want[:, :4, 7]
+    assert torch.equal(o, want)
 
 
 def test_attend_reports_bad_device_data():
