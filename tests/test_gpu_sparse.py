@@ -19,6 +19,7 @@ import torch
 import paged_kv_cache_loc_gb300 as pkv
 from oracle import sparse_oracle as S
 from paged_kv_cache_loc_gb300 import _lib, build
+from paged_kv_cache_loc_gb300 import pool as pkv_pool
 
 pytestmark = pytest.mark.gpu
 
@@ -1203,3 +1204,54 @@ def test_a_request_grows_over_pages():
         assert np.array_equal(host(sel), want[0]) and np.array_equal(host(counts), want[1])
         ref, reach = S.decode_selected(flat_k, flat_v, tab, range(batch), lens, *want, host(q), ps, d ** -0.5)
         close(o, ref, reach, flat_v, top_k * ps, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompts_on_tables_from_the_gpu_with_pages_of_the_host_pool(dtype):
+    """Two prompt chunks behind cached prefixes and one request without new
+    tokens: tables from q_lens, the step's entries from q_lens and positions
+    without a look at the host, the free list from PagePool and back to it."""
+    rng = np.random.default_rng(57)
+    ps, kv, heads, d, top_k, n_pages = 8, 2, 8, 64, 6, 96
+    host_pool = pkv_pool.PagePool(n_pages, ps)
+    old, q_lens = np.array([90, 33, 50]), np.array([40, 0, 17])
+    lens, n_new = old + q_lens, int(q_lens.sum())
+    rows = np.array([2, 0, 1])
+    table = np.full((3, 20), -1)
+    for b in range(3):
+        table[rows[b], :-(-old[b] // ps)] = [host_pool.alloc() for _ in range(-(-old[b] // ps))]
+    free = [host_pool.alloc() for _ in range(12)]
+    k, v = pool(rng, 1, n_pages, ps, kv, d, dtype)
+    ints = dict(dtype=torch.int32, device="cuda")
+    cache = pkv.KVCache(k_buffer=k, v_buffer=v, req_to_token=torch.zeros(3, 20 * ps, **ints), req_pool_indices=dev(rows), seq_lens=dev(lens),
+                        out_cache_loc=torch.zeros(n_new, **ints), max_len=int(lens.max()))
+    pg = pkv.SparsePages.for_cache(cache, dev(table), ps, top_k, 1, 1)
+    bounds = np.zeros((n_pages, kv, 2, d))
+    for b in range(3):
+        p = np.arange(old[b])
+        slots = table[rows[b], p // ps] * ps + p % ps
+        bounds = S.page_bounds(bounds, host(k)[0][slots], slots, ps)
+    pg.page_bounds[0].copy_(torch.from_numpy(bounds))
+    start, end, positions, ql = dev([0]), dev([0]), torch.zeros(n_new, **ints), dev(q_lens)
+    kn, vn, q = (torch.randn(n_new, h, d, device="cuda").to(DT[dtype]) for h in (kv, kv, heads))
+    pkv.build_tables(cache, pg.req_to_page, ps, dev(free), start, end, positions, ql)
+    entry_rows = torch.repeat_interleave(cache.req_pool_indices, ql, output_size=n_new)
+    step = dataclasses.replace(cache, req_pool_indices=entry_rows, seq_lens=positions + 1)
+    o, sel, counts = pkv.sparse_decode_step(step, 0, pg, kn, vn, q, workspace=ws_for(n_new, kv, cache.max_len, ps))
+    clean()
+    want = S.build_tables(rows, lens, q_lens, table, ps, free, 0)
+    assert np.array_equal(host(pg.req_to_page), want["req_to_page"])
+    bounds = S.page_bounds(bounds, host(kn), want["out_cache_loc"], ps)
+    assert np.array_equal(host(pg.page_bounds)[0], bounds)
+    e_rows, e_lens = np.repeat(rows, q_lens), want["positions"] + 1
+    chosen = S.select_pages(bounds, want["req_to_page"], e_rows, e_lens, host(q), ps, top_k, 1, 1)
+    assert np.array_equal(host(sel), chosen[0]) and np.array_equal(host(counts), chosen[1])
+    ref, reach = S.decode_selected(host(k)[0], host(v)[0], want["req_to_page"], e_rows, e_lens, *chosen, host(q), ps, d ** -0.5)
+    close(o, ref, reach, host(v)[0], top_k * ps, dtype)
+    # the requests end: their pages and the rest of the list go back
+    for b in range(3):
+        for page in host(pg.req_to_page)[rows[b], :-(-lens[b] // ps)]:
+            host_pool.free(int(page))
+    for page in free[int(end):]:
+        host_pool.free(page)
+    assert host_pool.num_free == n_pages
