@@ -1,10 +1,12 @@
 // pkv_bounds.cu -- the pages' key bounds of the sparse decode (pkv_page_bounds):
 // per page, kv head and channel the minimum and maximum of the keys written,
 // brought up to date with a batch of new keys, and the same together with the
-// cache write (a sparse decode step).  Bound by the bytes of the new rows and,
-// below a few thousand of them, by latency: 2.5 us for 32 keys, 12.3 us for 17.4K
-// keys of 8 kv heads (40 MB, 3.3 TB/s with the launch; 14.5 with every slot's
-// neighbours loaded one after the other).
+// cache write (a sparse decode step).  Bound by the latency of dependent loads
+// (slots, then a page's rows eight at a time): 2.4 us for 32 keys; 17.4K keys of 8
+// kv heads (40 MB) 12.4 us in a call with other inputs before it, 3.2 TB/s, half
+// of the copy rate (14.5 with every slot's neighbours loaded one after the
+// other), 7.2 with the rows in L2.  A third of its CTAs hold no token that begins
+// a page.
 #include "pkv_launch.h"
 #include "pkv_sparse.cuh"
 

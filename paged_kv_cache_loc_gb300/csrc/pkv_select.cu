@@ -916,9 +916,11 @@ cudaError_t launch_select(SelectParams p, cudaStream_t s) {
     cfg.gridDim = dim3(p.n_kv_heads, p.batch);
     cfg.dynamicSmemBytes = p.page_cap <= kStagedPages ? static_cast<size_t>(p.page_cap) * 4 : 0;
     cfg.numAttrs = 1;
-    // Long contexts are few: more threads for each (16 x 128K positions: 45.0 us
-    // with 512 threads, 54.9 with 256).  Many short ones: more CTAs per SM (256
-    // queries over 1024 pages: 196 us with 512, 170 with 256).
+    // More threads for a long list, more CTAs per SM for short ones.  Measured with
+    // 512 threads against 256: 16 x 128K positions in pages of 32 42 us against 55,
+    // one x 128K in pages of 16 18 against 52, 64 x 64K 206 against 214; 256 queries
+    // over 1024 pages 165 against 147, 256 x 4K 93 against 73.  (Between them 512
+    // measured a little better for 16 x 32K, 38 against 42.)
     cfg.blockDim = dim3(p.page_cap > 2048 ? 512 : 256);
     return p.page_cap > 2048 ? cudaLaunchKernelEx(&cfg, select_pages_kernel<T, D, G, 512>, p)
                              : cudaLaunchKernelEx(&cfg, select_pages_kernel<T, D, G, 256>, p);
@@ -947,10 +949,11 @@ bool sparse_supported(int dtype, int head_dim, int group) {
 // and the latency of the passes.  Two launches where the bounds are many: the
 // cluster's CTAs would hold their SMs while one of them selects, and the queries
 // of one request would not share bounds.  Measured, GPU time of the call in one
-// launch against two: selection for 32 x 4K positions 10.1 us against 15.2, a
-// step of one request at 32K 17.9 against 20.1, of 16 x 4K 23.2 against 27.7;
-// selection for 16 x 128K 46.4 against 45.0, a step of 256 queries of one prompt
-// 218 against 170.
+// launch against two: selection for 32 x 4K positions 10.4 us against 13.6, a
+// step of one request at 32K 17.3 against 19.2, of 16 x 4K 22.6 against 26.3;
+// selection for 16 x 128K in pages of 32 47.8 against 42.3, a step of 256 queries
+// of one prompt 199 against 147.  Batches of contexts that share nothing lie
+// between: 64 x 4K 20 against 22, 16 x 32K 35 against 42, 64 x 32K 103 against 112.
 void select_plan(SelectParams *p, int sms) {
     const int64_t units = static_cast<int64_t>(p->batch) * p->n_kv_heads, groups = p->page_cap / kScoreGroup;
     const int64_t warps = 16LL * sms;
