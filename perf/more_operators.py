@@ -79,7 +79,7 @@ def draw(rng):
     if op in ("copy", "compact"):
         c["layers"] = log(1, 32)
         c["bounds"] = rng.random() < 0.5
-        most = max(8, min(60000, (1 << 30) // (c["layers"] * 2 * ps * row)))
+        most = max(8, min(60000, (1 << 30) // (c["layers"] * 2 * (ps + 1) * row)))
         c["pages"] = log(8, most)
         c["moves"] = log(1, max(2, c["pages"] // (4 if op == "compact" else 2)))
         c["ctx_hi"] = log(1, 4096)
