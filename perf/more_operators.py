@@ -86,7 +86,7 @@ def draw(rng):
     elif op == "fork":
         c["layers"] = log(1, 32)
         c["fan"] = rng.randint(1, min(8, c["batch"]))
-        c["ctx_hi"] = log(1, max(2, min(8192, (1 << 31) // (c["layers"] * 2 * row * c["batch"]))))
+        c["ctx_hi"] = log(1, max(2, min(8192, (1 << 29) // (c["layers"] * 2 * row * c["batch"]))))
         c["ctx_lo"] = rng.randint(0, c["ctx_hi"])
         c["bounds"] = rng.random() < 0.5
     elif op == "release":
