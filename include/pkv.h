@@ -494,6 +494,117 @@ int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pag
                            int32_t *sel_counts, const pkv_workspace *ws, void *stream);
 
 /*
+ * The life of a cache's pages on the GPU.  pkv_build_tables takes pages from a
+ * free list; the calls below share, copy, give back and move them.  They work
+ * on the page table of pkv_build_tables and on one more array:
+ *   shares      int32 [size / page_size]: references to each page beyond the
+ *               first.  0 for a free page and for one that a single request
+ *               row holds, so that the pages of pkv_build_tables need no entry;
+ *               a caller that holds a page by other means than the table (a
+ *               cached prefix) adds one for it.
+ *   free_pages  int32 [n_free], free_start, free_end: as for
+ *               pkv_build_tables.  Taking pages moves the list's place
+ *               forward, giving back moves it backward and writes the pages in
+ *               front of it.
+ *   req_to_token (may be NULL) [num_reqs, c->max_ctx_len] and page_bounds (may
+ *               be NULL) are kept in step where they are given.
+ * None of the calls allocates or waits.  A page that several rows hold is not
+ * to be written to: before a row writes into a shared page (its length was cut
+ * back into one), give it a page of its own (pkv_copy_pages).
+ */
+typedef struct pkv_page_state {
+    int32_t *req_to_page;        /* [num_reqs, max_pages], in and out */
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t *shares;             /* [size / page_size], in and out */
+    int32_t *free_pages;         /* [n_free] */
+    const int32_t *free_start;   /* [1] */
+    int32_t *free_end;           /* [1], not free_start's word */
+    int32_t n_free;
+    int32_t *req_to_token;       /* [num_reqs, max_ctx_len], or NULL */
+    void *page_bounds;           /* [n_layers, size / page_size, n_kv_heads, 2, head_dim], or NULL */
+} pkv_page_state;
+
+/*
+ * For i < n: page dst[i] becomes a copy of page src[i], in k_buffer, v_buffer
+ * and page_bounds (where given) of every layer.  Bit-exact.  src, dst: int32
+ * [n] device arrays; a pair whose src is -1, or whose two pages are the same,
+ * is passed over.  A page may be the source of several pairs; a page that is
+ * the destination of two pairs, or of one and the source of another, ends
+ * with unspecified contents.  Other pages outside [0, size / page_size) are
+ * device-data errors, and their pairs are passed over.  Requires 16-byte
+ * aligned buffers (page_bounds too) and, as the calls below that copy, less
+ * than 2^30 16-byte chunks in a page's rows and bounds of all layers.
+ */
+int pkv_copy_pages(const pkv_kvcache *c, int32_t page_size, void *page_bounds, const int32_t *src,
+                   const int32_t *dst, int32_t n, void *stream);
+
+/*
+ * Fork request rows.  For entry b < c->batch the row r = c->req_pool_indices[b]
+ * takes over the first n = c->seq_lens[b] positions of row parents[b] (int32
+ * [batch]).  With ps = page_size:
+ *   - the pages of its floor(n / ps) full pages are the parent's, and their
+ *     shares go up by one;
+ *   - a partly filled last page is a page of its own: the entries take one each
+ *     from free_pages[*free_start ..] in entry order, and the parent page's
+ *     first n % ps rows of every layer, and its bounds (those of all keys
+ *     written to the parent's page), are copied to it;
+ *   - *free_end = *free_start + the pages taken;
+ *   - req_to_token[r, 0 .. n) is written where it is given.
+ * What the row held before is forgotten (pkv_release_pages gives it back).
+ * A parent may have several children in one call; the rows that take over must
+ * be distinct and no entry's parent (else the tables, counts and copied pages
+ * of the rows concerned are unspecified).  Device-data errors: a row outside
+ * [0, num_reqs), a row forked from itself, a length outside [0, max_pages * ps]
+ * (or beyond max_ctx_len with req_to_token) - such an entry counts as n = 0 -;
+ * a page of the parent outside [0, size / ps) (-1 in its place); a free list
+ * that runs out (-1), or holds such a page; *free_start outside [0, n_free].
+ */
+int pkv_fork_requests(const pkv_kvcache *c, const pkv_page_state *t, const int32_t *parents,
+                      void *stream);
+
+/*
+ * Give pages back.  Entry b < c->batch keeps the first keep_lens[b] (int32
+ * [batch]; NULL: 0) of the n = c->seq_lens[b] positions of row
+ * c->req_pool_indices[b]: its pages ceil(keep / ps) .. ceil(n / ps) - 1 lose
+ * one reference each and their entries of req_to_page become -1.  A page whose
+ * last reference that was is free: the m pages that this call frees are
+ * written to free_pages[*free_start - m .. *free_start) in ascending order,
+ * and *free_end = *free_start - m.  The order does not depend on that of the
+ * entries.  Reads neither the pool's rows nor c->max_len; req_to_token and
+ * page_bounds are left as they are.  Device-data errors: a row outside [0,
+ * num_reqs), a length outside [0, max_pages * ps], keep outside [0, n] (such
+ * an entry gives nothing back); a table entry outside [0, size / ps) (passed
+ * over; of a row that is named twice the second finds -1); more references
+ * dropped than a page has (the page is freed once); m above *free_start (the
+ * lowest pages are lost, and *free_end is 0); *free_start outside [0, n_free].
+ */
+int pkv_release_pages(const pkv_kvcache *c, const pkv_page_state *t, const int32_t *keep_lens,
+                      void *stream);
+
+/*
+ * Move the used pages to the pool's front.  A page is free if it stands in
+ * free_pages[*free_start .. n_free), used if not; U pages are used.  The used
+ * pages behind the first U go to the free pages among the first U, lowest to
+ * lowest, with their rows of every layer, their bounds and their shares.  Then
+ *   remap       int32 [size / page_size]: where each page went; itself for
+ *               pages that stay and for free ones;
+ *   req_to_page, req_to_token (where given): every entry in range, of all
+ *               num_reqs rows, follows remap; others stay as they are;
+ *   free_out    int32 [n_free]: free_out[*free_start ..] = U, U + 1, ...;
+ *               what lies before is not written.  May be free_pages itself.
+ * The list's place stays where it is; free_end is not used.  The workspace
+ * (pkv_compact_workspace_bytes) serves one call at a time.  Device-data
+ * errors: a page in the list outside [0, size / page_size), or a second time;
+ * *free_start outside [0, n_free].
+ */
+int pkv_compact_pages(const pkv_kvcache *c, const pkv_page_state *t, int32_t *free_out,
+                      int32_t *remap, const pkv_workspace *ws, void *stream);
+
+/* Workspace bytes that pkv_compact_pages needs (0 if n_pages < 1). */
+size_t pkv_compact_workspace_bytes(int64_t n_pages);
+
+/*
  * Paged decode for callers that cannot allocate device memory: code running
  * while another component holds a stream capture open in global mode (where
  * cudaMalloc is not allowed), plugins inside engines whose allocator owns all
@@ -534,7 +645,10 @@ int pkv_paged_decode_noalloc(const pkv_kvcache *c, int32_t layer_id, const void 
  *                  from its group's first entry's (head_dim 64);
  *   -200000 - c    shared-prefix CTA c was handed more positions than it
  *                  stages (not expected: the host sizes the grid for it);
- *   -300000 - b    the free list of pkv_build_tables ran out at entry b.
+ *   -300000 - b    the free list of pkv_build_tables or pkv_fork_requests ran
+ *                  out at entry b;
+ *   -400000 - b    pkv_release_pages: entry b dropped a reference that its
+ *                  page did not have.
  * An offending value can itself be negative (a negative slot, say).
  */
 int pkv_last_device_error(void *stream, int64_t *detail);

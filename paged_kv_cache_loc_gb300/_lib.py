@@ -90,6 +90,22 @@ class PkvPages(ctypes.Structure):
     ]
 
 
+class PkvPageState(ctypes.Structure):
+    """struct pkv_page_state."""
+    _fields_ = [
+        ("req_to_page", _vp),
+        ("max_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("shares", _vp),
+        ("free_pages", _vp),
+        ("free_start", _vp),
+        ("free_end", _vp),
+        ("n_free", ctypes.c_int32),
+        ("req_to_token", _vp),
+        ("page_bounds", _vp),
+    ]
+
+
 # name -> (restype, argtypes); every symbol declared in include/pkv.h
 SIGNATURES = {
     "pkv_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 4),
@@ -138,6 +154,15 @@ SIGNATURES = {
                                               ctypes.POINTER(PkvPages), _vp, _vp, ctypes.c_int32,
                                               _vp, _vp, ctypes.c_int32, ctypes.c_float, _vp, _vp,
                                               ctypes.POINTER(PkvWorkspace), _vp]),
+    "pkv_copy_pages": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.c_int32, _vp, _vp, _vp,
+                                      ctypes.c_int32, _vp]),
+    "pkv_fork_requests": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.POINTER(PkvPageState), _vp,
+                                         _vp]),
+    "pkv_release_pages": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.POINTER(PkvPageState), _vp,
+                                         _vp]),
+    "pkv_compact_pages": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.POINTER(PkvPageState), _vp,
+                                         _vp, ctypes.POINTER(PkvWorkspace), _vp]),
+    "pkv_compact_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64]),
     "pkv_last_device_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_int64)]),
     # include/pkv_pool.h (host page allocator)
     "pkv_pool_create": (_vp, [ctypes.c_int32, ctypes.c_int32]),

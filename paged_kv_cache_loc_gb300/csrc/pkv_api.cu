@@ -915,6 +915,170 @@ int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pag
     return map_launch(pkv::launch_decode_selected(ap, c->dtype, c->head_dim, group, s));
 }
 
+namespace {
+
+// The pages of the pool as runs of 16-byte chunks.  The chunks of one page in
+// all layers are counted in 31 bits.
+int page_runs(const pkv_kvcache *c, int32_t page_size, void *page_bounds, pkv::PageRuns *out) {
+    int rc = check_pool(c, 0);
+    if (rc) return rc;
+    if (page_size <= 0 || c->size % page_size || !aligned16(page_bounds)) return PKV_ERR_ARG;
+    pkv::PageRuns &r = *out;
+    r = pkv::PageRuns{};
+    const int64_t row_chunks = static_cast<int64_t>(c->n_kv_heads) * c->head_dim * elem_bytes(c->dtype) / 16;
+    r.k_buffer = c->k_buffer;
+    r.v_buffer = c->v_buffer;
+    r.page_bounds = page_bounds;
+    r.n_pages = c->size / page_size;
+    if (row_chunks > INT32_MAX) return PKV_ERR_ARG;
+    r.page_chunks = row_chunks * page_size;
+    r.bound_chunks = 2 * row_chunks;
+    r.n_layers = c->n_layers;
+    if (r.page_chunks + r.bound_chunks > INT32_MAX / 2 / c->n_layers) return PKV_ERR_ARG;
+    pkv::page_runs_units(&r);
+    return PKV_OK;
+}
+
+// What fork, release and compact share; *max_len: positions that a row of the
+// tables holds.
+int check_state(const pkv_kvcache *c, const pkv_page_state *t, int32_t *max_len) {
+    if (!c || !t) return PKV_ERR_ARG;
+    if (c->num_reqs <= 0 || t->max_pages <= 0 || t->page_size <= 0 || t->n_free < 0) return PKV_ERR_ARG;
+    if (c->size <= 0 || c->size > INT32_MAX || c->size % t->page_size) return PKV_ERR_ARG;
+    if (static_cast<int64_t>(t->max_pages) * t->page_size > INT32_MAX) return PKV_ERR_ARG;
+    if (t->req_to_token && c->max_ctx_len <= 0) return PKV_ERR_ARG;
+    if (!t->req_to_page || !t->shares || !t->free_start || (t->n_free > 0 && !t->free_pages)) return PKV_ERR_ARG;
+    *max_len = t->max_pages * t->page_size;
+    if (t->req_to_token && c->max_ctx_len < *max_len) *max_len = c->max_ctx_len;
+    return check_visible({c->req_pool_indices, c->seq_lens, t->req_to_page, t->shares, t->free_pages, t->free_start,
+                          t->free_end, t->req_to_token});
+}
+
+}  // namespace
+
+int pkv_copy_pages(const pkv_kvcache *c, int32_t page_size, void *page_bounds, const int32_t *src, const int32_t *dst,
+                   int32_t n, void *stream) {
+    pkv::CopyPagesParams p{};
+    int rc = page_runs(c, page_size, page_bounds, &p.runs);
+    if (rc) return rc;
+    if (n < 0) return PKV_ERR_ARG;
+    if (n == 0) return PKV_OK;
+    if (!src || !dst) return PKV_ERR_ARG;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({c->k_buffer, c->v_buffer, page_bounds, src, dst});
+    if (rc) return rc;
+    p.src = src;
+    p.dst = dst;
+    p.n = n;
+    p.err = di.err;
+    return map_launch(pkv::launch_copy_pages(p, di.sms, static_cast<cudaStream_t>(stream)));
+}
+
+int pkv_fork_requests(const pkv_kvcache *c, const pkv_page_state *t, const int32_t *parents, void *stream) {
+    pkv::ForkParams p{};
+    int rc = check_state(c, t, &p.max_len);
+    if (rc) return rc;
+    rc = page_runs(c, t->page_size, t->page_bounds, &p.runs);
+    if (rc) return rc;
+    if (c->batch < 0 || c->batch > 65535 || !t->free_end || t->free_start == t->free_end) return PKV_ERR_ARG;
+    if (c->batch > 0 && (!c->req_pool_indices || !c->seq_lens || !parents)) return PKV_ERR_ARG;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({c->k_buffer, c->v_buffer, t->page_bounds, parents});
+    if (rc) return rc;
+    p.children = c->req_pool_indices;
+    p.parents = parents;
+    p.seq_lens = c->seq_lens;
+    p.req_to_page = t->req_to_page;
+    p.shares = t->shares;
+    p.free_pages = t->free_pages;
+    p.free_start = t->free_start;
+    p.free_end = t->free_end;
+    p.req_to_token = t->req_to_token;
+    p.n_pages = p.runs.n_pages;
+    p.batch = c->batch;
+    p.num_reqs = c->num_reqs;
+    p.max_pages = t->max_pages;
+    p.max_ctx_len = c->max_ctx_len;
+    p.page_size = t->page_size;
+    p.n_free = t->n_free;
+    p.err = di.err;
+    return map_launch(pkv::launch_fork(p, di.sms, static_cast<cudaStream_t>(stream)));
+}
+
+int pkv_release_pages(const pkv_kvcache *c, const pkv_page_state *t, const int32_t *keep_lens, void *stream) {
+    pkv::ReleaseParams p{};
+    int32_t max_len;
+    int rc = check_state(c, t, &max_len);
+    if (rc) return rc;
+    if (c->batch < 0 || c->batch > 65535 || !t->free_end || t->free_start == t->free_end) return PKV_ERR_ARG;
+    if (c->batch > 0 && (!c->req_pool_indices || !c->seq_lens)) return PKV_ERR_ARG;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({keep_lens});
+    if (rc) return rc;
+    p.req_pool_indices = c->req_pool_indices;
+    p.seq_lens = c->seq_lens;
+    p.keep_lens = keep_lens;
+    p.req_to_page = t->req_to_page;
+    p.shares = t->shares;
+    p.free_pages = t->free_pages;
+    p.free_start = t->free_start;
+    p.free_end = t->free_end;
+    p.n_pages = c->size / t->page_size;
+    p.batch = c->batch;
+    p.num_reqs = c->num_reqs;
+    p.max_pages = t->max_pages;
+    p.max_len = t->max_pages * t->page_size;
+    p.page_size = t->page_size;
+    p.n_free = t->n_free;
+    p.err = di.err;
+    return map_launch(pkv::launch_release(p, di.sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pkv_compact_workspace_bytes(int64_t n_pages) {
+    if (n_pages < 1 || n_pages > INT32_MAX) return 0;
+    return (4 + 2 * static_cast<size_t>(n_pages / 2)) * sizeof(int32_t);
+}
+
+int pkv_compact_pages(const pkv_kvcache *c, const pkv_page_state *t, int32_t *free_out, int32_t *remap,
+                      const pkv_workspace *ws, void *stream) {
+    pkv::CompactParams p{};
+    int32_t max_len;
+    int rc = check_state(c, t, &max_len);
+    if (rc) return rc;
+    rc = page_runs(c, t->page_size, t->page_bounds, &p.runs);
+    if (rc) return rc;
+    if (!remap || (t->n_free > 0 && !free_out)) return PKV_ERR_ARG;
+    rc = ws_check(ws);
+    if (rc) return rc;
+    if (ws->bytes < pkv_compact_workspace_bytes(p.runs.n_pages)) return PKV_ERR_WORKSPACE;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({c->k_buffer, c->v_buffer, t->page_bounds, free_out, remap, ws->base});
+    if (rc) return rc;
+    p.req_to_page = t->req_to_page;
+    p.req_to_token = t->req_to_token;
+    p.shares = t->shares;
+    p.free_pages = t->free_pages;
+    p.free_start = t->free_start;
+    p.free_out = free_out;
+    p.remap = remap;
+    p.moves = static_cast<int32_t *>(ws->base);
+    p.cap = p.runs.n_pages / 2;
+    p.table_entries = static_cast<int64_t>(c->num_reqs) * t->max_pages;
+    p.token_entries = t->req_to_token ? static_cast<int64_t>(c->num_reqs) * c->max_ctx_len : 0;
+    p.page_size = t->page_size;
+    p.n_free = t->n_free;
+    p.err = di.err;
+    return map_launch(pkv::launch_compact(p, di.sms, static_cast<cudaStream_t>(stream)));
+}
+
 int pkv_last_device_error(void *stream, int64_t *detail) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
     DeviceInfo di;

@@ -254,6 +254,88 @@ struct SelectedParams {
     DevErr *err;
 };
 
+// The runs of a page (pkv_pages.cu): page p of layer l is page_chunks 16-byte
+// chunks from (l * n_pages + p) * page_chunks on in each buffer, and
+// bound_chunks of them in page_bounds (null: none).
+struct PageRuns {
+    void *k_buffer;
+    void *v_buffer;
+    void *page_bounds;
+    int64_t n_pages;
+    int64_t page_chunks;
+    int64_t bound_chunks;
+    int32_t n_layers;
+    int32_t page_units;           // pieces per page and buffer, set by page_runs_units
+    int32_t layer_units;          // pieces per page and layer
+};
+
+struct CopyPagesParams {
+    PageRuns runs;
+    const int32_t *src;           // [n]
+    const int32_t *dst;
+    int64_t n;
+    DevErr *err;
+};
+
+struct ForkParams {
+    PageRuns runs;
+    const int32_t *children;      // [batch] request rows
+    const int32_t *parents;
+    const int32_t *seq_lens;
+    int32_t *req_to_page;         // [num_reqs, max_pages]
+    int32_t *shares;              // [n_pages]
+    const int32_t *free_pages;    // [n_free]
+    const int32_t *free_start;    // [1]
+    int32_t *free_end;            // [1]
+    int32_t *req_to_token;        // [num_reqs, max_ctx_len] or null
+    int64_t n_pages;
+    int32_t batch;
+    int32_t num_reqs;
+    int32_t max_pages;
+    int32_t max_ctx_len;
+    int32_t max_len;              // positions that a row of the tables holds
+    int32_t page_size;
+    int32_t n_free;
+    DevErr *err;
+};
+
+struct ReleaseParams {
+    const int32_t *req_pool_indices;   // [batch]
+    const int32_t *seq_lens;
+    const int32_t *keep_lens;          // [batch] or null
+    int32_t *req_to_page;
+    int32_t *shares;
+    int32_t *free_pages;
+    const int32_t *free_start;
+    int32_t *free_end;
+    int64_t n_pages;
+    int32_t batch;
+    int32_t num_reqs;
+    int32_t max_pages;
+    int32_t max_len;
+    int32_t page_size;
+    int32_t n_free;
+    DevErr *err;
+};
+
+struct CompactParams {
+    PageRuns runs;
+    int32_t *req_to_page;
+    int32_t *req_to_token;        // or null
+    int32_t *shares;
+    const int32_t *free_pages;
+    const int32_t *free_start;
+    int32_t *free_out;            // [n_free], may be free_pages
+    int32_t *remap;               // [n_pages]
+    int32_t *moves;               // workspace: 4 + 2 cap ints
+    int64_t cap;                  // moves at most
+    int64_t table_entries;        // num_reqs * max_pages
+    int64_t token_entries;        // num_reqs * max_ctx_len, 0 without req_to_token
+    int32_t page_size;
+    int32_t n_free;
+    DevErr *err;
+};
+
 constexpr int kScoreGroup = 16;         // pages scored together
 
 constexpr int kDecodeMaxChunk = 2048;   // slot indices staged per split (or per piece)
@@ -267,6 +349,11 @@ cudaError_t launch_kv_write(const KvWriteParams &p, cudaStream_t s, bool step = 
 cudaError_t launch_rope_kv_write(const KvWriteParams &p, cudaStream_t s);
 cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t s);
 cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t s);
+void page_runs_units(PageRuns *r);
+cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t s);
+cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t s);
+cudaError_t launch_release(const ReleaseParams &p, int sms, cudaStream_t s);
+cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t s);
 // Whether the selection and the attention over it have a kernel for this shape.
 bool sparse_supported(int dtype, int head_dim, int group);
 // Sets p->splits and p->entries.
