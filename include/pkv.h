@@ -605,6 +605,48 @@ int pkv_compact_pages(const pkv_kvcache *c, const pkv_page_state *t, int32_t *fr
 size_t pkv_compact_workspace_bytes(int64_t n_pages);
 
 /*
+ * Attention of a chunk of new tokens through the page table of
+ * pkv_paged_decode_pages: drafts to verify, the next part of a prompt, single
+ * tokens beside both, or (causal = 0) queries over the states of an encoder.
+ * Entry b has the q_len = qo_indptr[b+1] - qo_indptr[b] rows from qo_indptr[b]
+ * on of q and o, and a context of n = c->seq_lens[b] positions.  Its row i,
+ * head h attends over the positions j <= n - q_len + i (causal: its new tokens,
+ * already written to the cache, are the last of the context) or over all n;
+ * position j is slot req_to_page[r * max_pages + j / page_size] * page_size +
+ * j % page_size, r = c->req_pool_indices[b].  A row that sees no position (n =
+ * 0; causal and n < q_len: the first q_len - n rows) gives 0.  q_len and n need
+ * not agree otherwise.  What a row does not see has no part in its result,
+ * whatever values stand there.
+ *   q, o        [n_q, n_heads, head_dim] of c->dtype, o not q; rows of o that
+ *               belong to no entry are left as they are.
+ *   max_q_len   host-side bound of q_len (max_q_len * G at most 65535 * 64);
+ *   c->max_len  that of n, max_pages * page_size at most.
+ * Scores, sums and outputs are held in fp32 and rounded once to the output;
+ * bf16 rounds the softmax's weights to bf16 for their product with V.  With few
+ * query rows the contexts are cut into splits whose partials go to the
+ * workspace and are joined by a second kernel: pkv_workspace_init(base, bytes,
+ * n_q, n_heads, head_dim, s, ..) holds s splits, and pkv_chunk_splits says how
+ * many a call of given sizes uses at most.  With a smaller workspace, or none,
+ * it uses fewer (one), with the same result up to fp32 rounding.  The workspace
+ * serves one call at a time.  Reads c->seq_lens, c->qo_indptr,
+ * c->req_pool_indices, c->num_reqs and the pool; not c->req_to_token,
+ * c->kv_indptr.  Supported: f32 and bf16, head_dim 64 or 128, G in {1, 2, 4, 8}.
+ * Device-data errors: a request row outside [0, num_reqs), rows outside [0,
+ * n_q), q_len outside [0, max_q_len], n outside [0, c->max_len] (the entry's
+ * rows are neither read nor written); a page outside [0, size / page_size)
+ * (page 0 in its place).
+ */
+int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_to_page,
+                    int32_t max_pages, int32_t page_size, const void *q, void *o, int32_t n_q,
+                    int32_t n_heads, int32_t max_q_len, int32_t causal, float sm_scale,
+                    const pkv_workspace *ws, void *stream);
+
+/* Splits that pkv_paged_chunk uses at most for these sizes (c->batch,
+ * c->max_len, the pool's heads and types), or a negative PKV_ERR_* code.
+ * Host-only; enqueues nothing. */
+int32_t pkv_chunk_splits(const pkv_kvcache *c, int32_t n_heads, int32_t max_q_len);
+
+/*
  * Paged decode for callers that cannot allocate device memory: code running
  * while another component holds a stream capture open in global mode (where
  * cudaMalloc is not allowed), plugins inside engines whose allocator owns all

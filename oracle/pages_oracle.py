@@ -87,3 +87,30 @@ def compact(k, v, bounds, ps, table, tokens, shares, free, start):
             if 0 <= tokens[i] < n_pages * ps:
                 tokens[i] = remap[tokens[i] // ps] * ps + tokens[i] % ps
     return k, v, bounds, table, tokens, shares, free, remap
+
+
+def chunk(k, v, table, ps, rows, lens, qo_indptr, q, causal, scale, o):
+    """Chunk attention in 64 bits over one layer's K and V [size, kv, d]; q [n_q,
+    heads, d].  Returns (o with the entries' rows replaced, the largest sum_c
+    |q_c k_c| |scale| of a pair that is seen, the largest |v| that is seen)."""
+    k, v, q, o = (np.asarray(x, np.float64) for x in (k, v, q, o))
+    o = o.copy()
+    kv, g = k.shape[1], q.shape[1] // k.shape[1]
+    most, largest = 0.0, 0.0
+    for b, (r, n) in enumerate(zip(rows, lens)):
+        lo, hi = qo_indptr[b], qo_indptr[b + 1]
+        pos = np.arange(n)
+        slots = table[r, pos // ps].astype(np.int64) * ps + pos % ps
+        for i in range(lo, hi):
+            m = n - (hi - lo) + (i - lo) + 1 if causal else n
+            if m <= 0:
+                o[i] = 0
+                continue
+            for h in range(kv):
+                kk, vv, qq = k[slots[:m], h], v[slots[:m], h], q[i, h * g:(h + 1) * g]
+                s = qq @ kk.T * scale
+                w = np.exp(s - s.max(-1, keepdims=True))
+                o[i, h * g:(h + 1) * g] = (w / w.sum(-1, keepdims=True)) @ vv
+                most = max(most, (np.abs(qq) @ np.abs(kk).T).max() * abs(scale))
+                largest = max(largest, np.abs(vv).max())
+    return o, most, largest

@@ -21,6 +21,7 @@ Operations (AstrAI docs/guides/inference.md):
   fork_requests   request rows that take over another row's context: full pages shared, the last one copied
   release_pages   pages given back to the free list
   compact_pages   the used pages moved to the pool's front
+  paged_chunk     attention of new tokens, one to thousands per entry, through a page table
   paged_prefill   ragged causal prefill over qo_indptr / kv_indptr ("Attention Backend")
 """
 from .ops import (KVCache, Workspace, decode_plan, decode_step, kv_write,  # noqa: F401
@@ -28,10 +29,11 @@ from .ops import (KVCache, Workspace, decode_plan, decode_step, kv_write,  # noq
                   paged_decode_shared, paged_prefill, rope_kv_write)
 from .sparse import (SparsePages, build_tables, page_bounds, paged_decode_selected,  # noqa: F401
                      select_pages, select_workspace, select_workspace_bytes, sparse_decode_step)
-from .pages import compact_pages, compact_workspace, copy_pages, fork_requests, release_pages  # noqa: F401
+from .pages import (chunk_workspace, compact_pages, compact_workspace, copy_pages, fork_requests,  # noqa: F401
+                    paged_chunk, release_pages)
 from ._lib import PkvError, load  # noqa: F401
 
 __all__ = ["KVCache", "Workspace", "kv_write", "rope_kv_write", "paged_decode", "decode_step",
            "paged_decode_pages", "paged_decode_shared", "paged_prefill", "paged_decode_noalloc", "decode_plan",
            "SparsePages", "build_tables", "page_bounds", "select_pages", "select_workspace", "select_workspace_bytes",
-           "paged_decode_selected", "sparse_decode_step", "copy_pages", "fork_requests", "release_pages", "compact_pages", "compact_workspace", "last_device_error", "PkvError", "load"]
+           "paged_decode_selected", "sparse_decode_step", "copy_pages", "fork_requests", "release_pages", "compact_pages", "compact_workspace", "paged_chunk", "chunk_workspace", "last_device_error", "PkvError", "load"]

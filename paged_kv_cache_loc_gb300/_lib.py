@@ -163,6 +163,11 @@ SIGNATURES = {
     "pkv_compact_pages": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.POINTER(PkvPageState), _vp,
                                          _vp, ctypes.POINTER(PkvWorkspace), _vp]),
     "pkv_compact_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64]),
+    "pkv_paged_chunk": (ctypes.c_int, [ctypes.POINTER(PkvKVCache), ctypes.c_int32, _vp, ctypes.c_int32,
+                                       ctypes.c_int32, _vp, _vp, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                       ctypes.POINTER(PkvWorkspace), _vp]),
+    "pkv_chunk_splits": (ctypes.c_int32, [ctypes.POINTER(PkvKVCache), ctypes.c_int32, ctypes.c_int32]),
     "pkv_last_device_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_int64)]),
     # include/pkv_pool.h (host page allocator)
     "pkv_pool_create": (_vp, [ctypes.c_int32, ctypes.c_int32]),

@@ -1079,6 +1079,99 @@ int pkv_compact_pages(const pkv_kvcache *c, const pkv_page_state *t, int32_t *fr
     return map_launch(pkv::launch_compact(p, di.sms, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+// What pkv_paged_chunk and pkv_chunk_splits refuse alike.
+int check_chunk(const pkv_kvcache *c, int32_t n_heads, int32_t max_q_len, int *group) {
+    int rc = check_pool(c, 0);
+    if (rc) return rc;
+    if (c->batch < 0 || c->batch > 65535 || c->max_len < 0 || max_q_len < 0) return PKV_ERR_ARG;
+    if (n_heads <= 0 || n_heads % c->n_kv_heads) return PKV_ERR_ARG;
+    *group = n_heads / c->n_kv_heads;
+    if (!pkv::chunk_supported(c->dtype, c->head_dim, *group)) return PKV_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_q_len) * *group > pkv::kChunkMaxRows) return PKV_ERR_ARG;
+    if (static_cast<int64_t>(max_q_len) * n_heads > INT32_MAX) return PKV_ERR_ARG;   // the join's grid
+    return PKV_OK;
+}
+
+}  // namespace
+
+int32_t pkv_chunk_splits(const pkv_kvcache *c, int32_t n_heads, int32_t max_q_len) {
+    int group;
+    int rc = check_chunk(c, n_heads, max_q_len, &group);
+    if (rc) return rc;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    if (c->batch == 0 || max_q_len == 0) return 1;
+    pkv::ChunkPlan plan;
+    pkv::chunk_plan(&plan, c->dtype, c->n_kv_heads, group, c->batch, max_q_len, c->max_len, di.sms, INT32_MAX);
+    return plan.n_splits;
+}
+
+int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_to_page, int32_t max_pages,
+                    int32_t page_size, const void *q, void *o, int32_t n_q, int32_t n_heads, int32_t max_q_len,
+                    int32_t causal, float sm_scale, const pkv_workspace *ws, void *stream) {
+    int group;
+    int rc = check_chunk(c, n_heads, max_q_len, &group);
+    if (rc) return rc;
+    if (layer_id < 0 || layer_id >= c->n_layers || !isfinite(sm_scale)) return PKV_ERR_ARG;
+    if (page_size <= 0 || c->size % page_size || !req_to_page || max_pages <= 0 || c->num_reqs <= 0) return PKV_ERR_ARG;
+    if (c->max_len > static_cast<int64_t>(max_pages) * page_size || n_q < 0) return PKV_ERR_ARG;
+    if (c->batch > 0 && (!c->req_pool_indices || !c->seq_lens || !c->qo_indptr)) return PKV_ERR_ARG;
+    if (c->batch == 0 || n_q == 0 || max_q_len == 0) return PKV_OK;
+    if (!q || !o || q == o || !aligned16(q) || !aligned16(o)) return PKV_ERR_ARG;
+    DeviceInfo di;
+    rc = device_info(&di);
+    if (rc) return rc;
+    rc = check_visible({c->k_buffer, c->v_buffer, req_to_page, c->req_pool_indices, c->seq_lens, c->qo_indptr, q, o,
+                        ws ? ws->base : nullptr});
+    if (rc) return rc;
+    int64_t most = 1;                            // splits whose partials the workspace holds
+    if (ws) {
+        rc = ws_check(ws);
+        if (rc) return rc;
+        const int64_t units = static_cast<int64_t>(ws->max_batch) * ws->n_heads * ws->max_splits;
+        const int64_t rows = static_cast<int64_t>(n_q) * n_heads;
+        most = units * ws->head_dim / (rows * c->head_dim);
+        if (units / rows < most) most = units / rows;
+    }
+    pkv::ChunkPlan plan;
+    pkv::chunk_plan(&plan, c->dtype, c->n_kv_heads, group, c->batch, max_q_len, c->max_len, di.sms, most > 1 ? most : 1);
+    pkv::ChunkParams p{};
+    p.q = q;
+    p.o = o;
+    p.k_buffer = c->k_buffer;
+    p.v_buffer = c->v_buffer;
+    p.req_to_page = req_to_page;
+    p.req_pool_indices = c->req_pool_indices;
+    p.seq_lens = c->seq_lens;
+    p.qo_indptr = c->qo_indptr;
+    if (plan.n_splits > 1) {
+        p.o_part = ws->o_part;
+        p.ml_part = ws->ml_part;
+    }
+    p.size = c->size;
+    p.layer_row0 = static_cast<int64_t>(layer_id) * c->size;
+    p.n_pages = c->size / page_size;
+    p.max_pages = max_pages;
+    p.page_size = page_size;
+    p.n_kv_heads = c->n_kv_heads;
+    p.n_heads = n_heads;
+    while (1 << p.group_shift < group) ++p.group_shift;
+    p.num_reqs = c->num_reqs;
+    p.batch = c->batch;
+    p.n_q = n_q;
+    p.max_q_len = max_q_len;
+    p.max_len = c->max_len;
+    p.causal = causal ? 1 : 0;
+    p.n_splits = plan.n_splits;
+    p.split_len = plan.split_len;
+    p.scale_log2 = sm_scale * 1.4426950408889634f;
+    p.err = di.err;
+    return map_launch(pkv::launch_chunk(p, c->dtype, c->head_dim, group, static_cast<cudaStream_t>(stream)));
+}
+
 int pkv_last_device_error(void *stream, int64_t *detail) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
     DeviceInfo di;

@@ -1,0 +1,342 @@
+// pkv_chunk.cu -- attention of each entry's new tokens over its context through
+// the page table (pkv_paged_chunk): the fp32 kernel and the join of a context's
+// splits.
+//
+// Row i of entry b, head h sees the positions j <= lim(i) (causal: n - q_len + i,
+// else n - 1) and gets
+//   o = sum_j softmax_j(scale q . k_j) v_j.
+// One pass over the keys with a running maximum m (in base-2 units of the scaled
+// score) and sum l; a context that is cut into splits ends in partials o / l and
+// (m, l), joined as o = sum_s l_s 2^(m_s - M) o_s / sum_s l_s 2^(m_s - M).
+//
+// fp32: products of fp32 rows have no tensor-core form that keeps 24 bits, so
+// this runs on the FMA units.  A CTA of 256 threads takes 64 rows (position,
+// head in group) and 64 keys at a time; a thread holds a 4 x 4 block of scores
+// and a 4 x (D / 16) block of o, so a 16-byte shared-memory load feeds eight
+// FMAs.  K of the next tile is copied while the softmax and P V run, V while
+// the next scores do.
+#include <atomic>
+
+#include "pkv_chunk.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 64;
+constexpr int kTok = 64;
+
+template <int D>
+struct Layout {
+    // Floats.  Unpadded; a 16-byte chunk c of a row stands at c ^ x, so that the
+    // rows that a warp reads at once meet different banks: x is r / 4 % 2 in Q
+    // and P (two row blocks per warp) and r % 8 in K.
+    static constexpr int kQ = 0;                      // [kRows][D]
+    static constexpr int kK = kQ + kRows * D;         // [kTok][D]
+    static constexpr int kV = kK + kTok * D;          // [kTok][D]
+    static constexpr int kP = kV + kTok * D;          // [kRows][kTok]
+    static constexpr int kFloats = kP + kRows * kTok;
+    static constexpr int kBytes = kFloats * 4 + 2 * kTok * 4;   // + slots of two tiles
+    static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_constant__ ChunkParams p) {
+    using L = Layout<D>;
+    extern __shared__ __align__(16) float smem[];
+    float *sQ = smem + L::kQ, *sK = smem + L::kK, *sV = smem + L::kV, *sP = smem + L::kP;
+    int *slots = reinterpret_cast<int *>(smem + L::kFloats);
+    constexpr int kChunks = D / 4, kOut = D / 64;       // 16-byte chunks per row; float4 columns of o per thread
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int g = blockIdx.x, split = blockIdx.y % p.n_splits, G = 1 << p.group_shift;
+    const ChunkEntry e = load_chunk_entry(p, blockIdx.z, g == 0 && blockIdx.y == 0 && tid == 0);
+    const int rows = e.q_len << p.group_shift;
+    // the entry's last rows, which see most, first
+    const int tile = (rows + kRows - 1) / kRows - 1 - static_cast<int>(blockIdx.y / p.n_splits);
+    if (tile < 0) return;
+    const int row0 = tile * kRows;
+    const int last = (min(row0 + kRows, rows) - 1) >> p.group_shift;
+    const int kv_lo = split * p.split_len;
+    const int kv_end = min(min(kv_lo + p.split_len, e.kv_len), chunk_limit(p, e, last) + 1);
+    // nothing to see: the first split gives zeros where no other one runs
+    if (kv_end <= kv_lo && (split > 0 || p.n_splits > 1)) {
+        return;
+    }
+    const int n_tiles = kv_end > kv_lo ? (kv_end - kv_lo + kTok - 1) / kTok : 0;
+    const int seen_by_all = chunk_limit(p, e, row0 >> p.group_shift);
+
+    const float *kbase = static_cast<const float *>(p.k_buffer) + (p.layer_row0 * p.n_kv_heads + g) * D;
+    const float *vbase = static_cast<const float *>(p.v_buffer) + (p.layer_row0 * p.n_kv_heads + g) * D;
+    const int64_t pitch = static_cast<int64_t>(p.n_kv_heads) * D;
+    const int32_t *table = p.req_to_page + static_cast<int64_t>(e.req) * p.max_pages;
+    auto stage_slots = [&](int t) {                     // of tile t; -1 behind the end
+        if (tid >= kTok) return;
+        const int j = kv_lo + t * kTok + tid;
+        int slot = -1;
+        if (j < kv_end) {
+            const int i = j / p.page_size, page = __ldg(table + i);
+            const bool ok = static_cast<unsigned long long>(static_cast<long long>(page)) < static_cast<unsigned long long>(p.n_pages);
+            if (!ok) record_error(p.err, page);
+            slot = (ok ? page : 0) * p.page_size + (j - i * p.page_size);
+        }
+        slots[(t & 1) * kTok + tid] = slot;
+    };
+    auto copy = [&](float *dst, int mask, const float *base, int t) {
+        const int *sl = slots + (t & 1) * kTok;
+#pragma unroll
+        for (int i = tid; i < kTok * kChunks; i += kThreads) {
+            const int r = i / kChunks, c = i % kChunks, slot = sl[r];
+            cp_async16(dst + r * D + (c ^ (r & mask)) * 4, slot >= 0 ? base + slot * pitch + c * 4 : base, slot >= 0 ? 16 : 0);
+        }
+        cp_async_commit();
+    };
+
+    if (n_tiles > 0) stage_slots(0);
+    for (int i = tid; i < kRows * kChunks; i += kThreads) {
+        const int r = i / kChunks, c = i % kChunks, R = row0 + r;
+        const float *q = static_cast<const float *>(p.q);
+        const bool ok = R < rows;
+        const int64_t at = (static_cast<int64_t>(e.qo0 + (R >> p.group_shift)) * p.n_heads + g * G + (R & (G - 1))) * D + c * 4;
+        cp_async16(sQ + r * D + (c ^ (r >> 2 & 1)) * 4, ok ? q + at : q, ok ? 16 : 0);
+    }
+    cp_async_commit();
+    __syncthreads();
+    if (n_tiles > 0) {
+        copy(sK, 7, kbase, 0);
+        copy(sV, 0, vbase, 0);
+    }
+
+    float o[4][4 * kOut], m[4], l[4];
+    int lim[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        const int R = row0 + ty * 4 + r;
+        lim[r] = R < rows ? chunk_limit(p, e, R >> p.group_shift) : -1;
+#pragma unroll
+        for (int c = 0; c < 4 * kOut; ++c) o[r][c] = 0.f;
+    }
+    for (int t = 0; t < n_tiles; ++t) {
+        cp_async_wait<1>();                             // K (and q) have landed, V may be in flight
+        if (t + 1 < n_tiles) stage_slots(t + 1);
+        __syncthreads();
+        float s[4][4] = {};
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            float4 a[4], b[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4 *>(sQ + (ty * 4 + r) * D + (d ^ (ty & 1) << 2));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * c) * D + (d ^ (tx & 7) << 2));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    s[r][c] = fmaf(a[r].x, b[c].x, s[r][c]);
+                    s[r][c] = fmaf(a[r].y, b[c].y, s[r][c]);
+                    s[r][c] = fmaf(a[r].z, b[c].z, s[r][c]);
+                    s[r][c] = fmaf(a[r].w, b[c].w, s[r][c]);
+                }
+        }
+        __syncthreads();                                // K's readers are done
+        if (t + 1 < n_tiles) copy(sK, 7, kbase, t + 1);
+        else cp_async_commit();
+        const int j0 = kv_lo + t * kTok;
+        const bool masked = j0 + kTok - 1 > min(seen_by_all, kv_end - 1);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float mt = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                s[r][c] *= p.scale_log2;
+                if (masked && j0 + tx + 16 * c > min(lim[r], kv_end - 1)) s[r][c] = -INFINITY;
+                mt = fmaxf(mt, s[r][c]);
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+            const float mn = fmaxf(m[r], mt);
+            const float ref = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: weights 2^-inf = 0
+            const float alpha = exp2f(m[r] - ref);
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                s[r][c] = exp2f(s[r][c] - ref);
+                sum += s[r][c];
+                sP[(ty * 4 + r) * kTok + ((tx + 16 * c) ^ (ty & 1) << 2)] = s[r][c];
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            m[r] = mn;
+            l[r] = l[r] * alpha + sum;
+#pragma unroll
+            for (int c = 0; c < 4 * kOut; ++c) o[r][c] *= alpha;
+        }
+        cp_async_wait<1>();                             // V has landed, the next K may be in flight
+        __syncthreads();
+#pragma unroll 2
+        for (int k = 0; k < kTok; k += 4) {
+            float4 w[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + r) * kTok + (k ^ (ty & 1) << 2));
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int c = 0; c < kOut; ++c) {
+                    const float4 v = *reinterpret_cast<const float4 *>(sV + (k + u) * D + tx * 4 + 64 * c);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = u == 0 ? w[r].x : u == 1 ? w[r].y : u == 2 ? w[r].z : w[r].w;
+                        // a value that the row does not see has no part in its sum, whatever it is
+                        const bool seen = !masked || j0 + k + u <= lim[r];
+                        o[r][4 * c] = fmaf(x, seen ? v.x : 0.f, o[r][4 * c]);
+                        o[r][4 * c + 1] = fmaf(x, seen ? v.y : 0.f, o[r][4 * c + 1]);
+                        o[r][4 * c + 2] = fmaf(x, seen ? v.z : 0.f, o[r][4 * c + 2]);
+                        o[r][4 * c + 3] = fmaf(x, seen ? v.w : 0.f, o[r][4 * c + 3]);
+                    }
+                }
+        }
+        __syncthreads();                                // V's and P's readers are done
+        if (t + 1 < n_tiles) copy(sV, 0, vbase, t + 1);
+        else cp_async_commit();
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int R = row0 + ty * 4 + r;
+        if (R >= rows) continue;
+        const int row = e.qo0 + (R >> p.group_shift), head = g * G + (R & (G - 1));
+        // a sum of 0 is that of a row that sees nothing here (the largest weight is 1)
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        const int64_t unit = chunk_unit(p, split, row, head);
+        float *dst = p.n_splits > 1 ? p.o_part + unit * D : static_cast<float *>(p.o) + (static_cast<int64_t>(row) * p.n_heads + head) * D;
+#pragma unroll
+        for (int c = 0; c < kOut; ++c)
+            *reinterpret_cast<float4 *>(dst + tx * 4 + 64 * c) =
+                make_float4(o[r][4 * c] * inv, o[r][4 * c + 1] * inv, o[r][4 * c + 2] * inv, o[r][4 * c + 3] * inv);
+        if (p.n_splits > 1 && tx == 0) *reinterpret_cast<float2 *>(p.ml_part + 2 * unit) = make_float2(m[r], l[r]);
+    }
+}
+
+// The join of the splits: a warp per (row, head).  A split whose first position
+// the row does not see has written nothing for it and is not read.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int kPer = D / 32;                        // elements per lane
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const ChunkEntry e = load_chunk_entry(p, blockIdx.z, false);
+    const int lane = threadIdx.x & 31;
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (u >= static_cast<int64_t>(e.q_len) * p.n_heads) return;
+    const int i = static_cast<int>(u / p.n_heads), head = static_cast<int>(u - static_cast<int64_t>(i) * p.n_heads);
+    const int lim = min(chunk_limit(p, e, i), e.kv_len - 1);
+    const int n = lim < 0 ? 0 : lim / p.split_len + 1;
+    float top = -INFINITY, sum = 0.f, acc[kPer] = {};
+    for (int s0 = 0; s0 < n; s0 += 32) {                // the splits' (m, l), a lane each
+        float m = -INFINITY, l = 0.f;
+        if (s0 + lane < n) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ml_part + 2 * chunk_unit(p, s0 + lane, e.qo0 + i, head)));
+            m = ml.x;
+            l = ml.y;
+        }
+        float mt = m;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+        const float mn = fmaxf(top, mt), ref = mn == -INFINITY ? 0.f : mn;
+        const float alpha = exp2f(top - ref);
+        const float w = l * exp2f(m - ref);
+        top = mn;
+        float ws = w;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+        sum = sum * alpha + ws;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[c] *= alpha;
+        const int cnt = min(32, n - s0);
+#pragma unroll 8
+        for (int s = 0; s < cnt; ++s) {
+            const float f = __shfl_sync(0xffffffffu, w, s);
+            const float *src = p.o_part + chunk_unit(p, s0 + s, e.qo0 + i, head) * D + lane * kPer;
+            if constexpr (kPer == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                acc[0] = fmaf(f, v.x, acc[0]);
+                acc[1] = fmaf(f, v.y, acc[1]);
+                acc[2] = fmaf(f, v.z, acc[2]);
+                acc[3] = fmaf(f, v.w, acc[3]);
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                acc[0] = fmaf(f, v.x, acc[0]);
+                acc[1] = fmaf(f, v.y, acc[1]);
+            }
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    T *dst = static_cast<T *>(p.o) + (static_cast<int64_t>(e.qo0 + i) * p.n_heads + head) * D + lane * kPer;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) dst[c] = Elem<T>::from_f(acc[c] * inv);
+}
+
+template <int D>
+cudaError_t run_f32(const ChunkParams &p, int group, cudaStream_t s) {
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_done.load() & bit)) {
+        e = cudaFuncSetAttribute(chunk_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+        if (e != cudaSuccess) return e;
+        attr_done.fetch_or(bit);
+    }
+    const int tiles = (p.max_q_len * group + kRows - 1) / kRows;
+    chunk_f32_kernel<D><<<dim3(p.n_kv_heads, tiles * p.n_splits, p.batch), kThreads, Layout<D>::kBytes, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t run_join(const ChunkParams &p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    const int64_t units = static_cast<int64_t>(p.max_q_len) * p.n_heads;
+    cfg.gridDim = dim3(static_cast<unsigned>((units + kThreads / 32 - 1) / (kThreads / 32)), 1, p.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T, D>, p);
+}
+
+}  // namespace
+
+bool chunk_supported(int dtype, int head_dim, int group) {
+    return dtype == PKV_F32 && (head_dim == 64 || head_dim == 128) && (group == 1 || group == 2 || group == 4 || group == 8);
+}
+
+void chunk_plan(ChunkPlan *out, int dtype, int n_kv_heads, int group, int batch, int max_q_len, int max_len, int sms,
+                int64_t most_splits) {
+    // Two CTAs sit on an SM.  With fewer than two rounds of them the contexts
+    // are cut, into pieces of four tiles at least.
+    const int64_t tiles = (static_cast<int64_t>(max_q_len) * group + kRows - 1) / kRows;
+    const int64_t ctas = tiles * n_kv_heads * batch, want = 4LL * sms;
+    const int64_t kv_tiles = (static_cast<int64_t>(max_len) + kTok - 1) / kTok;
+    int64_t splits = ctas > 0 ? (want + ctas - 1) / ctas : 1;
+    if (splits > kv_tiles / 4) splits = kv_tiles / 4;
+    if (splits > most_splits) splits = most_splits;
+    if (splits > 65535 / tiles) splits = 65535 / tiles;
+    if (splits < 1) splits = 1;
+    const int64_t per = (kv_tiles + splits - 1) / splits;
+    out->split_len = static_cast<int32_t>((per < 1 ? 1 : per) * kTok);
+    out->n_splits = static_cast<int32_t>(kv_tiles <= 0 ? 1 : (kv_tiles + per - 1) / per);
+    (void)dtype;
+}
+
+cudaError_t launch_chunk(const ChunkParams &p, int dtype, int head_dim, int group, cudaStream_t s) {
+    if (!chunk_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
+    cudaError_t e = head_dim == 128 ? run_f32<128>(p, group, s) : run_f32<64>(p, group, s);
+    if (e != cudaSuccess || p.n_splits == 1) return e;
+    return head_dim == 128 ? run_join<float, 128>(p, s) : run_join<float, 64>(p, s);
+}
+
+}  // namespace pkv

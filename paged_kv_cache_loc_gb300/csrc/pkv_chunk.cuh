@@ -1,0 +1,48 @@
+// pkv_chunk.cuh -- what the kernels of the chunk attention share (internal).
+#pragma once
+
+#include "pkv_common.cuh"
+#include "pkv_launch.h"
+
+namespace pkv {
+
+// Entry b's rows of q and its context, checked: an entry with an error has no
+// rows.  first = position that its first row sees up to (causal), below 0 if
+// that row sees nothing.
+struct ChunkEntry {
+    int req, qo0, q_len, kv_len, first;
+};
+
+__device__ __forceinline__ ChunkEntry load_chunk_entry(const ChunkParams &p, int b, bool report) {
+    ChunkEntry e;
+    e.req = __ldg(p.req_pool_indices + b);
+    e.qo0 = __ldg(p.qo_indptr + b);
+    const int end = __ldg(p.qo_indptr + b + 1);
+    e.kv_len = __ldg(p.seq_lens + b);
+    const long long q_len = static_cast<long long>(end) - e.qo0;
+    e.q_len = static_cast<int>(q_len);
+    bool ok = true;
+    int bad = 0;
+    if (static_cast<unsigned>(e.req) >= static_cast<unsigned>(p.num_reqs)) ok = false, bad = e.req;
+    else if (e.qo0 < 0 || end > p.n_q || q_len < 0) ok = false, bad = e.qo0 < 0 || e.qo0 > p.n_q ? e.qo0 : end;
+    else if (q_len > p.max_q_len) ok = false, bad = e.q_len;
+    else if (static_cast<unsigned>(e.kv_len) > static_cast<unsigned>(p.max_len)) ok = false, bad = e.kv_len;
+    if (!ok) {
+        if (report) record_error(p.err, bad);
+        e.req = e.qo0 = e.q_len = e.kv_len = 0;
+    }
+    e.first = p.causal ? e.kv_len - e.q_len : e.kv_len - 1;
+    return e;
+}
+
+// last position that the row at place i of its entry sees
+__device__ __forceinline__ int chunk_limit(const ChunkParams &p, const ChunkEntry &e, int i) {
+    return p.causal ? e.first + i : e.first;
+}
+
+// the partial sums of split `split`: row `row` of q, head `head`
+__device__ __forceinline__ int64_t chunk_unit(const ChunkParams &p, int split, int row, int head) {
+    return (static_cast<int64_t>(split) * p.n_q + row) * p.n_heads + head;
+}
+
+}  // namespace pkv

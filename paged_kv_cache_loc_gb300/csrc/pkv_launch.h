@@ -336,6 +336,43 @@ struct CompactParams {
     DevErr *err;
 };
 
+// Attention of new tokens through the page table (pkv_chunk.cu,
+// pkv_chunk_tc.cu).
+struct ChunkParams {
+    const void *q;                // [n_q, n_heads, head_dim]
+    void *o;
+    const void *k_buffer;
+    const void *v_buffer;
+    const int32_t *req_to_page;   // [num_reqs, max_pages]
+    const int32_t *req_pool_indices;
+    const int32_t *seq_lens;
+    const int32_t *qo_indptr;     // [batch + 1]
+    float *o_part;                // [n_splits, n_q, n_heads, head_dim] (more than one split)
+    float *ml_part;               // [n_splits, n_q, n_heads, 2]
+    int64_t size;
+    int64_t layer_row0;
+    int64_t n_pages;
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t n_heads;
+    int32_t group_shift;          // log2(n_heads / n_kv_heads)
+    int32_t num_reqs;
+    int32_t batch;
+    int32_t n_q;
+    int32_t max_q_len;
+    int32_t max_len;
+    int32_t causal;
+    int32_t n_splits;
+    int32_t split_len;            // positions per split
+    float scale_log2;
+    DevErr *err;
+};
+struct ChunkPlan {
+    int32_t n_splits;
+    int32_t split_len;
+};
+
 constexpr int kScoreGroup = 16;         // pages scored together
 
 constexpr int kDecodeMaxChunk = 2048;   // slot indices staged per split (or per piece)
@@ -354,6 +391,13 @@ cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t s)
 cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t s);
 cudaError_t launch_release(const ReleaseParams &p, int sms, cudaStream_t s);
 cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t s);
+bool chunk_supported(int dtype, int head_dim, int group);
+// How the contexts are cut, into most_splits pieces at most.
+void chunk_plan(ChunkPlan *out, int dtype, int n_kv_heads, int group, int batch, int max_q_len, int max_len, int sms,
+                int64_t most_splits);
+cudaError_t launch_chunk(const ChunkParams &p, int dtype, int head_dim, int group, cudaStream_t s);
+// Query rows (position, head in group) of a call at most, per kv head and entry.
+constexpr int64_t kChunkMaxRows = 65535LL * 64;
 // Whether the selection and the attention over it have a kernel for this shape.
 bool sparse_supported(int dtype, int head_dim, int group);
 // Sets p->splits and p->entries.

@@ -11,16 +11,17 @@ place.
 from __future__ import annotations
 
 import ctypes
+import math
 import struct
 from typing import Optional
 
 import torch
 
 from . import _lib
-from ._lib import PkvPageState
+from ._lib import PkvKVCache, PkvPageState, check
 from .ops import KVCache, Workspace, _DTYPES
 from . import sparse
-from .sparse import _byref, _call, _i32, _int32, _ints, _pack_cache, _ptr, _st, _vp
+from .sparse import _call, _f32, _heads, _i32, _int32, _ints, _output, _pack_cache, _ptr, _rows, _st, _vp
 
 _pack_state = struct.Struct("PiiPPPPiPP")
 assert _pack_state.size == ctypes.sizeof(PkvPageState)
@@ -29,12 +30,13 @@ sparse._ARGS.update({
     "pkv_fork_requests": [_st, _st, _vp, _vp],
     "pkv_release_pages": [_st, _st, _vp, _vp],
     "pkv_compact_pages": [_st, _st, _vp, _vp, _vp, _vp],
+    "pkv_paged_chunk": [_st, _i32, _vp, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _f32, _vp, _vp],
 })
 
 
-def _describe(cache: KVCache, num_reqs: int, max_ctx_len: int, index: int, batched: bool) -> bytes:
+def _describe(cache: KVCache, num_reqs: int, max_ctx_len: int, index: int, batched: bool, chunk: bool = False) -> bytes:
     """The packed descriptor of a cache's pool and, where `batched`, of its
-    entries (request rows and lengths)."""
+    entries (request rows and lengths; with `chunk`, the places of their rows)."""
     kb, vb = cache.k_buffer, cache.v_buffer
     dtype, shape = kb.dtype, kb.shape
     code = _DTYPES.get(dtype)
@@ -42,14 +44,18 @@ def _describe(cache: KVCache, num_reqs: int, max_ctx_len: int, index: int, batch
         raise TypeError(f"unsupported storage dtype {dtype}")
     if len(shape) != 4 or vb.shape != shape:
         raise ValueError("k_buffer/v_buffer must both be [n_layers, size, n_kv_heads, head_dim]")
-    batch = rows = lens = 0
+    batch = rows = lens = qo = 0
     if batched:
         batch = cache.req_pool_indices.numel()
         if cache.seq_lens is None:
             raise ValueError("seq_lens is needed")
         rows, lens = _ptr(cache.req_pool_indices, "req_pool_indices", _int32, index), _ints(cache.seq_lens, "seq_lens", index, batch)
+    if chunk:
+        if cache.qo_indptr is None:
+            raise ValueError("qo_indptr is needed")
+        qo = _ints(cache.qo_indptr, "qo_indptr", index, batch + 1)
     return _pack_cache.pack(_ptr(kb, "k_buffer", dtype, index), _ptr(vb, "v_buffer", dtype, index), code, shape[0], shape[2],
-                            shape[3], shape[1], 0, num_reqs, max_ctx_len, rows, lens, 0, 0, 0, batch, cache.max_len)
+                            shape[3], shape[1], 0, num_reqs, max_ctx_len, rows, lens, 0, qo, 0, batch, cache.max_len)
 
 
 def _index(cache: KVCache) -> int:
@@ -161,3 +167,40 @@ def compact_pages(cache: KVCache, req_to_page: torch.Tensor, page_size: int, sha
     _call("pkv_compact_pages", index, stream, c, t, _ints(free_out, "free_out", index, free_pages.numel()),
           _ints(remap, "remap", index, n_pages), sparse._workspace(workspace, index))
     return remap
+
+
+def chunk_workspace(cache: KVCache, n_rows: int, n_heads: int, max_q_len: int) -> Workspace:
+    """A workspace for paged_chunk calls of cache's batch and max_len with n_rows
+    query rows (max_q_len for an entry) at most.  It holds the splits that such a
+    call uses; a call with fewer rows may use more splits and then takes as many
+    as fit."""
+    index = _index(cache)
+    c = PkvKVCache.from_buffer_copy(_describe(cache, 0, 0, index, True))
+    with torch.cuda.device(index):
+        splits = _lib.load().pkv_chunk_splits(ctypes.byref(c), n_heads, max_q_len)
+    if splits < 1:
+        check(splits, "pkv_chunk_splits")
+    if splits == 1:                                       # nothing is split: no partials
+        return Workspace(1, 1, 64, 1, device=cache.k_buffer.device)
+    return Workspace(max(1, n_rows), n_heads, cache.k_buffer.shape[3], splits, device=cache.k_buffer.device)
+
+
+def paged_chunk(cache: KVCache, layer_id: int, req_to_page: torch.Tensor, page_size: int, q: torch.Tensor, max_q_len: int,
+                causal: bool = True, o: Optional[torch.Tensor] = None, sm_scale: Optional[float] = None,
+                workspace: Optional[Workspace] = None, stream=None) -> torch.Tensor:
+    """Attention of each entry's rows cache.qo_indptr[b] .. cache.qo_indptr[b + 1]
+    of q [n_q, n_heads, head_dim] (max_q_len at most) over its context of
+    cache.seq_lens[b] positions (cache.max_len at most) through the page table:
+    causal (the rows are the context's last tokens) or over all of it.  Rows that
+    see nothing give 0."""
+    if req_to_page.dim() != 2:
+        raise ValueError("req_to_page must be [num_reqs, max_pages]")
+    index = _index(cache)
+    c = _describe(cache, req_to_page.shape[0], 0, index, True, chunk=True)
+    heads, n_q, head_dim, dtype = _heads(q), q.shape[0], cache.k_buffer.shape[3], cache.k_buffer.dtype
+    qp = _rows(q, "q", dtype, index, n_q, heads, head_dim)
+    o, op = _output(o, q, dtype, index, stream)
+    _call("pkv_paged_chunk", index, stream, c, layer_id, _ptr(req_to_page, "req_to_page", _int32, index), req_to_page.shape[1],
+          page_size, qp, op, n_q, heads, max_q_len, 1 if causal else 0,
+          1.0 / math.sqrt(head_dim) if sm_scale is None else sm_scale, sparse._workspace(workspace, index))
+    return o
