@@ -311,32 +311,38 @@ cudaError_t run_join(const ChunkParams &p, cudaStream_t s) {
 }  // namespace
 
 bool chunk_supported(int dtype, int head_dim, int group) {
-    return dtype == PKV_F32 && (head_dim == 64 || head_dim == 128) && (group == 1 || group == 2 || group == 4 || group == 8);
+    return (dtype == PKV_F32 || dtype == PKV_BF16) && (head_dim == 64 || head_dim == 128) &&
+           (group == 1 || group == 2 || group == 4 || group == 8);
 }
 
 void chunk_plan(ChunkPlan *out, int dtype, int n_kv_heads, int group, int batch, int max_q_len, int max_len, int sms,
                 int64_t most_splits) {
-    // Two CTAs sit on an SM.  With fewer than two rounds of them the contexts
-    // are cut, into pieces of four tiles at least.
-    const int64_t tiles = (static_cast<int64_t>(max_q_len) * group + kRows - 1) / kRows;
-    const int64_t ctas = tiles * n_kv_heads * batch, want = 4LL * sms;
-    const int64_t kv_tiles = (static_cast<int64_t>(max_len) + kTok - 1) / kTok;
+    // CTAs per SM, rows and keys per tile of the kernel that the call takes.
+    // With fewer than two rounds of CTAs the contexts are cut, into pieces of
+    // four tiles at least.
+    const bool wide = dtype == PKV_BF16 && chunk_wide(max_q_len, group);
+    const int64_t per_sm = wide ? 1 : 2, rows = wide ? 256 : dtype == PKV_BF16 ? 128 : kRows, tok = wide ? 128 : 64;
+    const int64_t tiles = (static_cast<int64_t>(max_q_len) * group + rows - 1) / rows;
+    const int64_t ctas = tiles * n_kv_heads * batch, want = 2 * per_sm * sms;
+    const int64_t kv_tiles = (static_cast<int64_t>(max_len) + tok - 1) / tok;
     int64_t splits = ctas > 0 ? (want + ctas - 1) / ctas : 1;
     if (splits > kv_tiles / 4) splits = kv_tiles / 4;
     if (splits > most_splits) splits = most_splits;
     if (splits > 65535 / tiles) splits = 65535 / tiles;
     if (splits < 1) splits = 1;
-    const int64_t per = (kv_tiles + splits - 1) / splits;
-    out->split_len = static_cast<int32_t>((per < 1 ? 1 : per) * kTok);
+    int64_t per = (kv_tiles + splits - 1) / splits;
+    if (per < 1) per = 1;
+    out->split_len = static_cast<int32_t>(per * tok);
     out->n_splits = static_cast<int32_t>(kv_tiles <= 0 ? 1 : (kv_tiles + per - 1) / per);
-    (void)dtype;
 }
 
 cudaError_t launch_chunk(const ChunkParams &p, int dtype, int head_dim, int group, cudaStream_t s) {
     if (!chunk_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
-    cudaError_t e = head_dim == 128 ? run_f32<128>(p, group, s) : run_f32<64>(p, group, s);
+    const bool f32 = dtype == PKV_F32;
+    cudaError_t e = !f32 ? launch_chunk_tc(p, head_dim, group, s) : head_dim == 128 ? run_f32<128>(p, group, s) : run_f32<64>(p, group, s);
     if (e != cudaSuccess || p.n_splits == 1) return e;
-    return head_dim == 128 ? run_join<float, 128>(p, s) : run_join<float, 64>(p, s);
+    if (f32) return head_dim == 128 ? run_join<float, 128>(p, s) : run_join<float, 64>(p, s);
+    return head_dim == 128 ? run_join<__nv_bfloat16, 128>(p, s) : run_join<__nv_bfloat16, 64>(p, s);
 }
 
 }  // namespace pkv

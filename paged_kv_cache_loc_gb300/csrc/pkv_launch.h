@@ -396,6 +396,10 @@ bool chunk_supported(int dtype, int head_dim, int group);
 void chunk_plan(ChunkPlan *out, int dtype, int n_kv_heads, int group, int batch, int max_q_len, int max_len, int sms,
                 int64_t most_splits);
 cudaError_t launch_chunk(const ChunkParams &p, int dtype, int head_dim, int group, cudaStream_t s);
+// bf16 on tensor cores (pkv_chunk_tc.cu), without the join; `wide`: the form with
+// two query tiles of 128 rows.
+bool chunk_wide(int max_q_len, int group);
+cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, cudaStream_t s);
 // Query rows (position, head in group) of a call at most, per kv head and entry.
 constexpr int64_t kChunkMaxRows = 65535LL * 64;
 // Whether the selection and the attention over it have a kernel for this shape.

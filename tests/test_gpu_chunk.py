@@ -26,7 +26,7 @@ from paged_kv_cache_loc_gb300 import _lib, build
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
-DTYPES = ["f32"]
+DTYPES = ["f32", "bf16"]
 
 
 @pytest.fixture(scope="module", autouse=True)
