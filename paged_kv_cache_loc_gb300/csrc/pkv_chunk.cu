@@ -328,7 +328,7 @@ void chunk_plan(ChunkPlan *out, int dtype, int n_kv_heads, int group, int batch,
     int64_t splits = ctas > 0 ? (want + ctas - 1) / ctas : 1;
     if (splits > kv_tiles / 4) splits = kv_tiles / 4;
     if (splits > most_splits) splits = most_splits;
-    if (splits > 65535 / tiles) splits = 65535 / tiles;
+    if (splits > 65535 / (tiles + 1)) splits = 65535 / (tiles + 1);   // grid y, tiles in pairs
     if (splits < 1) splits = 1;
     int64_t per = (kv_tiles + splits - 1) / splits;
     if (per < 1) per = 1;

@@ -40,13 +40,13 @@ namespace {
 constexpr int kRows = 128;                  // query rows per tile (tensor-memory lanes)
 constexpr int kSlots = 2;                   // K tiles and V tiles in shared memory
 constexpr float kRescale = 8.f;             // the reference is raised by 2^8 at least
-constexpr int kGuarded = 4;                 // V tiles of a CTA that are looked at, at most
+constexpr int kGuarded = 6;                 // V tiles that are looked at, at most
 
 template <int D, int NQ>
 struct Tc {
     static constexpr int kTok = NQ == 2 ? 128 : 64;
     static constexpr int kThreads = NQ * 128 + 128;
-    static constexpr int kMmaWarp = NQ * 4, kCopyWarp = kMmaWarp + 1, kGuardWarp = kMmaWarp + 2;
+    static constexpr int kMmaWarp = 0, kCopyWarp = 1, kGuardWarp = 2, kSoftmaxWarp = 4;
     static constexpr int kQBytes = kRows * D * 2, kTileBytes = kTok * D * 2;
     static constexpr int kSmemQ = 0, kSmemK = NQ * kQBytes, kSmemV = kSmemK + kSlots * kTileBytes;
     static constexpr int kSmemBar = kSmemV + kSlots * kTileBytes;
@@ -74,21 +74,71 @@ __device__ __forceinline__ uint32_t sw_at(int tile_rows, int r, int ch) {
     return (ch >> 3) * (tile_rows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
 
+// One lane of a whole warp.  (With `lane == 0` instead the compiler does not know
+// that one thread issues the asynchronous instructions behind it, and each costs
+// several times as much.)
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
 __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
 }
+// TMA copies of a box of rows, or of four rows; kBoth: to the same place in both
+// CTAs of the cluster, completing the barrier of each.
+template <bool kBoth>
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int row, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
-        "l"(map), "r"(x), "r"(row), "r"(bar)
-        : "memory");
+    if constexpr (kBoth)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
+            "[%4], %5;\n" ::"r"(dst),
+            "l"(map), "r"(x), "r"(row), "r"(bar), "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+            "l"(map), "r"(x), "r"(row), "r"(bar)
+            : "memory");
 }
+template <bool kBoth>
 __device__ __forceinline__ void copy_rows4(uint32_t dst, const CUtensorMap *map, int x, const int (&row)[4], uint32_t bar) {
+    if constexpr (kBoth)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
+            "%3, %4, %5, %6}], [%7], %8;\n" ::"r"(dst),
+            "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar), "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+            "[%7];\n" ::"r"(dst),
+            "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
+            : "memory");
+}
+// arrives on the barrier at this place in both CTAs once the products so far are done
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+// bar_wait of the warp that issues the products, with one answer for all lanes:
+// what is done already, as it mostly is, costs one test that falls through.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity) { return bar_wait(bar, parity); }
+__device__ __forceinline__ bool wait_fast(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-        "[%7];\n" ::"r"(dst),
-        "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
         : "memory");
+    if (__builtin_expect(__all_sync(0xffffffffu, ok != 0), 1)) return true;
+    return __all_sync(0xffffffffu, wait_on(bar, parity));
 }
 
 struct Maps {
@@ -114,31 +164,33 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     uint32_t *s_bad = reinterpret_cast<uint32_t *>(sm + L::kSmemBad);
     auto bar = [&](int i) -> uint32_t { return s_base + L::kSmemBar + 8 * i; };
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = blockIdx.x, split = blockIdx.y % p.n_splits, shift = p.group_shift, G = 1 << shift;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    // Wide form: a cluster of two CTAs takes two neighbouring pairs of tiles and
+    // the same keys; each copies half of every K/V tile to both.
+    const int g = blockIdx.x, shift = p.group_shift, G = 1 << shift;
+    const int rank = NQ == 2 ? blockIdx.y & 1 : 0, unit = NQ == 2 ? blockIdx.y >> 1 : blockIdx.y, split = unit % p.n_splits;
     const ChunkEntry e = load_chunk_entry(p, blockIdx.z, g == 0 && blockIdx.y == 0 && tid == 0);
     const int rows = e.q_len << shift;
     // the entry's last rows, which see most, first
-    const int tile = (rows + NQ * kRows - 1) / (NQ * kRows) - 1 - static_cast<int>(blockIdx.y / p.n_splits);
+    const int last_tile = (rows + NQ * kRows - 1) / (NQ * kRows) - 1 - unit / p.n_splits * NQ;
+    const int tile = last_tile - (NQ - 1) + rank;
     if (tile < 0) return;
-    const int row0 = tile * NQ * kRows;
+    const bool both = NQ == 2 && last_tile > 0;          // the cluster's other CTA has rows too
+    const int row0 = tile * NQ * kRows, first_row = both ? (last_tile - 1) * NQ * kRows : row0;
     const int kv_lo = split * p.split_len;
-    int n_x[NQ], kv_end = kv_lo;
+    // keys [kv_lo, end) that the rows up to `row` see in this split
+    auto end_of = [&](int row) -> int { return min(min(kv_lo + p.split_len, e.kv_len), chunk_limit(p, e, row >> shift) + 1); };
+    int n_x[NQ];                                         // tiles of keys of each query tile
 #pragma unroll
     for (int X = 0; X < NQ; ++X) {
-        const int r0 = row0 + X * kRows;
-        n_x[X] = 0;
-        if (r0 < rows) {
-            const int last = (min(r0 + kRows, rows) - 1) >> shift;
-            const int end = min(min(kv_lo + p.split_len, e.kv_len), chunk_limit(p, e, last) + 1);
-            if (end > kv_lo) n_x[X] = (end - kv_lo + kTok - 1) / kTok;
-            kv_end = max(kv_end, end);
-        }
+        const int r0 = row0 + X * kRows, end = r0 < rows ? end_of(min(r0 + kRows, rows) - 1) : kv_lo;
+        n_x[X] = end > kv_lo ? (end - kv_lo + kTok - 1) / kTok : 0;
     }
-    const int n_tiles = NQ == 2 ? max(n_x[0], n_x[NQ - 1]) : n_x[0];
+    const int kv_end = max(kv_lo, end_of(min((last_tile + 1) * NQ * kRows, rows) - 1));
+    const int n_tiles = (kv_end - kv_lo + kTok - 1) / kTok;   // of the cluster
     if (n_tiles == 0 && p.n_splits > 1) return;       // nothing to see: the join does not read this split
-    // from tile `guard` on, some row does not see all of a tile
-    const int all_see = min(chunk_limit(p, e, row0 >> shift), kv_end - 1);
+    // from tile `guard` on, some row of the cluster does not see all of a tile
+    const int all_see = min(chunk_limit(p, e, first_row >> shift), kv_end - 1);
     const int guard = all_see < kv_lo ? 0 : (all_see + 1 - kv_lo) / kTok;
 
     // ---- barriers, tensor memory
@@ -146,6 +198,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         for (int i = 0; i < L::kBars; ++i) {
             uint32_t count = 1;
             if (i >= L::kVClean && i < L::kSFull) count = 2;
+            else if (both && ((i >= L::kKEmpty && i < L::kVFull) || (i >= L::kVEmpty && i < L::kVRaw))) count = 2;   // both CTAs' products
             else if (i >= L::kPFull && i < L::kODone) {        // the tile's warps that hold rows
                 const int left = rows - row0 - (NQ == 2 ? (i - L::kPFull) * kRows : 0);
                 count = max(1, (min(left, kRows) + 31) / 32);
@@ -162,8 +215,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     }
     fence_before();
     __syncthreads();
+    if (both) cluster_sync();        // the other CTA copies and arrives here
     fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::kSmemTmem);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sm + L::kSmemTmem), 0);
     auto give_up = [&](int code) {
         if (lane == 0 && *s_abort == 0) {
             *s_abort = 1;
@@ -183,12 +237,13 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         return (ok ? page : 0) * p.page_size + (j - i * p.page_size);
     };
 
-    if (warp >= L::kMmaWarp) {
+    if (warp < L::kSoftmaxWarp) {
         if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kOtherRegs));
         if (warp == L::kCopyWarp) {
             // ================= copies: a lane takes a box of rows, or four rows
             const int per = box > 0 ? box : 4;
-            const bool active = lane < kTok / per;
+            // (of both CTAs' copies this one makes every other box, or four rows)
+            const bool active = lane < kTok / per && (!both || (lane & 1) == rank);
             int next[4] = {0, 0, 0, 0};
             auto fetch = [&](int t) {
                 if (!active || t >= n_tiles) return;
@@ -203,12 +258,17 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             auto issue = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, const int (&row)[4]) {
                 if (lane == 0) expect_bytes(full, L::kTileBytes);
                 __syncwarp();
-                if (active) {
+                if (!active) return;
 #pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        const uint32_t to = dst + h * (kTok * 128) + lane * per * 128;
-                        if (box > 0) copy_box(to, map, g * D + h * 64, row[0], full);
-                        else copy_rows4(to, map, g * D + h * 64, row, full);
+                for (int h = 0; h < D / 64; ++h) {
+                    const uint32_t to = dst + h * (kTok * 128) + lane * per * 128;
+                    const int x = g * D + h * 64;
+                    if (NQ == 2 && both) {
+                        if (box > 0) copy_box<true>(to, map, x, row[0], full);
+                        else copy_rows4<true>(to, map, x, row, full);
+                    } else {
+                        if (box > 0) copy_box<false>(to, map, x, row[0], full);
+                        else copy_rows4<false>(to, map, x, row, full);
                     }
                 }
             };
@@ -231,86 +291,87 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             for (int t = max(0, issued_k - kSlots); t < issued_k; ++t) bar_wait(bar(L::kKFull + t % kSlots), phase(t));
             for (int t = max(0, issued_v - kSlots); t < issued_v; ++t) bar_wait(v_landed(t), v_phase(t));
         } else if (warp == L::kMmaWarp) {
-            // ================= products
-            const uint32_t id_s = idesc(kRows, kTok, 0), id_o = idesc(kRows, D, 1);
-            const uint64_t dq = sdesc(s_base + L::kSmemQ, 16, 1024), dk = sdesc(s_base + L::kSmemK, 16, 1024);
-            const uint64_t dv = sdesc(s_base + L::kSmemV, kTok * 128, 1024);
-            const uint32_t hi = static_cast<uint32_t>(dq >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
-            const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), v_lo = static_cast<uint32_t>(dv);
-            auto issue_s = [&](int X, int buf, int slot) {
-                if (lane == 0) {
+            // ================= products: one thread issues them all.  It blocks
+            // while the tensor core is busy, so what it does in between is
+            // time in which the tensor core runs dry: it waits for K and V
+            // while the products before them run, and looks at nothing else.
+            if (n_tiles > 0) {
+                const uint32_t id_s = idesc(kRows, kTok, 0), id_o = idesc(kRows, D, 1);
+                const uint64_t dq = sdesc(s_base + L::kSmemQ, 16, 1024), dk = sdesc(s_base + L::kSmemK, 16, 1024);
+                const uint64_t dv = sdesc(s_base + L::kSmemV, kTok * 128, 1024);
+                const uint32_t hi = static_cast<uint32_t>(dq >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
+                const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), v_lo = static_cast<uint32_t>(dv);
+                auto issue_s = [&](int X, int buf, int slot) {
+                    if (!elect()) return;
                     const uint32_t qa = q_lo + X * (L::kQBytes >> 4), ka = k_lo + slot * (L::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
                         mma_f16(tmem + L::s_col(buf), desc_at(qa + (((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4), hi),
                                 desc_at(ka + (((ks >> 2) * (kTok * 128) + (ks & 3) * 32) >> 4), hi), id_s, ks > 0);
                     mma_commit(bar(L::kSFull + buf));
-                }
-            };
-            auto issue_pv = [&](int X, int buf, int slot, bool acc) {
-                if (lane == 0) {
+                };
+                auto issue_pv = [&](int X, int buf, int slot, bool acc) {
+                    if (!elect()) return;
                     const uint32_t va = v_lo + slot * (L::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kTok / 16; ++ks)
                         mma_f16_ta(tmem + L::o_col(X), tmem + L::s_col(buf) + ks * 8, desc_at(va + ks * (16 * 128 >> 4), v_hi), id_o,
                                    (acc || ks > 0) ? 1u : 0u);
-                }
-            };
-            auto commit = [&](int b) {
-                if (lane == 0) mma_commit(bar(b));
-            };
-            auto wait_v = [&](int t) -> bool {
-                return bar_wait(bar((t < guard ? L::kVFull : L::kVClean) + t % kSlots), v_phase(t));
-            };
-            bool ok = n_tiles > 0 && bar_wait(bar(L::kQFull), 0) && bar_wait(bar(L::kKFull), 0);
-            if (n_tiles > 0 && !__all_sync(0xffffffffu, ok)) give_up(-5003), ok = false;
-            if (ok) {
-                fence_after();
-                if (n_x[0] > 0) issue_s(0, 0, 0);
-                if (NQ == 2 && n_x[NQ - 1] > 0) issue_s(1, 1, 0);
-                commit(L::kKEmpty);
-            }
-            for (int j = 0; ok && j < n_tiles; ++j) {
-                const int slot = j % kSlots, slot1 = (j + 1) % kSlots;
-                const bool more = j + 1 < n_tiles;
-                if (__any_sync(0xffffffffu, *s_abort)) break;
-                if constexpr (NQ == 2) {
-                    if (!__all_sync(0xffffffffu, wait_v(j))) { give_up(-5004); break; }
-                    if (j < n_x[0]) {
-                        if (!__all_sync(0xffffffffu, bar_wait(bar(L::kPFull), j & 1))) { give_up(-5005); break; }
-                        fence_after();
-                        issue_pv(0, 0, slot, j > 0);
-                        if (j == n_x[0] - 1) commit(L::kODone);
-                    }
-                    if (more) {
-                        if (!__all_sync(0xffffffffu, bar_wait(bar(L::kKFull + slot1), phase(j + 1)))) { give_up(-5006); break; }
-                        fence_after();
-                        if (j + 1 < n_x[0]) issue_s(0, 0, slot1);
-                    }
-                    if (j < n_x[1]) {
-                        if (!__all_sync(0xffffffffu, bar_wait(bar(L::kPFull + 1), j & 1))) { give_up(-5007); break; }
-                        fence_after();
-                        issue_pv(1, 1, slot, j > 0);
-                        if (j == n_x[1] - 1) commit(L::kODone + 1);
-                    }
-                    commit(L::kVEmpty + slot);
-                    if (more) {
-                        if (j + 1 < n_x[1]) issue_s(1, 1, slot1);
-                        commit(L::kKEmpty + slot1);
-                    }
-                } else {
-                    if (more) {
-                        if (!__all_sync(0xffffffffu, bar_wait(bar(L::kKFull + slot1), phase(j + 1)))) { give_up(-5006); break; }
-                        fence_after();
-                        issue_s(0, (j + 1) & 1, slot1);
-                        commit(L::kKEmpty + slot1);
-                    }
-                    if (!__all_sync(0xffffffffu, wait_v(j) && bar_wait(bar(L::kPFull + (j & 1)), (j >> 1) & 1))) { give_up(-5004); break; }
+                };
+                auto commit = [&](int i) {
+                    if (elect()) mma_commit(bar(i));
+                };
+                auto release = [&](int i) {     // a tile of K or V, in both CTAs
+                    if (!elect()) return;
+                    if (NQ == 2 && both) mma_commit_both(bar(i));
+                    else mma_commit(bar(i));
+                };
+                auto wait_k = [&](int t) -> bool { return wait_fast(bar(L::kKFull + t % kSlots), phase(t)); };
+                auto wait_v = [&](int t) -> bool { return wait_fast(bar((t < guard ? L::kVFull : L::kVClean) + t % kSlots), v_phase(t)); };
+                bool ok = wait_fast(bar(L::kQFull), 0) && wait_k(0);
+                if (ok) {
                     fence_after();
-                    issue_pv(0, j & 1, slot, j > 0);
-                    commit(L::kVEmpty + slot);
-                    if (!more) commit(L::kODone);
+                    if (n_x[0] > 0) issue_s(0, 0, 0);
+                    if (NQ == 2 && n_x[NQ - 1] > 0) issue_s(1, 1, 0);
+                    release(L::kKEmpty);
+                    ok = wait_v(0) && (n_tiles == 1 || wait_k(1));
                 }
+                for (int j = 0; ok && j < n_tiles; ++j) {
+                    const int slot = j % kSlots, slot1 = (j + 1) % kSlots;
+                    const bool more = j + 1 < n_tiles;
+                    if constexpr (NQ == 2) {
+                        if (j < n_x[0]) {
+                            if (!wait_fast(bar(L::kPFull), j & 1)) { ok = false; break; }
+                            fence_after();
+                            issue_pv(0, 0, slot, j > 0);
+                            if (j == n_x[0] - 1) commit(L::kODone);
+                        }
+                        if (j + 1 < n_x[0]) issue_s(0, 0, slot1);
+                        if (more && !wait_v(j + 1)) { ok = false; break; }
+                        if (j < n_x[1]) {
+                            if (!wait_fast(bar(L::kPFull + 1), j & 1)) { ok = false; break; }
+                            fence_after();
+                            issue_pv(1, 1, slot, j > 0);
+                            if (j == n_x[1] - 1) commit(L::kODone + 1);
+                        }
+                        release(L::kVEmpty + slot);
+                        if (j + 1 < n_x[1]) issue_s(1, 1, slot1);
+                        if (more) release(L::kKEmpty + slot1);
+                        if (j + 2 < n_tiles) ok = wait_k(j + 2);
+                    } else {
+                        if (more) {
+                            issue_s(0, (j + 1) & 1, slot1);
+                            release(L::kKEmpty + slot1);
+                        }
+                        if (!wait_fast(bar(L::kPFull + (j & 1)), (j >> 1) & 1)) { ok = false; break; }
+                        fence_after();
+                        issue_pv(0, j & 1, slot, j > 0);
+                        release(L::kVEmpty + slot);
+                        if (!more) commit(L::kODone);
+                        else ok = wait_v(j + 1) && (j + 2 >= n_tiles || wait_k(j + 2));
+                    }
+                }
+                if (!ok) give_up(-5003);
             }
             __syncwarp();
         } else {
@@ -349,7 +410,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     } else {
         // ================= softmax: the rows of tile X, a thread each
         if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(L::kSoftmaxRegs));
-        const int X = NQ == 2 ? warp >> 2 : 0, row = tid & (kRows - 1), R0 = row0 + X * kRows, R = R0 + row;
+        const int X = NQ == 2 ? (warp - L::kSoftmaxWarp) >> 2 : 0, row = tid & (kRows - 1), R0 = row0 + X * kRows, R = R0 + row;
         {
             // The maximum is of the products, so a scale below 0 is taken into q,
             // and one of 0 makes q 0.
@@ -544,6 +605,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     }
     fence_before();
     __syncthreads();
+    if (both) cluster_sync();        // nothing of the other CTA is on its way here
     if (warp == L::kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(L::kCols));
 }
 
@@ -602,13 +664,23 @@ cudaError_t run(const ChunkParams &p, int group, cudaStream_t s) {
     }
     // rows of a page that a box may take: the largest power of two in page_size
     int box = p.page_size & -p.page_size;
-    if (box > L::kTok) box = L::kTok;
+    if (box > L::kTok / NQ) box = L::kTok / NQ;   // (two boxes at least where two CTAs share the copies)
     if (box < 8) box = 0;                    // below a swizzle atom: four rows at a time
     Maps maps;
     if (!pool_map(&maps.k, p.k_buffer, p, D, box) || !pool_map(&maps.v, p.v_buffer, p, D, box)) return cudaErrorInvalidValue;
     const int tiles = (p.max_q_len * group + NQ * kRows - 1) / (NQ * kRows);
-    chunk_tc_kernel<D, NQ><<<dim3(p.n_kv_heads, tiles * p.n_splits, p.batch), L::kThreads, L::kBytes, s>>>(p, maps, box);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_kv_heads, (tiles + NQ - 1) / NQ * NQ * p.n_splits, p.batch);
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.y = NQ;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, NQ>, p, maps, box);
 }
 
 }  // namespace
