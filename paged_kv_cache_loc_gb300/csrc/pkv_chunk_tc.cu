@@ -68,10 +68,14 @@ struct Tc {
     static_assert(kBytes <= 227 * 1024 && (NQ == 2 || 2 * (kBytes + 1024) <= 228 * 1024), "shared memory");
 };
 
-// byte offset of 16-byte chunk ch of row r in a tile of `tile_rows` rows: 64-column
-// halves of rows x 128 bytes, chunk c of a row at c ^ (r % 8)
-__device__ __forceinline__ uint32_t sw_at(int tile_rows, int r, int ch) {
-    return (ch >> 3) * (tile_rows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+// Byte offset of 16-byte chunk ch of row r in a tile: eight rows at a time, their
+// 64-column halves as 8 x 128 bytes one after the other, chunk c of a row at c ^
+// (r % 8).  So a run of rows of a page is one box of the tensor map, and the
+// steps between groups of rows (D * 16 bytes) and halves (1024) are those of a
+// matrix descriptor.
+template <int D>
+__device__ __forceinline__ uint32_t sw_at(int r, int ch) {
+    return (r >> 3) * (D * 16) + (ch >> 3) * 1024 + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
 
 // One lane of a whole warp.  (With `lane == 0` instead the compiler does not know
@@ -88,17 +92,17 @@ __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
 // TMA copies of a box of rows, or of four rows; kBoth: to the same place in both
 // CTAs of the cluster, completing the barrier of each.
 template <bool kBoth>
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int row, uint32_t bar) {
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int half, int group, uint32_t bar) {
     if constexpr (kBoth)
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
-            "[%4], %5;\n" ::"r"(dst),
-            "l"(map), "r"(x), "r"(row), "r"(bar), "h"(static_cast<uint16_t>(3))
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %2, %3, "
+            "%4}], [%5], %6;\n" ::"r"(dst),
+            "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar), "h"(static_cast<uint16_t>(3))
             : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
-            "l"(map), "r"(x), "r"(row), "r"(bar)
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];\n" ::"r"(dst),
+            "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar)
             : "memory");
 }
 template <bool kBoth>
@@ -138,6 +142,22 @@ __device__ __forceinline__ bool wait_fast(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity)
         : "memory");
     if (__builtin_expect(__all_sync(0xffffffffu, ok != 0), 1)) return true;
+    return __all_sync(0xffffffffu, wait_on(bar, parity));
+}
+
+// The wait for P, which the tensor core stands still for: it polls (a waiting test
+// wakes up some 200 cycles late).
+__device__ __forceinline__ bool wait_poll(uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < 1000; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok != 0)) return true;
+    }
     return __all_sync(0xffffffffu, wait_on(bar, parity));
 }
 
@@ -259,16 +279,16 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                 if (lane == 0) expect_bytes(full, L::kTileBytes);
                 __syncwarp();
                 if (!active) return;
+                if (box > 0) {
+                    const uint32_t to = dst + lane * per * (D * 2);
+                    if (NQ == 2 && both) copy_box<true>(to, map, g * (D / 64), row[0] >> 3, full);
+                    else copy_box<false>(to, map, g * (D / 64), row[0] >> 3, full);
+                } else {
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    const uint32_t to = dst + h * (kTok * 128) + lane * per * 128;
-                    const int x = g * D + h * 64;
-                    if (NQ == 2 && both) {
-                        if (box > 0) copy_box<true>(to, map, x, row[0], full);
-                        else copy_rows4<true>(to, map, x, row, full);
-                    } else {
-                        if (box > 0) copy_box<false>(to, map, x, row[0], full);
-                        else copy_rows4<false>(to, map, x, row, full);
+                    for (int h = 0; h < D / 64; ++h) {
+                        const uint32_t to = dst + (lane >> 1) * (D * 16) + h * 1024 + (lane & 1) * 512;
+                        if (NQ == 2 && both) copy_rows4<true>(to, map, g * D + h * 64, row, full);
+                        else copy_rows4<false>(to, map, g * D + h * 64, row, full);
                     }
                 }
             };
@@ -297,8 +317,8 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             // while the products before them run, and looks at nothing else.
             if (n_tiles > 0) {
                 const uint32_t id_s = idesc(kRows, kTok, 0), id_o = idesc(kRows, D, 1);
-                const uint64_t dq = sdesc(s_base + L::kSmemQ, 16, 1024), dk = sdesc(s_base + L::kSmemK, 16, 1024);
-                const uint64_t dv = sdesc(s_base + L::kSmemV, kTok * 128, 1024);
+                const uint64_t dq = sdesc(s_base + L::kSmemQ, 16, D * 16), dk = sdesc(s_base + L::kSmemK, 16, D * 16);
+                const uint64_t dv = sdesc(s_base + L::kSmemV, 1024, D * 16);
                 const uint32_t hi = static_cast<uint32_t>(dq >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
                 const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), v_lo = static_cast<uint32_t>(dv);
                 auto issue_s = [&](int X, int buf, int slot) {
@@ -306,8 +326,8 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     const uint32_t qa = q_lo + X * (L::kQBytes >> 4), ka = k_lo + slot * (L::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        mma_f16(tmem + L::s_col(buf), desc_at(qa + (((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4), hi),
-                                desc_at(ka + (((ks >> 2) * (kTok * 128) + (ks & 3) * 32) >> 4), hi), id_s, ks > 0);
+                        mma_f16(tmem + L::s_col(buf), desc_at(qa + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), hi),
+                                desc_at(ka + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), hi), id_s, ks > 0);
                     mma_commit(bar(L::kSFull + buf));
                 };
                 auto issue_pv = [&](int X, int buf, int slot, bool acc) {
@@ -315,7 +335,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     const uint32_t va = v_lo + slot * (L::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kTok / 16; ++ks)
-                        mma_f16_ta(tmem + L::o_col(X), tmem + L::s_col(buf) + ks * 8, desc_at(va + ks * (16 * 128 >> 4), v_hi), id_o,
+                        mma_f16_ta(tmem + L::o_col(X), tmem + L::s_col(buf) + ks * 8, desc_at(va + ks * (2 * D * 16 >> 4), v_hi), id_o,
                                    (acc || ks > 0) ? 1u : 0u);
                 };
                 auto commit = [&](int i) {
@@ -341,7 +361,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     const bool more = j + 1 < n_tiles;
                     if constexpr (NQ == 2) {
                         if (j < n_x[0]) {
-                            if (!wait_fast(bar(L::kPFull), j & 1)) { ok = false; break; }
+                            if (!wait_poll(bar(L::kPFull), j & 1)) { ok = false; break; }
                             fence_after();
                             issue_pv(0, 0, slot, j > 0);
                             if (j == n_x[0] - 1) commit(L::kODone);
@@ -349,7 +369,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                         if (j + 1 < n_x[0]) issue_s(0, 0, slot1);
                         if (more && !wait_v(j + 1)) { ok = false; break; }
                         if (j < n_x[1]) {
-                            if (!wait_fast(bar(L::kPFull + 1), j & 1)) { ok = false; break; }
+                            if (!wait_poll(bar(L::kPFull + 1), j & 1)) { ok = false; break; }
                             fence_after();
                             issue_pv(1, 1, slot, j > 0);
                             if (j == n_x[1] - 1) commit(L::kODone + 1);
@@ -363,7 +383,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                             issue_s(0, (j + 1) & 1, slot1);
                             release(L::kKEmpty + slot1);
                         }
-                        if (!wait_fast(bar(L::kPFull + (j & 1)), (j >> 1) & 1)) { ok = false; break; }
+                        if (!wait_poll(bar(L::kPFull + (j & 1)), (j >> 1) & 1)) { ok = false; break; }
                         fence_after();
                         issue_pv(0, j & 1, slot, j > 0);
                         release(L::kVEmpty + slot);
@@ -384,18 +404,18 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     const int j = kv_lo + t * kTok + r;
                     if (j <= all_see) continue;
                     if (j >= kv_end) {
-                        for (int c = 0; c < kChunks; ++c) *reinterpret_cast<uint4 *>(v + sw_at(kTok, r, c)) = make_uint4(0, 0, 0, 0);
+                        for (int c = 0; c < kChunks; ++c) *reinterpret_cast<uint4 *>(v + sw_at<D>(r, c)) = make_uint4(0, 0, 0, 0);
                         continue;
                     }
                     bool bad = false;
 #pragma unroll 4
                     for (int c = 0; c < kChunks; ++c) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(v + sw_at(kTok, r, c));
+                        const uint4 w = *reinterpret_cast<const uint4 *>(v + sw_at<D>(r, c));
                         bad |= not_finite(w.x) || not_finite(w.y) || not_finite(w.z) || not_finite(w.w);
                     }
                     if (bad) {
                         for (int i = 0; i < D; ++i) {
-                            uint16_t *x = reinterpret_cast<uint16_t *>(v + sw_at(kTok, r, i / 8)) + (i & 7);
+                            uint16_t *x = reinterpret_cast<uint16_t *>(v + sw_at<D>(r, i / 8)) + (i & 7);
                             if ((*x & 0x7f80u) == 0x7f80u) *x = 0;
                         }
                         atomicOr(s_bad + ((t - guard) * kTok + r) / 32, 1u << (r & 31));
@@ -419,7 +439,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
 #pragma unroll 4
             for (int i = row; i < kRows * kChunks; i += kRows) {
                 const int r = i / kChunks, ch = i % kChunks, Rq = R0 + r;
-                uint4 *dst = reinterpret_cast<uint4 *>(sm + L::kSmemQ + X * L::kQBytes + sw_at(kRows, r, ch));
+                uint4 *dst = reinterpret_cast<uint4 *>(sm + L::kSmemQ + X * L::kQBytes + sw_at<D>(r, ch));
                 const int64_t at = (static_cast<int64_t>(e.qo0 + (Rq >> shift)) * p.n_heads + g * G + (Rq & (G - 1))) * D + ch * 8;
                 uint4 w = make_uint4(0u, 0u, 0u, 0u);
                 if (Rq < rows) w = *reinterpret_cast<const uint4 *>(q + at);
@@ -632,16 +652,20 @@ EncodeTiled encoder() {
     return f;
 }
 
-// One layer of the pool as a matrix of `size` rows, read in boxes of 64 columns.
+// One layer of the pool.  Boxes: 64 columns x 8 rows x the halves of a head x
+// groups of 8 rows, in the tile's order; single rows: a matrix of `size` rows.
 bool pool_map(CUtensorMap *map, const void *base, const ChunkParams &p, int D, int box) {
     const EncodeTiled f = encoder();
     if (!f) return false;
-    const cuuint64_t width = static_cast<cuuint64_t>(p.n_kv_heads) * D;
-    const cuuint64_t dims[2] = {width, static_cast<cuuint64_t>(p.size)}, strides[1] = {width * 2};
-    const cuuint32_t boxes[2] = {64, static_cast<cuuint32_t>(box > 0 ? box : 1)}, steps[2] = {1, 1};
-    void *at = const_cast<char *>(static_cast<const char *>(base) + static_cast<size_t>(p.layer_row0) * width * 2);
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, at, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t width = static_cast<cuuint64_t>(p.n_kv_heads) * D, row = width * 2, size = static_cast<cuuint64_t>(p.size);
+    const cuuint64_t dims4[4] = {64, 8, width / 64, size / 8}, dims2[2] = {width, size};
+    const cuuint64_t strides4[3] = {row, 128, 8 * row}, strides2[1] = {row};
+    const cuuint32_t box4[4] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(box / 8)}, box2[2] = {64, 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    void *at = const_cast<char *>(static_cast<const char *>(base) + static_cast<size_t>(p.layer_row0) * row);
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, box > 0 ? 4 : 2, at, box > 0 ? dims4 : dims2, box > 0 ? strides4 : strides2,
+             box > 0 ? box4 : box2, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int NQ>
