@@ -317,15 +317,17 @@ bool chunk_supported(int dtype, int head_dim, int group) {
 
 void chunk_plan(ChunkPlan *out, int dtype, int n_kv_heads, int group, int batch, int max_q_len, int max_len, int sms,
                 int64_t most_splits) {
-    // CTAs per SM, rows and keys per tile of the kernel that the call takes.
-    // With fewer than two rounds of CTAs the contexts are cut, into pieces of
-    // four tiles at least.
+    // CTAs per SM, rows and keys per tile of the kernel that the call takes.  A
+    // CTA's start and end cost as much as some 400 keys, so the contexts are cut
+    // only where one round of CTAs has room for the pieces, of four tiles at least
+    // (512 rows at 64K positions, bf16: 406 us in one round of 128 CTAs, 399 to 554
+    // in up to three).
     const bool wide = dtype == PKV_BF16 && chunk_wide(max_q_len, group);
     const int64_t per_sm = wide ? 1 : 2, rows = wide ? 256 : dtype == PKV_BF16 ? 128 : kRows, tok = wide ? 128 : 64;
     const int64_t tiles = (static_cast<int64_t>(max_q_len) * group + rows - 1) / rows;
-    const int64_t ctas = tiles * n_kv_heads * batch, want = 2 * per_sm * sms;
+    const int64_t ctas = tiles * n_kv_heads * batch;
     const int64_t kv_tiles = (static_cast<int64_t>(max_len) + tok - 1) / tok;
-    int64_t splits = ctas > 0 ? (want + ctas - 1) / ctas : 1;
+    int64_t splits = ctas > 0 ? per_sm * sms / ctas : 1;
     if (splits > kv_tiles / 4) splits = kv_tiles / 4;
     if (splits > most_splits) splits = most_splits;
     if (splits > 65535 / (tiles + 1)) splits = 65535 / (tiles + 1);   // grid y, tiles in pairs

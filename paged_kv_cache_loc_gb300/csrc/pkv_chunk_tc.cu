@@ -145,22 +145,6 @@ __device__ __forceinline__ bool wait_fast(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_on(bar, parity));
 }
 
-// The wait for P, which the tensor core stands still for: it polls (a waiting test
-// wakes up some 200 cycles late).
-__device__ __forceinline__ bool wait_poll(uint32_t bar, uint32_t parity) {
-    for (int i = 0; i < 1000; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (__all_sync(0xffffffffu, ok != 0)) return true;
-    }
-    return __all_sync(0xffffffffu, wait_on(bar, parity));
-}
-
 struct Maps {
     CUtensorMap k, v;
 };
@@ -361,7 +345,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     const bool more = j + 1 < n_tiles;
                     if constexpr (NQ == 2) {
                         if (j < n_x[0]) {
-                            if (!wait_poll(bar(L::kPFull), j & 1)) { ok = false; break; }
+                            if (!wait_fast(bar(L::kPFull), j & 1)) { ok = false; break; }
                             fence_after();
                             issue_pv(0, 0, slot, j > 0);
                             if (j == n_x[0] - 1) commit(L::kODone);
@@ -369,7 +353,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                         if (j + 1 < n_x[0]) issue_s(0, 0, slot1);
                         if (more && !wait_v(j + 1)) { ok = false; break; }
                         if (j < n_x[1]) {
-                            if (!wait_poll(bar(L::kPFull + 1), j & 1)) { ok = false; break; }
+                            if (!wait_fast(bar(L::kPFull + 1), j & 1)) { ok = false; break; }
                             fence_after();
                             issue_pv(1, 1, slot, j > 0);
                             if (j == n_x[1] - 1) commit(L::kODone + 1);
@@ -383,7 +367,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                             issue_s(0, (j + 1) & 1, slot1);
                             release(L::kKEmpty + slot1);
                         }
-                        if (!wait_poll(bar(L::kPFull + (j & 1)), (j >> 1) & 1)) { ok = false; break; }
+                        if (!wait_fast(bar(L::kPFull + (j & 1)), (j >> 1) & 1)) { ok = false; break; }
                         fence_after();
                         issue_pv(0, j & 1, slot, j > 0);
                         release(L::kVEmpty + slot);
