@@ -623,11 +623,11 @@ size_t pkv_compact_workspace_bytes(int64_t n_pages);
  *   c->max_len  that of n, max_pages * page_size at most.
  * Scores, sums and outputs are held in fp32 and rounded once to the output;
  * bf16 rounds the softmax's weights to bf16 for their product with V.  With few
- * query rows the contexts are cut into splits whose partials go to the
- * workspace and are joined by a second kernel: pkv_workspace_init(base, bytes,
- * n_q, n_heads, head_dim, s, ..) holds s splits, and pkv_chunk_splits says how
- * many a call of given sizes uses at most.  With a smaller workspace, or none,
- * it uses fewer (one), with the same result up to fp32 rounding.  The workspace
+ * query rows the contexts are cut into pieces whose partials go to the
+ * workspace and are joined by a second kernel.  A workspace of
+ * pkv_chunk_workspace_bytes(...) holds them; with less (ws->bytes), or none, the
+ * contexts stay whole, or in fewer pieces: the same result up to fp32 rounding,
+ * later.  The workspace
  * serves one call at a time.  Reads c->seq_lens, c->qo_indptr,
  * c->req_pool_indices, c->num_reqs and the pool; not c->req_to_token,
  * c->kv_indptr.  Supported: f32 and bf16, head_dim 64 or 128, G in {1, 2, 4, 8}.
@@ -641,10 +641,12 @@ int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_t
                     int32_t n_heads, int32_t max_q_len, int32_t causal, float sm_scale,
                     const pkv_workspace *ws, void *stream);
 
-/* Splits that pkv_paged_chunk uses at most for these sizes (c->batch,
- * c->max_len, the pool's heads and types), or a negative PKV_ERR_* code.
- * Host-only; enqueues nothing. */
-int32_t pkv_chunk_splits(const pkv_kvcache *c, int32_t n_heads, int32_t max_q_len);
+/* Workspace bytes of a pkv_paged_chunk call of these sizes (c->batch, c->max_len,
+ * the pool's heads and types; n_q rows of q), 256 at least; 0 for sizes that it
+ * refuses.  A call of fewer rows or a smaller batch may use more than one of the
+ * largest: size it for each, or take what fits. */
+size_t pkv_chunk_workspace_bytes(const pkv_kvcache *c, int32_t n_q, int32_t n_heads,
+                                 int32_t max_q_len);
 
 /*
  * Paged decode for callers that cannot allocate device memory: code running

@@ -29,11 +29,12 @@ from .ops import (KVCache, Workspace, decode_plan, decode_step, kv_write,  # noq
                   paged_decode_shared, paged_prefill, rope_kv_write)
 from .sparse import (SparsePages, build_tables, page_bounds, paged_decode_selected,  # noqa: F401
                      select_pages, select_workspace, select_workspace_bytes, sparse_decode_step)
-from .pages import (chunk_workspace, compact_pages, compact_workspace, copy_pages, fork_requests,  # noqa: F401
+from .pages import (chunk_workspace, chunk_workspace_bytes, compact_pages, compact_workspace, copy_pages, fork_requests,  # noqa: F401
                     paged_chunk, release_pages)
 from ._lib import PkvError, load  # noqa: F401
 
 __all__ = ["KVCache", "Workspace", "kv_write", "rope_kv_write", "paged_decode", "decode_step",
            "paged_decode_pages", "paged_decode_shared", "paged_prefill", "paged_decode_noalloc", "decode_plan",
            "SparsePages", "build_tables", "page_bounds", "select_pages", "select_workspace", "select_workspace_bytes",
-           "paged_decode_selected", "sparse_decode_step", "copy_pages", "fork_requests", "release_pages", "compact_pages", "compact_workspace", "paged_chunk", "chunk_workspace", "last_device_error", "PkvError", "load"]
+           "paged_decode_selected", "sparse_decode_step", "copy_pages", "fork_requests", "release_pages", "compact_pages", "compact_workspace", "paged_chunk", "chunk_workspace", "chunk_workspace_bytes",
+           "last_device_error", "PkvError", "load"]

@@ -167,7 +167,7 @@ SIGNATURES = {
                                        ctypes.c_int32, _vp, _vp, ctypes.c_int32, ctypes.c_int32,
                                        ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
                                        ctypes.POINTER(PkvWorkspace), _vp]),
-    "pkv_chunk_splits": (ctypes.c_int32, [ctypes.POINTER(PkvKVCache), ctypes.c_int32, ctypes.c_int32]),
+    "pkv_chunk_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PkvKVCache)] + [ctypes.c_int32] * 3),
     "pkv_last_device_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_int64)]),
     # include/pkv_pool.h (host page allocator)
     "pkv_pool_create": (_vp, [ctypes.c_int32, ctypes.c_int32]),

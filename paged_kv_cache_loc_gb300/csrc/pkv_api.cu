@@ -1081,12 +1081,12 @@ int pkv_compact_pages(const pkv_kvcache *c, const pkv_page_state *t, int32_t *fr
 
 namespace {
 
-// What pkv_paged_chunk and pkv_chunk_splits refuse alike.
-int check_chunk(const pkv_kvcache *c, int32_t n_heads, int32_t max_q_len, int *group) {
+// What pkv_paged_chunk and pkv_chunk_workspace_bytes refuse alike.
+int check_chunk(const pkv_kvcache *c, int32_t n_q, int32_t n_heads, int32_t max_q_len, int *group) {
     int rc = check_pool(c, 0);
     if (rc) return rc;
-    if (c->batch < 0 || c->batch > 65535 || c->max_len < 0 || max_q_len < 0) return PKV_ERR_ARG;
-    if (n_heads <= 0 || n_heads % c->n_kv_heads) return PKV_ERR_ARG;
+    if (c->batch < 0 || c->batch > 65535 || c->max_len < 0 || max_q_len < 0 || n_q < 0) return PKV_ERR_ARG;
+    if (n_heads <= 0 || n_heads % c->n_kv_heads || c->n_kv_heads > 65535) return PKV_ERR_ARG;
     *group = n_heads / c->n_kv_heads;
     if (!pkv::chunk_supported(c->dtype, c->head_dim, *group)) return PKV_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(max_q_len) * *group > pkv::kChunkMaxRows) return PKV_ERR_ARG;
@@ -1096,28 +1096,25 @@ int check_chunk(const pkv_kvcache *c, int32_t n_heads, int32_t max_q_len, int *g
 
 }  // namespace
 
-int32_t pkv_chunk_splits(const pkv_kvcache *c, int32_t n_heads, int32_t max_q_len) {
+size_t pkv_chunk_workspace_bytes(const pkv_kvcache *c, int32_t n_q, int32_t n_heads, int32_t max_q_len) {
     int group;
-    int rc = check_chunk(c, n_heads, max_q_len, &group);
-    if (rc) return rc;
     DeviceInfo di;
-    rc = device_info(&di);
-    if (rc) return rc;
-    if (c->batch == 0 || max_q_len == 0) return 1;
+    if (check_chunk(c, n_q, n_heads, max_q_len, &group) || device_info(&di)) return 0;
+    if (c->batch == 0 || n_q == 0 || max_q_len == 0) return 256;
     pkv::ChunkPlan plan;
-    pkv::chunk_plan(&plan, c->dtype, c->n_kv_heads, group, c->batch, max_q_len, c->max_len, di.sms, INT32_MAX);
-    return plan.n_splits;
+    pkv::chunk_plan(&plan, c->dtype, c->head_dim, c->n_kv_heads, group, c->batch, n_q, max_q_len, c->max_len, di.sms, SIZE_MAX);
+    return plan.bytes > 256 ? plan.bytes : 256;
 }
 
 int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_to_page, int32_t max_pages,
                     int32_t page_size, const void *q, void *o, int32_t n_q, int32_t n_heads, int32_t max_q_len,
                     int32_t causal, float sm_scale, const pkv_workspace *ws, void *stream) {
     int group;
-    int rc = check_chunk(c, n_heads, max_q_len, &group);
+    int rc = check_chunk(c, n_q, n_heads, max_q_len, &group);
     if (rc) return rc;
     if (layer_id < 0 || layer_id >= c->n_layers || !isfinite(sm_scale)) return PKV_ERR_ARG;
     if (page_size <= 0 || c->size % page_size || !req_to_page || max_pages <= 0 || c->num_reqs <= 0) return PKV_ERR_ARG;
-    if (c->max_len > static_cast<int64_t>(max_pages) * page_size || n_q < 0) return PKV_ERR_ARG;
+    if (c->max_len > static_cast<int64_t>(max_pages) * page_size) return PKV_ERR_ARG;
     if (c->batch > 0 && (!c->req_pool_indices || !c->seq_lens || !c->qo_indptr)) return PKV_ERR_ARG;
     if (c->batch == 0 || n_q == 0 || max_q_len == 0) return PKV_OK;
     if (!q || !o || q == o || !aligned16(q) || !aligned16(o)) return PKV_ERR_ARG;
@@ -1127,17 +1124,13 @@ int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_t
     rc = check_visible({c->k_buffer, c->v_buffer, req_to_page, c->req_pool_indices, c->seq_lens, c->qo_indptr, q, o,
                         ws ? ws->base : nullptr});
     if (rc) return rc;
-    int64_t most = 1;                            // splits whose partials the workspace holds
     if (ws) {
         rc = ws_check(ws);
         if (rc) return rc;
-        const int64_t units = static_cast<int64_t>(ws->max_batch) * ws->n_heads * ws->max_splits;
-        const int64_t rows = static_cast<int64_t>(n_q) * n_heads;
-        most = units * ws->head_dim / (rows * c->head_dim);
-        if (units / rows < most) most = units / rows;
     }
     pkv::ChunkPlan plan;
-    pkv::chunk_plan(&plan, c->dtype, c->n_kv_heads, group, c->batch, max_q_len, c->max_len, di.sms, most > 1 ? most : 1);
+    pkv::chunk_plan(&plan, c->dtype, c->head_dim, c->n_kv_heads, group, c->batch, n_q, max_q_len, c->max_len, di.sms,
+                    ws ? ws->bytes : 0);
     pkv::ChunkParams p{};
     p.q = q;
     p.o = o;
@@ -1147,10 +1140,13 @@ int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_t
     p.req_pool_indices = c->req_pool_indices;
     p.seq_lens = c->seq_lens;
     p.qo_indptr = c->qo_indptr;
-    if (plan.n_splits > 1) {
-        p.o_part = ws->o_part;
-        p.ml_part = ws->ml_part;
+    if (plan.bytes > 0) {
+        char *base = static_cast<char *>(ws->base);
+        p.o_part = reinterpret_cast<float *>(base);
+        p.ml_part = reinterpret_cast<float *>(base + plan.o_bytes);
+        if (plan.parts > 0) p.cum = reinterpret_cast<long long *>(base + plan.o_bytes + plan.ml_bytes);
     }
+    p.part_rows = max_q_len * group;
     p.size = c->size;
     p.layer_row0 = static_cast<int64_t>(layer_id) * c->size;
     p.n_pages = c->size / page_size;
@@ -1169,7 +1165,7 @@ int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_t
     p.split_len = plan.split_len;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.err = di.err;
-    return map_launch(pkv::launch_chunk(p, c->dtype, c->head_dim, group, static_cast<cudaStream_t>(stream)));
+    return map_launch(pkv::launch_chunk(p, plan.parts, c->dtype, c->head_dim, group, static_cast<cudaStream_t>(stream)));
 }
 
 int pkv_last_device_error(void *stream, int64_t *detail) {

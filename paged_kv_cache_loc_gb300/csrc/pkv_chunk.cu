@@ -17,7 +17,7 @@
 // the next scores do.
 #include <atomic>
 
-#include "pkv_chunk.cuh"
+#include "pkv_chunk_join.cuh"
 
 namespace pkv {
 namespace {
@@ -222,7 +222,6 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
 // the row does not see has written nothing for it and is not read.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
-    constexpr int kPer = D / 32;                        // elements per lane
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const ChunkEntry e = load_chunk_entry(p, blockIdx.z, false);
     const int lane = threadIdx.x & 31;
@@ -231,49 +230,7 @@ __global__ void __launch_bounds__(kThreads) chunk_join_kernel(const __grid_const
     const int i = static_cast<int>(u / p.n_heads), head = static_cast<int>(u - static_cast<int64_t>(i) * p.n_heads);
     const int lim = min(chunk_limit(p, e, i), e.kv_len - 1);
     const int n = lim < 0 ? 0 : lim / p.split_len + 1;
-    float top = -INFINITY, sum = 0.f, acc[kPer] = {};
-    for (int s0 = 0; s0 < n; s0 += 32) {                // the splits' (m, l), a lane each
-        float m = -INFINITY, l = 0.f;
-        if (s0 + lane < n) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ml_part + 2 * chunk_unit(p, s0 + lane, e.qo0 + i, head)));
-            m = ml.x;
-            l = ml.y;
-        }
-        float mt = m;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-        const float mn = fmaxf(top, mt), ref = mn == -INFINITY ? 0.f : mn;
-        const float alpha = exp2f(top - ref);
-        const float w = l * exp2f(m - ref);
-        top = mn;
-        float ws = w;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
-        sum = sum * alpha + ws;
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) acc[c] *= alpha;
-        const int cnt = min(32, n - s0);
-#pragma unroll 8
-        for (int s = 0; s < cnt; ++s) {
-            const float f = __shfl_sync(0xffffffffu, w, s);
-            const float *src = p.o_part + chunk_unit(p, s0 + s, e.qo0 + i, head) * D + lane * kPer;
-            if constexpr (kPer == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                acc[0] = fmaf(f, v.x, acc[0]);
-                acc[1] = fmaf(f, v.y, acc[1]);
-                acc[2] = fmaf(f, v.z, acc[2]);
-                acc[3] = fmaf(f, v.w, acc[3]);
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                acc[0] = fmaf(f, v.x, acc[0]);
-                acc[1] = fmaf(f, v.y, acc[1]);
-            }
-        }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    T *dst = static_cast<T *>(p.o) + (static_cast<int64_t>(e.qo0 + i) * p.n_heads + head) * D + lane * kPer;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) dst[c] = Elem<T>::from_f(acc[c] * inv);
+    join_row<T, D>(p, n, [&](int s) { return chunk_unit(p, s, e.qo0 + i, head); }, (static_cast<int64_t>(e.qo0 + i) * p.n_heads + head) * D);
 }
 
 template <int D>
@@ -315,32 +272,52 @@ bool chunk_supported(int dtype, int head_dim, int group) {
            (group == 1 || group == 2 || group == 4 || group == 8);
 }
 
-void chunk_plan(ChunkPlan *out, int dtype, int n_kv_heads, int group, int batch, int max_q_len, int max_len, int sms,
-                int64_t most_splits) {
+void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int group, int batch, int n_q, int max_q_len, int max_len,
+                int sms, size_t room) {
+    ChunkPlan &plan = *out;
+    plan = ChunkPlan{};
+    plan.n_splits = 1;
+    plan.split_len = 1 << 30;
+    if (dtype == PKV_BF16 && !chunk_wide(max_q_len, group)) {
+        // a CTA on every SM, and partials of one row of an item per step along the tiles
+        plan.parts = sms > 0 ? sms : 1;
+        const size_t units = (static_cast<size_t>(plan.parts) + static_cast<size_t>(batch) * n_kv_heads) * max_q_len * group;
+        plan.o_bytes = units * head_dim * sizeof(float);
+        plan.ml_bytes = units * 2 * sizeof(float);
+        plan.bytes = plan.o_bytes + plan.ml_bytes + (static_cast<size_t>(batch) + 1) * sizeof(int64_t);
+        if (plan.bytes > room) plan.bytes = 0;            // nothing is cut
+        return;
+    }
     // CTAs per SM, rows and keys per tile of the kernel that the call takes.  A
     // CTA's start and end cost as much as some 400 keys, so the contexts are cut
     // only where one round of CTAs has room for the pieces, of four tiles at least
     // (512 rows at 64K positions, bf16: 406 us in one round of 128 CTAs, 399 to 554
     // in up to three).
-    const bool wide = dtype == PKV_BF16 && chunk_wide(max_q_len, group);
-    const int64_t per_sm = wide ? 1 : 2, rows = wide ? 256 : dtype == PKV_BF16 ? 128 : kRows, tok = wide ? 128 : 64;
+    const bool wide = dtype == PKV_BF16;
+    const int64_t per_sm = wide ? 1 : 2, rows = wide ? 256 : kRows, tok = wide ? 128 : 64;
     const int64_t tiles = (static_cast<int64_t>(max_q_len) * group + rows - 1) / rows;
     const int64_t ctas = tiles * n_kv_heads * batch;
     const int64_t kv_tiles = (static_cast<int64_t>(max_len) + tok - 1) / tok;
+    const size_t per_split = static_cast<size_t>(n_q) * n_kv_heads * group;
+    const size_t most = per_split > 0 ? room / (per_split * (head_dim + 2) * sizeof(float)) : 0;
     int64_t splits = ctas > 0 ? per_sm * sms / ctas : 1;
     if (splits > kv_tiles / 4) splits = kv_tiles / 4;
-    if (splits > most_splits) splits = most_splits;
+    if (splits > 0 && static_cast<size_t>(splits) > most) splits = static_cast<int64_t>(most);
     if (splits > 65535 / (tiles + 1)) splits = 65535 / (tiles + 1);   // grid y, tiles in pairs
-    if (splits < 1) splits = 1;
-    int64_t per = (kv_tiles + splits - 1) / splits;
-    if (per < 1) per = 1;
-    out->split_len = static_cast<int32_t>(per * tok);
-    out->n_splits = static_cast<int32_t>(kv_tiles <= 0 ? 1 : (kv_tiles + per - 1) / per);
+    if (splits <= 1) return;
+    const int64_t per = (kv_tiles + splits - 1) / splits;
+    plan.split_len = static_cast<int32_t>(per * tok);
+    plan.n_splits = static_cast<int32_t>((kv_tiles + per - 1) / per);
+    if (plan.n_splits == 1) return;
+    plan.o_bytes = per_split * plan.n_splits * head_dim * sizeof(float);
+    plan.ml_bytes = per_split * plan.n_splits * 2 * sizeof(float);
+    plan.bytes = plan.o_bytes + plan.ml_bytes;
 }
 
-cudaError_t launch_chunk(const ChunkParams &p, int dtype, int head_dim, int group, cudaStream_t s) {
+cudaError_t launch_chunk(const ChunkParams &p, int parts, int dtype, int head_dim, int group, cudaStream_t s) {
     if (!chunk_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
     const bool f32 = dtype == PKV_F32;
+    if (parts > 0) return launch_chunk_rows(p, parts, head_dim, group, s);
     cudaError_t e = !f32 ? launch_chunk_tc(p, head_dim, group, s) : head_dim == 128 ? run_f32<128>(p, group, s) : run_f32<64>(p, group, s);
     if (e != cudaSuccess || p.n_splits == 1) return e;
     if (f32) return head_dim == 128 ? run_join<float, 128>(p, s) : run_join<float, 64>(p, s);

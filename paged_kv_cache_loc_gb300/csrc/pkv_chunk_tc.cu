@@ -2,53 +2,48 @@
 // (pkv_paged_chunk), bf16, on the 5th-generation tensor cores.
 //
 // The mathematics is that of pkv_chunk.cu: one pass over the keys with a running
-// maximum and sum, O rescaled when the maximum is raised.  A CTA takes one kv
-// head of one entry, NQ tiles of 128 rows (position, head in group), and the
-// keys of one split, kTok at a time:
+// maximum and sum, O rescaled when the maximum is raised.  This kernel takes
+// entries of more than 128 rows (position, head in group); pkv_chunk_rows.cu those
+// of fewer.  A CTA takes one kv head of one entry, two tiles of 128 rows, and the
+// keys of one split, 128 at a time:
 //   S = Q K^T  (tcgen05.mma, fp32 in tensor memory), P = 2^(S - m) as bf16 over
 //   S's columns, O += P V (P read from tensor memory).
+// The two tiles share every K/V tile, and the tensor core works on one while the
+// softmax runs on the other.  Two CTAs of a cluster, neighbouring rows of the same
+// entry and head, share the K/V tiles too: each copies every other box to both,
+// which halves what every SM fetches (the SMs together fetch 7 to 8 TB/s at most,
+// from L2 or not; one CTA alone wants 64 KB in 1.4 us, 7 TB/s).
 // Warps hand over through mbarriers, every wait bounded:
-//   4 NQ softmax warps, one thread per row: the row maximum needs no exchange;
+//   8 softmax warps, one thread per row: the row maximum needs no exchange;
 //   one warp that issues the products;
 //   one warp that copies K and V with TMA.  Positions of a page are consecutive
-//     rows of the pool, so a box of min(gcd(page_size, 128), kTok) rows never
-//     crosses a page; pages of other sizes are gathered four rows at a time
-//     (tile::gather4).  All rows that a copy names lie in the pool: behind the
-//     split's end it reads page 0, whose rows then count for nothing;
+//     rows of the pool, so a box of as many rows as the largest power of two in
+//     page_size never crosses a page; pages of other sizes are gathered four
+//     rows at a time (tile::gather4).  All rows that a copy names lie in the
+//     pool: behind the split's end it reads page 0, whose rows then count for
+//     nothing;
 //   two warps that look at the V tiles which some row of the CTA does not see
 //     wholly: a product with the weight 0 must not meet a value that is not
 //     finite.  Rows behind the end become 0; a value that is not finite is
 //     taken out and noted, and the epilogue adds it to the rows that see it.
-//
-// Two forms, by the rows of the longest entry:
-//   NQ = 2, kTok = 128: two query tiles share every K/V tile, and the tensor core
-//     works on one while the softmax runs on the other.  One CTA per SM, 512
-//     columns of tensor memory.
-//   NQ = 1, kTok = 64, two S buffers: up to 128 rows (drafts, single tokens),
-//     where the memory's rate bounds; two CTAs per SM, so that one's start and
-//     end lie under the other's stream.
-#include <cuda.h>
-
 #include <atomic>
 
-#include "pkv_chunk.cuh"
-#include "pkv_tcgen05.cuh"
+#include "pkv_chunk_tc.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kRows = 128;                  // query rows per tile (tensor-memory lanes)
+constexpr int kPair = 2 * kRows;            // query rows per CTA
 constexpr int kSlots = 2;                   // K tiles and V tiles in shared memory
-constexpr float kRescale = 8.f;             // the reference is raised by 2^8 at least
 constexpr int kGuarded = 6;                 // V tiles that are looked at, at most
 
-template <int D, int NQ>
+template <int D>
 struct Tc {
-    static constexpr int kTok = NQ == 2 ? 128 : 64;
-    static constexpr int kThreads = NQ * 128 + 128;
+    static constexpr int kTok = 128, kThreads = 384;
     static constexpr int kMmaWarp = 0, kCopyWarp = 1, kGuardWarp = 2, kSoftmaxWarp = 4;
     static constexpr int kQBytes = kRows * D * 2, kTileBytes = kTok * D * 2;
-    static constexpr int kSmemQ = 0, kSmemK = NQ * kQBytes, kSmemV = kSmemK + kSlots * kTileBytes;
+    static constexpr int kSmemQ = 0, kSmemK = 2 * kQBytes, kSmemV = kSmemK + kSlots * kTileBytes;
     static constexpr int kSmemBar = kSmemV + kSlots * kTileBytes;
     // barriers
     static constexpr int kKFull = 0, kKEmpty = kSlots, kVFull = 2 * kSlots, kVEmpty = 3 * kSlots;
@@ -58,108 +53,21 @@ struct Tc {
     static constexpr int kBadWords = kGuarded * kTok / 32 + 1;      // bits of rows, then: any
     static constexpr int kBytes = kSmemBad + kBadWords * 4 + 1024;  // + alignment slack
     // registers: the launch's, and how the warps share them
-    // (two tiles: 128 scores per softmax thread; with one, 64, all have enough)
+    // (a softmax thread holds 128 scores)
     static constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
     static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "no more than the launch holds");
     // tensor memory
-    static constexpr uint32_t kCols = NQ == 2 ? 512 : 256;
-    __device__ static constexpr uint32_t s_col(int buf) { return NQ == 2 ? buf * 256 : buf * 64; }
-    __device__ static constexpr uint32_t o_col(int X) { return NQ == 2 ? X * 256 + 128 : 128; }
-    static_assert(kBytes <= 227 * 1024 && (NQ == 2 || 2 * (kBytes + 1024) <= 228 * 1024), "shared memory");
+    static constexpr uint32_t kCols = 512;
+    __device__ static constexpr uint32_t s_col(int X) { return X * 256; }
+    __device__ static constexpr uint32_t o_col(int X) { return X * 256 + 128; }
+    static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-// Byte offset of 16-byte chunk ch of row r in a tile: eight rows at a time, their
-// 64-column halves as 8 x 128 bytes one after the other, chunk c of a row at c ^
-// (r % 8).  So a run of rows of a page is one box of the tensor map, and the
-// steps between groups of rows (D * 16 bytes) and halves (1024) are those of a
-// matrix descriptor.
 template <int D>
-__device__ __forceinline__ uint32_t sw_at(int r, int ch) {
-    return (r >> 3) * (D * 16) + (ch >> 3) * 1024 + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-}
-
-// One lane of a whole warp.  (With `lane == 0` instead the compiler does not know
-// that one thread issues the asynchronous instructions behind it, and each costs
-// several times as much.)
-__device__ __forceinline__ bool elect() {
-    uint32_t one;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
-    return one != 0;
-}
-__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
-}
-// TMA copies of a box of rows, or of four rows; kBoth: to the same place in both
-// CTAs of the cluster, completing the barrier of each.
-template <bool kBoth>
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int half, int group, uint32_t bar) {
-    if constexpr (kBoth)
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %2, %3, "
-            "%4}], [%5], %6;\n" ::"r"(dst),
-            "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar), "h"(static_cast<uint16_t>(3))
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];\n" ::"r"(dst),
-            "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar)
-            : "memory");
-}
-template <bool kBoth>
-__device__ __forceinline__ void copy_rows4(uint32_t dst, const CUtensorMap *map, int x, const int (&row)[4], uint32_t bar) {
-    if constexpr (kBoth)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
-            "%3, %4, %5, %6}], [%7], %8;\n" ::"r"(dst),
-            "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar), "h"(static_cast<uint16_t>(3))
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-            "[%7];\n" ::"r"(dst),
-            "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
-            : "memory");
-}
-// arrives on the barrier at this place in both CTAs once the products so far are done
-__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
-                 "h"(static_cast<uint16_t>(3))
-                 : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-
-// bar_wait of the warp that issues the products, with one answer for all lanes:
-// what is done already, as it mostly is, costs one test that falls through.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity) { return bar_wait(bar, parity); }
-__device__ __forceinline__ bool wait_fast(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (__builtin_expect(__all_sync(0xffffffffu, ok != 0), 1)) return true;
-    return __all_sync(0xffffffffu, wait_on(bar, parity));
-}
-
-struct Maps {
-    CUtensorMap k, v;
-};
-
-// Whether a word of two bf16 holds a value that is not finite.
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-    const uint32_t e = w & 0x7f807f80u;
-    return (e & 0xffffu) == 0x7f80u || (e >> 16) == 0x7f80u;
-}
-
-template <int D, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
+__global__ void __launch_bounds__(384, 1)
 chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, const int box) {
     using bf16 = __nv_bfloat16;
-    using L = Tc<D, NQ>;
+    using L = Tc<D>;
     constexpr int kTok = L::kTok, kChunks = D / 8;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -169,28 +77,28 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     auto bar = [&](int i) -> uint32_t { return s_base + L::kSmemBar + 8 * i; };
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    // Wide form: a cluster of two CTAs takes two neighbouring pairs of tiles and
+    // A cluster of two CTAs takes two neighbouring pairs of tiles and
     // the same keys; each copies half of every K/V tile to both.
     const int g = blockIdx.x, shift = p.group_shift, G = 1 << shift;
-    const int rank = NQ == 2 ? blockIdx.y & 1 : 0, unit = NQ == 2 ? blockIdx.y >> 1 : blockIdx.y, split = unit % p.n_splits;
+    const int rank = blockIdx.y & 1, unit = blockIdx.y >> 1, split = unit % p.n_splits;
     const ChunkEntry e = load_chunk_entry(p, blockIdx.z, g == 0 && blockIdx.y == 0 && tid == 0);
     const int rows = e.q_len << shift;
     // the entry's last rows, which see most, first
-    const int last_tile = (rows + NQ * kRows - 1) / (NQ * kRows) - 1 - unit / p.n_splits * NQ;
-    const int tile = last_tile - (NQ - 1) + rank;
+    const int last_tile = (rows + kPair - 1) / kPair - 1 - unit / p.n_splits * 2;
+    const int tile = last_tile - 1 + rank;
     if (tile < 0) return;
-    const bool both = NQ == 2 && last_tile > 0;          // the cluster's other CTA has rows too
-    const int row0 = tile * NQ * kRows, first_row = both ? (last_tile - 1) * NQ * kRows : row0;
+    const bool both = last_tile > 0;          // the cluster's other CTA has rows too
+    const int row0 = tile * kPair, first_row = both ? (last_tile - 1) * kPair : row0;
     const int kv_lo = split * p.split_len;
     // keys [kv_lo, end) that the rows up to `row` see in this split
     auto end_of = [&](int row) -> int { return min(min(kv_lo + p.split_len, e.kv_len), chunk_limit(p, e, row >> shift) + 1); };
-    int n_x[NQ];                                         // tiles of keys of each query tile
+    int n_x[2];                                         // tiles of keys of each query tile
 #pragma unroll
-    for (int X = 0; X < NQ; ++X) {
+    for (int X = 0; X < 2; ++X) {
         const int r0 = row0 + X * kRows, end = r0 < rows ? end_of(min(r0 + kRows, rows) - 1) : kv_lo;
         n_x[X] = end > kv_lo ? (end - kv_lo + kTok - 1) / kTok : 0;
     }
-    const int kv_end = max(kv_lo, end_of(min((last_tile + 1) * NQ * kRows, rows) - 1));
+    const int kv_end = max(kv_lo, end_of(min((last_tile + 1) * kPair, rows) - 1));
     const int n_tiles = (kv_end - kv_lo + kTok - 1) / kTok;   // of the cluster
     if (n_tiles == 0 && p.n_splits > 1) return;       // nothing to see: the join does not read this split
     // from tile `guard` on, some row of the cluster does not see all of a tile
@@ -204,9 +112,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             if (i >= L::kVClean && i < L::kSFull) count = 2;
             else if (both && ((i >= L::kKEmpty && i < L::kVFull) || (i >= L::kVEmpty && i < L::kVRaw))) count = 2;   // both CTAs' products
             else if (i >= L::kPFull && i < L::kODone) {        // the tile's warps that hold rows
-                const int left = rows - row0 - (NQ == 2 ? (i - L::kPFull) * kRows : 0);
+                const int left = rows - row0 - (i - L::kPFull) * kRows;
                 count = max(1, (min(left, kRows) + 31) / 32);
-            } else if (i == L::kQFull) count = NQ * 128;
+            } else if (i == L::kQFull) count = 256;
             mbar_init(bar(i), count);
         }
         for (int i = 0; i < L::kBadWords; ++i) s_bad[i] = 0;
@@ -242,7 +150,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     };
 
     if (warp < L::kSoftmaxWarp) {
-        if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kOtherRegs));
         if (warp == L::kCopyWarp) {
             // ================= copies: a lane takes a box of rows, or four rows
             const int per = box > 0 ? box : 4;
@@ -265,13 +173,13 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                 if (!active) return;
                 if (box > 0) {
                     const uint32_t to = dst + lane * per * (D * 2);
-                    if (NQ == 2 && both) copy_box<true>(to, map, g * (D / 64), row[0] >> 3, full);
+                    if (both) copy_box<true>(to, map, g * (D / 64), row[0] >> 3, full);
                     else copy_box<false>(to, map, g * (D / 64), row[0] >> 3, full);
                 } else {
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h) {
                         const uint32_t to = dst + (lane >> 1) * (D * 16) + h * 1024 + (lane & 1) * 512;
-                        if (NQ == 2 && both) copy_rows4<true>(to, map, g * D + h * 64, row, full);
+                        if (both) copy_rows4<true>(to, map, g * D + h * 64, row, full);
                         else copy_rows4<false>(to, map, g * D + h * 64, row, full);
                     }
                 }
@@ -305,21 +213,21 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                 const uint64_t dv = sdesc(s_base + L::kSmemV, 1024, D * 16);
                 const uint32_t hi = static_cast<uint32_t>(dq >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
                 const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), v_lo = static_cast<uint32_t>(dv);
-                auto issue_s = [&](int X, int buf, int slot) {
+                auto issue_s = [&](int X, int slot) {
                     if (!elect()) return;
                     const uint32_t qa = q_lo + X * (L::kQBytes >> 4), ka = k_lo + slot * (L::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        mma_f16(tmem + L::s_col(buf), desc_at(qa + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), hi),
+                        mma_f16(tmem + L::s_col(X), desc_at(qa + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), hi),
                                 desc_at(ka + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), hi), id_s, ks > 0);
-                    mma_commit(bar(L::kSFull + buf));
+                    mma_commit(bar(L::kSFull + X));
                 };
-                auto issue_pv = [&](int X, int buf, int slot, bool acc) {
+                auto issue_pv = [&](int X, int slot, bool acc) {
                     if (!elect()) return;
                     const uint32_t va = v_lo + slot * (L::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kTok / 16; ++ks)
-                        mma_f16_ta(tmem + L::o_col(X), tmem + L::s_col(buf) + ks * 8, desc_at(va + ks * (2 * D * 16 >> 4), v_hi), id_o,
+                        mma_f16_ta(tmem + L::o_col(X), tmem + L::s_col(X) + ks * 8, desc_at(va + ks * (2 * D * 16 >> 4), v_hi), id_o,
                                    (acc || ks > 0) ? 1u : 0u);
                 };
                 auto commit = [&](int i) {
@@ -327,7 +235,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                 };
                 auto release = [&](int i) {     // a tile of K or V, in both CTAs
                     if (!elect()) return;
-                    if (NQ == 2 && both) mma_commit_both(bar(i));
+                    if (both) mma_commit_both(bar(i));
                     else mma_commit(bar(i));
                 };
                 auto wait_k = [&](int t) -> bool { return wait_fast(bar(L::kKFull + t % kSlots), phase(t)); };
@@ -335,45 +243,32 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                 bool ok = wait_fast(bar(L::kQFull), 0) && wait_k(0);
                 if (ok) {
                     fence_after();
-                    if (n_x[0] > 0) issue_s(0, 0, 0);
-                    if (NQ == 2 && n_x[NQ - 1] > 0) issue_s(1, 1, 0);
+                    if (n_x[0] > 0) issue_s(0, 0);
+                    if (n_x[1] > 0) issue_s(1, 0);
                     release(L::kKEmpty);
                     ok = wait_v(0) && (n_tiles == 1 || wait_k(1));
                 }
                 for (int j = 0; ok && j < n_tiles; ++j) {
                     const int slot = j % kSlots, slot1 = (j + 1) % kSlots;
                     const bool more = j + 1 < n_tiles;
-                    if constexpr (NQ == 2) {
-                        if (j < n_x[0]) {
-                            if (!wait_fast(bar(L::kPFull), j & 1)) { ok = false; break; }
-                            fence_after();
-                            issue_pv(0, 0, slot, j > 0);
-                            if (j == n_x[0] - 1) commit(L::kODone);
-                        }
-                        if (j + 1 < n_x[0]) issue_s(0, 0, slot1);
-                        if (more && !wait_v(j + 1)) { ok = false; break; }
-                        if (j < n_x[1]) {
-                            if (!wait_fast(bar(L::kPFull + 1), j & 1)) { ok = false; break; }
-                            fence_after();
-                            issue_pv(1, 1, slot, j > 0);
-                            if (j == n_x[1] - 1) commit(L::kODone + 1);
-                        }
-                        release(L::kVEmpty + slot);
-                        if (j + 1 < n_x[1]) issue_s(1, 1, slot1);
-                        if (more) release(L::kKEmpty + slot1);
-                        if (j + 2 < n_tiles) ok = wait_k(j + 2);
-                    } else {
-                        if (more) {
-                            issue_s(0, (j + 1) & 1, slot1);
-                            release(L::kKEmpty + slot1);
-                        }
-                        if (!wait_fast(bar(L::kPFull + (j & 1)), (j >> 1) & 1)) { ok = false; break; }
+                    if (j < n_x[0]) {
+                        if (!wait_fast(bar(L::kPFull), j & 1)) { ok = false; break; }
                         fence_after();
-                        issue_pv(0, j & 1, slot, j > 0);
-                        release(L::kVEmpty + slot);
-                        if (!more) commit(L::kODone);
-                        else ok = wait_v(j + 1) && (j + 2 >= n_tiles || wait_k(j + 2));
+                        issue_pv(0, slot, j > 0);
+                        if (j == n_x[0] - 1) commit(L::kODone);
                     }
+                    if (j + 1 < n_x[0]) issue_s(0, slot1);
+                    if (more && !wait_v(j + 1)) { ok = false; break; }
+                    if (j < n_x[1]) {
+                        if (!wait_fast(bar(L::kPFull + 1), j & 1)) { ok = false; break; }
+                        fence_after();
+                        issue_pv(1, slot, j > 0);
+                        if (j == n_x[1] - 1) commit(L::kODone + 1);
+                    }
+                    release(L::kVEmpty + slot);
+                    if (j + 1 < n_x[1]) issue_s(1, slot1);
+                    if (more) release(L::kKEmpty + slot1);
+                    if (j + 2 < n_tiles) ok = wait_k(j + 2);
                 }
                 if (!ok) give_up(-5003);
             }
@@ -413,8 +308,8 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         }
     } else {
         // ================= softmax: the rows of tile X, a thread each
-        if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(L::kSoftmaxRegs));
-        const int X = NQ == 2 ? (warp - L::kSoftmaxWarp) >> 2 : 0, row = tid & (kRows - 1), R0 = row0 + X * kRows, R = R0 + row;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(L::kSoftmaxRegs));
+        const int X = (warp - L::kSoftmaxWarp) >> 2, row = tid & (kRows - 1), R0 = row0 + X * kRows, R = R0 + row;
         {
             // The maximum is of the products, so a scale below 0 is taken into q,
             // and one of 0 makes q 0.
@@ -433,7 +328,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             fence_async_smem();
             mbar_arrive(bar(L::kQFull));
         }
-        const int mine = NQ == 2 ? (X ? n_x[NQ - 1] : n_x[0]) : n_x[0];   // tiles
+        const int mine = X ? n_x[1] : n_x[0];   // tiles
         const bool busy = R0 + (warp & 3) * 32 < rows;                     // the warp holds rows
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_o = tmem + L::o_col(X) + lane_off;
@@ -442,11 +337,10 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         float m = -INFINITY, l = 0.f;
         bool live = busy;
         for (int j = 0; live && j < mine; ++j) {
-            const int buf = NQ == 2 ? X : j & 1;
-            bool ok = *s_abort == 0 && bar_wait(bar(L::kSFull + buf), NQ == 2 ? j & 1 : (j >> 1) & 1);
+            bool ok = *s_abort == 0 && bar_wait(bar(L::kSFull + X), j & 1);
             if (!__all_sync(0xffffffffu, ok)) { give_up(-5009); live = false; break; }
             fence_after();
-            const uint32_t t_s = tmem + L::s_col(buf) + lane_off;
+            const uint32_t t_s = tmem + L::s_col(X) + lane_off;
             float sv[kTok / 64][64];
 #pragma unroll
             for (int h = 0; h < kTok / 64; ++h) tmem_ld64(t_s + h * 64, sv[h]);
@@ -466,12 +360,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             const bool raise = mt > m + kRescale || (m == -INFINITY && mt != -INFINITY);
             const bool touch = raise && j > 0 && m != -INFINITY;
             const float alpha = raise ? exp2f(m - mt) : 1.f;
-            if (__any_sync(0xffffffffu, touch)) {
-                if (NQ == 1) {      // P V of the tile before may still run (with two tiles S follows it)
-                    ok = bar_wait(bar(L::kVEmpty + (j - 1) % kSlots), phase(j - 1));
-                    if (!__all_sync(0xffffffffu, ok)) { give_up(-5010); live = false; break; }
-                    fence_after();
-                }
+            if (__any_sync(0xffffffffu, touch)) {      // (P V of the tile before came before this S)
                 const float f = touch ? alpha : 1.f;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -510,7 +399,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::kPFull + buf));
+            if (lane == 0) mbar_arrive(bar(L::kPFull + X));
         }
         // ---- epilogue: O is final once its last product is done
         if (busy && live) {     // (nothing to see: the query tile, whose place the rows go through)
@@ -523,6 +412,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             const bool some_bad = mine > 0 && *static_cast<volatile uint32_t *>(s_bad + L::kBadWords - 1) != 0;
             // columns [c0, c0 + 32) of this row
             auto load_o = [&](int c0, float (&v)[32]) {
+                __syncwarp();
                 if (mine == 0) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -617,6 +507,42 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
 // host
 // ---------------------------------------------------------------------------
 
+template <int D>
+cudaError_t run(const ChunkParams &p, int group, cudaStream_t s) {
+    using L = Tc<D>;
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_done.load() & bit)) {
+        e = cudaFuncSetAttribute(chunk_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+        if (e != cudaSuccess) return e;
+        // the warps' shares add up to the launch's registers: fewer, and they would wait for more
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, chunk_tc_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs < L::kLaunchRegs) return cudaErrorNotSupported;
+        attr_done.fetch_or(bit);
+    }
+    const int box = box_rows(p.page_size, L::kTok / 2);    // (two boxes at least, for two CTAs)
+    Maps maps;
+    if (!pool_maps(&maps, p, D, box)) return cudaErrorInvalidValue;
+    const int tiles = (p.max_q_len * group + kPair - 1) / kPair;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_kv_heads, (tiles + 1) / 2 * 2 * p.n_splits, p.batch);
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.y = 2;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D>, p, maps, box);
+}
+
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                  const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -652,53 +578,16 @@ bool pool_map(CUtensorMap *map, const void *base, const ChunkParams &p, int D, i
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NQ>
-cudaError_t run(const ChunkParams &p, int group, cudaStream_t s) {
-    using L = Tc<D, NQ>;
-    static std::atomic<uint64_t> attr_done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(attr_done.load() & bit)) {
-        e = cudaFuncSetAttribute(chunk_tc_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-        if (e != cudaSuccess) return e;
-        // the warps' shares add up to the launch's registers: fewer, and they would wait for more
-        cudaFuncAttributes attr;
-        e = cudaFuncGetAttributes(&attr, chunk_tc_kernel<D, NQ>);
-        if (e != cudaSuccess) return e;
-        if (NQ == 2 && attr.numRegs < L::kLaunchRegs) return cudaErrorNotSupported;
-        attr_done.fetch_or(bit);
-    }
-    // rows of a page that a box may take: the largest power of two in page_size
-    int box = p.page_size & -p.page_size;
-    if (box > L::kTok / NQ) box = L::kTok / NQ;   // (two boxes at least where two CTAs share the copies)
-    if (box < 8) box = 0;                    // below a swizzle atom: four rows at a time
-    Maps maps;
-    if (!pool_map(&maps.k, p.k_buffer, p, D, box) || !pool_map(&maps.v, p.v_buffer, p, D, box)) return cudaErrorInvalidValue;
-    const int tiles = (p.max_q_len * group + NQ * kRows - 1) / (NQ * kRows);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_kv_heads, (tiles + NQ - 1) / NQ * NQ * p.n_splits, p.batch);
-    cfg.blockDim = dim3(L::kThreads);
-    cfg.dynamicSmemBytes = L::kBytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
-    attr[0].val.clusterDim.y = NQ;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, NQ>, p, maps, box);
-}
-
 }  // namespace
+
+bool pool_maps(Maps *maps, const ChunkParams &p, int D, int box) {
+    return pool_map(&maps->k, p.k_buffer, p, D, box) && pool_map(&maps->v, p.v_buffer, p, D, box);
+}
 
 bool chunk_wide(int max_q_len, int group) { return static_cast<int64_t>(max_q_len) * group > kRows; }
 
 cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, cudaStream_t s) {
-    const bool wide = chunk_wide(p.max_q_len, group);
-    if (head_dim == 128) return wide ? run<128, 2>(p, group, s) : run<128, 1>(p, group, s);
-    return wide ? run<64, 2>(p, group, s) : run<64, 1>(p, group, s);
+    return head_dim == 128 ? run<128>(p, group, s) : run<64>(p, group, s);
 }
 
 }  // namespace pkv

@@ -349,6 +349,10 @@ struct ChunkParams {
     const int32_t *qo_indptr;     // [batch + 1]
     float *o_part;                // [n_splits, n_q, n_heads, head_dim] (more than one split)
     float *ml_part;               // [n_splits, n_q, n_heads, 2]
+    // few rows: o_part [CTAs + items, part_rows, head_dim], ml_part likewise, and the
+    // entries' first tiles [batch + 1] (null: no room, items stay whole)
+    long long *cum;
+    int32_t part_rows;            // max_q_len * G
     int64_t size;
     int64_t layer_row0;
     int64_t n_pages;
@@ -371,6 +375,10 @@ struct ChunkParams {
 struct ChunkPlan {
     int32_t n_splits;
     int32_t split_len;
+    int32_t parts;                // few rows: CTAs that share all tiles (else 0)
+    size_t o_bytes;               // of the partials
+    size_t ml_bytes;
+    size_t bytes;                 // of the workspace that the plan uses; 0: none
 };
 
 constexpr int kScoreGroup = 16;         // pages scored together
@@ -392,14 +400,15 @@ cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t s);
 cudaError_t launch_release(const ReleaseParams &p, int sms, cudaStream_t s);
 cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t s);
 bool chunk_supported(int dtype, int head_dim, int group);
-// How the contexts are cut, into most_splits pieces at most.
-void chunk_plan(ChunkPlan *out, int dtype, int n_kv_heads, int group, int batch, int max_q_len, int max_len, int sms,
-                int64_t most_splits);
-cudaError_t launch_chunk(const ChunkParams &p, int dtype, int head_dim, int group, cudaStream_t s);
-// bf16 on tensor cores (pkv_chunk_tc.cu), without the join; `wide`: the form with
-// two query tiles of 128 rows.
+// How the contexts are cut with `room` bytes of workspace.
+void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int group, int batch, int n_q, int max_q_len, int max_len,
+                int sms, size_t room);
+cudaError_t launch_chunk(const ChunkParams &p, int parts, int dtype, int head_dim, int group, cudaStream_t s);
+// bf16 on tensor cores, without the join: entries of more than 128 rows (`wide`,
+// pkv_chunk_tc.cu); of fewer, with it (pkv_chunk_rows.cu).
 bool chunk_wide(int max_q_len, int group);
 cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, cudaStream_t s);
+cudaError_t launch_chunk_rows(const ChunkParams &p, int parts, int head_dim, int group, cudaStream_t s);
 // Query rows (position, head in group) of a call at most, per kv head and entry.
 constexpr int64_t kChunkMaxRows = 65535LL * 64;
 // Whether the selection and the attention over it have a kernel for this shape.

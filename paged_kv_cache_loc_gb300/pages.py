@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import PkvKVCache, PkvPageState, check
+from ._lib import PkvKVCache, PkvPageState
 from .ops import KVCache, Workspace, _DTYPES
 from . import sparse
 from .sparse import _call, _f32, _heads, _i32, _int32, _ints, _output, _pack_cache, _ptr, _rows, _st, _vp
@@ -169,20 +169,21 @@ def compact_pages(cache: KVCache, req_to_page: torch.Tensor, page_size: int, sha
     return remap
 
 
-def chunk_workspace(cache: KVCache, n_rows: int, n_heads: int, max_q_len: int) -> Workspace:
-    """A workspace for paged_chunk calls of cache's batch and max_len with n_rows
-    query rows (max_q_len for an entry) at most.  It holds the splits that such a
-    call uses; a call with fewer rows may use more splits and then takes as many
-    as fit."""
+def chunk_workspace_bytes(cache: KVCache, n_rows: int, n_heads: int, max_q_len: int) -> int:
+    """Workspace bytes of a paged_chunk call of cache's batch and max_len with
+    n_rows query rows, max_q_len for an entry at most."""
     index = _index(cache)
     c = PkvKVCache.from_buffer_copy(_describe(cache, 0, 0, index, True))
     with torch.cuda.device(index):
-        splits = _lib.load().pkv_chunk_splits(ctypes.byref(c), n_heads, max_q_len)
-    if splits < 1:
-        check(splits, "pkv_chunk_splits")
-    if splits == 1:                                       # nothing is split: no partials
-        return Workspace(1, 1, 64, 1, device=cache.k_buffer.device)
-    return Workspace(max(1, n_rows), n_heads, cache.k_buffer.shape[3], splits, device=cache.k_buffer.device)
+        return _lib.load().pkv_chunk_workspace_bytes(ctypes.byref(c), n_rows, n_heads, max_q_len)
+
+
+def chunk_workspace(cache: KVCache, n_rows: int, n_heads: int, max_q_len: int) -> Workspace:
+    """A workspace for paged_chunk calls of these sizes.  Other calls take what fits."""
+    need = chunk_workspace_bytes(cache, n_rows, n_heads, max_q_len)
+    if need == 0:
+        raise ValueError("sizes that paged_chunk refuses")
+    return Workspace(1, 1, 64, -(-need // 256), device=cache.k_buffer.device)      # 256 bytes of partials per split
 
 
 def paged_chunk(cache: KVCache, layer_id: int, req_to_page: torch.Tensor, page_size: int, q: torch.Tensor, max_q_len: int,

@@ -384,6 +384,6 @@ def test_refusals():
             c.run(sm_scale=scale)
     with pytest.raises(pkv.PkvError):
         c.run(o=c.q)
-    with pytest.raises(pkv.PkvError):
+    with pytest.raises(ValueError, match="refuses"):
         pkv.chunk_workspace(x, 16, 6, 8)
     clean()
