@@ -1144,7 +1144,7 @@ int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_t
         char *base = static_cast<char *>(ws->base);
         p.o_part = reinterpret_cast<float *>(base);
         p.ml_part = reinterpret_cast<float *>(base + plan.o_bytes);
-        if (plan.parts > 0) p.cum = reinterpret_cast<long long *>(base + plan.o_bytes + plan.ml_bytes);
+        if (plan.parts > 0) p.cut = reinterpret_cast<int32_t *>(base + plan.o_bytes + plan.ml_bytes);
     }
     p.part_rows = max_q_len * group;
     p.size = c->size;

@@ -284,7 +284,7 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
         const size_t units = (static_cast<size_t>(plan.parts) + static_cast<size_t>(batch) * n_kv_heads) * max_q_len * group;
         plan.o_bytes = units * head_dim * sizeof(float);
         plan.ml_bytes = units * 2 * sizeof(float);
-        plan.bytes = plan.o_bytes + plan.ml_bytes + (static_cast<size_t>(batch) + 1) * sizeof(int64_t);
+        plan.bytes = plan.o_bytes + plan.ml_bytes + static_cast<size_t>(batch) * n_kv_heads * 2 * sizeof(int32_t);
         if (plan.bytes > room) plan.bytes = 0;            // nothing is cut
         return;
     }

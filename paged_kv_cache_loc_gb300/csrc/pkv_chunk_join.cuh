@@ -16,18 +16,32 @@ struct ChunkDeal {
         return x < most ? (x < 1 ? 1 : static_cast<int>(x)) : most;
     }
     __device__ __forceinline__ long long begin(int c) const { return tiles * c / parts(); }
-    // the largest c with begin(c) <= x
-    __device__ __forceinline__ int owner(long long x) const { return static_cast<int>(((x + 1) * parts() - 1) / tiles); }
 };
 
 // o[at ..] = sum_s l_s 2^(m_s - M) o_s / sum_s l_s 2^(m_s - M) over the n pieces of a
 // row, piece s at unit(s), by a warp.
 template <typename T, int D, typename Unit>
 __device__ __forceinline__ void join_row(const ChunkParams &p, int n, Unit unit, int64_t at) {
-    constexpr int kPer = D / 32;                        // elements per lane
+    constexpr int kPer = D / 32, kLoads = 16;           // elements per lane, pieces in flight
     const int lane = threadIdx.x & 31;
     float top = -INFINITY, sum = 0.f, acc[kPer] = {};
+    float v[kLoads][kPer];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int s = 0; s < kLoads; ++s) {
+            if (s0 + s >= n) break;
+            const float *src = p.o_part + unit(s0 + s) * D + lane * kPer;
+            if constexpr (kPer == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                v[s][0] = x.x, v[s][1] = x.y, v[s][2] = x.z, v[s][3] = x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                v[s][0] = x.x, v[s][1] = x.y;
+            }
+        }
+    };
     for (int s0 = 0; s0 < n; s0 += 32) {                // the pieces' (m, l), a lane each
+        load(s0);                                       // (the first of the pieces beside them)
         float m = -INFINITY, l = 0.f;
         if (s0 + lane < n) {
             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ml_part + 2 * unit(s0 + lane)));
@@ -47,21 +61,15 @@ __device__ __forceinline__ void join_row(const ChunkParams &p, int n, Unit unit,
         sum = sum * alpha + ws;
 #pragma unroll
         for (int c = 0; c < kPer; ++c) acc[c] *= alpha;
-        const int cnt = min(32, n - s0);
-#pragma unroll 8
-        for (int s = 0; s < cnt; ++s) {
-            const float f = __shfl_sync(0xffffffffu, w, s);
-            const float *src = p.o_part + unit(s0 + s) * D + lane * kPer;
-            if constexpr (kPer == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                acc[0] = fmaf(f, v.x, acc[0]);
-                acc[1] = fmaf(f, v.y, acc[1]);
-                acc[2] = fmaf(f, v.z, acc[2]);
-                acc[3] = fmaf(f, v.w, acc[3]);
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                acc[0] = fmaf(f, v.x, acc[0]);
-                acc[1] = fmaf(f, v.y, acc[1]);
+#pragma unroll
+        for (int h = 0; h < 32 / kLoads; ++h) {
+            if (h > 0 && s0 + h * kLoads < n) load(s0 + h * kLoads);
+#pragma unroll
+            for (int s = 0; s < kLoads; ++s) {
+                const float f = __shfl_sync(0xffffffffu, w, h * kLoads + s);
+                if (s0 + h * kLoads + s >= n) continue;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) acc[c] = fmaf(f, v[s][c], acc[c]);
             }
         }
     }

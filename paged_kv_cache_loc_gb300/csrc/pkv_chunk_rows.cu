@@ -56,7 +56,7 @@ struct Lay {
     static constexpr int kBadWords = kGuarded * kTok / 32;
     static constexpr int kSmemBad = kSmemSeg + kSegs * static_cast<int>(sizeof(Segment));   // [kSegs][kBadWords + 1]: bits, then any
     static constexpr int kSmemMisc = kSmemBad + kSegs * (kBadWords + 1) * 4;                // tensor memory, abort
-    static constexpr int kBytes = kSmemMisc + 8 + kThreads / 32 * 8 + 32 + 1024;            // sums, borders; alignment slack
+    static constexpr int kBytes = kSmemMisc + 8 + kThreads / 32 * 8 + 32 + 32 + 1024;       // sums, borders, entry; alignment slack
     static constexpr uint32_t kCols = 512;
     static_assert(sizeof(Segment) == 64 && kSmemMisc % 8 == 0 && kBytes <= 227 * 1024, "shared memory");
 };
@@ -77,6 +77,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     long long *s_sum = reinterpret_cast<long long *>(sm + L::kSmemMisc + 8);           // a warp's tiles
     int(*s_at)[4] = reinterpret_cast<int(*)[4]>(sm + L::kSmemMisc + 8 + kThreads / 32 * 8);   // where the CTA's tiles begin and end:
                                                          // entry, head, tile, the item's tiles
+    ChunkEntry *s_entry = reinterpret_cast<ChunkEntry *>(sm + L::kSmemMisc + 8 + kThreads / 32 * 8 + 32);
     Segment *segs = reinterpret_cast<Segment *>(sm + L::kSmemSeg);
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + L::kSmemMisc + 4);
     auto bar = [&](int i) -> uint32_t { return s_base + L::kSmemBar + 8 * i; };
@@ -84,6 +85,23 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     const int shift = p.group_shift, G = 1 << shift, HK = p.n_kv_heads, c = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
+    // ---- barriers, tensor memory
+    if (tid == 0) {
+        for (int i = 0; i < L::kBars; ++i) {
+            uint32_t count = 1;
+            if ((i >= L::kPFull && i < L::kODone) || (i >= L::kOEmpty && i < L::kQFull)) count = 4;
+            else if (i >= L::kSegEmpty) count = 7;       // products, query tiles, V tiles, four softmax warps
+            mbar_init(bar(i), count);
+        }
+        *s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (tid == 32) asm volatile("prefetch.tensormap [%0];\nprefetch.tensormap [%1];\n" ::"l"(&maps.k), "l"(&maps.v) : "memory");
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(s_base + L::kSmemMisc), "r"(L::kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    fence_before();
     // ---- this CTA's tiles: sums of the entries' tiles, a run of entries per thread
     long long n_all;                                     // tiles of all items
     int n;                                               // of this CTA
@@ -107,28 +125,22 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         }
         n_all = total * HK;
         const ChunkDeal deal{n_all, static_cast<int>(gridDim.x)};
-        if (c == 0 && p.cum) {
-            long long at = pre;
-            for (int b = b0; b < b1; ++b) {
-                p.cum[b] = at;
-                at += tiles_of(load_chunk_entry(p, b, false));
-            }
-            if (tid == 0) p.cum[p.batch] = total;
-        }
-        if (n_all == 0 || c >= deal.parts()) return;
-        const long long x[2] = {deal.begin(c), deal.begin(c + 1)};
+        const bool mine_some = n_all > 0 && c < deal.parts();
+        const long long x[2] = {mine_some ? deal.begin(c) : 0, mine_some ? deal.begin(c + 1) : 0};
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (x[k] >= pre * HK && x[k] < (pre + mine) * HK) {
                 long long at = pre * HK;
                 for (int b = b0; b < b1; ++b) {
-                    const int t = tiles_of(load_chunk_entry(p, b, false));
+                    const ChunkEntry e = load_chunk_entry(p, b, false);
+                    const int t = tiles_of(e);
                     if (x[k] < at + static_cast<long long>(t) * HK) {
                         const long long in = x[k] - at;
                         s_at[k][0] = b;
                         s_at[k][1] = static_cast<int>(in / t);
                         s_at[k][2] = static_cast<int>(in % t);
                         s_at[k][3] = t;
+                        if (k == 0) *s_entry = e;
                         break;
                     }
                     at += static_cast<long long>(t) * HK;
@@ -136,34 +148,18 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             }
         __syncthreads();
         long long lo = x[0], hi = x[1];
-        if (!p.cum) {                                    // whole items: those that begin in [lo, hi)
+        if (mine_some && !p.cut) {                       // whole items: those that begin in [lo, hi)
             if (s_at[0][2] > 0) lo += s_at[0][3] - s_at[0][2];
             if (hi < n_all && s_at[1][2] > 0) hi += s_at[1][3] - s_at[1][2];
         }
         n = static_cast<int>(hi - lo);                   // (a CTA's tiles are far fewer than 2^31)
     }
-    if (n <= 0) return;
-
-    // ---- barriers, tensor memory
-    if (tid == 0) {
-        for (int i = 0; i < L::kBars; ++i) {
-            uint32_t count = 1;
-            if ((i >= L::kPFull && i < L::kODone) || (i >= L::kOEmpty && i < L::kQFull)) count = 4;
-            else if (i >= L::kSegEmpty) count = 7;       // products, query tiles, V tiles, four softmax warps
-            mbar_init(bar(i), count);
-        }
-        *s_abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];\nprefetch.tensormap [%1];\n" ::"l"(&maps.k), "l"(&maps.v) : "memory");
-    }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(s_base + L::kSmemMisc), "r"(L::kCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-    }
-    fence_before();
-    __syncthreads();
     fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sm + L::kSmemMisc), 0);
+    if (n <= 0) {
+        if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(L::kCols));
+        return;
+    }
     auto give_up = [&](int code) {
         if (lane == 0 && *s_abort == 0) {
             *s_abort = 1;
@@ -191,7 +187,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     if (warp == 1) {
         // ================= the list of segments, and the copies
         int b = s_at[0][0], g = s_at[0][1], t0 = s_at[0][2], left = n, listed = 0;
-        ChunkEntry e = load_chunk_entry(p, b, false);
+        ChunkEntry e = *s_entry;
         int t_item = tiles_of(e);
         auto next_item = [&]() {
             t0 = 0;
@@ -209,7 +205,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
                 t_item = tiles_of(e);
             }
         };
-        if (!p.cum && t0 > 0) next_item();
+        if (!p.cut && t0 > 0) next_item();
         auto list = [&]() -> bool {
             if (left == 0) return true;
             if (!empty(L::kSegEmpty, kSegs, listed)) return false;
@@ -225,6 +221,11 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             if (lane == 0) {
                 segs[listed % kSegs] = s;
                 mbar_arrive(bar(L::kSegFull + listed % kSegs));
+                if (p.cut) {                              // the CTAs of the item's first and last tile
+                    const int64_t item = static_cast<int64_t>(b) * HK + g;
+                    if (t0 == 0) p.cut[2 * item] = c;
+                    if (t0 + len == t_item) p.cut[2 * item + 1] = c;
+                }
             }
             __syncwarp();
             ++listed;
@@ -260,9 +261,10 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         };
         int s = 0, t = 0, plain = 0, raw = 0, done_k = 0;           // segment, tile in it; V tiles of either kind so far
         bool ok = true;
-        for (int i = 0; ok && i < kAhead; ++i) ok = list();
         int next[4] = {0, 0, 0, 0};
+        ok = list();
         if (ok) fetch(0, 0, next);
+        for (int i = 1; ok && i < kAhead; ++i) ok = list();
         for (int i = 0; ok && i < n; ++i) {
             const int row[4] = {next[0], next[1], next[2], next[3]};
             const int head = segs[s % kSegs].g, len = segs[s % kSegs].n_tiles, guard = segs[s % kSegs].guard;
@@ -566,20 +568,16 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
 
 // The join of the items that lie in several CTAs: a warp per row of an item.
 template <int D>
-__global__ void __launch_bounds__(kThreads) rows_join_kernel(const __grid_constant__ ChunkParams p, int parts) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int b = blockIdx.z, g = blockIdx.y, row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), HK = p.n_kv_heads;
-    const long long at = __ldcg(p.cum + b), tiles = __ldcg(p.cum + b + 1) - at;
-    if (tiles == 0) return;
-    const ChunkDeal deal{__ldcg(p.cum + p.batch) * HK, parts};
-    const long long first = at * HK + g * tiles;
-    const int c0 = deal.owner(first), c1 = deal.owner(first + tiles - 1);
-    if (c0 == c1) return;
+__global__ void __launch_bounds__(kThreads) rows_join_kernel(const __grid_constant__ ChunkParams p) {
+    const int b = blockIdx.z, g = blockIdx.y, row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), G = 1 << p.group_shift;
     const ChunkEntry e = load_chunk_entry(p, b, false);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (row >= e.q_len << p.group_shift) return;
-    const int64_t unit = (static_cast<int64_t>(c0) + static_cast<int64_t>(b) * HK + g) * p.part_rows + row;
-    const int G = 1 << p.group_shift;
-    join_row<__nv_bfloat16, D>(p, c1 - c0 + 1, [&](int s) { return unit + static_cast<int64_t>(s) * p.part_rows; },
+    const int64_t item = static_cast<int64_t>(b) * p.n_kv_heads + g;
+    const int2 c = __ldcg(reinterpret_cast<const int2 *>(p.cut) + item);
+    if (c.x == c.y) return;
+    const int64_t unit = (c.x + item) * p.part_rows + row;
+    join_row<__nv_bfloat16, D>(p, c.y - c.x + 1, [&](int s) { return unit + static_cast<int64_t>(s) * p.part_rows; },
                                (static_cast<int64_t>(e.qo0 + (row >> p.group_shift)) * p.n_heads + g * G + (row & (G - 1))) * D);
 }
 
@@ -601,7 +599,7 @@ cudaError_t run(const ChunkParams &p, int parts, int group, cudaStream_t s) {
     if (!pool_maps(&maps, p, D, box)) return cudaErrorInvalidValue;
     chunk_rows_kernel<D><<<parts, kThreads, L::kBytes, s>>>(p, maps, box);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !p.cum) return e;
+    if (e != cudaSuccess || !p.cut) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((p.max_q_len * group + kThreads / 32 - 1) / (kThreads / 32), p.n_kv_heads, p.batch);
     cfg.blockDim = dim3(kThreads);
@@ -611,7 +609,7 @@ cudaError_t run(const ChunkParams &p, int parts, int group, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rows_join_kernel<D>, p, parts);
+    return cudaLaunchKernelEx(&cfg, rows_join_kernel<D>, p);
 }
 
 }  // namespace

@@ -350,8 +350,8 @@ struct ChunkParams {
     float *o_part;                // [n_splits, n_q, n_heads, head_dim] (more than one split)
     float *ml_part;               // [n_splits, n_q, n_heads, 2]
     // few rows: o_part [CTAs + items, part_rows, head_dim], ml_part likewise, and the
-    // entries' first tiles [batch + 1] (null: no room, items stay whole)
-    long long *cum;
+    // first and last CTA of each item (null: no room, items stay whole)
+    int32_t *cut;
     int32_t part_rows;            // max_q_len * G
     int64_t size;
     int64_t layer_row0;
