@@ -691,8 +691,8 @@ int pkv_paged_decode_noalloc(const pkv_kvcache *c, int32_t layer_id, const void 
  *                  stages (not expected: the host sizes the grid for it);
  *   -300000 - b    the free list of pkv_build_tables or pkv_fork_requests ran
  *                  out at entry b;
- *   -400000 - b    pkv_release_pages: entry b dropped a reference that its
- *                  page did not have.
+ *   -400000 - p    pkv_release_pages dropped more references to page p than
+ *                  there were.
  * An offending value can itself be negative (a negative slot, say).
  */
 int pkv_last_device_error(void *stream, int64_t *detail);

@@ -288,11 +288,13 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
         if (plan.bytes > room) plan.bytes = 0;            // nothing is cut
         return;
     }
-    // CTAs per SM, rows and keys per tile of the kernel that the call takes.  A
-    // CTA's start and end cost as much as some 400 keys, so the contexts are cut
-    // only where one round of CTAs has room for the pieces, of four tiles at least
-    // (512 rows at 64K positions, bf16: 406 us in one round of 128 CTAs, 399 to 554
-    // in up to three).
+    // CTAs per SM, rows and keys per tile of the kernel that the call takes.  On
+    // tensor cores a CTA's start and end cost as much as some 800 keys, so the
+    // contexts are cut only where one round of CTAs has room for the pieces, of
+    // four tiles at least (512 rows at 64K positions: 406 us in one round of 128
+    // CTAs, 399 to 554 in up to three).  In fp32 a tile takes longer than start
+    // and end do: two rounds (13 entries of up to 1777 positions: 94 us against
+    // 260 in one round, whole).
     const bool wide = dtype == PKV_BF16;
     const int64_t per_sm = wide ? 1 : 2, rows = wide ? 256 : kRows, tok = wide ? 128 : 64;
     const int64_t tiles = (static_cast<int64_t>(max_q_len) * group + rows - 1) / rows;
@@ -300,7 +302,7 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
     const int64_t kv_tiles = (static_cast<int64_t>(max_len) + tok - 1) / tok;
     const size_t per_split = static_cast<size_t>(n_q) * n_kv_heads * group;
     const size_t most = per_split > 0 ? room / (per_split * (head_dim + 2) * sizeof(float)) : 0;
-    int64_t splits = ctas > 0 ? per_sm * sms / ctas : 1;
+    int64_t splits = ctas <= 0 ? 1 : wide ? per_sm * sms / ctas : (2 * per_sm * sms + ctas - 1) / ctas;
     if (splits > kv_tiles / 4) splits = kv_tiles / 4;
     if (splits > 0 && static_cast<size_t>(splits) > most) splits = static_cast<int64_t>(most);
     if (splits > 65535 / (tiles + 1)) splits = 65535 / (tiles + 1);   // grid y, tiles in pairs

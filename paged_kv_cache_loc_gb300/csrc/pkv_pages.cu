@@ -238,21 +238,21 @@ __device__ __forceinline__ ReleaseEntry load_release(const ReleaseParams &p, int
     return {row, ceil_div(keep, p.page_size), ceil_div(len, p.page_size)};
 }
 
-// Column i of entry b's row is given up.  The exchange makes a row that is
+// Column i of an entry's row is given up.  The exchange makes a row that is
 // named twice give each page up once.
-__device__ __forceinline__ void drop_page(const ReleaseParams &p, int b, const ReleaseEntry &e, int i) {
+__device__ __forceinline__ void drop_page(const ReleaseParams &p, const ReleaseEntry &e, int i) {
     const int page = atomicExch(p.req_to_page + static_cast<int64_t>(e.row) * p.max_pages + i, -1);
     if (!in_range(page, p.n_pages)) {
         record_error(p.err, page);
         return;
     }
-    if (atomicSub(p.shares + page, 1) < 0) record_error(p.err, -400000LL - b);
+    atomicSub(p.shares + page, 1);
 }
 
 __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ ReleaseParams p) {
     const int b = blockIdx.y;
     const ReleaseEntry e = load_release(p, b, blockIdx.x == 0 && threadIdx.x == 0);
-    for (int i = e.lo + blockIdx.x * kThreads + threadIdx.x; i < e.hi; i += gridDim.x * kThreads) drop_page(p, b, e, i);
+    for (int i = e.lo + blockIdx.x * kThreads + threadIdx.x; i < e.hi; i += gridDim.x * kThreads) drop_page(p, e, i);
 }
 
 // Exclusive sum of the warps' counts over the cluster, in warp order, and their
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kScanThreads) collect_kernel(const __grid_cons
     if (kDrop) {
         for (int b = (threadIdx.x >> 5) * blocks + rank; b < p.batch; b += blocks * kScanWarps) {
             const ReleaseEntry e = load_release(p, b, lane == 0);
-            for (int i = e.lo + lane; i < e.hi; i += 32) drop_page(p, b, e, i);
+            for (int i = e.lo + lane; i < e.hi; i += 32) drop_page(p, e, i);
         }
         cluster.sync();
     } else {
@@ -317,11 +317,23 @@ __global__ void __launch_bounds__(kScanThreads) collect_kernel(const __grid_cons
     int64_t lo, hi;
     warp_range(rank, blocks, p.n_pages, &lo, &hi);
     const bool vec = (reinterpret_cast<uintptr_t>(p.shares) & 15) == 0;
+    // both passes load kBlocks blocks of 128 pages before they look at the first
+    constexpr int kBlocks = 4;
+    int4 v[kBlocks];
+    auto load = [&](int64_t i0) {
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) v[k] = load4(p.shares, i0 + 128 * k + 4 * lane, hi, 0, vec);
+    };
     int n = 0;
-#pragma unroll 4
-    for (int64_t i = lo + 4 * lane; i < hi; i += 128) {
-        const int4 v = load4(p.shares, i, hi, 0, vec);
-        n += (v.x < 0) + (v.y < 0) + (v.z < 0) + (v.w < 0);
+    for (int64_t i0 = lo; i0 < hi; i0 += 128 * kBlocks) {
+        load(i0);
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+            const int least = min(min(v[k].x, v[k].y), min(v[k].z, v[k].w));
+            n += (v[k].x < 0) + (v[k].y < 0) + (v[k].z < 0) + (v[k].w < 0);
+            if (least < -1)                              // more references dropped than there were
+                record_error(p.err, -400000LL - (i0 + 128 * k + 4 * lane + (v[k].x < -1 ? 0 : v[k].y < -1 ? 1 : v[k].z < -1 ? 2 : 3)));
+        }
     }
     n = __reduce_add_sync(0xffffffffu, n);
     int before, total;
@@ -332,26 +344,30 @@ __global__ void __launch_bounds__(kScanThreads) collect_kernel(const __grid_cons
     }
     if (n == 0) return;
     int at = start - total + before;
-    for (int64_t i0 = lo; i0 < hi; i0 += 128) {
-        const int64_t i = i0 + 4 * lane;
-        const int4 v = load4(p.shares, i, hi, 0, vec);
-        const int c[4] = {v.x, v.y, v.z, v.w};
-        const int k = (v.x < 0) + (v.y < 0) + (v.z < 0) + (v.w < 0);
-        int inc = k;
+    for (int64_t i0 = lo; i0 < hi; i0 += 128 * kBlocks) {
+        load(i0);
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += y;
-        }
-        int place = at + inc - k;
+        for (int k = 0; k < kBlocks; ++k) {
+            const int c[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            const int mine = (c[0] < 0) + (c[1] < 0) + (c[2] < 0) + (c[3] < 0);
+            if (!__any_sync(0xffffffffu, mine)) continue;
+            int inc = mine;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (c[u] < 0) {
-                if (place >= 0) p.free_pages[place] = static_cast<int>(i + u);
-                ++place;
-                p.shares[i + u] = 0;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += y;
             }
-        at += __shfl_sync(0xffffffffu, inc, 31);
+            int place = at + inc - mine;
+            const int64_t i = i0 + 128 * k + 4 * lane;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (c[u] < 0) {
+                    if (place >= 0) p.free_pages[place] = static_cast<int>(i + u);
+                    ++place;
+                    p.shares[i + u] = 0;
+                }
+            at += __shfl_sync(0xffffffffu, inc, 31);
+        }
     }
 }
 
