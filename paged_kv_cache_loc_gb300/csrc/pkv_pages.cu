@@ -255,21 +255,24 @@ __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ 
     for (int i = e.lo + blockIdx.x * kThreads + threadIdx.x; i < e.hi; i += gridDim.x * kThreads) drop_page(p, e, i);
 }
 
-// Exclusive sum of the warps' counts over the cluster, in warp order, and their
-// total.  Ends with every CTA's counts read.
-__device__ __forceinline__ void cluster_prefix(cg::cluster_group &cluster, int *counts, int mine, int *before, int *total) {
+// Exclusive sums of two counts of the warps over the cluster, in warp order, and
+// their totals.  Ends with every CTA's counts read.
+__device__ __forceinline__ void cluster_prefix(cg::cluster_group &cluster, int2 *counts, int2 mine, int2 *before, int2 *total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster.block_rank();
     if (lane == 0) counts[warp] = mine;
     cluster.sync();
-    int pre = 0, all = 0;
+    int2 pre = make_int2(0, 0), all = make_int2(0, 0);
     for (int r = 0; r < static_cast<int>(cluster.num_blocks()); ++r) {
-        const int x = cluster.map_shared_rank(counts, r)[lane];
-        all += __reduce_add_sync(0xffffffffu, x);
-        pre += __reduce_add_sync(0xffffffffu, r < rank || (r == rank && lane < warp) ? x : 0);
+        const int2 x = cluster.map_shared_rank(counts, r)[lane];
+        const bool earlier = r < rank || (r == rank && lane < warp);
+        pre.x += earlier ? x.x : 0;
+        pre.y += earlier ? x.y : 0;
+        all.x += x.x;
+        all.y += x.y;
     }
     cluster.sync();
-    *before = pre;
-    *total = all;
+    *before = make_int2(__reduce_add_sync(0xffffffffu, pre.x), __reduce_add_sync(0xffffffffu, pre.y));
+    *total = make_int2(__reduce_add_sync(0xffffffffu, all.x), __reduce_add_sync(0xffffffffu, all.y));
 }
 
 // Pages [lo, hi) of this warp of the cluster: whole 128-page blocks.
@@ -297,7 +300,8 @@ __device__ __forceinline__ int4 load4(const int32_t *a, int64_t i, int64_t hi, i
 // entry at a time.
 template <bool kDrop>
 __global__ void __launch_bounds__(kScanThreads) collect_kernel(const __grid_constant__ ReleaseParams p) {
-    __shared__ int counts[kScanWarps];
+    __shared__ int2 counts[kScanWarps];
+    __shared__ int lists[kScanWarps][128];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = cluster.block_rank(), blocks = cluster.num_blocks(), lane = threadIdx.x & 31;
     if (kDrop) {
@@ -336,14 +340,16 @@ __global__ void __launch_bounds__(kScanThreads) collect_kernel(const __grid_cons
         }
     }
     n = __reduce_add_sync(0xffffffffu, n);
-    int before, total;
-    cluster_prefix(cluster, counts, n, &before, &total);
+    int2 sums_before, sums;
+    cluster_prefix(cluster, counts, make_int2(n, 0), &sums_before, &sums);
+    const int before = sums_before.x, total = sums.x;
     if (rank == 0 && threadIdx.x == 0) {
         if (total > start) record_error(p.err, total);
         *p.free_end = max(0, start - total);
     }
     if (n == 0) return;
     int at = start - total + before;
+    int *list = lists[threadIdx.x >> 5];                 // a block's pages, so that they are stored side by side
     for (int64_t i0 = lo; i0 < hi; i0 += 128 * kBlocks) {
         load(i0);
 #pragma unroll
@@ -357,16 +363,27 @@ __global__ void __launch_bounds__(kScanThreads) collect_kernel(const __grid_cons
                 const int y = __shfl_up_sync(0xffffffffu, inc, off);
                 if (lane >= off) inc += y;
             }
-            int place = at + inc - mine;
             const int64_t i = i0 + 128 * k + 4 * lane;
+            int to = inc - mine;
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (c[u] < 0) {
-                    if (place >= 0) p.free_pages[place] = static_cast<int>(i + u);
-                    ++place;
-                    p.shares[i + u] = 0;
-                }
-            at += __shfl_sync(0xffffffffu, inc, 31);
+                if (c[u] < 0) list[to++] = static_cast<int>(i + u);
+            if (vec && i + 3 < hi) {
+                if (mine) *reinterpret_cast<int4 *>(p.shares + i) = make_int4(max(c[0], 0), max(c[1], 0), max(c[2], 0), max(c[3], 0));
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (c[u] < 0) p.shares[i + u] = 0;
+            }
+            __syncwarp();
+            const int n_block = __shfl_sync(0xffffffffu, inc, 31);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int s = lane + 32 * u;
+                if (s < n_block && at + s >= 0) p.free_pages[at + s] = list[s];
+            }
+            __syncwarp();
+            at += n_block;
         }
     }
 }
@@ -379,7 +396,7 @@ __global__ void __launch_bounds__(kScanThreads) collect_kernel(const __grid_cons
 // 0 used); moves[0] becomes the number of moves, then the places they go to and,
 // from `cap` on, the pages they come from, each in ascending order.
 __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const __grid_constant__ CompactParams p) {
-    __shared__ int counts[kScanWarps];
+    __shared__ int2 counts[kScanWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = cluster.block_rank(), blocks = cluster.num_blocks(), lane = threadIdx.x & 31;
     const int64_t first = static_cast<int64_t>(rank) * kScanThreads + threadIdx.x, step = static_cast<int64_t>(blocks) * kScanThreads;
@@ -398,56 +415,64 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const __grid
         if (!in_range(page, n) || atomicExch(p.remap + page, -1) == -1) record_error(p.err, page);
         else ++mine;
     }
-    int before, n_free;
-    cluster_prefix(cluster, counts, __reduce_add_sync(0xffffffffu, mine), &before, &n_free);
+    int2 before, sums;
+    cluster_prefix(cluster, counts, make_int2(__reduce_add_sync(0xffffffffu, mine), 0), &before, &sums);
+    const int n_free = sums.x;
     const int64_t used = n - n_free;
     int64_t lo, hi;
     warp_range(rank, blocks, n, &lo, &hi);
     const bool vec = (reinterpret_cast<uintptr_t>(p.remap) & 15) == 0;
-    // a warp's pages that are free among the first `used`, or used behind them
+    // The free pages before each warp's, and those among the first `used`: as many
+    // used pages stand behind.  A hole's rank is the free pages before it, a used
+    // page's behind the first `used` what is left of its place without them.
     auto marks = [&](int64_t i, int (&m)[4]) {
         const int4 v = load4(p.remap, i, hi, 0, vec);
-        const int c[4] = {v.x, v.y, v.z, v.w};
-        int holes = 0, movers = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            m[u] = i + u >= hi ? 0 : i + u < used ? (c[u] ? 1 : 0) : (c[u] ? 0 : 2);
-            holes += m[u] & 1;
-            movers += m[u] >> 1;
-        }
-        return holes + (movers << 16);                    // 128 a step at most
+        m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
     };
-    int holes = 0, movers = 0;
+    int free = 0, holes = 0;
     for (int64_t i = lo + 4 * lane; i < hi; i += 128) {
         int m[4];
-        const int c = marks(i, m);
-        holes += c & 0xffff;
-        movers += c >> 16;
+        marks(i, m);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            free += m[u] != 0;
+            holes += m[u] != 0 && i + u < used;
+        }
     }
-    int hole_at, mover_at, n_moves, n_movers;
-    cluster_prefix(cluster, counts, __reduce_add_sync(0xffffffffu, holes), &hole_at, &n_moves);
-    cluster_prefix(cluster, counts, __reduce_add_sync(0xffffffffu, movers), &mover_at, &n_movers);
+    cluster_prefix(cluster, counts, make_int2(__reduce_add_sync(0xffffffffu, free), __reduce_add_sync(0xffffffffu, holes)), &before, &sums);
+    int at = before.x;
+    const int n_moves = sums.y;
     int32_t *to = p.moves + 4, *from = to + p.cap;
     for (int64_t i0 = lo; i0 < hi; i0 += 128) {
         const int64_t i = i0 + 4 * lane;
         int m[4];
-        const int c = marks(i, m);
+        marks(i, m);
+        const int c = (m[0] != 0) + (m[1] != 0) + (m[2] != 0) + (m[3] != 0);
         int inc = c;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += y;
         }
-        int h = hole_at + ((inc - c) & 0xffff), v = mover_at + ((inc - c) >> 16);
+        int before_me = at + inc - c;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            if (m[u] == 1) to[h++] = static_cast<int>(i + u);
-            if (m[u] == 2) from[v++] = static_cast<int>(i + u);
-            if (i + u < hi) p.remap[i + u] = static_cast<int>(i + u);
+            if (i + u >= hi) break;
+            if (i + u < used) {
+                if (m[u]) to[before_me] = static_cast<int>(i + u);
+            } else if (!m[u]) {
+                from[i + u - used - (before_me - n_moves)] = static_cast<int>(i + u);
+            }
+            before_me += m[u] != 0;
         }
-        const int sum = __shfl_sync(0xffffffffu, inc, 31);
-        hole_at += sum & 0xffff;
-        mover_at += sum >> 16;
+        at += __shfl_sync(0xffffffffu, inc, 31);
+        if (vec && i + 3 < hi) {
+            *reinterpret_cast<int4 *>(p.remap + i) = make_int4(static_cast<int>(i), static_cast<int>(i + 1), static_cast<int>(i + 2), static_cast<int>(i + 3));
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u < hi) p.remap[i + u] = static_cast<int>(i + u);
+        }
     }
     cluster.sync();
     for (int64_t i = first; i < n_moves; i += step) {
