@@ -16,11 +16,21 @@
 // FMAs.  K of the next tile is copied while the softmax and P V run, V while
 // the next scores do.
 #include <atomic>
+#include <type_traits>
 
 #include "pkv_chunk_join.cuh"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace {
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float f2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
 constexpr int kThreads = 256;
 constexpr int kRows = 64;
@@ -106,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
         copy(sV, 0, vbase, 0);
     }
 
-    float o[4][4 * kOut], m[4], l[4];
+    uint64_t o[4][2 * kOut];                            // two columns each
+    float m[4], l[4];
     int lim[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -115,30 +126,38 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
         const int R = row0 + ty * 4 + r;
         lim[r] = R < rows ? chunk_limit(p, e, R >> p.group_shift) : -1;
 #pragma unroll
-        for (int c = 0; c < 4 * kOut; ++c) o[r][c] = 0.f;
+        for (int c = 0; c < 2 * kOut; ++c) o[r][c] = 0ull;
     }
     for (int t = 0; t < n_tiles; ++t) {
         cp_async_wait<1>();                             // K (and q) have landed, V may be in flight
         if (t + 1 < n_tiles) stage_slots(t + 1);
         __syncthreads();
-        float s[4][4] = {};
+        // two partial sums per score, of the even and the odd channels
+        uint64_t s2[4][4] = {};
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
-            float4 a[4], b[4];
+            ulonglong2 a[4], b[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4 *>(sQ + (ty * 4 + r) * D + (d ^ (ty & 1) << 2));
+            for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const ulonglong2 *>(sQ + (ty * 4 + r) * D + (d ^ (ty & 1) << 2));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * c) * D + (d ^ (tx & 7) << 2));
+            for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const ulonglong2 *>(sK + (tx + 16 * c) * D + (d ^ (tx & 7) << 2));
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    s[r][c] = fmaf(a[r].x, b[c].x, s[r][c]);
-                    s[r][c] = fmaf(a[r].y, b[c].y, s[r][c]);
-                    s[r][c] = fmaf(a[r].z, b[c].z, s[r][c]);
-                    s[r][c] = fmaf(a[r].w, b[c].w, s[r][c]);
+                    s2[r][c] = f2_fma(a[r].x, b[c].x, s2[r][c]);
+                    s2[r][c] = f2_fma(a[r].y, b[c].y, s2[r][c]);
                 }
         }
+        float s[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float even, odd;
+                f2_unpack(s2[r][c], even, odd);
+                s[r][c] = even + odd;
+            }
         __syncthreads();                                // K's readers are done
         if (t + 1 < n_tiles) copy(sK, 7, kbase, t + 1);
         else cp_async_commit();
@@ -169,33 +188,39 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
             for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             m[r] = mn;
             l[r] = l[r] * alpha + sum;
+            const uint64_t alpha2 = f2_pack(alpha, alpha);
 #pragma unroll
-            for (int c = 0; c < 4 * kOut; ++c) o[r][c] *= alpha;
+            for (int c = 0; c < 2 * kOut; ++c) o[r][c] = f2_mul(o[r][c], alpha2);
         }
         cp_async_wait<1>();                             // V has landed, the next K may be in flight
         __syncthreads();
+        // (two loops: the choices below cost as much as the products)
+        auto times_v = [&](auto some) {
+            constexpr bool kMasked = decltype(some)::value;
 #pragma unroll 2
-        for (int k = 0; k < kTok; k += 4) {
-            float4 w[4];
+            for (int k = 0; k < kTok; k += 4) {
+                float4 w[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + r) * kTok + (k ^ (ty & 1) << 2));
+                for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + r) * kTok + (k ^ (ty & 1) << 2));
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int c = 0; c < kOut; ++c) {
-                    const float4 v = *reinterpret_cast<const float4 *>(sV + (k + u) * D + tx * 4 + 64 * c);
+                    for (int c = 0; c < kOut; ++c) {
+                        ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sV + (k + u) * D + tx * 4 + 64 * c);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = u == 0 ? w[r].x : u == 1 ? w[r].y : u == 2 ? w[r].z : w[r].w;
-                        // a value that the row does not see has no part in its sum, whatever it is
-                        const bool seen = !masked || j0 + k + u <= lim[r];
-                        o[r][4 * c] = fmaf(x, seen ? v.x : 0.f, o[r][4 * c]);
-                        o[r][4 * c + 1] = fmaf(x, seen ? v.y : 0.f, o[r][4 * c + 1]);
-                        o[r][4 * c + 2] = fmaf(x, seen ? v.z : 0.f, o[r][4 * c + 2]);
-                        o[r][4 * c + 3] = fmaf(x, seen ? v.w : 0.f, o[r][4 * c + 3]);
+                        for (int r = 0; r < 4; ++r) {
+                            const float x = u == 0 ? w[r].x : u == 1 ? w[r].y : u == 2 ? w[r].z : w[r].w;
+                            // a value that the row does not see has no part in its sum, whatever it is
+                            const bool seen = !kMasked || j0 + k + u <= lim[r];
+                            const uint64_t x2 = f2_pack(x, x);
+                            o[r][2 * c] = f2_fma(x2, seen ? v.x : 0ull, o[r][2 * c]);
+                            o[r][2 * c + 1] = f2_fma(x2, seen ? v.y : 0ull, o[r][2 * c + 1]);
+                        }
                     }
-                }
-        }
+            }
+        };
+        if (masked) times_v(std::true_type{});
+        else times_v(std::false_type{});
         __syncthreads();                                // V's and P's readers are done
         if (t + 1 < n_tiles) copy(sV, 0, vbase, t + 1);
         else cp_async_commit();
@@ -213,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
 #pragma unroll
         for (int c = 0; c < kOut; ++c)
             *reinterpret_cast<float4 *>(dst + tx * 4 + 64 * c) =
-                make_float4(o[r][4 * c] * inv, o[r][4 * c + 1] * inv, o[r][4 * c + 2] * inv, o[r][4 * c + 3] * inv);
+                make_float4(f2_lo(o[r][2 * c]) * inv, f2_hi(o[r][2 * c]) * inv, f2_lo(o[r][2 * c + 1]) * inv, f2_hi(o[r][2 * c + 1]) * inv);
         if (p.n_splits > 1 && tx == 0) *reinterpret_cast<float2 *>(p.ml_part + 2 * unit) = make_float2(m[r], l[r]);
     }
 }
