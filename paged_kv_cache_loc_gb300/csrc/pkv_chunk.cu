@@ -11,9 +11,9 @@
 //
 // fp32: products of fp32 rows have no tensor-core form that keeps 24 bits, so
 // this runs on the FMA units.  A CTA of 256 threads takes 64 rows (position,
-// head in group) and 64 keys at a time; a thread holds a 4 x 4 block of scores
-// and a 4 x (D / 16) block of o, so a 16-byte shared-memory load feeds eight
-// FMAs.  K of the next tile is copied while the softmax and P V run, V while
+// head in group; 16 or 32 where an entry has no more) and 64 keys at a time; a
+// thread holds a 4 x 4 block of scores and a 4 x (D / 16) block of o, so a
+// 16-byte shared-memory load feeds eight FMAs (two lanes to an instruction).  K of the next tile is copied while the softmax and P V run, V while
 // the next scores do.
 #include <atomic>
 #include <type_traits>
@@ -33,13 +33,13 @@ __device__ __forceinline__ float f2_lo(uint64_t v) { return __uint_as_float(stat
 __device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
 constexpr int kThreads = 256;
-constexpr int kRows = 64;
 constexpr int kTok = 64;
 
-template <int D>
+template <int D, int R>
 struct Layout {
+    static constexpr int kRows = 16 * R;
     // Floats.  Unpadded; a 16-byte chunk c of a row stands at c ^ x, so that the
-    // rows that a warp reads at once meet different banks: x is r / 4 % 2 in Q
+    // rows that a warp reads at once meet different banks: x is r / R % 2 in Q
     // and P (two row blocks per warp) and r % 8 in K.
     static constexpr int kQ = 0;                      // [kRows][D]
     static constexpr int kK = kQ + kRows * D;         // [kTok][D]
@@ -50,9 +50,10 @@ struct Layout {
     static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_constant__ ChunkParams p) {
-    using L = Layout<D>;
+    using L = Layout<D, R>;
+    constexpr int kRows = L::kRows;
     extern __shared__ __align__(16) float smem[];
     float *sQ = smem + L::kQ, *sK = smem + L::kK, *sV = smem + L::kV, *sP = smem + L::kP;
     int *slots = reinterpret_cast<int *>(smem + L::kFloats);
@@ -103,11 +104,11 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
 
     if (n_tiles > 0) stage_slots(0);
     for (int i = tid; i < kRows * kChunks; i += kThreads) {
-        const int r = i / kChunks, c = i % kChunks, R = row0 + r;
+        const int r = i / kChunks, c = i % kChunks, row = row0 + r;
         const float *q = static_cast<const float *>(p.q);
-        const bool ok = R < rows;
-        const int64_t at = (static_cast<int64_t>(e.qo0 + (R >> p.group_shift)) * p.n_heads + g * G + (R & (G - 1))) * D + c * 4;
-        cp_async16(sQ + r * D + (c ^ (r >> 2 & 1)) * 4, ok ? q + at : q, ok ? 16 : 0);
+        const bool ok = row < rows;
+        const int64_t at = (static_cast<int64_t>(e.qo0 + (row >> p.group_shift)) * p.n_heads + g * G + (row & (G - 1))) * D + c * 4;
+        cp_async16(sQ + r * D + (c ^ (r / R & 1)) * 4, ok ? q + at : q, ok ? 16 : 0);
     }
     cp_async_commit();
     __syncthreads();
@@ -116,15 +117,15 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
         copy(sV, 0, vbase, 0);
     }
 
-    uint64_t o[4][2 * kOut];                            // two columns each
-    float m[4], l[4];
-    int lim[4];
+    uint64_t o[R][2 * kOut];                            // two columns each
+    float m[R], l[R];
+    int lim[R];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
-        const int R = row0 + ty * 4 + r;
-        lim[r] = R < rows ? chunk_limit(p, e, R >> p.group_shift) : -1;
+        const int row = row0 + ty * R + r;
+        lim[r] = row < rows ? chunk_limit(p, e, row >> p.group_shift) : -1;
 #pragma unroll
         for (int c = 0; c < 2 * kOut; ++c) o[r][c] = 0ull;
     }
@@ -133,25 +134,25 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
         if (t + 1 < n_tiles) stage_slots(t + 1);
         __syncthreads();
         // two partial sums per score, of the even and the odd channels
-        uint64_t s2[4][4] = {};
+        uint64_t s2[R][4] = {};
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
-            ulonglong2 a[4], b[4];
+            ulonglong2 a[R], b[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const ulonglong2 *>(sQ + (ty * 4 + r) * D + (d ^ (ty & 1) << 2));
+            for (int r = 0; r < R; ++r) a[r] = *reinterpret_cast<const ulonglong2 *>(sQ + (ty * R + r) * D + (d ^ (ty & 1) << 2));
 #pragma unroll
             for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const ulonglong2 *>(sK + (tx + 16 * c) * D + (d ^ (tx & 7) << 2));
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     s2[r][c] = f2_fma(a[r].x, b[c].x, s2[r][c]);
                     s2[r][c] = f2_fma(a[r].y, b[c].y, s2[r][c]);
                 }
         }
-        float s[4][4];
+        float s[R][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float even, odd;
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
         const int j0 = kv_lo + t * kTok;
         const bool masked = j0 + kTok - 1 > min(seen_by_all, kv_end - 1);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < R; ++r) {
             float mt = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
             for (int c = 0; c < 4; ++c) {
                 s[r][c] = exp2f(s[r][c] - ref);
                 sum += s[r][c];
-                sP[(ty * 4 + r) * kTok + ((tx + 16 * c) ^ (ty & 1) << 2)] = s[r][c];
+                sP[(ty * R + r) * kTok + ((tx + 16 * c) ^ (ty & 1) << 2)] = s[r][c];
             }
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -199,16 +200,16 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
             constexpr bool kMasked = decltype(some)::value;
 #pragma unroll 2
             for (int k = 0; k < kTok; k += 4) {
-                float4 w[4];
+                float4 w[R];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + r) * kTok + (k ^ (ty & 1) << 2));
+                for (int r = 0; r < R; ++r) w[r] = *reinterpret_cast<const float4 *>(sP + (ty * R + r) * kTok + (k ^ (ty & 1) << 2));
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int c = 0; c < kOut; ++c) {
                         ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sV + (k + u) * D + tx * 4 + 64 * c);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
+                        for (int r = 0; r < R; ++r) {
                             const float x = u == 0 ? w[r].x : u == 1 ? w[r].y : u == 2 ? w[r].z : w[r].w;
                             // a value that the row does not see has no part in its sum, whatever it is
                             const bool seen = !kMasked || j0 + k + u <= lim[r];
@@ -227,10 +228,10 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
     }
     cp_async_wait<0>();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int R = row0 + ty * 4 + r;
-        if (R >= rows) continue;
-        const int row = e.qo0 + (R >> p.group_shift), head = g * G + (R & (G - 1));
+    for (int r = 0; r < R; ++r) {
+        const int at = row0 + ty * R + r;
+        if (at >= rows) continue;
+        const int row = e.qo0 + (at >> p.group_shift), head = g * G + (at & (G - 1));
         // a sum of 0 is that of a row that sees nothing here (the largest weight is 1)
         const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
         const int64_t unit = chunk_unit(p, split, row, head);
@@ -258,21 +259,37 @@ __global__ void __launch_bounds__(kThreads) chunk_join_kernel(const __grid_const
     join_row<T, D>(p, n, [&](int s) { return chunk_unit(p, s, e.qo0 + i, head); }, (static_cast<int64_t>(e.qo0 + i) * p.n_heads + head) * D);
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t run_f32(const ChunkParams &p, int group, cudaStream_t s) {
+    using L = Layout<D, R>;
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(attr_done.load() & bit)) {
-        e = cudaFuncSetAttribute(chunk_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+        e = cudaFuncSetAttribute(chunk_f32_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
         if (e != cudaSuccess) return e;
         attr_done.fetch_or(bit);
     }
-    const int tiles = (p.max_q_len * group + kRows - 1) / kRows;
-    chunk_f32_kernel<D><<<dim3(p.n_kv_heads, tiles * p.n_splits, p.batch), kThreads, Layout<D>::kBytes, s>>>(p);
+    const int tiles = (p.max_q_len * group + L::kRows - 1) / L::kRows;
+    chunk_f32_kernel<D, R><<<dim3(p.n_kv_heads, tiles * p.n_splits, p.batch), kThreads, L::kBytes, s>>>(p);
     return cudaGetLastError();
+}
+
+// Rows per CTA: 64, or 16 or 32 where an entry has no more.
+int f32_rows(int max_q_len, int group) {
+    const int64_t rows = static_cast<int64_t>(max_q_len) * group;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+template <int D>
+cudaError_t run_f32_rows(const ChunkParams &p, int group, cudaStream_t s) {
+    switch (f32_rows(p.max_q_len, group)) {
+        case 16: return run_f32<D, 1>(p, group, s);
+        case 32: return run_f32<D, 2>(p, group, s);
+        default: return run_f32<D, 4>(p, group, s);
+    }
 }
 
 template <typename T, int D>
@@ -321,7 +338,7 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
     // and end do: two rounds (13 entries of up to 1777 positions: 94 us against
     // 260 in one round, whole).
     const bool wide = dtype == PKV_BF16;
-    const int64_t per_sm = wide ? 1 : 2, rows = wide ? 256 : kRows, tok = wide ? 128 : 64;
+    const int64_t per_sm = wide ? 1 : 2, rows = wide ? 256 : f32_rows(max_q_len, group), tok = wide ? 128 : 64;
     const int64_t tiles = (static_cast<int64_t>(max_q_len) * group + rows - 1) / rows;
     const int64_t ctas = tiles * n_kv_heads * batch;
     const int64_t kv_tiles = (static_cast<int64_t>(max_len) + tok - 1) / tok;
@@ -345,7 +362,7 @@ cudaError_t launch_chunk(const ChunkParams &p, int parts, int dtype, int head_di
     if (!chunk_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
     const bool f32 = dtype == PKV_F32;
     if (parts > 0) return launch_chunk_rows(p, parts, head_dim, group, s);
-    cudaError_t e = !f32 ? launch_chunk_tc(p, head_dim, group, s) : head_dim == 128 ? run_f32<128>(p, group, s) : run_f32<64>(p, group, s);
+    cudaError_t e = !f32 ? launch_chunk_tc(p, head_dim, group, s) : head_dim == 128 ? run_f32_rows<128>(p, group, s) : run_f32_rows<64>(p, group, s);
     if (e != cudaSuccess || p.n_splits == 1) return e;
     if (f32) return head_dim == 128 ? run_join<float, 128>(p, s) : run_join<float, 64>(p, s);
     return head_dim == 128 ? run_join<__nv_bfloat16, 128>(p, s) : run_join<__nv_bfloat16, 64>(p, s);
