@@ -65,7 +65,7 @@ struct Tc {
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
-chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, const int box) {
+chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, const int box, const bool pair) {
     using bf16 = __nv_bfloat16;
     using L = Tc<D>;
     constexpr int kTok = L::kTok, kChunks = D / 8;
@@ -87,7 +87,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     const int last_tile = (rows + kPair - 1) / kPair - 1 - unit / p.n_splits * 2;
     const int tile = last_tile - 1 + rank;
     if (tile < 0) return;
-    const bool both = last_tile > 0;          // the cluster's other CTA has rows too
+    const bool both = pair && last_tile > 0;          // the cluster's other CTA has rows too
     const int row0 = tile * kPair, first_row = both ? (last_tile - 1) * kPair : row0;
     const int kv_lo = split * p.split_len;
     // keys [kv_lo, end) that the rows up to `row` see in this split
@@ -526,6 +526,11 @@ cudaError_t run(const ChunkParams &p, int group, cudaStream_t s) {
         attr_done.fetch_or(bit);
     }
     const int box = box_rows(p.page_size, L::kTok / 2);    // (two boxes at least, for two CTAs)
+    // Two CTAs to a cluster where contexts are long: 4 x 2048 tokens at 8K to 16K
+    // take 977 us with it and 1034 without, 16 chunks of up to 448 tokens over up
+    // to 1500 states 61 and 49 (a cluster starts, and ends, together); 8 x 512
+    // tokens at 2K 132 and 130, at 4K 225 and 230.
+    const bool pair = p.max_len >= 4096;
     Maps maps;
     if (!pool_maps(&maps, p, D, box)) return cudaErrorInvalidValue;
     const int tiles = (p.max_q_len * group + kPair - 1) / kPair;
@@ -537,10 +542,10 @@ cudaError_t run(const ChunkParams &p, int group, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
-    attr[0].val.clusterDim.y = 2;
+    attr[0].val.clusterDim.y = pair ? 2 : 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D>, p, maps, box);
+    return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D>, p, maps, box, pair);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,

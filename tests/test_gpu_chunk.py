@@ -387,3 +387,110 @@ def test_refusals():
     with pytest.raises(ValueError, match="refuses"):
         pkv.chunk_workspace(x, 16, 6, 8)
     clean()
+
+
+def test_a_run_of_the_page_operators():
+    """A prompt in two chunks, three samples forked from it that each verify a
+    draft, the drafts cut back, one sample ended, the pool compacted: the
+    attention of every sample is what its own tokens say, and moving the pages
+    changes no bit of it."""
+    ps, layers, kv, G, d, n_pages = 16, 2, 2, 4, 128, 64
+    gen = torch.Generator("cuda").manual_seed(1)
+    rng = np.random.default_rng(1)
+
+    def rnd(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    def zeros(n):
+        return torch.zeros(n, dtype=torch.int32, device="cuda")
+
+    pool = [torch.full((layers, n_pages * ps, kv, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    table, tokens = dev(np.full((5, 16), -1)), dev(np.full((5, 256), -1))
+    free, shares, places = dev(rng.permutation(n_pages)), zeros(n_pages), [zeros(1), zeros(1)]
+    history = {0: [[], []]}                                    # row -> its K and V rows, per layer
+
+    def cache(rows, lens, n_new=0, q_lens=None):
+        c = pkv.KVCache(k_buffer=pool[0], v_buffer=pool[1], req_to_token=tokens, req_pool_indices=dev(rows), seq_lens=dev(lens),
+                        out_cache_loc=zeros(n_new) if n_new else None, max_len=max(lens), qo_indptr=zeros(len(rows) + 1))
+        if q_lens is not None:
+            pkv.build_tables(c, table, ps, free, places[0], places[1], q_lens=dev(q_lens))
+            places.reverse()
+        return c
+
+    def add(rows, lens, q_lens):
+        """New tokens of the rows, written and attended to; checked in 64 bits."""
+        n = sum(q_lens)
+        c = cache(rows, lens, n, q_lens)
+        q = rnd(n, kv * G, d)
+        for layer in range(layers):
+            k, v = rnd(n, kv, d), rnd(n, kv, d)
+            pkv.kv_write(c, layer, k, v)
+            at = 0
+            for r, m in zip(rows, q_lens):
+                for x, new in zip(history[r], (k, v)):
+                    x.append((layer, new[at:at + m]))
+                at += m
+            look(c, rows, q, layer, max(q_lens))
+        return c, q
+
+    def look(c, rows, q, layer, max_q):
+        ws = pkv.chunk_workspace(c, q.shape[0], kv * G, max_q)
+        o = pkv.paged_chunk(c, layer, table, ps, q, max_q, workspace=ws)
+        clean()
+        at, indptr = 0, host(c.qo_indptr)
+        for i, r in enumerate(rows):
+            k, v = (torch.cat([x for l, x in history[r][u] if l == layer]) for u in range(2))
+            m = int(indptr[i + 1] - indptr[i])
+            one = dataclasses.replace(c, k_buffer=k[None], v_buffer=v[None], req_pool_indices=dev([0]), seq_lens=dev([len(k)]),
+                                      qo_indptr=dev([0, m]), max_len=len(k))
+            alone = Case(one, dev([np.arange(len(k))]), 1, q[at:at + m], 0, m)
+            ref, tol = want(alone)
+            check(o[at:at + m], ref, tol)
+            at += m
+        return o
+
+    add([0], [70], [70])
+    add([0], [101], [31])
+    start = int(places[0])
+    # three samples of the prompt; the third takes over 96 positions, whole pages alone
+    history.update({r: [list(x) for x in history[0]] for r in (1, 2)})
+    third = [[(l, x[:max(0, 96 - before)]) for (l, x), before in zip(history[0][u], [0, 0, 70, 70])] for u in range(2)]
+    history[3] = third
+    pkv.fork_requests(cache([1, 2, 3], [101, 101, 96]), table, ps, dev([0, 0, 0]), shares, free, places[0], places[1])
+    places.reverse()
+    clean()
+    assert int(places[0]) == start + 2 and host(shares).sum() == 3 * 6
+    c, q = add([0, 1, 2, 3], [109, 104, 117, 97], [8, 3, 16, 1])
+    # of the drafts 2, 1, 5 and 1 tokens stay
+    keep = [103, 102, 106, 97]
+    pkv.release_pages(cache([0, 1, 2, 3], [109, 104, 117, 97]), table, ps, shares, free, places[0], places[1], dev(keep))
+    places.reverse()
+    clean()
+    for r, n in zip(range(4), keep):
+        for u in range(2):
+            per = {l: torch.cat([x for k, x in history[r][u] if k == l])[:n] for l in range(layers)}
+            history[r][u] = list(per.items())
+    c, q = add([0, 1, 2, 3], [n + 2 for n in keep], [2] * 4)
+    before = [look(c, [0, 1, 2, 3], q, layer, 2) for layer in range(layers)]
+    # row 1 ends, and the used pages move to the front
+    pkv.release_pages(cache([1], [104]), table, ps, shares, free, places[0], places[1])
+    places.reverse()
+    used = n_pages - (n_pages - int(places[0]))
+    remap = pkv.compact_pages(cache([0], [1]), table, ps, shares, free, places[0], workspace=pkv.compact_workspace(n_pages))
+    clean()
+    t = host(table)
+    assert (t[1] == -1).all() and t.max() < used == len({p for p in t.flatten() if p >= 0})
+    assert (host(remap) < n_pages).all()
+    three = [0, 2, 3]
+    c3 = cache(three, [keep[r] + 2 for r in three])
+    c3.qo_indptr = dev([0, 2, 4, 6])
+    q3 = torch.cat([q[2 * r:2 * r + 2] for r in three])
+    for layer in range(layers):
+        o = look(c3, three, q3, layer, 2)
+        for i, r in enumerate(three):
+            # the same pieces of each context, so the same sums
+            alone = [cache([r], [keep[r] + 2]) for _ in range(1)][0]
+            alone.qo_indptr = dev([0, 2])
+            a = pkv.paged_chunk(alone, layer, table, ps, q[2 * r:2 * r + 2].contiguous(), 2)
+            assert torch.equal(a, pkv.paged_chunk(alone, layer, table, ps, q[2 * r:2 * r + 2].contiguous(), 2))
+            assert torch.allclose(o[2 * i:2 * i + 2].float(), before[layer][2 * r:2 * r + 2].float(), atol=0.05)
