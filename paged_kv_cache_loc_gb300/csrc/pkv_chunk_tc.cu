@@ -315,15 +315,23 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             // and one of 0 makes q 0.
             const uint32_t q_and = p.scale_log2 == 0.f ? 0u : ~0u, q_xor = p.scale_log2 < 0.f ? 0x80008000u : 0u;
             const bf16 *q = static_cast<const bf16 *>(p.q);
-#pragma unroll 4
-            for (int i = row; i < kRows * kChunks; i += kRows) {
-                const int r = i / kChunks, ch = i % kChunks, Rq = R0 + r;
-                uint4 *dst = reinterpret_cast<uint4 *>(sm + L::kSmemQ + X * L::kQBytes + sw_at<D>(r, ch));
-                const int64_t at = (static_cast<int64_t>(e.qo0 + (Rq >> shift)) * p.n_heads + g * G + (Rq & (G - 1))) * D + ch * 8;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (Rq < rows) w = *reinterpret_cast<const uint4 *>(q + at);
-                w.x = (w.x & q_and) ^ q_xor, w.y = (w.y & q_and) ^ q_xor, w.z = (w.z & q_and) ^ q_xor, w.w = (w.w & q_and) ^ q_xor;
-                *dst = w;
+            // (all of a thread's chunks on their way before the first is stored: one
+            // round trip in front of the first product)
+            uint4 w[kChunks];
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+                const int i = row + k * kRows, r = i / kChunks, ch = i % kChunks, Rq = R0 + r;
+                w[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (Rq < rows)
+                    w[k] = *reinterpret_cast<const uint4 *>(
+                        q + (static_cast<int64_t>(e.qo0 + (Rq >> shift)) * p.n_heads + g * G + (Rq & (G - 1))) * D + ch * 8);
+            }
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+                const int i = row + k * kRows, r = i / kChunks, ch = i % kChunks;
+                w[k].x = (w[k].x & q_and) ^ q_xor, w[k].y = (w[k].y & q_and) ^ q_xor;
+                w[k].z = (w[k].z & q_and) ^ q_xor, w[k].w = (w[k].w & q_and) ^ q_xor;
+                *reinterpret_cast<uint4 *>(sm + L::kSmemQ + X * L::kQBytes + sw_at<D>(r, ch)) = w[k];
             }
             fence_async_smem();
             mbar_arrive(bar(L::kQFull));
