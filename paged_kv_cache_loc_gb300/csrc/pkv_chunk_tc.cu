@@ -105,6 +105,29 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     const int all_see = min(chunk_limit(p, e, first_row >> shift), kv_end - 1);
     const int guard = all_see < kv_lo ? 0 : (all_see + 1 - kv_lo) / kTok;
 
+    auto slot_of = [&](int j) -> int {
+        const int i = j / p.page_size, page = __ldg(p.req_to_page + static_cast<int64_t>(e.req) * p.max_pages + i);
+        const bool ok = static_cast<unsigned long long>(static_cast<long long>(page)) < static_cast<unsigned long long>(p.n_pages);
+        if (!ok) record_error(p.err, page);
+        return (ok ? page : 0) * p.page_size + (j - i * p.page_size);
+    };
+    // ---- copies: a lane takes a box of rows, or four rows (of both CTAs' every
+    // other one).  The first rows are looked up before the barriers are made.
+    const int per = box > 0 ? box : 4;
+    const bool active = lane < kTok / per && (!both || (lane & 1) == rank);
+    int next[4] = {0, 0, 0, 0};
+    auto fetch = [&](int t) {
+        if (!active || t >= n_tiles) return;
+        const int j = kv_lo + t * kTok + lane * per;
+        if (box > 0) {
+            next[0] = j < kv_end ? slot_of(j) : 0;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) next[u] = j + u < kv_end ? slot_of(j + u) : 0;
+        }
+    };
+    if (warp == L::kCopyWarp) fetch(0);
+
     // ---- barriers, tensor memory
     if (tid == 0) {
         for (int i = 0; i < L::kBars; ++i) {
@@ -142,31 +165,11 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     // each barrier's phases are waited for one after the other.
     auto v_landed = [&](int t) -> uint32_t { return bar((t < guard ? L::kVFull : L::kVRaw) + t % kSlots); };
     auto v_phase = [&](int t) -> uint32_t { return t < guard ? phase(t) : phase(t - guard); };
-    auto slot_of = [&](int j) -> int {
-        const int i = j / p.page_size, page = __ldg(p.req_to_page + static_cast<int64_t>(e.req) * p.max_pages + i);
-        const bool ok = static_cast<unsigned long long>(static_cast<long long>(page)) < static_cast<unsigned long long>(p.n_pages);
-        if (!ok) record_error(p.err, page);
-        return (ok ? page : 0) * p.page_size + (j - i * p.page_size);
-    };
 
     if (warp < L::kSoftmaxWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kOtherRegs));
         if (warp == L::kCopyWarp) {
-            // ================= copies: a lane takes a box of rows, or four rows
-            const int per = box > 0 ? box : 4;
-            // (of both CTAs' copies this one makes every other box, or four rows)
-            const bool active = lane < kTok / per && (!both || (lane & 1) == rank);
-            int next[4] = {0, 0, 0, 0};
-            auto fetch = [&](int t) {
-                if (!active || t >= n_tiles) return;
-                const int j = kv_lo + t * kTok + lane * per;
-                if (box > 0) {
-                    next[0] = j < kv_end ? slot_of(j) : 0;
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) next[u] = j + u < kv_end ? slot_of(j + u) : 0;
-                }
-            };
+            // ================= copies
             auto issue = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, const int (&row)[4]) {
                 if (lane == 0) expect_bytes(full, L::kTileBytes);
                 __syncwarp();
@@ -184,7 +187,6 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     }
                 }
             };
-            fetch(0);
             int issued_k = 0, issued_v = 0;
             for (int t = 0; t < n_tiles; ++t) {
                 const int row[4] = {next[0], next[1], next[2], next[3]};
