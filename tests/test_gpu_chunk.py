@@ -337,6 +337,43 @@ def test_streams_and_graphs(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_few_rows_beside_many(dtype):
+    """Single tokens with long contexts in the batch of a prompt's chunk, and a
+    prompt of its own length beside an entry without rows."""
+    c = case([1, 300, 1, 0, 129], [900, 400, 33, 70, 129], dtype=dtype, kv=1)
+    ref, tol = want(c)
+    check(c.run(), ref, tol)
+    check(c.run(workspace=c.workspace()), ref, tol)
+    clean()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_contexts_that_two_ctas_share(dtype):
+    """Contexts of 4096 positions and more, entries of one to five pairs of
+    query tiles, causal and not."""
+    c = case([70, 600, 129, 200], [4200, 4500, 300, 129], dtype=dtype, kv=1, G=2, d=64)
+    for causal in (True, False):
+        ref, tol = want(c, causal)
+        check(c.run(causal), ref, tol)
+    for ps in (1, 8, 128):
+        c = case([300], [4100], dtype=dtype, kv=1, G=2, d=128, ps=ps)
+        ref, tol = want(c)
+        check(c.run(workspace=c.workspace()), ref, tol)
+    clean()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_workspace_that_is_none(dtype):
+    c = case([8], [3000], dtype=dtype)
+    ws = c.workspace()
+    ws.desc.magic = 0
+    with pytest.raises(pkv.PkvError) as e:
+        c.run(workspace=ws)
+    assert e.value.status == _lib.PKV_ERR_WORKSPACE
+    clean()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_pinned_host_memory(dtype):
     c = case([8, 3], [300, 250], dtype=dtype)
     ref, tol = want(c)

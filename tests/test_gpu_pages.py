@@ -513,6 +513,57 @@ def test_compact_refusals():
     clean()
 
 
+@pytest.mark.parametrize("what", ["compact", "release"])
+def test_calls_of_two_kernels_in_a_graph(what):
+    """Replayed on other counts and tables than those of the capture."""
+    rng = np.random.default_rng(4)
+    if what == "compact":
+        p = compact_case(rng, 700, 300)
+        ws, out = pkv.compact_workspace(700), p.free.clone()
+        remap = torch.zeros(700, dtype=torch.int32, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run_compact(p, ws=ws, free_out=out, remap=remap)
+        other = compact_case(np.random.default_rng(5), 700, 300)
+        for mine, theirs in ((p.table, other.table), (p.shares, other.shares), (p.free, other.free),
+                             (p.cache.req_to_token, other.cache.req_to_token)):
+            mine.copy_(theirs)
+        out.copy_(p.free)
+        want = want_compact(p)
+        g.replay()
+        clean()
+        check_compact(p, want, remap, out)
+    else:
+        p = release_case(rng, [300, 5, 77, 1000], 3, width=20000)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run_release(p)
+        other = release_case(np.random.default_rng(6), [300, 5, 77, 1000], 3, width=20000)
+        for mine, theirs in ((p.table, other.table), (p.shares, other.shares), (p.free, other.free), (p.start, other.start),
+                             (p.cache.req_pool_indices, other.cache.req_pool_indices)):
+            mine.copy_(theirs)
+        want = want_release(p)
+        g.replay()
+        clean()
+        check_release(p, want)
+
+
+def test_two_streams():
+    """Two pools at once, each on a stream of its own."""
+    rng = np.random.default_rng(14)
+    a, b = (release_case(rng, rng.integers(1, 400, 100), 2) for _ in range(2))
+    want = [want_release(a), want_release(b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for p, s in zip((a, b), streams):
+        run_release(p, stream=s)
+    torch.cuda.synchronize()
+    clean()
+    for p, w in zip((a, b), want):
+        check_release(p, w)
+
+
 # ---------------------------------------------------------------------------
 # refusals of the binding, and a run of them together
 # ---------------------------------------------------------------------------
