@@ -518,7 +518,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
 // ---------------------------------------------------------------------------
 
 template <int D>
-cudaError_t run(const ChunkParams &p, int group, cudaStream_t s) {
+cudaError_t run(const ChunkParams &p, int group, int sms, cudaStream_t s) {
     using L = Tc<D>;
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
@@ -536,14 +536,17 @@ cudaError_t run(const ChunkParams &p, int group, cudaStream_t s) {
         attr_done.fetch_or(bit);
     }
     const int box = box_rows(p.page_size, L::kTok / 2);    // (two boxes at least, for two CTAs)
-    // Two CTAs to a cluster where contexts are long: 4 x 2048 tokens at 8K to 16K
-    // take 977 us with it and 1034 without, 16 chunks of up to 448 tokens over up
-    // to 1500 states 61 and 49 (a cluster starts, and ends, together); 8 x 512
-    // tokens at 2K 132 and 130, at 4K 225 and 230.
-    const bool pair = p.max_len >= 4096;
     Maps maps;
     if (!pool_maps(&maps, p, D, box)) return cudaErrorInvalidValue;
     const int tiles = (p.max_q_len * group + kPair - 1) / kPair;
+    // Two CTAs to a cluster, which copy a tile once for both, where contexts are
+    // long and an odd tile's empty partner costs no further round of CTAs: 4 x 2048
+    // tokens at 8K to 16K take 953 us with it and 1034 without, 4 x 704 at 8K 301 and
+    // 317; 16 chunks of up to 448 tokens over up to 1500 states 61 and 49 (a cluster
+    // starts, and ends, together); three tiles, 2 x 192 tokens at 8K, 97 and 61, one
+    // tile, 8 x 64 tokens at 16K, 251 and 144.
+    const int64_t each = static_cast<int64_t>(p.n_kv_heads) * p.n_splits * p.batch, padded = (tiles + 1) / 2 * 2;
+    const bool pair = p.max_len >= 4096 && tiles > 1 && (each * padded + sms - 1) / sms == (each * tiles + sms - 1) / sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.n_kv_heads, (tiles + 1) / 2 * 2 * p.n_splits, p.batch);
     cfg.blockDim = dim3(L::kThreads);
@@ -601,8 +604,8 @@ bool pool_maps(Maps *maps, const ChunkParams &p, int D, int box) {
 
 bool chunk_wide(int max_q_len, int group) { return static_cast<int64_t>(max_q_len) * group > kRows; }
 
-cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, cudaStream_t s) {
-    return head_dim == 128 ? run<128>(p, group, s) : run<64>(p, group, s);
+cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, int sms, cudaStream_t s) {
+    return head_dim == 128 ? run<128>(p, group, sms, s) : run<64>(p, group, sms, s);
 }
 
 }  // namespace pkv

@@ -363,6 +363,20 @@ def test_contexts_that_two_ctas_share(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_long_contexts_that_no_ctas_share(dtype):
+    """One query tile, and an odd number of them in so many entries that empty
+    partners would not fit beside the others."""
+    c = case([100], [4500], dtype=dtype, kv=1, G=2, d=64)
+    ref, tol = want(c)
+    check(c.run(), ref, tol)
+    check(c.run(workspace=c.workspace()), ref, tol)
+    c = case([300] + [257] * 39, [4100] + [300] * 39, dtype=dtype, kv=1, G=2, d=64)
+    ref, tol = want(c)
+    check(c.run(), ref, tol)
+    clean()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_workspace_that_is_none(dtype):
     c = case([8], [3000], dtype=dtype)
     ws = c.workspace()
