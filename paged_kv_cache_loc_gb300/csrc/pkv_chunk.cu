@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
     constexpr int kChunks = D / 4, kOut = D / 64;       // 16-byte chunks per row; float4 columns of o per thread
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int g = blockIdx.x, split = blockIdx.y % p.n_splits, G = 1 << p.group_shift;
-    const ChunkEntry e = load_chunk_entry(p, blockIdx.z, g == 0 && blockIdx.y == 0 && tid == 0);
+    const ChunkEntry e = entry_of_lane(load_chunk_entry(p, blockIdx.z, g == 0 && blockIdx.y == 0 && tid == 0), 0);
     const int rows = e.q_len << p.group_shift;
     // the entry's last rows, which see most, first
     const int tile = (rows + kRows - 1) / kRows - 1 - static_cast<int>(blockIdx.y / p.n_splits);

@@ -35,6 +35,32 @@ __device__ __forceinline__ ChunkEntry load_chunk_entry(const ChunkParams &p, int
     return e;
 }
 
+// The entry that lane `from` holds, by a whole warp: values that are then known to be
+// one for all lanes, so that branches on them take no care of lanes that part (4 x 2048
+// tokens at 8K to 16K: 896 us, 953 without; in fp32 4 x 512 at 2K 1060 and 1084).
+__device__ __forceinline__ ChunkEntry entry_of_lane(ChunkEntry e, int from) {
+    e.req = __shfl_sync(0xffffffffu, e.req, from), e.qo0 = __shfl_sync(0xffffffffu, e.qo0, from);
+    e.q_len = __shfl_sync(0xffffffffu, e.q_len, from), e.kv_len = __shfl_sync(0xffffffffu, e.kv_len, from);
+    e.first = __shfl_sync(0xffffffffu, e.first, from);
+    return e;
+}
+
+// The entry that the CTAs of grid z take, by a whole warp: among 32 neighbouring ones
+// that of the z-th longest context, so that the short ones fill the gaps at the end.
+// report: the warp of grid z looks at all 32 (one does for each 32).
+__device__ __forceinline__ ChunkEntry load_longest_entry(const ChunkParams &p, int z, bool report) {
+    const int lane = threadIdx.x & 31, b = (z & ~31) + lane, at = z & 31;
+    ChunkEntry e = load_chunk_entry(p, min(b, p.batch - 1), report && at == 0 && b < p.batch);
+    const int len = b >= p.batch ? -2 : e.q_len == 0 ? -1 : e.kv_len;
+    int longer = 0;                                    // entries before this one
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const int other = __shfl_sync(0xffffffffu, len, j);
+        longer += other > len || (other == len && j < lane);
+    }
+    return entry_of_lane(e, __ffs(__ballot_sync(0xffffffffu, longer == at)) - 1);
+}
+
 // last position that the row at place i of its entry sees
 __device__ __forceinline__ int chunk_limit(const ChunkParams &p, const ChunkEntry &e, int i) {
     return p.causal ? e.first + i : e.first;

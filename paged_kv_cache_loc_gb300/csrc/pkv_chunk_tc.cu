@@ -35,12 +35,13 @@ namespace {
 
 constexpr int kRows = 128;                  // query rows per tile (tensor-memory lanes)
 constexpr int kPair = 2 * kRows;            // query rows per CTA
-constexpr int kSlots = 2;                   // K tiles and V tiles in shared memory
 constexpr int kGuarded = 6;                 // V tiles that are looked at, at most
 
 template <int D>
 struct Tc {
     static constexpr int kTok = 128, kThreads = 384;
+    static constexpr int kSlots = D == 64 ? 4 : 2;      // K tiles and V tiles in shared memory
+    static constexpr bool kOwnP = D == 64;              // P has columns of its own
     static constexpr int kMmaWarp = 0, kCopyWarp = 1, kGuardWarp = 2, kSoftmaxWarp = 4;
     static constexpr int kQBytes = kRows * D * 2, kTileBytes = kTok * D * 2;
     static constexpr int kSmemQ = 0, kSmemK = 2 * kQBytes, kSmemV = kSmemK + kSlots * kTileBytes;
@@ -48,7 +49,8 @@ struct Tc {
     // barriers
     static constexpr int kKFull = 0, kKEmpty = kSlots, kVFull = 2 * kSlots, kVEmpty = 3 * kSlots;
     static constexpr int kVRaw = 4 * kSlots, kVClean = 5 * kSlots;      // in VFull's place for tiles that are looked at
-    static constexpr int kSFull = 6 * kSlots, kPFull = kSFull + 2, kODone = kPFull + 2, kQFull = kODone + 2, kBars = kQFull + 1;
+    static constexpr int kSFull = 6 * kSlots, kPFull = kSFull + 2, kODone = kPFull + 2, kSRead = kODone + 2;
+    static constexpr int kQFull = kSRead + 2, kBars = kQFull + 1;
     static constexpr int kSmemTmem = kSmemBar + kBars * 8, kSmemAbort = kSmemTmem + 4, kSmemBad = kSmemAbort + 4;
     static constexpr int kBadWords = kGuarded * kTok / 32 + 1;      // bits of rows, then: any
     static constexpr int kBytes = kSmemBad + kBadWords * 4 + 1024;  // + alignment slack
@@ -60,6 +62,7 @@ struct Tc {
     static constexpr uint32_t kCols = 512;
     __device__ static constexpr uint32_t s_col(int X) { return X * 256; }
     __device__ static constexpr uint32_t o_col(int X) { return X * 256 + 128; }
+    __device__ static constexpr uint32_t p_col(int X) { return kOwnP ? X * 256 + 192 : s_col(X); }
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -68,7 +71,7 @@ __global__ void __launch_bounds__(384, 1)
 chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, const int box, const bool pair) {
     using bf16 = __nv_bfloat16;
     using L = Tc<D>;
-    constexpr int kTok = L::kTok, kChunks = D / 8;
+    constexpr int kTok = L::kTok, kChunks = D / 8, kSlots = L::kSlots;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t s_base = smem_u32(sm);
@@ -81,7 +84,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     // the same keys; each copies half of every K/V tile to both.
     const int g = blockIdx.x, shift = p.group_shift, G = 1 << shift;
     const int rank = blockIdx.y & 1, unit = blockIdx.y >> 1, split = unit % p.n_splits;
-    const ChunkEntry e = load_chunk_entry(p, blockIdx.z, g == 0 && blockIdx.y == 0 && tid == 0);
+    const ChunkEntry e = load_longest_entry(p, blockIdx.z, g == 0 && blockIdx.y == 0 && warp == 0);
     const int rows = e.q_len << shift;
     // the entry's last rows, which see most, first
     const int last_tile = (rows + kPair - 1) / kPair - 1 - unit / p.n_splits * 2;
@@ -134,8 +137,8 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             uint32_t count = 1;
             if (i >= L::kVClean && i < L::kSFull) count = 2;
             else if (both && ((i >= L::kKEmpty && i < L::kVFull) || (i >= L::kVEmpty && i < L::kVRaw))) count = 2;   // both CTAs' products
-            else if (i >= L::kPFull && i < L::kODone) {        // the tile's warps that hold rows
-                const int left = rows - row0 - (i - L::kPFull) * kRows;
+            else if ((i >= L::kPFull && i < L::kODone) || (i >= L::kSRead && i < L::kQFull)) {    // the tile's warps that hold rows
+                const int left = rows - row0 - ((i - L::kPFull) & 1) * kRows;
                 count = max(1, (min(left, kRows) + 31) / 32);
             } else if (i == L::kQFull) count = 256;
             mbar_init(bar(i), count);
@@ -229,7 +232,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     const uint32_t va = v_lo + slot * (L::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kTok / 16; ++ks)
-                        mma_f16_ta(tmem + L::o_col(X), tmem + L::s_col(X) + ks * 8, desc_at(va + ks * (2 * D * 16 >> 4), v_hi), id_o,
+                        mma_f16_ta(tmem + L::o_col(X), tmem + L::p_col(X) + ks * 8, desc_at(va + ks * (2 * D * 16 >> 4), v_hi), id_o,
                                    (acc || ks > 0) ? 1u : 0u);
                 };
                 auto commit = [&](int i) {
@@ -248,9 +251,37 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     if (n_x[0] > 0) issue_s(0, 0);
                     if (n_x[1] > 0) issue_s(1, 0);
                     release(L::kKEmpty);
-                    ok = wait_v(0) && (n_tiles == 1 || wait_k(1));
+                    ok = L::kOwnP || (wait_v(0) && (n_tiles == 1 || wait_k(1)));
                 }
-                for (int j = 0; ok && j < n_tiles; ++j) {
+                // P in columns of its own: S of the next tiles runs as soon as the last is
+                // read, while the softmax works on it
+                for (int j = 0; L::kOwnP && ok && j < n_tiles; ++j) {
+                    const int slot = j % kSlots, slot1 = (j + 1) % kSlots;
+                    if (j + 1 < n_tiles) {
+                        if (!wait_k(j + 1)) { ok = false; break; }
+#pragma unroll
+                        for (int X = 0; X < 2; ++X)
+                            if (ok && j + 1 < n_x[X]) {
+                                ok = wait_fast(bar(L::kSRead + X), j & 1);
+                                fence_after();
+                                if (ok) issue_s(X, slot1);
+                            }
+                        if (!ok) break;
+                        release(L::kKEmpty + slot1);
+                    }
+                    if (!wait_v(j)) { ok = false; break; }
+#pragma unroll
+                    for (int X = 0; X < 2; ++X)
+                        if (ok && j < n_x[X]) {
+                            ok = wait_fast(bar(L::kPFull + X), j & 1);
+                            fence_after();
+                            if (!ok) continue;
+                            issue_pv(X, slot, j > 0);
+                            commit(L::kODone + X);
+                        }
+                    release(L::kVEmpty + slot);
+                }
+                for (int j = 0; !L::kOwnP && ok && j < n_tiles; ++j) {
                     const int slot = j % kSlots, slot1 = (j + 1) % kSlots;
                     const bool more = j + 1 < n_tiles;
                     if (j < n_x[0]) {
@@ -354,6 +385,11 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             float sv[kTok / 64][64];
 #pragma unroll
             for (int h = 0; h < kTok / 64; ++h) tmem_ld64(t_s + h * 64, sv[h]);
+            if (L::kOwnP) {                            // the next S may come
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kSRead + X));
+            }
             auto s = [&](int i) -> float & { return sv[i >> 6][i & 63]; };
             const int j0 = kv_lo + j * kTok;
             if (j0 + kTok - 1 > lim) {
@@ -370,7 +406,12 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             const bool raise = mt > m + kRescale || (m == -INFINITY && mt != -INFINITY);
             const bool touch = raise && j > 0 && m != -INFINITY;
             const float alpha = raise ? exp2f(m - mt) : 1.f;
-            if (__any_sync(0xffffffffu, touch)) {      // (P V of the tile before came before this S)
+            if (L::kOwnP && j > 0) {                   // P V of the tile before: O and P's place
+                ok = *s_abort == 0 && bar_wait(bar(L::kODone + X), (j - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) { give_up(-5010); live = false; break; }
+                fence_after();
+            }
+            if (__any_sync(0xffffffffu, touch)) {      // (else P V of the tile before came before this S)
                 const float f = touch ? alpha : 1.f;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -400,7 +441,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
                     pk[i >> 1] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                tmem_st8u(t_s + c / 2, pk);
+                tmem_st8u(tmem + L::p_col(X) + lane_off + c / 2, pk);
             }
             float a0, a1, a2, a3;
             f2_unpack(sum[0], a0, a1);
@@ -413,7 +454,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         }
         // ---- epilogue: O is final once its last product is done
         if (busy && live) {     // (nothing to see: the query tile, whose place the rows go through)
-            const bool ok = *s_abort == 0 && bar_wait(bar(mine > 0 ? L::kODone + X : L::kQFull), 0);
+            const bool ok = *s_abort == 0 && bar_wait(bar(mine > 0 ? L::kODone + X : L::kQFull), L::kOwnP && mine > 0 ? (mine - 1) & 1 : 0);
             if (!__all_sync(0xffffffffu, ok)) give_up(-5011), live = false;
         }
         fence_after();
