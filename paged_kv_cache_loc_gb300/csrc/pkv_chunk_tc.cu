@@ -7,7 +7,7 @@
 // of fewer.  A CTA takes one kv head of one entry, two tiles of 128 rows, and the
 // keys of one split, 128 at a time:
 //   S = Q K^T  (tcgen05.mma, fp32 in tensor memory), P = 2^(S - m) as bf16 over
-//   S's columns, O += P V (P read from tensor memory).
+//   S's columns (head_dim 64: beside them), O += P V (P read from tensor memory).
 // The two tiles share every K/V tile, and the tensor core works on one while the
 // softmax runs on the other.  Two CTAs of a cluster, neighbouring rows of the same
 // entry and head, share the K/V tiles too: each copies every other box to both,
@@ -207,6 +207,11 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             // no copy is in flight when the CTA ends, also after a wait that gave up
             for (int t = max(0, issued_k - kSlots); t < issued_k; ++t) bar_wait(bar(L::kKFull + t % kSlots), phase(t));
             for (int t = max(0, issued_v - kSlots); t < issued_v; ++t) bar_wait(v_landed(t), v_phase(t));
+            // and no release, which come from both CTAs
+            for (int t = max(0, n_tiles - kSlots); t < n_tiles && issued_v == n_tiles && *s_abort == 0; ++t) {
+                bar_wait(bar(L::kKEmpty + t % kSlots), phase(t));
+                bar_wait(bar(L::kVEmpty + t % kSlots), phase(t));
+            }
         } else if (warp == L::kMmaWarp) {
             // ================= products: one thread issues them all.  It blocks
             // while the tensor core is busy, so what it does in between is
@@ -253,8 +258,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     release(L::kKEmpty);
                     ok = L::kOwnP || (wait_v(0) && (n_tiles == 1 || wait_k(1)));
                 }
-                // P in columns of its own: S of the next tiles runs as soon as the last is
-                // read, while the softmax works on it
+                // P in columns of its own (head_dim 64 leaves 64): S of the next tiles runs
+                // as soon as the last is read, while the softmax works on it (4 x 2048
+                // tokens at 8K to 16K 724 us, 761 with P over S)
                 for (int j = 0; L::kOwnP && ok && j < n_tiles; ++j) {
                     const int slot = j % kSlots, slot1 = (j + 1) % kSlots;
                     if (j + 1 < n_tiles) {
@@ -377,6 +383,19 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         const float sc = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
         float m = -INFINITY, l = 0.f;
         bool live = busy;
+        // A look at a barrier ahead of its wait, whose answer takes some 200 cycles while
+        // the tensor core reads shared memory (head_dim 64, 4 x 2048 tokens at 8K to
+        // 16K: 695 us, 724 without).
+        auto look = [&](int i, int parity) -> bool {
+            uint32_t ok;
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                " selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(ok)
+                : "r"(bar(i)), "r"(parity)
+                : "memory");
+            return ok != 0;
+        };
         for (int j = 0; live && j < mine; ++j) {
             bool ok = *s_abort == 0 && bar_wait(bar(L::kSFull + X), j & 1);
             if (!__all_sync(0xffffffffu, ok)) { give_up(-5009); live = false; break; }
@@ -397,6 +416,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                 for (int i = 0; i < kTok; ++i)
                     if (j0 + i > lim) s(i) = -INFINITY;
             }
+            const bool pv_done = L::kOwnP && j > 0 && look(L::kODone + X, (j - 1) & 1);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < kTok; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s(i), s(i + 1));
@@ -407,8 +427,10 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             const bool touch = raise && j > 0 && m != -INFINITY;
             const float alpha = raise ? exp2f(m - mt) : 1.f;
             if (L::kOwnP && j > 0) {                   // P V of the tile before: O and P's place
-                ok = *s_abort == 0 && bar_wait(bar(L::kODone + X), (j - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) { give_up(-5010); live = false; break; }
+                if (!__all_sync(0xffffffffu, pv_done)) {
+                    ok = *s_abort == 0 && bar_wait(bar(L::kODone + X), (j - 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) { give_up(-5010); live = false; break; }
+                }
                 fence_after();
             }
             if (__any_sync(0xffffffffu, touch)) {      // (else P V of the tile before came before this S)
