@@ -47,6 +47,8 @@ __device__ __forceinline__ ChunkEntry entry_of_lane(ChunkEntry e, int from) {
 
 // The entry that the CTAs of grid z take, by a whole warp: among 32 neighbouring ones
 // that of the z-th longest context, so that the short ones fill the gaps at the end.
+// (16 chunks of up to 448 tokens over up to 1500 states 41.7 us, in their own order
+// 48.3; 16 prompts of up to 2048 tokens at up to 6K 724 and 739.)
 // report: the warp of grid z looks at all 32 (one does for each 32).
 __device__ __forceinline__ ChunkEntry load_longest_entry(const ChunkParams &p, int z, bool report) {
     const int lane = threadIdx.x & 31, b = (z & ~31) + lane, at = z & 31;

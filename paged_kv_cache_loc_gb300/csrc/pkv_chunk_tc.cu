@@ -604,12 +604,13 @@ cudaError_t run(const ChunkParams &p, int group, int sms, cudaStream_t s) {
     const int tiles = (p.max_q_len * group + kPair - 1) / kPair;
     // Two CTAs to a cluster, which copy a tile once for both, where contexts are
     // long and an odd tile's empty partner costs no further round of CTAs: 4 x 2048
-    // tokens at 8K to 16K take 953 us with it and 1034 without, 4 x 704 at 8K 301 and
-    // 317; 16 chunks of up to 448 tokens over up to 1500 states 61 and 49 (a cluster
-    // starts, and ends, together); three tiles, 2 x 192 tokens at 8K, 97 and 61, one
-    // tile, 8 x 64 tokens at 16K, 251 and 144.
+    // tokens at 8K to 16K take 905 us with it and 929 without, 4 x 704 at 8K 282 and
+    // 293, 8 x 512 at 4K 209 and 211, at 2K 124 and 118 (a cluster starts, and ends,
+    // together); head_dim 64, 8 x 512 at 2K 91 and 96, 16 chunks of up to 448 tokens
+    // over up to 1500 states 51 and 38; three tiles, 2 x 192 tokens at 8K, 91 and
+    // 58, one tile, 8 x 64 tokens at 16K, 239 and 138.
     const int64_t each = static_cast<int64_t>(p.n_kv_heads) * p.n_splits * p.batch, padded = (tiles + 1) / 2 * 2;
-    const bool pair = p.max_len >= 4096 && tiles > 1 && (each * padded + sms - 1) / sms == (each * tiles + sms - 1) / sms;
+    const bool pair = p.max_len >= (D == 64 ? 2048 : 4096) && tiles > 1 && (each * padded + sms - 1) / sms == (each * tiles + sms - 1) / sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.n_kv_heads, (tiles + 1) / 2 * 2 * p.n_splits, p.batch);
     cfg.blockDim = dim3(L::kThreads);

@@ -265,6 +265,28 @@ def test_many_entries(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_entries_of_many_rows(dtype, causal):
+    """More entries than a warp has lanes, some without rows, in an order of
+    lengths with equal ones, and one of the later ones with an error."""
+    rng = np.random.default_rng(4)
+    q_lens = rng.integers(0, 160, 70) * (rng.integers(0, 5, 70) > 0)
+    q_lens[50] = 159
+    c = case(q_lens, rng.integers(0, 6, 70) * 61, dtype=dtype, d=64, kv=1, G=2)
+    o = torch.full_like(c.q, 2.5)
+    ref, tol = want(c, causal, o=o)
+    check(c.run(causal, o=o), ref, tol)
+    clean()
+    c.cache.seq_lens[50] = -7
+    o.fill_(2.5)
+    c.run(causal, o=o)
+    assert error() == -7
+    got, lo = host(o), int(q_lens[:50].sum())
+    assert (got[lo:lo + 159] == 2.5).all()
+    assert (np.abs(got - ref) <= tol)[:lo].all() and (np.abs(got - ref) <= tol)[lo + 159:].all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("what,value", [("row", 99), ("row", -1), ("len", -1), ("len", 10**6), ("rows", 10**6), ("rows", -5), ("back", 0)])
 def test_bad_entry_is_left_out(dtype, what, value):
     c = case([10, 20, 30], [50, 60, 70], dtype=dtype)
