@@ -208,10 +208,10 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             for (int t = max(0, issued_k - kSlots); t < issued_k; ++t) bar_wait(bar(L::kKFull + t % kSlots), phase(t));
             for (int t = max(0, issued_v - kSlots); t < issued_v; ++t) bar_wait(v_landed(t), v_phase(t));
             // and no release, which come from both CTAs
-            for (int t = max(0, n_tiles - kSlots); t < n_tiles && issued_v == n_tiles && *s_abort == 0; ++t) {
-                bar_wait(bar(L::kKEmpty + t % kSlots), phase(t));
-                bar_wait(bar(L::kVEmpty + t % kSlots), phase(t));
-            }
+            bool reached = issued_v == n_tiles;
+            for (int t = max(0, n_tiles - kSlots); reached && t < n_tiles; ++t)
+                reached = *s_abort == 0 && bar_wait(bar(L::kKEmpty + t % kSlots), phase(t)) && bar_wait(bar(L::kVEmpty + t % kSlots), phase(t));
+            __syncwarp();
         } else if (warp == L::kMmaWarp) {
             // ================= products: one thread issues them all.  It blocks
             // while the tensor core is busy, so what it does in between is
