@@ -336,8 +336,11 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
     // contexts are cut only where one round of CTAs has room for the pieces, of
     // four tiles at least (512 rows at 64K positions: 406 us in one round of 128
     // CTAs, 399 to 554 in up to three).  In fp32 a tile takes longer than start
-    // and end do: two rounds (13 entries of up to 1777 positions: 94 us against
-    // 260 in one round, whole).
+    // and end do: CTAs for twelve rounds, of two tiles at least, which even out
+    // entries of different lengths, unless they fill three rounds whole (16 x 1 to
+    // 8 tokens at 0.5K to 4K 199 us against 273 for two rounds, 6 x 10 to 200 at up
+    // to 2.5K 519 and 650, 13 entries of up to 1777 positions 70.5 and 69.5; 4 x
+    // 512 at 2K, three rounds and a half, 1165 in pieces and 1059 whole).
     const bool wide = dtype == PKV_BF16;
     const int64_t per_sm = wide ? 1 : 2, rows = wide ? 256 : f32_rows(max_q_len, group), tok = wide ? 128 : 64;
     const int64_t tiles = (static_cast<int64_t>(max_q_len) * group + rows - 1) / rows;
@@ -345,8 +348,9 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
     const int64_t kv_tiles = (static_cast<int64_t>(max_len) + tok - 1) / tok;
     const size_t per_split = static_cast<size_t>(n_q) * n_kv_heads * group;
     const size_t most = per_split > 0 ? room / (per_split * (head_dim + 2) * sizeof(float)) : 0;
-    int64_t splits = ctas <= 0 ? 1 : wide ? per_sm * sms / ctas : (2 * per_sm * sms + ctas - 1) / ctas;
-    if (splits > kv_tiles / 4) splits = kv_tiles / 4;
+    const int64_t round = per_sm * sms;
+    int64_t splits = ctas <= 0 ? 1 : wide ? round / ctas : ctas > 3 * round ? 1 : 12 * round / ctas;
+    if (splits > kv_tiles / (wide ? 4 : 2)) splits = kv_tiles / (wide ? 4 : 2);
     if (splits > 0 && static_cast<size_t>(splits) > most) splits = static_cast<int64_t>(most);
     if (splits > 65535 / (tiles + 1)) splits = 65535 / (tiles + 1);   // grid y, tiles in pairs
     if (splits <= 1) return;
