@@ -1165,7 +1165,7 @@ int pkv_paged_chunk(const pkv_kvcache *c, int32_t layer_id, const int32_t *req_t
     p.split_len = plan.split_len;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.err = di.err;
-    return map_launch(pkv::launch_chunk(p, plan.parts, c->dtype, c->head_dim, group, di.sms, static_cast<cudaStream_t>(stream)));
+    return map_launch(pkv::launch_chunk(p, plan.parts, c->dtype, c->head_dim, group, static_cast<cudaStream_t>(stream)));
 }
 
 int pkv_last_device_error(void *stream, int64_t *detail) {

@@ -352,7 +352,7 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
     int64_t splits = ctas <= 0 ? 1 : wide ? round / ctas : ctas > 3 * round ? 1 : 12 * round / ctas;
     if (splits > kv_tiles / (wide ? 4 : 2)) splits = kv_tiles / (wide ? 4 : 2);
     if (splits > 0 && static_cast<size_t>(splits) > most) splits = static_cast<int64_t>(most);
-    if (splits > 65535 / (tiles + 1)) splits = 65535 / (tiles + 1);   // grid y, tiles in pairs
+    if (splits > 65535 / tiles) splits = 65535 / tiles;   // grid y
     if (splits <= 1) return;
     const int64_t per = (kv_tiles + splits - 1) / splits;
     plan.split_len = static_cast<int32_t>(per * tok);
@@ -363,11 +363,11 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
     plan.bytes = plan.o_bytes + plan.ml_bytes;
 }
 
-cudaError_t launch_chunk(const ChunkParams &p, int parts, int dtype, int head_dim, int group, int sms, cudaStream_t s) {
+cudaError_t launch_chunk(const ChunkParams &p, int parts, int dtype, int head_dim, int group, cudaStream_t s) {
     if (!chunk_supported(dtype, head_dim, group)) return cudaErrorNotSupported;
     const bool f32 = dtype == PKV_F32;
     if (parts > 0) return launch_chunk_rows(p, parts, head_dim, group, s);
-    cudaError_t e = !f32 ? launch_chunk_tc(p, head_dim, group, sms, s) : head_dim == 128 ? run_f32_rows<128>(p, group, s) : run_f32_rows<64>(p, group, s);
+    cudaError_t e = !f32 ? launch_chunk_tc(p, head_dim, group, s) : head_dim == 128 ? run_f32_rows<128>(p, group, s) : run_f32_rows<64>(p, group, s);
     if (e != cudaSuccess || p.n_splits == 1) return e;
     if (f32) return head_dim == 128 ? run_join<float, 128>(p, s) : run_join<float, 64>(p, s);
     return head_dim == 128 ? run_join<__nv_bfloat16, 128>(p, s) : run_join<__nv_bfloat16, 64>(p, s);

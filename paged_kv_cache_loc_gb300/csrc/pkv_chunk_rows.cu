@@ -252,11 +252,11 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             __syncwarp();
             if (!active) return;
             if (box > 0) {
-                copy_box<false>(dst + lane * per * (D * 2), map, head * (D / 64), row[0] >> 3, bar_full);
+                copy_box(dst + lane * per * (D * 2), map, head * (D / 64), row[0] >> 3, bar_full);
             } else {
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
-                    copy_rows4<false>(dst + (lane >> 1) * (D * 16) + h * 1024 + (lane & 1) * 512, map, head * D + h * 64, row, bar_full);
+                    copy_rows4(dst + (lane >> 1) * (D * 16) + h * 1024 + (lane & 1) * 512, map, head * D + h * 64, row, bar_full);
             }
         };
         int s = 0, t = 0, plain = 0, raw = 0, done_k = 0;           // segment, tile in it; V tiles of either kind so far

@@ -9,10 +9,8 @@
 //   S = Q K^T  (tcgen05.mma, fp32 in tensor memory), P = 2^(S - m) as bf16 over
 //   S's columns (head_dim 64: beside them), O += P V (P read from tensor memory).
 // The two tiles share every K/V tile, and the tensor core works on one while the
-// softmax runs on the other.  Two CTAs of a cluster, neighbouring rows of the same
-// entry and head, share the K/V tiles too: each copies every other box to both,
-// which halves what every SM fetches (the SMs together fetch 7 to 8 TB/s at most,
-// from L2 or not; one CTA alone wants 64 KB in 1.4 us, 7 TB/s).
+// softmax runs on the other.  Every CTA fetches its own K/V tiles: 64 KB in 1.4 us
+// on each SM, 7 TB/s together, which is about what the SMs can fetch, from L2 or not.
 // Warps hand over through mbarriers, every wait bounded:
 //   8 softmax warps, one thread per row: the row maximum needs no exchange;
 //   one warp that issues the products;
@@ -35,7 +33,7 @@ namespace {
 
 constexpr int kRows = 128;                  // query rows per tile (tensor-memory lanes)
 constexpr int kPair = 2 * kRows;            // query rows per CTA
-constexpr int kGuarded = 6;                 // V tiles that are looked at, at most
+constexpr int kGuarded = 3;                 // V tiles that are looked at, at most (256 positions)
 
 template <int D>
 struct Tc {
@@ -68,7 +66,7 @@ struct Tc {
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
-chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, const int box, const bool pair) {
+chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, const int box) {
     using bf16 = __nv_bfloat16;
     using L = Tc<D>;
     constexpr int kTok = L::kTok, kChunks = D / 8, kSlots = L::kSlots;
@@ -80,18 +78,13 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     auto bar = [&](int i) -> uint32_t { return s_base + L::kSmemBar + 8 * i; };
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    // A cluster of two CTAs takes two neighbouring pairs of tiles and
-    // the same keys; each copies half of every K/V tile to both.
-    const int g = blockIdx.x, shift = p.group_shift, G = 1 << shift;
-    const int rank = blockIdx.y & 1, unit = blockIdx.y >> 1, split = unit % p.n_splits;
+    const int g = blockIdx.x, shift = p.group_shift, G = 1 << shift, split = blockIdx.y % p.n_splits;
     const ChunkEntry e = load_longest_entry(p, blockIdx.z, g == 0 && blockIdx.y == 0 && warp == 0);
     const int rows = e.q_len << shift;
     // the entry's last rows, which see most, first
-    const int last_tile = (rows + kPair - 1) / kPair - 1 - unit / p.n_splits * 2;
-    const int tile = last_tile - 1 + rank;
+    const int tile = (rows + kPair - 1) / kPair - 1 - static_cast<int>(blockIdx.y / p.n_splits);
     if (tile < 0) return;
-    const bool both = pair && last_tile > 0;          // the cluster's other CTA has rows too
-    const int row0 = tile * kPair, first_row = both ? (last_tile - 1) * kPair : row0;
+    const int row0 = tile * kPair;
     const int kv_lo = split * p.split_len;
     // keys [kv_lo, end) that the rows up to `row` see in this split
     auto end_of = [&](int row) -> int { return min(min(kv_lo + p.split_len, e.kv_len), chunk_limit(p, e, row >> shift) + 1); };
@@ -101,11 +94,11 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         const int r0 = row0 + X * kRows, end = r0 < rows ? end_of(min(r0 + kRows, rows) - 1) : kv_lo;
         n_x[X] = end > kv_lo ? (end - kv_lo + kTok - 1) / kTok : 0;
     }
-    const int kv_end = max(kv_lo, end_of(min((last_tile + 1) * kPair, rows) - 1));
-    const int n_tiles = (kv_end - kv_lo + kTok - 1) / kTok;   // of the cluster
+    const int kv_end = max(kv_lo, end_of(min(row0 + kPair, rows) - 1));
+    const int n_tiles = (kv_end - kv_lo + kTok - 1) / kTok;
     if (n_tiles == 0 && p.n_splits > 1) return;       // nothing to see: the join does not read this split
-    // from tile `guard` on, some row of the cluster does not see all of a tile
-    const int all_see = min(chunk_limit(p, e, first_row >> shift), kv_end - 1);
+    // from tile `guard` on, some row does not see all of a tile
+    const int all_see = min(chunk_limit(p, e, row0 >> shift), kv_end - 1);
     const int guard = all_see < kv_lo ? 0 : (all_see + 1 - kv_lo) / kTok;
 
     auto slot_of = [&](int j) -> int {
@@ -114,10 +107,10 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         if (!ok) record_error(p.err, page);
         return (ok ? page : 0) * p.page_size + (j - i * p.page_size);
     };
-    // ---- copies: a lane takes a box of rows, or four rows (of both CTAs' every
-    // other one).  The first rows are looked up before the barriers are made.
+    // ---- copies: a lane takes a box of rows, or four rows.  The first rows are
+    // looked up before the barriers are made.
     const int per = box > 0 ? box : 4;
-    const bool active = lane < kTok / per && (!both || (lane & 1) == rank);
+    const bool active = lane < kTok / per;
     int next[4] = {0, 0, 0, 0};
     auto fetch = [&](int t) {
         if (!active || t >= n_tiles) return;
@@ -136,7 +129,6 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         for (int i = 0; i < L::kBars; ++i) {
             uint32_t count = 1;
             if (i >= L::kVClean && i < L::kSFull) count = 2;
-            else if (both && ((i >= L::kKEmpty && i < L::kVFull) || (i >= L::kVEmpty && i < L::kVRaw))) count = 2;   // both CTAs' products
             else if ((i >= L::kPFull && i < L::kODone) || (i >= L::kSRead && i < L::kQFull)) {    // the tile's warps that hold rows
                 const int left = rows - row0 - ((i - L::kPFull) & 1) * kRows;
                 count = max(1, (min(left, kRows) + 31) / 32);
@@ -153,7 +145,6 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     }
     fence_before();
     __syncthreads();
-    if (both) cluster_sync();        // the other CTA copies and arrives here
     fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sm + L::kSmemTmem), 0);
     auto give_up = [&](int code) {
@@ -178,16 +169,11 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                 __syncwarp();
                 if (!active) return;
                 if (box > 0) {
-                    const uint32_t to = dst + lane * per * (D * 2);
-                    if (both) copy_box<true>(to, map, g * (D / 64), row[0] >> 3, full);
-                    else copy_box<false>(to, map, g * (D / 64), row[0] >> 3, full);
+                    copy_box(dst + lane * per * (D * 2), map, g * (D / 64), row[0] >> 3, full);
                 } else {
 #pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        const uint32_t to = dst + (lane >> 1) * (D * 16) + h * 1024 + (lane & 1) * 512;
-                        if (both) copy_rows4<true>(to, map, g * D + h * 64, row, full);
-                        else copy_rows4<false>(to, map, g * D + h * 64, row, full);
-                    }
+                    for (int h = 0; h < D / 64; ++h)
+                        copy_rows4(dst + (lane >> 1) * (D * 16) + h * 1024 + (lane & 1) * 512, map, g * D + h * 64, row, full);
                 }
             };
             int issued_k = 0, issued_v = 0;
@@ -207,7 +193,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
             // no copy is in flight when the CTA ends, also after a wait that gave up
             for (int t = max(0, issued_k - kSlots); t < issued_k; ++t) bar_wait(bar(L::kKFull + t % kSlots), phase(t));
             for (int t = max(0, issued_v - kSlots); t < issued_v; ++t) bar_wait(v_landed(t), v_phase(t));
-            // and no release, which come from both CTAs
+            // and no release
             bool reached = issued_v == n_tiles;
             for (int t = max(0, n_tiles - kSlots); reached && t < n_tiles; ++t)
                 reached = *s_abort == 0 && bar_wait(bar(L::kKEmpty + t % kSlots), phase(t)) && bar_wait(bar(L::kVEmpty + t % kSlots), phase(t));
@@ -243,11 +229,6 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                 auto commit = [&](int i) {
                     if (elect()) mma_commit(bar(i));
                 };
-                auto release = [&](int i) {     // a tile of K or V, in both CTAs
-                    if (!elect()) return;
-                    if (both) mma_commit_both(bar(i));
-                    else mma_commit(bar(i));
-                };
                 auto wait_k = [&](int t) -> bool { return wait_fast(bar(L::kKFull + t % kSlots), phase(t)); };
                 auto wait_v = [&](int t) -> bool { return wait_fast(bar((t < guard ? L::kVFull : L::kVClean) + t % kSlots), v_phase(t)); };
                 bool ok = wait_fast(bar(L::kQFull), 0) && wait_k(0);
@@ -255,7 +236,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     fence_after();
                     if (n_x[0] > 0) issue_s(0, 0);
                     if (n_x[1] > 0) issue_s(1, 0);
-                    release(L::kKEmpty);
+                    commit(L::kKEmpty);
                     ok = L::kOwnP || (wait_v(0) && (n_tiles == 1 || wait_k(1)));
                 }
                 // P in columns of its own (head_dim 64 leaves 64): S of the next tiles runs
@@ -273,7 +254,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                                 if (ok) issue_s(X, slot1);
                             }
                         if (!ok) break;
-                        release(L::kKEmpty + slot1);
+                        commit(L::kKEmpty + slot1);
                     }
                     if (!wait_v(j)) { ok = false; break; }
 #pragma unroll
@@ -285,7 +266,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                             issue_pv(X, slot, j > 0);
                             commit(L::kODone + X);
                         }
-                    release(L::kVEmpty + slot);
+                    commit(L::kVEmpty + slot);
                 }
                 for (int j = 0; !L::kOwnP && ok && j < n_tiles; ++j) {
                     const int slot = j % kSlots, slot1 = (j + 1) % kSlots;
@@ -304,9 +285,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                         issue_pv(1, slot, j > 0);
                         if (j == n_x[1] - 1) commit(L::kODone + 1);
                     }
-                    release(L::kVEmpty + slot);
+                    commit(L::kVEmpty + slot);
                     if (j + 1 < n_x[1]) issue_s(1, slot1);
-                    if (more) release(L::kKEmpty + slot1);
+                    if (more) commit(L::kKEmpty + slot1);
                     if (j + 2 < n_tiles) ok = wait_k(j + 2);
                 }
                 if (!ok) give_up(-5003);
@@ -572,7 +553,6 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
     }
     fence_before();
     __syncthreads();
-    if (both) cluster_sync();        // nothing of the other CTA is on its way here
     if (warp == L::kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(L::kCols));
 }
 
@@ -581,7 +561,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
 // ---------------------------------------------------------------------------
 
 template <int D>
-cudaError_t run(const ChunkParams &p, int group, int sms, cudaStream_t s) {
+cudaError_t run(const ChunkParams &p, int group, cudaStream_t s) {
     using L = Tc<D>;
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
@@ -598,31 +578,12 @@ cudaError_t run(const ChunkParams &p, int group, int sms, cudaStream_t s) {
         if (attr.numRegs < L::kLaunchRegs) return cudaErrorNotSupported;
         attr_done.fetch_or(bit);
     }
-    const int box = box_rows(p.page_size, L::kTok / 2);    // (two boxes at least, for two CTAs)
+    const int box = box_rows(p.page_size, L::kTok);
     Maps maps;
     if (!pool_maps(&maps, p, D, box)) return cudaErrorInvalidValue;
     const int tiles = (p.max_q_len * group + kPair - 1) / kPair;
-    // Two CTAs to a cluster, which copy a tile once for both, where contexts are
-    // long and an odd tile's empty partner costs no further round of CTAs: 4 x 2048
-    // tokens at 8K to 16K take 905 us with it and 929 without, 4 x 704 at 8K 282 and
-    // 293, 8 x 512 at 4K 209 and 211, at 2K 124 and 118 (a cluster starts, and ends,
-    // together); head_dim 64, 8 x 512 at 2K 91 and 96, 16 chunks of up to 448 tokens
-    // over up to 1500 states 51 and 38; three tiles, 2 x 192 tokens at 8K, 91 and
-    // 58, one tile, 8 x 64 tokens at 16K, 239 and 138.
-    const int64_t each = static_cast<int64_t>(p.n_kv_heads) * p.n_splits * p.batch, padded = (tiles + 1) / 2 * 2;
-    const bool pair = p.max_len >= (D == 64 ? 2048 : 4096) && tiles > 1 && (each * padded + sms - 1) / sms == (each * tiles + sms - 1) / sms;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_kv_heads, (tiles + 1) / 2 * 2 * p.n_splits, p.batch);
-    cfg.blockDim = dim3(L::kThreads);
-    cfg.dynamicSmemBytes = L::kBytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
-    attr[0].val.clusterDim.y = pair ? 2 : 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D>, p, maps, box, pair);
+    chunk_tc_kernel<D><<<dim3(p.n_kv_heads, tiles * p.n_splits, p.batch), L::kThreads, L::kBytes, s>>>(p, maps, box);
+    return cudaGetLastError();
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -668,8 +629,8 @@ bool pool_maps(Maps *maps, const ChunkParams &p, int D, int box) {
 
 bool chunk_wide(int max_q_len, int group) { return static_cast<int64_t>(max_q_len) * group > kRows; }
 
-cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, int sms, cudaStream_t s) {
-    return head_dim == 128 ? run<128>(p, group, sms, s) : run<64>(p, group, sms, s);
+cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, cudaStream_t s) {
+    return head_dim == 128 ? run<128>(p, group, s) : run<64>(p, group, s);
 }
 
 }  // namespace pkv

@@ -32,45 +32,19 @@ __device__ __forceinline__ bool elect() {
 __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
 }
-// TMA copies of a box of rows, or of four rows; kBoth: to the same place in both
-// CTAs of the cluster, completing the barrier of each.
-template <bool kBoth>
+// TMA copies of a box of rows, or of four rows, to this CTA.
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int half, int group, uint32_t bar) {
-    if constexpr (kBoth)
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %2, %3, "
-            "%4}], [%5], %6;\n" ::"r"(dst),
-            "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar), "h"(static_cast<uint16_t>(3))
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];\n" ::"r"(dst),
-            "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar)
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar)
+        : "memory");
 }
-template <bool kBoth>
 __device__ __forceinline__ void copy_rows4(uint32_t dst, const CUtensorMap *map, int x, const int (&row)[4], uint32_t bar) {
-    if constexpr (kBoth)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
-            "%3, %4, %5, %6}], [%7], %8;\n" ::"r"(dst),
-            "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar), "h"(static_cast<uint16_t>(3))
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-            "[%7];\n" ::"r"(dst),
-            "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
-            : "memory");
-}
-// arrives on the barrier at this place in both CTAs once the products so far are done
-__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
-                 "h"(static_cast<uint16_t>(3))
-                 : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+        "[%7];\n" ::"r"(dst),
+        "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
+        : "memory");
 }
 
 // bar_wait of the warp that issues the products, with one answer for all lanes:

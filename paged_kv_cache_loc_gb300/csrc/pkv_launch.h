@@ -403,11 +403,11 @@ bool chunk_supported(int dtype, int head_dim, int group);
 // How the contexts are cut with `room` bytes of workspace.
 void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int group, int batch, int n_q, int max_q_len, int max_len,
                 int sms, size_t room);
-cudaError_t launch_chunk(const ChunkParams &p, int parts, int dtype, int head_dim, int group, int sms, cudaStream_t s);
+cudaError_t launch_chunk(const ChunkParams &p, int parts, int dtype, int head_dim, int group, cudaStream_t s);
 // bf16 on tensor cores, without the join: entries of more than 128 rows (`wide`,
 // pkv_chunk_tc.cu); of fewer, with it (pkv_chunk_rows.cu).
 bool chunk_wide(int max_q_len, int group);
-cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, int sms, cudaStream_t s);
+cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, cudaStream_t s);
 cudaError_t launch_chunk_rows(const ChunkParams &p, int parts, int head_dim, int group, cudaStream_t s);
 // Query rows (position, head in group) of a call at most, per kv head and entry.
 constexpr int64_t kChunkMaxRows = 65535LL * 64;
