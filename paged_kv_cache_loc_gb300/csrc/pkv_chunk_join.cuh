@@ -18,6 +18,14 @@ struct ChunkDeal {
     __device__ __forceinline__ long long begin(int c) const { return tiles * c / parts(); }
 };
 
+// Pieces of an item whose first and last tile the CTAs `first` and `last` of `parts`
+// list; 0 where one CTA has it whole.  A CTA whose wait gave up has not listed the
+// rest of its items: what stands in the workspace for them may be anything, and a
+// pair that no CTAs can have is passed over (the call ends with its error code).
+__host__ __device__ inline int item_pieces(int first, int last, int parts) {
+    return first >= 0 && first < last && last < parts ? last - first + 1 : 0;
+}
+
 // o[at ..] = sum_s l_s 2^(m_s - M) o_s / sum_s l_s 2^(m_s - M) over the n pieces of a
 // row, piece s at unit(s), by a warp.
 template <typename T, int D, typename Unit>

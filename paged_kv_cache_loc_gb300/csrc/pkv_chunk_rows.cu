@@ -578,16 +578,17 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
 
 // The join of the items that lie in several CTAs: a warp per row of an item.
 template <int D>
-__global__ void __launch_bounds__(kThreads) rows_join_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kThreads) rows_join_kernel(const __grid_constant__ ChunkParams p, const int parts) {
     const int b = blockIdx.z, g = blockIdx.y, row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), G = 1 << p.group_shift;
     const ChunkEntry e = load_chunk_entry(p, b, false);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (row >= e.q_len << p.group_shift) return;
     const int64_t item = static_cast<int64_t>(b) * p.n_kv_heads + g;
     const int2 c = __ldcg(reinterpret_cast<const int2 *>(p.cut) + item);
-    if (c.x == c.y) return;
+    const int n = item_pieces(c.x, c.y, parts);
+    if (n == 0) return;
     const int64_t unit = (c.x + item) * p.part_rows + row;
-    join_row<__nv_bfloat16, D>(p, c.y - c.x + 1, [&](int s) { return unit + static_cast<int64_t>(s) * p.part_rows; },
+    join_row<__nv_bfloat16, D>(p, n, [&](int s) { return unit + static_cast<int64_t>(s) * p.part_rows; },
                                (static_cast<int64_t>(e.qo0 + (row >> p.group_shift)) * p.n_heads + g * G + (row & (G - 1))) * D);
 }
 
@@ -619,7 +620,7 @@ cudaError_t run(const ChunkParams &p, int parts, int group, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rows_join_kernel<D>, p);
+    return cudaLaunchKernelEx(&cfg, rows_join_kernel<D>, p, parts);
 }
 
 }  // namespace

@@ -2,7 +2,9 @@
 hold, the guard of the join of pieces, and refusals."""
 import glob
 import os
+import subprocess
 
+from paged_kv_cache_loc_gb300 import build
 from test_abi import ROOT
 
 CSRC = os.path.join(ROOT, "paged_kv_cache_loc_gb300", "csrc")
@@ -15,3 +17,28 @@ def test_no_copy_goes_to_several_ctas():
     sources = [f for ext in ("*.cu", "*.cuh", "*.h", "*.cpp") for f in glob.glob(os.path.join(CSRC, ext))]
     assert len(sources) > 10
     assert [f for f in sources if "multicast" in open(f).read()] == []
+
+
+def test_join_takes_no_unwritten_pair(tmp_path):
+    """The words that name an item's pieces lie in the caller's workspace, and a
+    wait that gives up leaves them unwritten.  Whatever stands there, the pieces
+    are ones that the workspace has room for: CTAs 0 .. parts - 1."""
+    prog = tmp_path / "pieces.cu"
+    prog.write_text(r'''
+#include <stdio.h>
+#include "pkv_chunk_join.cuh"
+int main() {
+  int first, last, parts;
+  while (scanf("%d %d %d", &first, &last, &parts) == 3) printf("%d\n", pkv::item_pieces(first, last, parts));
+  return 0;
+}''')
+    exe = tmp_path / "pieces"
+    subprocess.check_call([build._nvcc(), *build.ARCH, "-std=c++17", "-I", build.INCLUDE, "-I", build.CSRC, str(prog), "-o", str(exe)])
+    top = 2**31 - 1
+    words = [-top - 1, -top, -1, 0, 1, 2, 150, 151, 152, 153, 0x3F800000, 0x7FC00000, top - 1, top]    # 1.0 and NaN among them
+    asked = [(a, b, n) for a in words for b in words for n in (1, 2, 152)]
+    out = subprocess.run([str(exe)], input="\n".join("%d %d %d" % x for x in asked), capture_output=True, text=True, check=True).stdout
+    got = [int(x) for x in out.split()]
+    assert len(got) == len(asked)
+    for (a, b, n), pieces in zip(asked, got):
+        assert pieces == (b - a + 1 if 0 <= a < b < n else 0), (a, b, n)
