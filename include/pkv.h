@@ -595,8 +595,9 @@ int pkv_release_pages(const pkv_kvcache *c, const pkv_page_state *t, const int32
  *               what lies before is not written.  May be free_pages itself.
  * The list's place stays where it is; free_end is not used.  The workspace
  * (pkv_compact_workspace_bytes) serves one call at a time.  Device-data
- * errors: a page in the list outside [0, size / page_size), or a second time;
- * *free_start outside [0, n_free].
+ * errors: a page in the list outside [0, size / page_size), or a second time
+ * (the free pages are the others, and as many places at free_out's end are -1);
+ * *free_start outside [0, n_free] (no page counts as free).
  */
 int pkv_compact_pages(const pkv_kvcache *c, const pkv_page_state *t, int32_t *free_out,
                       int32_t *remap, const pkv_workspace *ws, void *stream);

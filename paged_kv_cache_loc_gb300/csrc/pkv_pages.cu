@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const __grid
         p.shares[d] = __ldcg(p.shares + s);
         p.shares[s] = 0;
     }
-    for (int64_t i = first; i < n_free; i += step) p.free_out[start + i] = static_cast<int>(used + i);
+    // (fewer than listed after an error: behind them no page that may hold a row's by now)
+    for (int64_t i = first; i < p.n_free - start; i += step) p.free_out[start + i] = i < n_free ? static_cast<int>(used + i) : -1;
     if (first == 0) p.moves[0] = n_moves;
 }
 
