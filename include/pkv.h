@@ -621,7 +621,7 @@ size_t pkv_compact_workspace_bytes(int64_t n_pages);
  *   q, o        [n_q, n_heads, head_dim] of c->dtype, o not q; rows of o that
  *               belong to no entry are left as they are.
  *   max_q_len   host-side bound of q_len (max_q_len * G at most 65535 * 64);
- *   c->max_len  that of n, max_pages * page_size at most.
+ *   c->max_len  that of n, max_pages * page_size and 2^30 at most.
  * The rows of two entries must not be the same (else they hold either's result).
  * Entries of one or a few rows beside one of thousands are right, but each is then
  * read by one CTA per kv head: a call of their own takes them faster.

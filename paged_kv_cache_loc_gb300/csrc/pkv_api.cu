@@ -1086,6 +1086,7 @@ int check_chunk(const pkv_kvcache *c, int32_t n_q, int32_t n_heads, int32_t max_
     int rc = check_pool(c, 0);
     if (rc) return rc;
     if (c->batch < 0 || c->batch > 65535 || c->max_len < 0 || max_q_len < 0 || n_q < 0) return PKV_ERR_ARG;
+    if (c->max_len > pkv::kChunkMaxLen) return PKV_ERR_ARG;
     if (n_heads <= 0 || n_heads % c->n_kv_heads || c->n_kv_heads > 65535) return PKV_ERR_ARG;
     *group = n_heads / c->n_kv_heads;
     if (!pkv::chunk_supported(c->dtype, c->head_dim, *group)) return PKV_ERR_UNSUPPORTED;

@@ -320,7 +320,7 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
     ChunkPlan &plan = *out;
     plan = ChunkPlan{};
     plan.n_splits = 1;
-    plan.split_len = 1 << 30;
+    plan.split_len = kChunkMaxLen;
     if (dtype == PKV_BF16 && !chunk_wide(max_q_len, group)) {
         // a CTA on every SM, and partials of one row of an item per step along the tiles
         plan.parts = sms > 0 ? sms : 1;

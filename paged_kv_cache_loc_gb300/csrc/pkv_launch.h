@@ -411,6 +411,8 @@ cudaError_t launch_chunk_tc(const ChunkParams &p, int head_dim, int group, cudaS
 cudaError_t launch_chunk_rows(const ChunkParams &p, int parts, int head_dim, int group, cudaStream_t s);
 // Query rows (position, head in group) of a call at most, per kv head and entry.
 constexpr int64_t kChunkMaxRows = 65535LL * 64;
+// Positions of a context at most: the kernels add a piece's length to its start in 32 bits.
+constexpr int32_t kChunkMaxLen = 1 << 30;
 // Whether the selection and the attention over it have a kernel for this shape.
 bool sparse_supported(int dtype, int head_dim, int group);
 // Sets p->splits and p->entries.

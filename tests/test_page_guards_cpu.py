@@ -1,13 +1,21 @@
 """Chunk attention and page operators without a GPU: what their sources must not
 hold, the guard of the join of pieces, and refusals."""
+import ctypes
 import glob
 import os
 import subprocess
 
-from paged_kv_cache_loc_gb300 import build
-from test_abi import ROOT
+import torch
+
+from paged_kv_cache_loc_gb300 import _lib, build
+from test_abi import O, Q, ROOT, fake_cache
 
 CSRC = os.path.join(ROOT, "paged_kv_cache_loc_gb300", "csrc")
+
+
+def build_and_load():
+    build.build()
+    return _lib.load()
 
 
 def test_no_copy_goes_to_several_ctas():
@@ -42,3 +50,22 @@ int main() {
     assert len(got) == len(asked)
     for (a, b, n), pieces in zip(asked, got):
         assert pieces == (b - a + 1 if 0 <= a < b < n else 0), (a, b, n)
+
+
+def test_chunk_refuses_contexts_of_more_positions_than_its_sums_hold():
+    """2^30 positions at most: pieces' ends are summed in 32 bits.  (A table may
+    name a page many times, so the pool's size does not bound a context.)"""
+    lib = build_and_load()
+
+    def call(max_len, dtype, max_q):
+        c = fake_cache(qo_indptr=0x9000, max_len=max_len, dtype=dtype, n_kv_heads=1)
+        return lib.pkv_paged_chunk(ctypes.byref(c), 0, ctypes.c_void_p(0x1000), 1 << 24, 128, Q, O, 4, 1, max_q, 1, 0.1, None, None)
+
+    for dtype in (_lib.PKV_F32, _lib.PKV_BF16):
+        for max_q in (1, 4, 500):
+            for max_len in (2**30 + 1, 2**31 - 128, 2**31 - 1):
+                assert call(max_len, dtype, max_q) == _lib.PKV_ERR_ARG
+                c = fake_cache(qo_indptr=0x9000, max_len=max_len, dtype=dtype, n_kv_heads=1)
+                assert lib.pkv_chunk_workspace_bytes(ctypes.byref(c), 4, 1, max_q) == 0
+            if not torch.cuda.is_available():     # not refused: it asks for the device
+                assert call(2**30, dtype, max_q) == _lib.PKV_ERR_CUDA
