@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
         }
         if (lead) mine[full] = fresh;
     }
-    for (int i = slice * kThreads + tid; i < full; i += gridDim.x * kThreads) {
+    // (unsigned: a row may hold 2^31 - 1 positions, and the last step goes beyond)
+    for (uint32_t i = slice * kThreads + tid; i < static_cast<uint32_t>(full); i += gridDim.x * kThreads) {
         int page = theirs[i];
         if (in_range(page, p.n_pages)) {
             atomicAdd(p.shares + page, 1);
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
     }
     if (p.req_to_token) {
         int32_t *tokens = p.req_to_token + static_cast<int64_t>(e.child) * p.max_ctx_len;
-        for (int j = slice * kThreads + tid; j < e.len; j += gridDim.x * kThreads) {
+        for (uint32_t j = slice * kThreads + tid; j < static_cast<uint32_t>(e.len); j += gridDim.x * kThreads) {
             const int i = j / ps;
             const int page = i < full ? theirs[i] : fresh;
             tokens[j] = in_range(page, p.n_pages) ? page * ps + (j - i * ps) : -1;
@@ -252,7 +253,8 @@ __device__ __forceinline__ void drop_page(const ReleaseParams &p, const ReleaseE
 __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ ReleaseParams p) {
     const int b = blockIdx.y;
     const ReleaseEntry e = load_release(p, b, blockIdx.x == 0 && threadIdx.x == 0);
-    for (int i = e.lo + blockIdx.x * kThreads + threadIdx.x; i < e.hi; i += gridDim.x * kThreads) drop_page(p, e, i);
+    // (unsigned: a row may hold 2^31 - 1 pages, and the last step goes beyond)
+    for (uint32_t i = e.lo + blockIdx.x * kThreads + threadIdx.x; i < static_cast<uint32_t>(e.hi); i += gridDim.x * kThreads) drop_page(p, e, i);
 }
 
 // Exclusive sums of two counts of the warps over the cluster, in warp order, and
@@ -572,7 +574,7 @@ cudaError_t launch_release(const ReleaseParams &p, int sms, cudaStream_t s) {
     // up to 64K table entries: the cluster that collects the pages drops the references too
     if (static_cast<int64_t>(p.batch) * p.max_pages <= 1 << 16)
         return launch(collect_kernel<true>, p, dim3(kScanCluster), kScanThreads, kScanCluster, false, s);
-    int64_t x = (p.max_pages + kThreads - 1) / kThreads;
+    int64_t x = (static_cast<int64_t>(p.max_pages) + kThreads - 1) / kThreads;
     const int64_t most = (16LL * sms + p.batch - 1) / p.batch;
     if (x > most) x = most;
     drop_kernel<<<dim3(static_cast<unsigned>(x), p.batch), kThreads, 0, s>>>(p);

@@ -39,3 +39,56 @@ def test_compact_bad_free_list_names_no_used_page(value, in_place):
     assert error() == -1
     taken = host(rows)[1:, 0].tolist()
     assert taken == [*range(45, 64), -1] and not set(taken[:19]) & set(table[table >= 0].tolist())
+
+
+# ---------------------------------------------------------------------------
+# rows of 2^31 - 1 positions: the step behind the last one passes 31 bits
+# ---------------------------------------------------------------------------
+
+TOP = 2**31 - 1
+
+
+def room(n_bytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < n_bytes + (8 << 30):
+        pytest.skip("not enough free memory")
+
+
+def small_pool(pages, layers=1, kv=1, d=8, dtype=torch.bfloat16):
+    return [torch.zeros(layers, pages, kv, d, dtype=dtype, device="cuda") for _ in range(2)]
+
+
+def test_release_the_end_of_a_row_of_two_billion_pages():
+    room(4 * TOP)
+    i32, n = dict(dtype=torch.int32, device="cuda"), 5000
+    k, v = small_pool(n)
+    table = torch.empty(1, TOP, **i32)
+    pages = dev(np.random.default_rng(0).permutation(n))
+    table[0, TOP - n - 99:TOP - n] = 7
+    table[0, TOP - n:] = pages
+    cache = pkv.KVCache(k_buffer=k, v_buffer=v, req_to_token=table, req_pool_indices=dev([0]), seq_lens=dev([TOP]))
+    shares, free, end = torch.zeros(n, **i32), torch.full((n,), -5, **i32), dev([-1])
+    shares[:100] = 3
+    pkv.release_pages(cache, table, 1, shares, free, dev([n]), end, dev([TOP - n]))
+    clean()
+    assert (table[0, TOP - n:] == -1).all() and (table[0, TOP - n - 99:TOP - n] == 7).all()
+    assert host(shares).tolist() == [2] * 100 + [0] * (n - 100)
+    assert int(end) == 100 and host(free).tolist() == [-5] * 100 + list(range(100, n))
+
+
+def test_fork_a_row_of_two_billion_positions():
+    room(6 * 4 * TOP)
+    i32, n = dict(dtype=torch.int32, device="cuda"), 64
+    k, v = small_pool(n, layers=32, kv=64, d=128, dtype=torch.float32)      # (a page of many pieces: many CTAs to the child)
+    table, tokens = torch.empty(2, TOP, **i32), torch.empty(2, TOP, **i32)
+    torch.arange(TOP, out=table[1])
+    table[1] %= n
+    table[0].fill_(-7)
+    tokens.fill_(-3)
+    cache = pkv.KVCache(k_buffer=k, v_buffer=v, req_to_token=tokens, req_pool_indices=dev([0]), seq_lens=dev([TOP]))
+    shares, end = torch.zeros(n, **i32), dev([-1])
+    pkv.fork_requests(cache, table, 1, dev([1]), shares, dev([]), dev([0]), end)
+    clean()
+    assert torch.equal(table[0], table[1]) and torch.equal(tokens[0], table[1])
+    assert (tokens[1] == -3).all() and int(end) == 0
+    assert host(shares).tolist() == [TOP // n + (p < TOP % n) for p in range(n)]
