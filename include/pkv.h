@@ -617,7 +617,9 @@ size_t pkv_compact_workspace_bytes(int64_t n_pages);
  * j % page_size, r = c->req_pool_indices[b].  A row that sees no position (n =
  * 0; causal and n < q_len: the first q_len - n rows) gives 0.  q_len and n need
  * not agree otherwise.  What a row does not see has no part in its result,
- * whatever values stand there.
+ * whatever values stand there.  A value that a row sees and that is not finite
+ * makes its channel of that row's outputs not finite; a score that is NaN or
+ * +inf, or scores that are all -inf, make them NaN.
  *   q, o        [n_q, n_heads, head_dim] of c->dtype, o not q; rows of o that
  *               belong to no entry are left as they are.
  *   max_q_len   host-side bound of q_len (max_q_len * G at most 65535 * 64);

@@ -233,8 +233,9 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
         const int at = row0 + ty * R + r;
         if (at >= rows) continue;
         const int row = e.qo0 + (at >> p.group_shift), head = g * G + (at & (G - 1));
-        // a sum of 0 is that of a row that sees nothing here (the largest weight is 1)
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        // a sum of 0 is that of a row that sees nothing here, or -inf alone (the largest
+        // weight is 1); the join tells them apart for all pieces together
+        const float inv = chunk_inverse(l[r], p.n_splits == 1 && lim[r] >= 0);
         const int64_t unit = chunk_unit(p, split, row, head);
         float *dst = p.n_splits > 1 ? p.o_part + unit * D : static_cast<float *>(p.o) + (static_cast<int64_t>(row) * p.n_heads + head) * D;
 #pragma unroll

@@ -68,6 +68,10 @@ __device__ __forceinline__ int chunk_limit(const ChunkParams &p, const ChunkEntr
     return p.causal ? e.first + i : e.first;
 }
 
+// What a row's weighted sum of values is multiplied by, l being the sum of its weights:
+// 0 for a row that sees nothing, NaN (0 / 0) for one whose scores are all -inf.
+__device__ __forceinline__ float chunk_inverse(float l, bool sees) { return l == 0.f ? (sees ? NAN : 0.f) : 1.f / l; }
+
 // the partial sums of split `split`: row `row` of q, head `head`
 __device__ __forceinline__ int64_t chunk_unit(const ChunkParams &p, int split, int row, int head) {
     return (static_cast<int64_t>(split) * p.n_q + row) * p.n_heads + head;

@@ -27,7 +27,7 @@ __host__ __device__ inline int item_pieces(int first, int last, int parts) {
 }
 
 // o[at ..] = sum_s l_s 2^(m_s - M) o_s / sum_s l_s 2^(m_s - M) over the n pieces of a
-// row, piece s at unit(s), by a warp.
+// row, piece s at unit(s), by a warp; n = 0 for a row that sees nothing.
 template <typename T, int D, typename Unit>
 __device__ __forceinline__ void join_row(const ChunkParams &p, int n, Unit unit, int64_t at) {
     constexpr int kPer = D / 32, kLoads = 16;           // elements per lane, pieces in flight
@@ -81,7 +81,7 @@ __device__ __forceinline__ void join_row(const ChunkParams &p, int n, Unit unit,
             }
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = chunk_inverse(sum, n > 0);
     T *dst = static_cast<T *>(p.o) + at + lane * kPer;
 #pragma unroll
     for (int c = 0; c < kPer; ++c) dst[c] = Elem<T>::from_f(acc[c] * inv);

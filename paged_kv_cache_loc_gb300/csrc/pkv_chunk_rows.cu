@@ -520,7 +520,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             if (!ok || !full(L::kODone, 2, s)) { ok = false; break; }
             if (busy) {
                 fence_after();
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = chunk_inverse(l, x.whole && lim >= 0);
                 const uint32_t *bad = reinterpret_cast<const uint32_t *>(sm + L::kSmemBad) + (s % kSegs) * (L::kBadWords + 1);
                 const bool some_bad = x.guard < x.n_tiles && *static_cast<const volatile uint32_t *>(bad + L::kBadWords) != 0;
                 const int64_t at = (static_cast<int64_t>(x.qo0 + (row >> shift)) * p.n_heads + x.g * G + (row & (G - 1))) * D;
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kThreads) rows_join_kernel(const __grid_consta
     if (row >= e.q_len << p.group_shift) return;
     const int64_t item = static_cast<int64_t>(b) * p.n_kv_heads + g;
     const int2 c = __ldcg(reinterpret_cast<const int2 *>(p.cut) + item);
-    const int n = item_pieces(c.x, c.y, parts);
+    const int n = item_pieces(c.x, c.y, parts);           // (several tiles: every row sees some position)
     if (n == 0) return;
     const int64_t unit = (c.x + item) * p.part_rows + row;
     join_row<__nv_bfloat16, D>(p, n, [&](int s) { return unit + static_cast<int64_t>(s) * p.part_rows; },

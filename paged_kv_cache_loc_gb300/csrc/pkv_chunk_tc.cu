@@ -462,7 +462,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         }
         fence_after();
         if (__all_sync(0xffffffffu, busy && live && *s_abort == 0 && (mine > 0 || p.n_splits == 1))) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float inv = chunk_inverse(l, p.n_splits == 1 && lim >= 0);
             const bool some_bad = mine > 0 && *static_cast<volatile uint32_t *>(s_bad + L::kBadWords - 1) != 0;
             // columns [c0, c0 + 32) of this row
             auto load_o = [&](int c0, float (&v)[32]) {

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import paged_kv_cache_loc_gb300 as pkv
-from paged_kv_cache_loc_gb300 import _lib
+from test_gpu_chunk import DTYPES, case, want
+from test_gpu_chunk import host as chunk_host
 from test_gpu_pages import (compact_case, dev, error, clean, gpu, host, run_compact, want_compact)  # noqa: F401 (gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +93,40 @@ def test_fork_a_row_of_two_billion_positions():
     assert torch.equal(table[0], table[1]) and torch.equal(tokens[0], table[1])
     assert (tokens[1] == -3).all() and int(end) == 0
     assert host(shares).tolist() == [TOP // n + (p < TOP % n) for p in range(n)]
+
+
+# ---------------------------------------------------------------------------
+# chunk attention: scores of -inf
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,q_lens,lens", [(1, [5, 2], [3, 40]), (4, [5, 2], [2000, 40]), (1, [300, 2], [200, 40]), (8, [40, 3], [4500, 40]),
+                                           (2, [400, 70], [520, 300])])
+def test_scores_of_minus_infinity(dtype, causal, d, G, q_lens, lens):
+    """Entry 0, kv head 0: a row whose scores are all -inf gives NaN (0 / 0), one
+    that sees nothing 0, and with one finite score its value alone, exactly."""
+    c = case(q_lens, lens, dtype=dtype, G=G, d=d, kv=2, ps=16)
+    c.q[..., 0] = c.q[..., 0].abs() + 0.5
+    ref, tol = want(c, causal)
+    n, q = lens[0], q_lens[0]
+    pos = np.arange(n)
+    slots = torch.from_numpy(chunk_host(c.table)[int(c.cache.req_pool_indices[0]), pos // 16] * 16 + pos % 16).cuda()
+    sees = np.arange(q) + n - q >= 0 if causal else np.ones(q, bool)
+    k, v = c.cache.k_buffer, c.cache.v_buffer
+    first = k[0, slots[0], 0].clone()
+    k[0, slots, 0, 0] = -float("inf")
+    for ws in (None, c.workspace()):
+        got = chunk_host(c.run(causal, workspace=ws))
+        assert np.isnan(got[:q, :G][sees]).all() and (got[:q, :G][~sees] == 0).all()
+        rest = np.ones(got.shape, bool)
+        rest[:q, :G] = False
+        assert (np.abs(got - ref) <= tol)[rest].all()
+    k[0, slots[0], 0] = first
+    alone = chunk_host(v[0, slots[0], 0])
+    for ws in (None, c.workspace()):
+        got = chunk_host(c.run(causal, workspace=ws))
+        assert (got[:q, :G][sees] == alone).all() and (got[:q, :G][~sees] == 0).all()
+        assert (np.abs(got - ref) <= tol)[rest].all()
+    clean()
