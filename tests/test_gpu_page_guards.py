@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import paged_kv_cache_loc_gb300 as pkv
-from test_gpu_chunk import DTYPES, case, want
+from test_gpu_chunk import DTYPES, case, check, want
 from test_gpu_chunk import host as chunk_host
 from test_gpu_pages import (compact_case, dev, error, clean, gpu, host, run_compact, want_compact)  # noqa: F401 (gpu: a fixture)
 
@@ -129,4 +129,105 @@ def test_scores_of_minus_infinity(dtype, causal, d, G, q_lens, lens):
         got = chunk_host(c.run(causal, workspace=ws))
         assert (got[:q, :G][sees] == alone).all() and (got[:q, :G][~sees] == 0).all()
         assert (np.abs(got - ref) <= tol)[rest].all()
+    clean()
+
+
+# ---------------------------------------------------------------------------
+# chunk attention: moved pages, values that are not finite, old workspaces
+# ---------------------------------------------------------------------------
+
+KINDS = [([5, 1], [700, 90]), ([8, 3], [4500, 1300]), ([300, 70], [900, 200]), ([40, 2], [4500, 64])]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ps", [3, 16])
+@pytest.mark.parametrize("q_lens,lens", KINDS)
+def test_moving_pages_changes_no_bit(dtype, d, ps, q_lens, lens):
+    """The same calls before and after the pool is compacted, alone and together,
+    with a workspace and without."""
+    c = case(q_lens, lens, dtype=dtype, d=d, G=8, ps=ps, kv=1, spare_pages=300)
+    entries = [dataclasses.replace(c, q=c.q[lo:hi].contiguous(), max_q=hi - lo, cache=dataclasses.replace(
+        c.cache, req_pool_indices=c.cache.req_pool_indices[i:i + 1].clone(), seq_lens=c.cache.seq_lens[i:i + 1].clone(), max_len=lens[i],
+        qo_indptr=dev([0, hi - lo]))) for i, (lo, hi) in enumerate(((0, q_lens[0]), (q_lens[0], sum(q_lens))))]
+    calls = [(x, ws) for x in [c, *entries] for ws in (None, x.workspace())]
+    before = [x.run(workspace=ws).clone() for x, ws in calls]
+    n_pages = c.cache.k_buffer.shape[1] // ps
+    held = set(chunk_host(c.table).flatten().tolist()) - {-1}
+    free = dev([p for p in np.random.default_rng(1).permutation(n_pages) if p not in held])
+    remap = pkv.compact_pages(c.cache, c.table, ps, dev(np.zeros(n_pages)), free, dev([0]), token_table=False,
+                              workspace=pkv.compact_workspace(n_pages))
+    assert int((remap != torch.arange(n_pages, device="cuda")).sum()) > 10 and int(c.table.max()) == len(held) - 1
+    for (x, ws), o in zip(calls, before):
+        assert torch.equal(x.run(workspace=ws), o)
+    clean()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("G,q_lens,lens", [(1, [600, 3], [4200, 10]), (2, [300, 3], [4200, 10]), (1, [128, 3], [4200, 10]), (8, [16, 3], [4200, 10])])
+def test_values_that_some_rows_see(dtype, d, bad, G, q_lens, lens):
+    """One value that is not finite, at places of the causal diagonal, before it
+    and behind tiles' borders: the rows that see it have their channel not
+    finite, everything else is as without it."""
+    c = case(q_lens, lens, dtype=dtype, d=d, G=G, kv=2, ps=8)
+    ref, tol = want(c)
+    n, q = lens[0], q_lens[0]
+    row = int(c.cache.req_pool_indices[0])
+    lim = np.r_[n - q + np.arange(q), np.full(q_lens[1], -1)]
+    for ws in (None, c.workspace()):
+        for j in {100, n - q, n - q + 1, n - q // 2, (n - 1) // 128 * 128, (n - 1) // 128 * 128 - 1, n - 1}:
+            slot = int(c.table[row, j // 8]) * 8 + j % 8
+            keep = c.cache.v_buffer[0, slot, 1, 7].clone()
+            c.cache.v_buffer[0, slot, 1, 7] = bad
+            got, sees = chunk_host(c.run(workspace=ws)), lim >= j
+            c.cache.v_buffer[0, slot, 1, 7] = keep
+            assert not np.isfinite(got[sees][:, G:, 7]).any(), j
+            rest = np.ones_like(got, bool)
+            rest[sees, G:, 7] = False
+            assert (np.abs(got - ref) <= tol)[rest].all(), j
+    clean()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens,lens", KINDS + [([2] * 40, [0, 1, 130, 2000] * 10)])
+def test_a_workspace_of_anything(dtype, d, q_lens, lens):
+    """What an earlier call, or nobody, left in the workspace does not matter, a
+    call repeats itself bit for bit, and nothing is written behind its bytes."""
+    c = case(q_lens, lens, dtype=dtype, d=d, G=8, kv=1, ps=16)
+    ref, tol = want(c)
+    ws = c.workspace()
+    start = ws.desc.base - ws.buffer.data_ptr()
+    end = start + ws.desc.bytes
+    outside = torch.cat([ws.buffer[:start], ws.buffer[end:]]).fill_(0xA5)
+    ws.buffer[:start], ws.buffer[end:] = 0xA5, 0xA5
+    first = None
+    for fill in (0x00, 0xFF, 0x7F, None, 0x01):
+        if fill is None:
+            other = case([1, 7, 3], [64, 3000, 500], dtype=dtype, d=d, G=8, kv=1, ps=16)
+            other.run(workspace=ws)
+        else:
+            ws.buffer[start:end] = fill
+        o = torch.full_like(c.q, float("nan"))
+        c.run(o=o, workspace=ws)
+        first = o if first is None else first
+        assert torch.equal(o, first)
+        assert torch.equal(torch.cat([ws.buffer[:start], ws.buffer[end:]]), outside)
+    check(first, ref, tol)
+    clean()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("q_lens,lens", KINDS)
+def test_rows_before_the_first_entry_stay(dtype, q_lens, lens):
+    c = case(q_lens, lens, dtype=dtype, spare_rows=20)
+    c.cache.qo_indptr += 13
+    o = torch.full_like(c.q, 3.25)
+    ref, tol = want(c, o=o)
+    for ws in (None, c.workspace()):
+        o.fill_(3.25)
+        check(c.run(o=o, workspace=ws), ref, tol)
+        assert (o[:13] == 3.25).all() and (o[13 + sum(q_lens):] == 3.25).all()
     clean()
