@@ -690,6 +690,13 @@ int pkv_paged_decode_noalloc(const pkv_kvcache *c, int32_t layer_id, const void 
  *   -2001, -2007   a prefill wait gave up (producer, softmax warps);
  *   -3002 .. -3006 a prefill wait of the thread issuing tensor-core
  *                  instructions gave up;
+ *   -5001 .. -5003, -5008 .. -5011
+ *                  a wait of pkv_paged_chunk (bf16, more than 128 rows of
+ *                  position and head in group per entry) gave up: copies of K,
+ *                  of V, products, the look at V, the softmax;
+ *   -5101 .. -5105 the same with up to 128 rows: copies, products, query
+ *                  tiles, the look at V, the softmax.  After one of these
+ *                  codes that call's outputs are unspecified;
  *   -100000 - b    a shared prefix was stated, but entry b's leading pages (or
  *                  slots) differ from the first entry's (head_dim 128) or
  *                  from its group's first entry's (head_dim 64);

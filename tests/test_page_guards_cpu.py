@@ -3,6 +3,7 @@ hold, the guard of the join of pieces, and refusals."""
 import ctypes
 import glob
 import os
+import re
 import subprocess
 
 import torch
@@ -69,3 +70,18 @@ def test_chunk_refuses_contexts_of_more_positions_than_its_sums_hold():
                 assert lib.pkv_chunk_workspace_bytes(ctypes.byref(c), 4, 1, max_q) == 0
             if not torch.cuda.is_available():     # not refused: it asks for the device
                 assert call(2**30, dtype, max_q) == _lib.PKV_ERR_CUDA
+
+
+def test_every_code_of_a_wait_is_documented():
+    """The codes that kernels record when a wait gives up, and the list at
+    pkv_last_device_error: the same numbers, none left out, none that is gone."""
+    recorded = set()
+    for f in glob.glob(os.path.join(CSRC, "*.cu")):
+        recorded |= {int(x) for x in re.findall(r"(?:give_up\(|record_error\(p\.err, )-(\d{4,5})[,)]", open(f).read())}
+    text = open(os.path.join(ROOT, "include", "pkv.h")).read()
+    text = text[text.index("one of these codes"):text.index("int pkv_last_device_error")]
+    listed = set()
+    for a, b in re.findall(r"-(\d{4})(?!\d)(?: \.\. -(\d{4})(?!\d))?", text):
+        listed |= set(range(int(a), int(b or a) + 1))
+    assert recorded and recorded <= listed, recorded - listed
+    assert {x for x in listed if x >= 5000} == {x for x in recorded if x >= 5000}
