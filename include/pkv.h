@@ -557,8 +557,10 @@ int pkv_copy_pages(const pkv_kvcache *c, int32_t page_size, void *page_bounds, c
  * of the rows concerned are unspecified).  Device-data errors: a row outside
  * [0, num_reqs), a row forked from itself, a length outside [0, max_pages * ps]
  * (or beyond max_ctx_len with req_to_token) - such an entry counts as n = 0 -;
- * a page of the parent outside [0, size / ps) (-1 in its place); a free list
- * that runs out (-1), or holds such a page; *free_start outside [0, n_free].
+ * a page of the parent outside [0, size / ps) (-1 in its place; where it is the
+ * partly filled one, the row has its page of the free list, without the copy);
+ * a free list that runs out (-1), or holds such a page; *free_start outside [0,
+ * n_free] (the list counts as empty).
  */
 int pkv_fork_requests(const pkv_kvcache *c, const pkv_page_state *t, const int32_t *parents,
                       void *stream);
@@ -632,8 +634,8 @@ size_t pkv_compact_workspace_bytes(int64_t n_pages);
  * query rows the contexts are cut into pieces whose partials go to the
  * workspace and are joined by a second kernel.  A workspace of
  * pkv_chunk_workspace_bytes(...) holds them; with less (ws->bytes), or none, the
- * contexts stay whole, or in fewer pieces: the same result up to fp32 rounding,
- * later.  The workspace
+ * contexts stay whole (or, fp32 and bf16 of more than 128 rows per entry, in
+ * fewer pieces): the same result up to fp32 rounding, later.  The workspace
  * serves one call at a time.  Reads c->seq_lens, c->qo_indptr,
  * c->req_pool_indices, c->num_reqs and the pool; not c->req_to_token,
  * c->kv_indptr.  Supported: f32 and bf16, head_dim 64 or 128, G in {1, 2, 4, 8}.

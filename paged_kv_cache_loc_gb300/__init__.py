@@ -36,5 +36,6 @@ from ._lib import PkvError, load  # noqa: F401
 __all__ = ["KVCache", "Workspace", "kv_write", "rope_kv_write", "paged_decode", "decode_step",
            "paged_decode_pages", "paged_decode_shared", "paged_prefill", "paged_decode_noalloc", "decode_plan",
            "SparsePages", "build_tables", "page_bounds", "select_pages", "select_workspace", "select_workspace_bytes",
-           "paged_decode_selected", "sparse_decode_step", "copy_pages", "fork_requests", "release_pages", "compact_pages", "compact_workspace", "paged_chunk", "chunk_workspace", "chunk_workspace_bytes",
+           "paged_decode_selected", "sparse_decode_step", "copy_pages", "fork_requests", "release_pages",
+           "compact_pages", "compact_workspace", "paged_chunk", "chunk_workspace", "chunk_workspace_bytes",
            "last_device_error", "PkvError", "load"]

@@ -973,7 +973,7 @@ int pkv_copy_pages(const pkv_kvcache *c, int32_t page_size, void *page_bounds, c
     p.dst = dst;
     p.n = n;
     p.err = di.err;
-    return map_launch(pkv::launch_copy_pages(p, di.sms, static_cast<cudaStream_t>(stream)));
+    return map_launch(pkv::launch_copy_pages(p, static_cast<cudaStream_t>(stream)));
 }
 
 int pkv_fork_requests(const pkv_kvcache *c, const pkv_page_state *t, const int32_t *parents, void *stream) {

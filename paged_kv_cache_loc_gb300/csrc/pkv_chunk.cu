@@ -9,8 +9,8 @@
 // score) and sum l; a context that is cut into splits ends in partials o / l and
 // (m, l), joined as o = sum_s l_s 2^(m_s - M) o_s / sum_s l_s 2^(m_s - M).
 //
-// fp32: products of fp32 rows have no tensor-core form that keeps 24 bits, so
-// this runs on the FMA units.  A CTA of 256 threads takes 64 rows (position,
+// fp32: the tensor cores have no product of 24-bit factors (three bf16 parts of each
+// and six products would make one; not built), so this runs on the FMA units.  A CTA of 256 threads takes 64 rows (position,
 // head in group; 16 or 32 where an entry has no more) and 64 keys at a time; a
 // thread holds a 4 x 4 block of scores and a 4 x (D / 16) block of o, so a
 // 16-byte shared-memory load feeds eight FMAs (two lanes to an instruction).  K of
@@ -252,7 +252,6 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const ChunkEntry e = load_chunk_entry(p, blockIdx.z, false);
-    const int lane = threadIdx.x & 31;
     const int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     if (u >= static_cast<int64_t>(e.q_len) * p.n_heads) return;
     const int i = static_cast<int>(u / p.n_heads), head = static_cast<int>(u - static_cast<int64_t>(i) * p.n_heads);
@@ -335,8 +334,9 @@ void chunk_plan(ChunkPlan *out, int dtype, int head_dim, int n_kv_heads, int gro
     // CTAs per SM, rows and keys per tile of the kernel that the call takes.  On
     // tensor cores a CTA's start and end cost as much as some 800 keys, so the
     // contexts are cut only where one round of CTAs has room for the pieces, of
-    // four tiles at least (512 rows at 64K positions: 406 us in one round of 128
-    // CTAs, 399 to 554 in up to three).  In fp32 a tile takes longer than start
+    // four tiles at least (8 x 64 tokens at 16K positions: 136 us in one round, 150
+    // and 152 in up to two and three, 208 uncut; 2 x 192 at 8K 58, 67, 80 and 106;
+    // 512 at 64K 391, 408, 376 and 729).  In fp32 a tile takes longer than start
     // and end do: CTAs for twelve rounds, of two tiles at least, which even out
     // entries of different lengths, unless they fill three rounds whole (16 x 1 to
     // 8 tokens at 0.5K to 4K 199 us against 273 for two rounds, 6 x 10 to 200 at up

@@ -37,7 +37,7 @@ __device__ __forceinline__ ChunkEntry load_chunk_entry(const ChunkParams &p, int
 
 // The entry that lane `from` holds, by a whole warp: values that are then known to be
 // one for all lanes, so that branches on them take no care of lanes that part (4 x 2048
-// tokens at 8K to 16K: 896 us, 953 without; in fp32 4 x 512 at 2K 1060 and 1084).
+// tokens at 8K to 16K: 914 us, 984 without; in fp32 4 x 512 at 2K 1060 and 1084).
 __device__ __forceinline__ ChunkEntry entry_of_lane(ChunkEntry e, int from) {
     e.req = __shfl_sync(0xffffffffu, e.req, from), e.qo0 = __shfl_sync(0xffffffffu, e.qo0, from);
     e.q_len = __shfl_sync(0xffffffffu, e.q_len, from), e.kv_len = __shfl_sync(0xffffffffu, e.kv_len, from);
@@ -47,8 +47,10 @@ __device__ __forceinline__ ChunkEntry entry_of_lane(ChunkEntry e, int from) {
 
 // The entry that the CTAs of grid z take, by a whole warp: among 32 neighbouring ones
 // that of the z-th longest context, so that the short ones fill the gaps at the end.
-// (16 chunks of up to 448 tokens over up to 1500 states 41.7 us, in their own order
-// 48.3; 16 prompts of up to 2048 tokens at up to 6K 724 and 739.)
+// (16 chunks of up to 448 tokens over up to 1500 states 37.9 us, in their own order
+// 41.5; 4 x 2048 tokens at 8K to 16K 792 and 804 at head_dim 64, 914 either way at
+// 128; entries of one length pay for the look at all 32: 8 prompts of 2048 tokens
+// 275 us, 271 in their own order.)
 // report: the warp of grid z looks at all 32 (one does for each 32).
 __device__ __forceinline__ ChunkEntry load_longest_entry(const ChunkParams &p, int z, bool report) {
     const int lane = threadIdx.x & 31, b = (z & ~31) + lane, at = z & 31;

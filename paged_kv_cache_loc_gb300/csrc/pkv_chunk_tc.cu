@@ -9,8 +9,10 @@
 //   S = Q K^T  (tcgen05.mma, fp32 in tensor memory), P = 2^(S - m) as bf16 over
 //   S's columns (head_dim 64: beside them), O += P V (P read from tensor memory).
 // The two tiles share every K/V tile, and the tensor core works on one while the
-// softmax runs on the other.  Every CTA fetches its own K/V tiles: 64 KB in 1.4 us
-// on each SM, 7 TB/s together, which is about what the SMs can fetch, from L2 or not.
+// softmax runs on the other.  Every CTA fetches its own K/V tiles: 64 KB in 1.5 us
+// on each SM, 6.6 TB/s together, near the 7 to 8 that the SMs fetch at most, from L2
+// or not.  4 x 2048 tokens at 8K to 16K, 32 / 8 heads of 128: 914 to 919 us, 1650
+// TFLOP/s; of 64: 790 us, 957 TFLOP/s.
 // Warps hand over through mbarriers, every wait bounded:
 //   8 softmax warps, one thread per row: the row maximum needs no exchange;
 //   one warp that issues the products;
@@ -240,8 +242,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
                     ok = L::kOwnP || (wait_v(0) && (n_tiles == 1 || wait_k(1)));
                 }
                 // P in columns of its own (head_dim 64 leaves 64): S of the next tiles runs
-                // as soon as the last is read, while the softmax works on it (4 x 2048
-                // tokens at 8K to 16K 724 us, 761 with P over S)
+                // as soon as the last is read, while the softmax works on it (16 chunks of
+                // up to 448 tokens over up to 1500 states 37.9 us, 40.5 with P over S; 8 x
+                // 512 tokens at 2K 96.0 and 96.7, but 4 x 2048 at 8K to 16K 792 and 781)
                 for (int j = 0; L::kOwnP && ok && j < n_tiles; ++j) {
                     const int slot = j % kSlots, slot1 = (j + 1) % kSlots;
                     if (j + 1 < n_tiles) {
@@ -366,7 +369,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ M
         bool live = busy;
         // A look at a barrier ahead of its wait, whose answer takes some 200 cycles while
         // the tensor core reads shared memory (head_dim 64, 4 x 2048 tokens at 8K to
-        // 16K: 695 us, 724 without).
+        // 16K: 792 us, 795 without; 16 chunks of up to 448 tokens 37.9 and 38.8).
         auto look = [&](int i, int parity) -> bool {
             uint32_t ok;
             asm volatile(

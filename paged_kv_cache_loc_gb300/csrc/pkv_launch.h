@@ -395,7 +395,7 @@ cudaError_t launch_rope_kv_write(const KvWriteParams &p, cudaStream_t s);
 cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t s);
 cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t s);
 void page_runs_units(PageRuns *r);
-cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t s);
+cudaError_t launch_copy_pages(const CopyPagesParams &p, cudaStream_t s);
 cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t s);
 cudaError_t launch_release(const ReleaseParams &p, int sms, cudaStream_t s);
 cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t s);

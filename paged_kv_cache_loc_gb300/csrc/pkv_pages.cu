@@ -550,16 +550,22 @@ void page_runs_units(PageRuns *r) {
     r->layer_units = 2 * r->page_units + bound_units;
 }
 
-cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t s) {
+cudaError_t launch_copy_pages(const CopyPagesParams &p, cudaStream_t s) {
+    // a CTA per piece of 32 KB, which the hardware hands out as others end (2.3 GB of pages
+    // of 16: 337 us; 342 with eight CTAs per SM that go on to their next pieces.  Runs of
+    // 2 KB, 1024 pages of one slot in 32 layers, 281 and 238)
     const int64_t units = p.n * p.runs.n_layers * p.runs.layer_units;
     const int64_t most = 1 << 20;
     copy_pages_kernel<<<static_cast<unsigned>(units < most ? units : most), kThreads, 0, s>>>(p);
-    (void)sms;
     return cudaGetLastError();
 }
 
 cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t s) {
-    // CTAs enough for eight on an SM, none with less than one step of a full page's copy
+    // CTAs enough for eight on an SM, none with less than one step of a full page's copy.
+    // Where a page is small and the parent long, the rows of the tables are then the work
+    // of few CTAs (one child of 128K positions in pages of 16, one layer: 35 us, 6 with
+    // CTAs by the row's length; 8 x 128K in pages of one 228 and 12; with a model's layers
+    // it makes no difference: 256 children of 0.5K to 4K, 8 layers, 27 either way)
     const int64_t chunks = p.runs.n_layers * (2 * p.runs.page_chunks + (p.runs.page_bounds ? p.runs.bound_chunks : 0));
     int64_t slices = (chunks + kPiece - 1) / kPiece;
     const int batch = p.batch > 0 ? p.batch : 1;
@@ -571,7 +577,12 @@ cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t s) {
 }
 
 cudaError_t launch_release(const ReleaseParams &p, int sms, cudaStream_t s) {
-    // up to 64K table entries: the cluster that collects the pages drops the references too
+    // Up to 64K table entries the cluster that collects the pages drops the references
+    // too, a warp per row: one launch in place of two saves the host 2.3 us of 11.5 a
+    // call.  The GPU takes longer by it, the more the longer the rows: 64 requests that
+    // give up to 12 positions each 10.3 us against 9.6 in two launches, 64 x 255 pages 14.4
+    // and 10.6, 512 x 127 17.4 and 11.4, one row of 4095 pages 59 and 10, of 65535 746 and 12.
+    // Above, two launches are far ahead (512 rows of 0.1K to 2K pages 30 us, 87 in one).
     if (static_cast<int64_t>(p.batch) * p.max_pages <= 1 << 16)
         return launch(collect_kernel<true>, p, dim3(kScanCluster), kScanThreads, kScanCluster, false, s);
     int64_t x = (static_cast<int64_t>(p.max_pages) + kThreads - 1) / kThreads;

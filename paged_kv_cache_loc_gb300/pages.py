@@ -179,7 +179,8 @@ def chunk_workspace_bytes(cache: KVCache, n_rows: int, n_heads: int, max_q_len: 
 
 
 def chunk_workspace(cache: KVCache, n_rows: int, n_heads: int, max_q_len: int) -> Workspace:
-    """A workspace for paged_chunk calls of these sizes.  Other calls take what fits."""
+    """A workspace for paged_chunk calls of these sizes.  Other calls cut their
+    contexts into the pieces that fit, or not at all: the same result, later."""
     need = chunk_workspace_bytes(cache, n_rows, n_heads, max_q_len)
     if need == 0:
         raise ValueError("sizes that paged_chunk refuses")

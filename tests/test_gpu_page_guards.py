@@ -9,7 +9,8 @@ import torch
 import paged_kv_cache_loc_gb300 as pkv
 from test_gpu_chunk import DTYPES, case, check, want
 from test_gpu_chunk import host as chunk_host
-from test_gpu_pages import (compact_case, dev, error, clean, gpu, host, run_compact, want_compact)  # noqa: F401 (gpu: a fixture)
+from test_gpu_pages import (clean, compact_case, dev, error, fork_case, gpu, host, run_compact, run_fork,  # noqa: F401 (gpu: a fixture)
+                            want_compact)
 
 pytestmark = pytest.mark.gpu
 
@@ -231,3 +232,31 @@ def test_rows_before_the_first_entry_stay(dtype, q_lens, lens):
         check(c.run(o=o, workspace=ws), ref, tol)
         assert (o[:13] == 3.25).all() and (o[13 + sum(q_lens):] == 3.25).all()
     clean()
+
+
+def test_fork_bad_last_page_of_the_parent():
+    """The child has a page of its own where the parent's partly filled one is
+    none of the pool's, without a copy: nothing of another page is written."""
+    p, parents = fork_case(np.random.default_rng(4), [40], 1, 16)
+    row, child = int(parents[0]), int(host(p.cache.req_pool_indices)[0])
+    p.cache.seq_lens.copy_(dev([40]))
+    p.table[row, 2] = -4
+    before, taken = p.data, int(p.free[2])
+    run_fork(p, parents)
+    assert error() == -4
+    assert host(p.table)[child, :3].tolist() == [*host(p.table)[row, :2].tolist(), taken] and int(p.end) == 3
+    p.same_data(*before)
+
+
+def test_fork_a_place_outside_the_list():
+    """No page is taken: the entries' partly filled pages are -1."""
+    for start in (-1, 10**6):
+        p, parents = fork_case(np.random.default_rng(4), [40, 32], 1, 16)
+        p.cache.seq_lens.copy_(dev([40, 32]))
+        order = host(p.cache.req_pool_indices)
+        p.start = dev([start])
+        before = p.data
+        run_fork(p, parents)
+        assert error() == start and int(p.end) == p.free.numel()
+        assert host(p.table)[order[0], 2] == -1
+        p.same_data(*before)
