@@ -10,14 +10,14 @@
 // (m, l), joined as o = sum_s l_s 2^(m_s - M) o_s / sum_s l_s 2^(m_s - M).
 //
 // fp32: the tensor cores have no product of 24-bit factors (three bf16 parts of each
-// and six products would make one; not built), so this runs on the FMA units.  A CTA of 256 threads takes 64 rows (position,
-// head in group; 16 or 32 where an entry has no more) and 64 keys at a time; a
-// thread holds a 4 x 4 block of scores and a 4 x (D / 16) block of o, so a
-// 16-byte shared-memory load feeds eight FMAs (two lanes to an instruction).  K of
-// the next tile is copied while the softmax and P V run, V while the next scores
-// do.  4 x 512 tokens at 1K to 2K positions, 32 / 8 heads of 128: 1083 us, 40
-// TFLOP/s of the units' 74 to 80; the loads from shared memory take three quarters
-// of the time that the products do.
+// and six products would make one; not built), so this runs on the FMA units.  A CTA
+// of 256 threads takes 64 rows (position, head in group; 16 or 32 where an entry has
+// no more) and 64 keys at a time; a thread holds a 4 x 4 block of scores and a 4 x
+// (D / 16) block of o, so a 16-byte shared-memory load feeds eight FMAs (two lanes
+// to an instruction).  K of the next tile is copied while the softmax and P V run, V
+// while the next scores do.  4 x 512 tokens at 1K to 2K positions, 32 / 8 heads of
+// 128: 1083 us, 40 TFLOP/s of the units' 74 to 80; the loads from shared memory take
+// three quarters of the time that the products do.
 #include <atomic>
 #include <type_traits>
 
