@@ -16,7 +16,7 @@
 // (D / 16) block of o, so a 16-byte shared-memory load feeds eight FMAs (two lanes
 // to an instruction).  K of the next tile is copied while the softmax and P V run, V
 // while the next scores do.  4 x 512 tokens at 1K to 2K positions, 32 / 8 heads of
-// 128: 1083 us, 40 TFLOP/s of the units' 74 to 80; the loads from shared memory take
+// 128: 1060 us, 40 TFLOP/s of the units' 74 to 80; the loads from shared memory take
 // three quarters of the time that the products do.
 #include <atomic>
 #include <type_traits>
